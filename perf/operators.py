@@ -280,7 +280,8 @@ def _put(st, part, scale, at, off):
     x = x.float()
     amax = x.abs().amax(2).clamp(AMAX_FLOOR, AMAX_CEIL)
     st[scale][at, :, off] = amax / E4M3_MAX
-    x = (x * (E4M3_MAX / amax)[:, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+    back = torch.full_like(amax, E4M3_MAX) / amax  # one rounding: a number over a tensor is a reciprocal's multiple
+    x = (x * back[:, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
     st[part].view(torch.uint8)[at, :, off] = x.view(torch.uint8)
 
 
