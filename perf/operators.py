@@ -187,7 +187,7 @@ def prepare(case, seed):
     if case["kv"] == "bf16":
         st["K"], st["V"] = (_normal((pages, k, page, d), g) for _ in range(2))
     else:
-        st["K"], st["V"] = (_normal((pages, k, page, d), g).mul_(80).to(torch.float8_e4m3fn) for _ in range(2))
+        st["K"], st["V"] = (_normal((pages, k, page, d), g).mul_(80).clamp_(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn) for _ in range(2))
         st["k_scale"], st["v_scale"] = (torch.rand((pages, k, page), generator=g, device="cuda") * 0.02 + 0.004
                                         for _ in range(2))
     if case["op"] == "read":
