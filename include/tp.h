@@ -99,7 +99,9 @@ enum {
     TP_OP_LAYER = 2,
     TP_OP_MLP_BACKWARD = 3,
     TP_OP_ATTN_BACKWARD = 4,
-    TP_OP_LAYER_BACKWARD = 5
+    TP_OP_LAYER_BACKWARD = 5,
+    TP_OP_ATTN_PAGED = 6,
+    TP_OP_ATTN_CACHED = 7
 };
 
 /* Index tables tp_plan_shard_table exports (int32, row-major):
@@ -186,7 +188,9 @@ TP_API int tp_plan_shard_table(tp_plan_t plan, int which, int32_t* out, int64_t 
 /* Read and clear the plan's device status word (synchronises `stream`).
  * TP_OK; TP_ERR_DEVICE_TIMEOUT when a kernel's bounded wait gave up;
  * TP_ERR_CUDA when a kernel found its shared-memory layout does not fit its
- * allocation and stopped without computing (its outputs are not written). */
+ * allocation and stopped without computing (its outputs are not written);
+ * TP_ERR_INVALID_ARG when a call over a tp_kv_cache met a position whose page
+ * is not one of the cache's (see tp_kv_cache). */
 TP_API int tp_get_device_status(tp_plan_t plan, void* stream);
 
 /* Thread-local description of the last error (never NULL). */
@@ -519,6 +523,139 @@ TP_API int tp_layer_forward(tp_plan_t plan, const tp_bf16* X, const tp_layer_wei
 TP_API int tp_layer_forward_traced(tp_plan_t plan, const tp_bf16* X, const tp_layer_weights* w,
                                    tp_bf16* Y, void* workspace, size_t ws_bytes, void* stream,
                                    void* const* events, int n_events);
+
+/* ------------------------------------------------------------ paged key/value cache */
+
+/* Element type of a key/value cache.
+ * BF16: the projections' values as they are.
+ * E4M3: 8-bit codes (4 exponent and 3 fraction bits, largest 448) with one
+ *       fp32 scale per token and KV head, value = code * scale. */
+enum { TP_KV_BF16 = 0, TP_KV_E4M3 = 1 };
+
+/* A cache of the keys and values of many sequences in pages of page_size
+ * tokens, and one call's view of it: which rows of the projection buffer are
+ * whose new tokens, and how long each sequence is with them.  Plain data, read
+ * during the call that takes it; the pointers are device memory of the
+ * caller's.  The page is the outermost axis, so the cache of shard i is the
+ * view of its KV heads (TP_TABLE_SHARD_KV); every KV head is stored once, also
+ * where the projection buffer holds replicas of it (k < t).
+ *
+ * Sequence s owns the rows q_start[s] .. q_start[s + 1] - 1 of the projection
+ * buffer.  They are its newest tokens: the i-th of its n new tokens stands at
+ * position kv_len[s] - n + i.  Position p of sequence s lives at row
+ * p % page_size of page page_table[s * max_pages + p / page_size].  Sequences
+ * may share pages that a call only reads; two tokens of one call that are
+ * written to the same place leave one of them there, unspecified which.
+ *
+ * q_start, kv_len and page_table are read on the device when the call runs, so
+ * a captured call sees what they hold at replay.  They are checked there: row
+ * numbers are clamped to [0, M] and a position whose page is not in
+ * [0, n_pages), or that lies past the page table, is neither read nor written
+ * (a key there counts as zero bytes, a token there is dropped), and
+ * tp_get_device_status then reports TP_ERR_INVALID_ARG. */
+typedef struct {
+    void *K, *V;                /* [n_pages][k][page_size][d], TP_KV_* elements       */
+    float *k_scale, *v_scale;   /* E4M3: [n_pages][k][page_size]; BF16: NULL          */
+    const int32_t* page_table;  /* [n_seqs][max_pages]                                */
+    const int32_t* q_start;     /* [n_seqs + 1], ascending; (not read by
+                                   tp_kv_cache_read)                                  */
+    const int32_t* kv_len;      /* [n_seqs], with this call's new tokens              */
+    int64_t n_pages;            /* >= 1                                               */
+    int32_t n_seqs;             /* >= 0                                               */
+    int32_t max_pages;          /* row length of page_table, >= 1                     */
+    int32_t page_size;          /* 16, 32, 64 or 128                                  */
+    int32_t kv_dtype;           /* TP_KV_*                                            */
+    int32_t kv_heads, head_dim; /* k and d, the plan's                                */
+    int32_t max_new;            /* the most new tokens that a sequence has in this
+                                   call, 0 = not known: chooses the attention kernel,
+                                   never the result's meaning                         */
+} tp_kv_cache;
+
+/* Host-only validation of a cache against a configuration that passes
+ * tp_config_check: the rules every call below checks, the geometry, types and
+ * alignment, with no device work (usable without a GPU).  needs_rows: 1 to
+ * require q_start (every call but tp_kv_cache_read). */
+TP_API int tp_kv_cache_check(const tp_config* cfg, const tp_kv_cache* cache, int needs_rows);
+
+/* Append: the K and V of every sequence's new tokens, out of the projection
+ * buffer QKV ([M][t * W], as tp_qkv_forward writes it), into the cache.
+ * BF16 copies.  E4M3 quantises each token and KV head on its own:
+ *   amax  = max_j |x_j| held to [2^-100, largest finite bf16], NaN ignored
+ *   scale = amax / 448,  code_j = e4m3(x_j * (448 / amax))
+ * with the quotients and the product rounded to fp32 and the code rounded to
+ * nearest even, at most 448 in magnitude; NaN stays NaN.  Rows of QKV that no
+ * sequence owns are not read, other cache rows are left as they are. */
+TP_API int tp_kv_cache_write(tp_plan_t plan, const tp_kv_cache* cache, const tp_bf16* QKV, void* stream);
+
+/* Read back: K_out[s][p], V_out[s][p] = the cached key and value of position
+ * p < min(kv_len[s], max_len) of sequence s, as bf16 (E4M3: code * scale in
+ * fp32, rounded once).  K_out, V_out: device [n_seqs][max_len][k][d] bf16; rows
+ * past a sequence's length are left as they are. */
+TP_API int tp_kv_cache_read(tp_plan_t plan, const tp_kv_cache* cache, int64_t max_len, tp_bf16* K_out,
+                            tp_bf16* V_out, void* stream);
+
+/* Causal GQA attention of every sequence's new tokens over the cache, which
+ * holds their own keys and values too (tp_kv_cache_write comes first).  For
+ * query head j of a new token at position p, with g = j / (a/k):
+ *   O = softmax_{p' <= p} (Q K_g[p'] / sqrt d) V_g[p'],  fp32 softmax;
+ * a token with nothing to see (a negative position) gets zeros.  One call
+ * serves single tokens, drafted tokens and chunks of prompts mixed.
+ * QKV: [M][t * W], only Q is read; O: device [M][a d] as
+ * tp_attn_core_forward's; rows that no sequence owns are left as they are.
+ * A non-finite V of a new token may reach the outputs of earlier tokens of the
+ * same sequence in this call (0 * inf), never another sequence's; what the
+ * pages hold past a sequence's length has no influence.
+ * workspace >= tp_plan_workspace_bytes(TP_OP_ATTN_PAGED); its contents need no
+ * preparation, and calls that overlap on the GPU need one each. */
+TP_API int tp_attn_paged_forward(tp_plan_t plan, const tp_kv_cache* cache, const tp_bf16* QKV, tp_bf16* O,
+                                 void* workspace, size_t ws_bytes, void* stream);
+
+/* The attention block over a cache, tp_attn_forward's serving form: QKV
+ * colwise, append to the cache, attention over it, o_proj rowwise, g:
+ * out = sum_i O_i Wo_i^T (+ residual).  The plan's tokens are the rows M of X;
+ * its batch and seq do not apply.  The residual and o_proj of rows that no
+ * sequence owns are computed from zeros (O = 0 there).  Other arguments as
+ * tp_attn_forward.  workspace >= tp_plan_workspace_bytes(TP_OP_ATTN_CACHED). */
+TP_API int tp_attn_cached_forward(tp_plan_t plan, const tp_kv_cache* cache, const tp_bf16* X,
+                                  const tp_bf16* Wq, const tp_bf16* Wk, const tp_bf16* Wv, const tp_bf16* Wo,
+                                  const tp_bf16* residual, void* partials, tp_bf16* out, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/* Verification of drafted tokens against the target's probabilities, from
+ * given random numbers (speculative sampling).  The rows
+ * q_start[s] .. q_start[s + 1] - 1 of sequence s hold, in ids, a token that is
+ * already settled and then its drafts; row r's logits are the target's for the
+ * token behind ids[r], and draft_logits' row r is the distribution that
+ * ids[r + 1] was drawn from (a sequence's last row of draft_logits is not
+ * read).  With T = temperature[s], p = softmax(logits / T) and
+ * q = softmax(draft_logits / T), drafts are taken in order while
+ *   u[r] * q_r(x) < p_r(x),   x = ids[r + 1];
+ * then one more token is drawn at row r, where the first draft was refused or
+ * behind the last: with w = max(0, p_r - q_r) (w = p_r behind the last draft,
+ * or where that leaves nothing), the token argmax_v w_v / noise[s][v], the
+ * lowest index among equals.  With noise drawn from the exponential
+ * distribution that is a draw from w; the tokens then follow the target's
+ * distribution.  T <= 0 (or NaN) is greedy: a draft is taken if it is the
+ * first of the row's largest logits, and that index is the token drawn.
+ * A sequence without drafts is ordinary sampling from one row.
+ *
+ * logits, draft_logits: device [M][v] bf16, vocabulary-sharded like
+ * tp_vocab_logits_forward's (draft_logits may be NULL where no sequence has
+ * drafts or all are greedy: it then counts as a distribution that is 0
+ * everywhere).  ids: device [M] int32; a draft outside [0, v) is refused.
+ * q_start: device [n_seqs + 1] int32, ascending, clamped to [0, M].
+ * temperature: device [n_seqs] fp32, NULL = 1.  u: device [M] fp32 in [0, 1).
+ * noise: device [n_seqs][v] fp32, > 0; NULL only if every sequence is greedy
+ * (it then counts as 1).
+ * accepted: device [n_seqs] int32, drafts taken (0 for a sequence without
+ * rows).  tokens: device [M] int32: row q_start[s] + i holds the i-th settled
+ * token, the taken drafts and then the drawn one; -1 behind them; rows that
+ * no sequence owns are left as they are.  A row without any probability (all
+ * logits -inf) draws -1.  (v / t) % 8 == 0. */
+TP_API int tp_vocab_verify_drafts(const tp_bf16* logits, const tp_bf16* draft_logits, int64_t M, int64_t v,
+                                  int32_t t, const int32_t* ids, const int32_t* q_start, int32_t n_seqs,
+                                  const float* temperature, const float* u, const float* noise,
+                                  int32_t* accepted, int32_t* tokens, void* stream);
 
 /* ------------------------------------------------------------ self test */
 

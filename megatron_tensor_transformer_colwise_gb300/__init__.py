@@ -34,7 +34,10 @@ __all__ = [
     "tp_packed_shard_table", "tp_packed_colwise_forward", "tp_vocab_embedding_forward",
     "tp_vocab_logits_forward", "tp_vocab_parallel_cross_entropy", "tp_sp_all_gather",
     "tp_sp_reduce_scatter", "tp_mlp_forward_train", "tp_mlp_backward", "tp_plan_attn_saved_bytes",
-    "tp_attn_forward_train", "tp_attn_backward", "tp_layer_backward", "EXPORTED",
+    "tp_attn_forward_train", "tp_attn_backward", "tp_layer_backward", "TPKVCache", "make_kv_cache",
+    "TP_KV_BF16", "TP_KV_E4M3", "TP_OP_ATTN_PAGED", "TP_OP_ATTN_CACHED", "tp_kv_cache_check", "tp_kv_cache_write",
+    "tp_kv_cache_read", "tp_attn_paged_forward", "tp_attn_cached_forward", "tp_vocab_verify_drafts",
+    "EXPORTED",
 ]
 
 TP_OK = 0
@@ -49,7 +52,8 @@ TP_ACT_GELU_ERF, TP_ACT_GELU_TANH, TP_ACT_SWIGLU, TP_ACT_NONE = 0, 1, 2, 3
 TP_REDUCE_FUSED, TP_REDUCE_PARTIALS = 0, 1
 TP_F32, TP_BF16 = 0, 1
 (TP_OP_MLP, TP_OP_ATTN, TP_OP_LAYER, TP_OP_MLP_BACKWARD, TP_OP_ATTN_BACKWARD,
- TP_OP_LAYER_BACKWARD) = range(6)
+ TP_OP_LAYER_BACKWARD, TP_OP_ATTN_PAGED, TP_OP_ATTN_CACHED) = range(8)
+TP_KV_BF16, TP_KV_E4M3 = 0, 1
 (TP_TABLE_FFN_SHARDS, TP_TABLE_Q_HEAD_SHARD, TP_TABLE_Q_HEAD_KV, TP_TABLE_SHARD_KV,
  TP_TABLE_QKV_COLUMNS) = range(5)
 
@@ -84,6 +88,18 @@ class TPLayerWeights(C.Structure):
 
 class TPLayerGrads(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("dWq", "dWk", "dWv", "dWo", "dW1", "dW3", "dW2")]
+
+
+class TPKVCache(C.Structure):
+    """tp_kv_cache of the header; make_kv_cache fills one from tensors."""
+
+    _fields_ = [
+        ("K", C.c_void_p), ("V", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+        ("page_table", C.c_void_p), ("q_start", C.c_void_p), ("kv_len", C.c_void_p),
+        ("n_pages", C.c_int64),
+        ("n_seqs", C.c_int32), ("max_pages", C.c_int32), ("page_size", C.c_int32),
+        ("kv_dtype", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("max_new", C.c_int32),
+    ]
 
 
 _VP = C.c_void_p
@@ -125,6 +141,12 @@ _SIGS = {
     "tp_sp_all_gather": [_VP, C.c_int32, C.c_int32, C.c_int32, C.c_int32, _VP, _VP],
     "tp_sp_reduce_scatter": [_VP, C.c_int, C.c_int32, C.c_int32, C.c_int32, C.c_int32, _VP, _VP, _VP,
                              C.c_float, _VP],
+    "tp_kv_cache_check": [C.POINTER(TPConfig), C.POINTER(TPKVCache), C.c_int],
+    "tp_kv_cache_write": [_VP, C.POINTER(TPKVCache), _VP, _VP],
+    "tp_kv_cache_read": [_VP, C.POINTER(TPKVCache), C.c_int64, _VP, _VP, _VP],
+    "tp_attn_paged_forward": [_VP, C.POINTER(TPKVCache), _VP, _VP, _VP, C.c_size_t, _VP],
+    "tp_attn_cached_forward": [_VP, C.POINTER(TPKVCache)] + [_VP] * 9 + [C.c_size_t, _VP],
+    "tp_vocab_verify_drafts": [_VP, _VP, C.c_int64, C.c_int64, C.c_int32, _VP, _VP, C.c_int32] + [_VP] * 6,
 }
 EXPORTED = tuple(sorted(list(_SIGS) + ["tp_last_error"]))
 
@@ -423,3 +445,68 @@ def tp_sp_reduce_scatter(partials, partial_dtype: int, t: int, batch: int, seq: 
                          residual_sp, out_sp, xn_sp=None, eps: float = 1e-5, stream=None) -> None:
     _call("tp_sp_reduce_scatter", _p(partials), partial_dtype, t, batch, seq, h, _p(residual_sp),
           _p(out_sp), _p(xn_sp), eps, _s(stream))
+
+
+def make_kv_cache(K, V, page_table, q_start, kv_len, k_scale=None, v_scale=None, max_new: int = 0) -> TPKVCache:
+    """tp_kv_cache of contiguous tensors: K, V [n_pages][k][page_size][d] in bf16, or in 8 bits
+    (float8_e4m3fn or uint8 codes) with fp32 scales [n_pages][k][page_size]; int32 page_table
+    [n_seqs][max_pages], q_start [n_seqs + 1] (None: tp_kv_cache_read alone) and kv_len [n_seqs].
+    The object keeps the tensors alive; q_start, kv_len and page_table may be rewritten in place
+    between calls."""
+    import torch
+    code = TP_KV_BF16 if K.dtype == torch.bfloat16 else TP_KV_E4M3
+    if K.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8) or V.dtype != K.dtype:
+        raise ValueError(f"K and V must both be bfloat16, float8_e4m3fn or uint8 (got {K.dtype}, {V.dtype})")
+    if K.dim() != 4 or V.shape != K.shape:
+        raise ValueError("K and V must have one shape [n_pages][kv_heads][page_size][head_dim]")
+    if (code == TP_KV_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale belong to an 8-bit cache, and to no other")
+    for x in (k_scale, v_scale):
+        if x is not None and (x.dtype != torch.float32 or x.shape != K.shape[:3]):
+            raise ValueError("scales must be float32 [n_pages][kv_heads][page_size]")
+    n_seqs = kv_len.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != n_seqs or (q_start is not None and q_start.shape != (n_seqs + 1,)):
+        raise ValueError("page_table [n_seqs][max_pages], q_start [n_seqs + 1] and kv_len [n_seqs] disagree")
+    every = [x for x in (K, V, k_scale, v_scale, page_table, q_start, kv_len) if x is not None]
+    if any(x.dtype != torch.int32 for x in (page_table, q_start, kv_len) if x is not None):
+        raise ValueError("page_table, q_start and kv_len must be int32")
+    if not all(x.is_contiguous() for x in every):
+        raise ValueError("the cache's tensors must be contiguous")
+    c = TPKVCache(_p(K), _p(V), _p(k_scale), _p(v_scale), _p(page_table), _p(q_start), _p(kv_len), K.shape[0],
+                  n_seqs, page_table.shape[1], K.shape[2], code, K.shape[1], K.shape[3], max_new)
+    c.tensors = every
+    return c
+
+
+def tp_kv_cache_check(cfg: TPConfig, cache: TPKVCache, needs_rows: bool = True) -> int:
+    """Host-only validation; returns the TP_* code (does not raise)."""
+    return lib().tp_kv_cache_check(C.byref(cfg), C.byref(cache), 1 if needs_rows else 0)
+
+
+def tp_kv_cache_write(plan: Plan, cache: TPKVCache, QKV, stream=None) -> None:
+    """Append the new tokens' keys and values to the cache."""
+    _call("tp_kv_cache_write", plan.handle, C.byref(cache), _p(QKV), _s(stream))
+
+
+def tp_kv_cache_read(plan: Plan, cache: TPKVCache, max_len: int, K_out, V_out, stream=None) -> None:
+    """Cached keys and values of every sequence as bf16 [n_seqs][max_len][k][d]."""
+    _call("tp_kv_cache_read", plan.handle, C.byref(cache), max_len, _p(K_out), _p(V_out), _s(stream))
+
+
+def tp_attn_paged_forward(plan: Plan, cache: TPKVCache, QKV, O, workspace, ws_bytes: int, stream=None) -> None:
+    """Causal GQA attention of the new tokens over the cache."""
+    _call("tp_attn_paged_forward", plan.handle, C.byref(cache), _p(QKV), _p(O), _p(workspace), ws_bytes, _s(stream))
+
+
+def tp_attn_cached_forward(plan: Plan, cache: TPKVCache, X, Wq, Wk, Wv, Wo, residual, partials, out, workspace,
+                           ws_bytes: int, stream=None) -> None:
+    """The attention block over a cache: QKV, append, attention, o_proj, g."""
+    _call("tp_attn_cached_forward", plan.handle, C.byref(cache), _p(X), _p(Wq), _p(Wk), _p(Wv), _p(Wo),
+          _p(residual), _p(partials), _p(out), _p(workspace), ws_bytes, _s(stream))
+
+
+def tp_vocab_verify_drafts(logits, draft_logits, M: int, v: int, t: int, ids, q_start, n_seqs: int, temperature, u,
+                           noise, accepted, tokens, stream=None) -> None:
+    """Take or refuse drafted tokens against the target's probabilities and draw the next one."""
+    _call("tp_vocab_verify_drafts", _p(logits), _p(draft_logits), M, v, t, _p(ids), _p(q_start), n_seqs,
+          _p(temperature), _p(u), _p(noise), _p(accepted), _p(tokens), _s(stream))

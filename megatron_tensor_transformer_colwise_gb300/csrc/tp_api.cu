@@ -120,6 +120,7 @@ struct Layout {
     size_t lug = 0;                                          // MLP pre-activations
     size_t lshared = 0;  // max(MLP backward, attention backward workspaces, [M][f] bf16)
     size_t lspx = 0, lspdy = 0, lspdx = 0;  // sequence parallel: X, dY, dX in token order [M][h] bf16
+    size_t paged = 0;  // paged attention: partial results of split work
 };
 
 int64_t seq_pad_of(const tp_plan_s* p) { return (p->cfg.seq + 63) / 64 * 64; }
@@ -136,7 +137,9 @@ Layout layout_of(const tp_plan_s* p, int op) {
         if (p->mlp_pieces > 1) L.mpart = align_up(static_cast<size_t>(p->mlp_pieces) * M * p->h * 4);
         L.mcnt = align_up(static_cast<size_t>(tpi::mlp_fused_counter_words(p->M, p->h, p->f)) * 4);
     }
-    if (op == TP_OP_ATTN || op == TP_OP_LAYER) {
+    if ((op == TP_OP_ATTN_PAGED || op == TP_OP_ATTN_CACHED) && p->has_attn)
+        L.paged = align_up(tpi::attn_paged_scratch_bytes(static_cast<int>(p->d)));
+    if (op == TP_OP_ATTN || op == TP_OP_LAYER || op == TP_OP_ATTN_CACHED) {
         if (p->has_attn) {
             L.qkv = align_up(M * p->t * p->qkv_w * 2);
             L.o = align_up(M * p->a * p->d * 2);
@@ -190,7 +193,7 @@ Layout layout_of(const tp_plan_s* p, int op) {
 size_t layout_total(const Layout& L) {
     return L.y + L.mpart + L.mcnt + L.qkv + L.o + L.xn + L.h1 + L.partials + L.ss + L.full + L.ug + L.dug + L.hact + L.bdo +
            L.bdstat + L.bdq + L.bdqkv + L.bqkv + L.bo + L.blse + L.lxn1 + L.lh1 + L.lxn2 + L.ldxn + L.ldh1 +
-           L.lqkv + L.lo + L.llse + L.lug + L.lshared + L.lspx + L.lspdy + L.lspdx;
+           L.lqkv + L.lo + L.llse + L.lug + L.lshared + L.lspx + L.lspdy + L.lspdx + L.paged;
 }
 
 int check_ws(const tp_plan_s* p, int op, void* ws, size_t bytes) {
@@ -485,7 +488,7 @@ int tp_plan_destroy(tp_plan_t plan) {
 
 int tp_plan_workspace_bytes(tp_plan_t plan, int op, size_t* bytes) {
     if (!plan || !bytes) return fail(TP_ERR_INVALID_ARG, "plan and bytes must be non-NULL");
-    if (op < TP_OP_MLP || op > TP_OP_LAYER_BACKWARD) return fail(TP_ERR_INVALID_ARG, "unknown op %d", op);
+    if (op < TP_OP_MLP || op > TP_OP_ATTN_CACHED) return fail(TP_ERR_INVALID_ARG, "unknown op %d", op);
     *bytes = layout_total(layout_of(plan, op));
     return TP_OK;
 }
@@ -544,8 +547,10 @@ int tp_get_device_status(tp_plan_t plan, void* stream) {
         cudaStreamSynchronize(s);
         if (word & 1u)
             return fail(TP_ERR_DEVICE_TIMEOUT, "a device-side wait exceeded its limit (status 0x%x)", word);
-        return fail(TP_ERR_CUDA, "a kernel found its shared-memory layout does not fit (status 0x%x)",
-                    word);
+        if (word & 2u)
+            return fail(TP_ERR_CUDA, "a kernel found its shared-memory layout does not fit (status 0x%x)",
+                        word);
+        return fail(TP_ERR_INVALID_ARG, "a position's page is not one of the cache's (status 0x%x)", word);
     }
     return TP_OK;
 }
@@ -1502,6 +1507,182 @@ extern "C" int tp_vocab_parallel_cross_entropy(const tp_bf16* logits, int64_t M,
     if ((rc = check_vocab(M, v, t, 8))) return rc;
     std::string err;
     return run(tpi::vocab_ce_launch(logits, M, v, t, labels, stats, loss, as_stream(stream), &err), err);
+}
+
+// ---------------------------------------------------------------------------
+// Paged key/value cache: append, read back, attention over it.
+namespace {
+
+int check_cache(const tp_plan_s* plan, const tp_kv_cache* c, bool needs_rows) {
+    if (!plan->has_attn) return fail(TP_ERR_INVALID_ARG, "the plan has no attention (n_heads == 0)");
+    if (!c) return fail(TP_ERR_INVALID_ARG, "cache is NULL");
+    int rc;
+    if ((rc = need_ptr(c->K, "cache K")) || (rc = need_ptr(c->V, "cache V"))) return rc;
+    if (c->kv_heads != plan->k || c->head_dim != plan->d)
+        return fail(TP_ERR_INVALID_ARG, "the cache has %d KV heads of dimension %d, the plan %lld of %lld", c->kv_heads,
+                    c->head_dim, (long long)plan->k, (long long)plan->d);
+    if (c->kv_dtype != TP_KV_BF16 && c->kv_dtype != TP_KV_E4M3)
+        return fail(TP_ERR_INVALID_ARG, "kv_dtype %d is not TP_KV_BF16(0) or TP_KV_E4M3(1)", c->kv_dtype);
+    if (c->kv_dtype == TP_KV_E4M3) {
+        if ((rc = need_ptr(c->k_scale, "cache k_scale")) || (rc = need_ptr(c->v_scale, "cache v_scale"))) return rc;
+    } else if (c->k_scale || c->v_scale) {
+        return fail(TP_ERR_INVALID_ARG, "k_scale and v_scale must be NULL unless kv_dtype is TP_KV_E4M3");
+    }
+    if (c->n_seqs < 0 || c->n_seqs > 1 << 20)
+        return fail(TP_ERR_INVALID_ARG, "n_seqs %d is not in [0, 2^20]", c->n_seqs);
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return fail(TP_ERR_UNSUPPORTED, "page_size %d: only 16, 32, 64 and 128 are built", c->page_size);
+    if (c->n_pages < 1 || c->n_pages > 0x7fffffffll)
+        return fail(TP_ERR_INVALID_ARG, "n_pages %lld is not in [1, 2^31)", (long long)c->n_pages);
+    if (c->max_pages < 1 || (int64_t)c->max_pages * c->page_size > (int64_t)1 << 30)
+        return fail(TP_ERR_INVALID_ARG, "max_pages %d x page_size %d is not in [1, 2^30] positions", c->max_pages,
+                    c->page_size);
+    if (c->max_new < 0) return fail(TP_ERR_INVALID_ARG, "max_new must be >= 0 (got %d)", c->max_new);
+    if ((rc = need_ptr(c->page_table, "page_table")) || (rc = need_ptr(c->kv_len, "kv_len")) ||
+        (needs_rows && (rc = need_ptr(c->q_start, "q_start"))))
+        return rc;
+    return TP_OK;
+}
+
+int paged_args(const tp_plan_s* plan, const tp_kv_cache* c, bool needs_rows, tpi::PagedArgs* out) {
+    if (!plan) return fail(TP_ERR_INVALID_ARG, "plan is NULL");
+    int rc;
+    if ((rc = check_device(plan)) || (rc = check_cache(plan, c, needs_rows))) return rc;
+    tpi::PagedArgs a;
+    a.K = c->K;
+    a.V = c->V;
+    a.k_scale = c->k_scale;
+    a.v_scale = c->v_scale;
+    a.e4m3 = c->kv_dtype == TP_KV_E4M3;
+    a.page_table = c->page_table;
+    a.q_start = c->q_start;
+    a.kv_len = c->kv_len;
+    a.n_pages = c->n_pages;
+    a.n_seqs = c->n_seqs;
+    a.max_pages = c->max_pages;
+    a.page_size = c->page_size;
+    a.max_new = c->max_new;
+    a.tokens = plan->M;
+    a.ld_qkv = plan->t * plan->qkv_w;
+    a.shard_w = plan->qkv_w;
+    a.q_w = plan->qw;
+    a.kv_w = plan->kvw;
+    a.heads = static_cast<int>(plan->a);
+    a.kv_heads = static_cast<int>(plan->k);
+    a.head_dim = static_cast<int>(plan->d);
+    a.t = static_cast<int>(plan->t);
+    a.status = plan->status;
+    a.timeout_ns = plan->timeout_ns;
+    *out = a;
+    return TP_OK;
+}
+
+int check_group(const tp_plan_s* plan) {
+    if (plan->a / plan->k > 128)
+        return fail(TP_ERR_UNSUPPORTED, "%lld query heads per KV head: at most 128 are built",
+                    (long long)(plan->a / plan->k));
+    return TP_OK;
+}
+
+}  // namespace
+
+extern "C" int tp_kv_cache_check(const tp_config* cfg, const tp_kv_cache* cache, int needs_rows) {
+    if (!cfg) return fail(TP_ERR_INVALID_ARG, "cfg is NULL");
+    tp_plan_s tmp;
+    const int rc = derive_plan(*cfg, &tmp);
+    return rc ? rc : check_cache(&tmp, cache, needs_rows != 0);
+}
+
+extern "C" int tp_kv_cache_write(tp_plan_t plan, const tp_kv_cache* cache, const tp_bf16* QKV, void* stream) {
+    tpi::PagedArgs a;
+    int rc;
+    if ((rc = paged_args(plan, cache, true, &a)) || (rc = need_ptr(QKV, "QKV"))) return rc;
+    a.QKV = QKV;
+    std::string err;
+    return run(tpi::kv_write_launch(a, as_stream(stream), &err), err);
+}
+
+extern "C" int tp_kv_cache_read(tp_plan_t plan, const tp_kv_cache* cache, int64_t max_len, tp_bf16* K_out,
+                                tp_bf16* V_out, void* stream) {
+    tpi::PagedArgs a;
+    int rc;
+    if ((rc = paged_args(plan, cache, false, &a)) || (rc = need_ptr(K_out, "K_out")) ||
+        (rc = need_ptr(V_out, "V_out")))
+        return rc;
+    if (max_len < 0 || max_len > (int64_t)1 << 30)
+        return fail(TP_ERR_INVALID_ARG, "max_len %lld is not in [0, 2^30]", (long long)max_len);
+    std::string err;
+    return run(tpi::kv_read_launch(a, max_len, K_out, V_out, as_stream(stream), &err), err);
+}
+
+extern "C" int tp_attn_paged_forward(tp_plan_t plan, const tp_kv_cache* cache, const tp_bf16* QKV, tp_bf16* O,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+    tpi::PagedArgs a;
+    int rc;
+    if ((rc = paged_args(plan, cache, true, &a)) || (rc = check_group(plan)) || (rc = need_ptr(QKV, "QKV")) ||
+        (rc = need_ptr(O, "O")) || (rc = check_ws(plan, TP_OP_ATTN_PAGED, workspace, ws_bytes)))
+        return rc;
+    a.QKV = QKV;
+    std::string err;
+    return run(tpi::attn_paged_launch(a, O, workspace, false, as_stream(stream), &err), err);
+}
+
+extern "C" int tp_attn_cached_forward(tp_plan_t plan, const tp_kv_cache* cache, const tp_bf16* X,
+                                      const tp_bf16* Wq, const tp_bf16* Wk, const tp_bf16* Wv, const tp_bf16* Wo,
+                                      const tp_bf16* residual, void* partials, tp_bf16* out, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+    tpi::PagedArgs a;
+    int rc;
+    if ((rc = paged_args(plan, cache, true, &a)) || (rc = check_group(plan)) || (rc = need_ptr(X, "X")) ||
+        (rc = need_ptr(Wq, "Wq")) || (rc = need_ptr(Wk, "Wk")) || (rc = need_ptr(Wv, "Wv")) ||
+        (rc = need_ptr(Wo, "Wo")) || (rc = need_ptr(out, "out")) || (rc = opt_ptr(residual, "residual")))
+        return rc;
+    const bool fused = plan->cfg.reduce_mode == TP_REDUCE_FUSED;
+    if (!fused && (rc = need_ptr(partials, "partials"))) return rc;
+    if ((rc = check_ws(plan, TP_OP_ATTN_CACHED, workspace, ws_bytes))) return rc;
+    const Layout L = layout_of(plan, TP_OP_ATTN_CACHED);
+    void* QKV = region(workspace, 0);
+    void* O = region(workspace, L.qkv);
+    void* scratch = region(workspace, L.qkv + L.o);
+    a.QKV = QKV;
+    cudaStream_t s = as_stream(stream);
+    std::string err;
+    if ((rc = do_qkv(plan, X, Wq, Wk, Wv, QKV, s))) return rc;
+    if ((rc = run(tpi::kv_write_launch(a, s, &err), err))) return rc;
+    if ((rc = run(tpi::attn_paged_launch(a, O, scratch, true, s, &err), err))) return rc;
+    if ((rc = do_rowwise(plan, O, plan->qw, Wo, plan->h, nullptr, residual, partials, out, fused, s))) return rc;
+    if (!fused) return do_reduce(plan, partials, nullptr, residual, out, plan->h, s);
+    return TP_OK;
+}
+
+extern "C" int tp_vocab_verify_drafts(const tp_bf16* logits, const tp_bf16* draft_logits, int64_t M, int64_t v,
+                                      int32_t t, const int32_t* ids, const int32_t* q_start, int32_t n_seqs,
+                                      const float* temperature, const float* u, const float* noise,
+                                      int32_t* accepted, int32_t* tokens, void* stream) {
+    int rc;
+    if ((rc = need_ptr(logits, "logits")) || (rc = opt_ptr(draft_logits, "draft_logits")) ||
+        (rc = need_ptr(ids, "ids")) || (rc = need_ptr(q_start, "q_start")) ||
+        (rc = opt_ptr(temperature, "temperature")) || (rc = need_ptr(u, "u")) || (rc = opt_ptr(noise, "noise")) ||
+        (rc = need_ptr(accepted, "accepted")) || (rc = need_ptr(tokens, "tokens")))
+        return rc;
+    if ((rc = check_vocab(M, v, t, 8))) return rc;
+    if (v >= (int64_t)1 << 31) return fail(TP_ERR_INVALID_ARG, "v out of range");
+    if (n_seqs < 0 || n_seqs > 1 << 20) return fail(TP_ERR_INVALID_ARG, "n_seqs %d is not in [0, 2^20]", n_seqs);
+    tpi::VerifyArgs a;
+    a.logits = logits;
+    a.draft_logits = draft_logits;
+    a.M = M;
+    a.v = v;
+    a.ids = ids;
+    a.q_start = q_start;
+    a.n_seqs = n_seqs;
+    a.temperature = temperature;
+    a.u = u;
+    a.noise = noise;
+    a.accepted = accepted;
+    a.tokens = tokens;
+    std::string err;
+    return run(tpi::verify_launch(a, as_stream(stream), &err), err);
 }
 
 // ---------------------------------------------------------------------------

@@ -208,6 +208,43 @@ int vocab_embedding_launch(const int32_t* ids, int64_t M, const void* E, int64_t
 int vocab_ce_launch(const void* logits, int64_t M, int64_t v, int t, const int32_t* labels,
                     float* stats, float* loss, cudaStream_t stream, std::string* err);
 
+// A paged key/value cache and one call's new tokens (tp_kv_cache with its
+// plan's geometry).
+struct PagedArgs {
+    void *K = nullptr, *V = nullptr;
+    float *k_scale = nullptr, *v_scale = nullptr;
+    bool e4m3 = false;
+    const int32_t *page_table = nullptr, *q_start = nullptr, *kv_len = nullptr;
+    int64_t n_pages = 0;
+    int n_seqs = 0, max_pages = 0, page_size = 0, max_new = 0;
+    const void* QKV = nullptr;               // [tokens][ld_qkv], shard-blocked
+    int64_t tokens = 0, ld_qkv = 0;
+    int64_t shard_w = 0, q_w = 0, kv_w = 0;  // column layout of one shard
+    int heads = 0, kv_heads = 0, head_dim = 0, t = 1;
+    unsigned* status = nullptr;
+    uint64_t timeout_ns = 2000000000ull;
+};
+// Append the new tokens' K and V; read sequences back as bf16 (tp_kv.cu).
+int kv_write_launch(const PagedArgs& a, cudaStream_t stream, std::string* err);
+int kv_read_launch(const PagedArgs& a, int64_t max_len, void* k_out, void* v_out, cudaStream_t stream,
+                   std::string* err);
+// Attention of the new tokens over the cache (tp_attn_paged.cu).  zero_rest:
+// rows of O that no sequence owns get zeros (else they are left alone).
+size_t attn_paged_scratch_bytes(int head_dim);
+int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest, cudaStream_t stream,
+                      std::string* err);
+
+// Verification of drafted tokens (tp_verify.cu).
+struct VerifyArgs {
+    const void *logits = nullptr, *draft_logits = nullptr;
+    int64_t M = 0, v = 0;
+    const int32_t *ids = nullptr, *q_start = nullptr;
+    int n_seqs = 0;
+    const float *temperature = nullptr, *u = nullptr, *noise = nullptr;
+    int32_t *accepted = nullptr, *tokens = nullptr;
+};
+int verify_launch(const VerifyArgs& a, cudaStream_t stream, std::string* err);
+
 // out = res + RMSNorm'(x)^T g per row (unit gain; bf16 [rows][h], h % 8 == 0,
 // h <= 8192); out may alias res.
 int rmsnorm_bwd_launch(const void* x, const void* g, const void* res, int64_t rows, int h, float eps,
