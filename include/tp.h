@@ -549,9 +549,9 @@ enum { TP_KV_BF16 = 0, TP_KV_E4M3 = 1 };
  *
  * q_start, kv_len and page_table are read on the device when the call runs, so
  * a captured call sees what they hold at replay.  They are checked there: row
- * numbers are clamped to [0, M] and a position whose page is not in
- * [0, n_pages), or that lies past the page table, is neither read nor written
- * (a key there counts as zero bytes, a token there is dropped), and
+ * numbers are clamped to [0, M]; a position whose page is not in [0, n_pages)
+ * is neither read nor written (a key there counts as zero bytes, a token there
+ * is dropped), nor is one past the page table (which no token sees), and
  * tp_get_device_status then reports TP_ERR_INVALID_ARG. */
 typedef struct {
     void *K, *V;                /* [n_pages][k][page_size][d], TP_KV_* elements       */

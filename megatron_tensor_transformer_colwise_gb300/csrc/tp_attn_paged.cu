@@ -1,14 +1,34 @@
 // tp_attn_paged.cu -- causal GQA attention of new tokens over a paged
-// key/value cache.
+// key/value cache: the kernel for few query rows per sequence and KV head
+// (single tokens, drafts), and the joining of split work.
 //
 // For query head j of a token at position p, with KV head g = j / (a/k):
-//   O = sum_{p' <= p} e^{s_p' - m} V[p'] / sum_{p' <= p} e^{s_p' - m},
-//   s_p' = Q . K[p'] / sqrt d,   m the running maximum,
-// one pass over the keys, fp32 throughout.
+//   O = sum_{p' <= p} 2^{x_p' - m} V[p'] / sum_{p' <= p} 2^{x_p' - m},
+//   x_p' = Q . K[p'] log2(e) / sqrt d,   m a running maximum,
+// one pass over the keys.  An 8-bit cache holds K[p'] = kc[p'] ks[p'] and
+// V[p'] = vc[p'] vs[p'] (codes and a scale a token): the scales stay outside
+// the products,
+//   x_p' = (Q . kc[p']) ks[p'] log2(e) / sqrt d,   sum 2^{x - m} vs vc.
+//
+// With G = a/k query rows per token and KV head, every key read from memory is
+// used by a few rows only, so the cache's bytes bound the kernel (16 rows a
+// tile: 16 multiply-adds a byte, a few per cent of the tensor cores' rate).
+// The work is cut into equal shares of key blocks (tp_paged_index.h), one
+// persistent CTA an SM:
+//   warp 8      producer: TMA boxes of one page each into a ring of key
+//               blocks; the page numbers of 32 pages are read at a time.
+//   warps 0..7  consumers, 16 keys of a block each: S = Q K^T and O += P V by
+//               mma.sync m16n8k16 (rows = the tile's 16 query rows, P straight
+//               from S's registers), a running maximum of their own; at a
+//               tile's end the eight are merged in shared memory.
+// mma.sync rather than tcgen05: the tile has 16 rows, tcgen05's least is 64,
+// and P would make a round trip through tensor memory.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cstring>
 #include <string>
 
 #include "tp_device.cuh"
@@ -19,109 +39,729 @@ namespace {
 
 using namespace tpk;
 
-struct PagedAttnParams {
+constexpr int R = 16;        // query rows of a tile
+constexpr int NW = 8;        // consumer warps
+constexpr int NT = 32 * (NW + 1);
+constexpr float RESCALE = 8.0f;  // log2 of the growth of a weight before the sums are rescaled
+
+// Head dimension, element type, warps that share a key block (16 keys each;
+// with 4 the two halves of the warps take alternate blocks), ring stages.
+template <int D_, bool E4M3_, int WPB_, int NST_>
+struct Cfg {
+    static constexpr int D = D_, WPB = WPB_, NST = NST_;
+    static constexpr bool E4M3 = E4M3_;
+    static constexpr int KB = 16 * WPB;
+    static constexpr int ROW = E4M3 ? D : 2 * D;       // bytes of a cached row
+    static constexpr int SEG = ROW < 128 ? ROW : 128;  // bytes of a TMA box row (one swizzle span)
+    static constexpr int NSEG = ROW / SEG;
+    static constexpr int TILE = KB * ROW;              // bytes of K (or V) of a block
+    static constexpr int SCALES = E4M3 ? 2 * KB * 4 : 0;
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int SC_OFF = NST * STAGE;
+    static constexpr int ACC_OFF = SC_OFF + NST * SCALES;
+    static constexpr int LD_ACC = D + 4;               // floats; 16-byte rows, shifted banks
+    static constexpr int XM_OFF = ACC_OFF + NW * R * LD_ACC * 4;
+    static constexpr int BAR_OFF = XM_OFF + 2 * NW * R * 4;
+    static constexpr int SCAN_OFF = BAR_OFF + 8 * 2 * NST;
+    static constexpr int DATA = SCAN_OFF + 8 * (NW + 1) + 32;
+    static constexpr int SMEM = DATA + 1024;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct Params {
+    CUtensorMap map_k, map_v;  // the cache as {d, page, k, n_pages}, box {SEG, min(page, KB), 1, 1}
     PagedView v;
-    const void *K, *V;
     const float *k_scale, *v_scale;
     const __nv_bfloat16* qkv;
     long long ld_qkv;
     __nv_bfloat16* o;
-    int heads, heads_per_shard, shard_w, group;
+    int heads, heads_per_shard, shard_w, group, box_rows;
     float scale_log2;
-    int zero_rest;
+    float* part_o;   // [grid][2][R][D]
+    float* part_ml;  // [grid][2][R][2]
+    int4* desc;      // [grid]: sequence, KV head, tile, parts of the tile that begins in a CTA's slot 1
     unsigned* status;
+    unsigned long long timeout_ns;
 };
 
-template <int D, bool E4M3>
-__device__ __forceinline__ void load_row(const void* base, const float* scale, long long at, int lane,
-                                         float (&x)[D / 32]) {
-    if constexpr (E4M3) {
-        const uint8_t* r = static_cast<const uint8_t*>(base) + at * D;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            x[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw(r[e * 32 + lane], __NV_E4M3))) * scale[at];
-    } else {
-        const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(base) + at * D;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) x[e] = __bfloat162float(r[e * 32 + lane]);
-    }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// One warp per (new token, query head); a key at a time, lanes over d.
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(256) attn_paged_simple_kernel(const PagedAttnParams p) {
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two e4m3 codes (low 16 bits) as two fp16: exact, NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// Contiguous copy to shared memory; addresses and size multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Byte offset of 16-byte piece c of row r in a box of SEG-byte rows written
+// by TMA with the swizzle of that span: 128 bytes XOR the row's 8 with the
+// piece, 64 bytes two rows to a 128-byte line.
+template <int SEG>
+__device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) {
+    if constexpr (SEG == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+    else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// The share of CTA blockIdx.x: its first sequence, block there, and number of
+// blocks; the same in all threads.  Every thread sums the blocks of a run of
+// sequences, and a scan of the sums finds the share's beginning.
+struct Share {
+    long long begin, count, per, seq_begin;  // seq_begin: number of the first sequence's first block
+    int s;
+};
+template <class C>
+__device__ __forceinline__ Share find_share(const Params& p, const Tiling& t, uint8_t* scratch) {
+    long long* sums = reinterpret_cast<long long*>(scratch);
+    long long* found = sums + NT / 32;
+    int* found_s = reinterpret_cast<int*>(found + 1);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int run = (p.v.n_seqs + NT - 1) / NT;
+    const int s0 = min(tid * run, p.v.n_seqs), s1 = min(s0 + run, p.v.n_seqs);
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) mine += seq_blocks(p.v, paged_seq(p.v, s), t) * p.v.kv_heads;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) sums[tid >> 5] = inc;
+    __syncthreads();
+    long long before = inc - mine, total = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < (tid >> 5)) before += sums[w];
+        total += sums[w];
+    }
+    Share x;
+    x.per = (total + gridDim.x - 1) / gridDim.x;
+    x.begin = pmin(static_cast<long long>(blockIdx.x) * x.per, total);
+    x.count = pmin(x.per, total - x.begin);
+    if (x.count > 0 && x.begin >= before && x.begin < before + mine) {
+        long long at = before;
+        int s = s0;
+        for (; s < s1; ++s) {
+            const long long n = seq_blocks(p.v, paged_seq(p.v, s), t) * p.v.kv_heads;
+            if (x.begin < at + n) break;
+            at += n;
+        }
+        *found = at;
+        *found_s = s;
+    }
+    __syncthreads();
+    x.seq_begin = *found;
+    x.s = x.count > 0 ? *found_s : 0;
+    return x;
+}
+
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > 200000000ull) break;  // 200 ms
+}
+
+template <class C>
+__global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__ Params p) {
+    constexpr int D = C::D, KB = C::KB, NST = C::NST;
+    constexpr bool E4M3 = C::E4M3;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int abort_word;
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const uint32_t full0 = base + C::BAR_OFF, empty0 = full0 + 8 * NST;
+    volatile int* abort_flag = &abort_word;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Tiling tiling = {R, KB, p.group};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, C::WPB);
+        }
+        abort_word = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&p.map_k);
+        tma_prefetch_desc(&p.map_v);
+    }
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long n_items = p.v.rows * p.heads;
-    const long long warps = static_cast<long long>(gridDim.x) * 8;
-    for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < n_items; it += warps) {
-        const int j = static_cast<int>(it % p.heads);
-        const long long row = it / p.heads;
-        __nv_bfloat16* o = p.o + row * p.heads * D + j * D;
-        const int s = paged_owner(p.v, row);
-        if (s < 0) {
-            if (p.zero_rest)
-                for (int e = 0; e < D / 32; ++e) o[e * 32 + lane] = __float2bfloat16_rn(0.0f);
-            continue;
-        }
-        const PagedSeq q = paged_seq(p.v, s);
-        const int pos = q.len - q.n + static_cast<int>(row - q.row0);
-        const __nv_bfloat16* x = p.qkv + row * p.ld_qkv + (j / p.heads_per_shard) * p.shard_w +
-                                 (j % p.heads_per_shard) * D;
-        float qv[D / 32], acc[D / 32], kv[D / 32];
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            qv[e] = __bfloat162float(x[e * 32 + lane]);
-            acc[e] = 0.0f;
-        }
-        float m = -INFINITY, l = 0.0f;
-        for (int c = 0; c <= pos; ++c) {
-            const long long page = paged_page(p.v, s, c);
-            if (page < 0) {
-                if (lane == 0 && p.status) atomicOr(p.status, kStatusPage);
+    const Share share = find_share<C>(p, tiling, gbase + C::SCAN_OFF);  // its barriers cover the set-up above
+    TileWalk w;
+    w.start(p.v, tiling, share.s, share.begin - share.seq_begin, share.count);
+
+    if (warp == NW) {
+        // ------------------------------------------------------ producer
+        bool ok = true;
+        int n = 0;  // blocks issued
+        for (; w.left > 0 && ok; w.next(p.v, tiling)) {
+            const int seg = w.segment();
+            const int page_rows = 1 << p.v.page_log2;
+            const int per_block = KB / p.box_rows;  // boxes (pages, or parts of one) of a block
+            int window = -32, held = -1;            // pages [window, window + 32) of the sequence, one a lane
+            for (int i = 0; i < seg && ok; ++i, ++n) {
+                const int st = n % NST;
+                const uint32_t full = full0 + 8 * st;
+                const int key0 = (w.kb + i) * KB;
+                const int first = key0 >> p.v.page_log2;
+                if (first + per_block > window + 32 || first < window) {
+                    window = first;
+                    const int pg = window + lane;
+                    held = -1;
+                    if (pg * static_cast<long long>(page_rows) < w.keys) {
+                        held = p.v.table[static_cast<long long>(w.s) * p.v.max_pages + pg];
+                        if (held < 0 || held >= p.v.n_pages) {
+                            held = -1;
+                            if (p.status) atomicOr(p.status, kStatusPage);
+                        }
+                    }
+                }
+                ok = mbar_wait(empty0 + 8 * st, ((n / NST) & 1) ^ 1, abort_flag, p.status, p.timeout_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                // Box b of the block: keys key0 + b * box_rows.  A box past the
+                // sequence's keys, or on a page outside the cache, is loaded
+                // from page -1: TMA fills it with zeros and reads nothing.
+                const int b = lane % per_block, seg_i = lane / per_block;  // lanes: boxes x spans of a row
+                const int k_box = key0 + b * p.box_rows;
+                int page = __shfl_sync(0xffffffffu, held, (k_box >> p.v.page_log2) - window);
+                if (k_box >= w.keys) page = -1;
+                const int off = k_box & (page_rows - 1);
+                if constexpr (E4M3) {
+                    const bool mine = seg_i == 0;
+                    const uint32_t sc = base + C::SC_OFF + st * C::SCALES + b * p.box_rows * 4;
+                    const unsigned scaled = __ballot_sync(0xffffffffu, mine && page >= 0);
+                    if (mine && page < 0) {  // scales of no page: zeros
+                        for (int x = 0; x < p.box_rows; x += 4) {
+                            st_shared_v4(sc + x * 4, 0, 0, 0, 0);
+                            st_shared_v4(sc + KB * 4 + x * 4, 0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(full, 2 * C::TILE + 8u * p.box_rows * __popc(scaled));
+                    __syncwarp();
+                    if (mine && page >= 0) {
+                        const long long at = paged_row(p.v, page, w.g, off);
+                        bulk_load(sc, p.k_scale + at, p.box_rows * 4, full);
+                        bulk_load(sc + KB * 4, p.v_scale + at, p.box_rows * 4, full);
+                    }
+                } else {
+                    if (lane == 0) mbar_arrive_expect_tx(full, 2 * C::TILE);
+                    __syncwarp();
+                }
+                if (seg_i < C::NSEG) {
+                    const uint32_t dst = base + st * C::STAGE + seg_i * (KB * C::SEG) + b * p.box_rows * C::SEG;
+                    const int c0 = seg_i * (E4M3 ? 128 : 64);
+                    tma_load_4d(dst, &p.map_k, full, c0, off, w.g, page);
+                    tma_load_4d(dst + C::TILE, &p.map_v, full, c0, off, w.g, page);
+                }
+                __syncwarp();
             }
-            const long long at = page < 0 ? 0 : paged_row(p.v, page, j / p.group, c);
-            float dot = 0.0f;
-            if (page >= 0) {
-                load_row<D, E4M3>(p.K, p.k_scale, at, lane, kv);
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) dot += qv[e] * kv[e];
-            }
-            for (int f = 16; f > 0; f >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, f);
-            dot *= p.scale_log2;
-            const float nm = fmaxf(m, dot);
-            const float alpha = exp2f(m - nm), w = exp2f(dot - nm);
-            m = nm;
-            l = l * alpha + w;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) kv[e] = 0.0f;
-            if (page >= 0) load_row<D, E4M3>(p.V, p.v_scale, at, lane, kv);
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) acc[e] = acc[e] * alpha + w * kv[e];
         }
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        // No copy may be in flight when the CTA's shared memory goes.
+        for (int i = max(0, n - NST); i < n; ++i) drain(full0 + 8 * (i % NST), (i / NST) & 1);
+    } else {
+        // ------------------------------------------------------ consumers
+        const int r0 = lane >> 2, t = lane & 3;  // fragment rows r0 and r0 + 8, column pair t
+        const int wk = warp % C::WPB;            // the warp's 16 keys of a block
+        float* xm = reinterpret_cast<float*>(gbase + C::XM_OFF);
+        float* xl = xm + NW * R;
+        float* acc_s = reinterpret_cast<float*>(gbase + C::ACC_OFF);
+        bool ok = true;
+        int n = 0;
+        if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+        for (; w.left > 0; w.next(p.v, tiling)) {
+            const int seg = w.segment();
+            const int rows = static_cast<int>(pmin(R, static_cast<long long>(w.q.n) * p.group - static_cast<long long>(w.tile) * R));
+            // Row i of the tile: its query head's row of the buffer, and the keys it sees.
+            auto q_row = [&](int i) -> const __nv_bfloat16* {
+                const long long r = static_cast<long long>(w.tile) * R + i;
+                const int j = w.g * p.group + static_cast<int>(r % p.group);
+                return p.qkv + (w.q.row0 + r / p.group) * p.ld_qkv +
+                       static_cast<long long>(j / p.heads_per_shard) * p.shard_w + (j % p.heads_per_shard) * D;
+            };
+            int lim[2];
+            uint32_t qf[D / 16][4];
+            float row_scale[2] = {p.scale_log2, p.scale_log2};
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e * 32 + lane] = __float2bfloat16_rn(acc[e] * inv);
+            for (int h = 0; h < 2; ++h) {
+                const int i = r0 + 8 * h;
+                lim[h] = i < rows ? row_keys(w.q, w.keys, static_cast<long long>(w.tile) * R + i, p.group) : 0;
+                const __nv_bfloat16* x = i < rows ? q_row(i) : nullptr;
+                if constexpr (!E4M3) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        qf[ks][h] = x ? *reinterpret_cast<const uint32_t*>(x + ks * 16 + 2 * t) : 0u;
+                        qf[ks][h + 2] = x ? *reinterpret_cast<const uint32_t*>(x + ks * 16 + 8 + 2 * t) : 0u;
+                    }
+                } else {
+                    // A product may take d in any order that Q and K share: lane t has the 16 codes
+                    // 64 hh + 16 t .. + 15 of a key's row in one load, step j of them the four at 4 j.
+                    // Q goes to fp16 after a power of two that brings the row's largest value to
+                    // [2^14, 2^15): what that pushes under fp16's range is below 2^-38 of the largest.
+                    float amax = 0.0f;
+                    uint32_t raw4[D / 64][8];
+#pragma unroll
+                    for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const uint4 u = x ? *reinterpret_cast<const uint4*>(x + hh * 64 + t * 16 + c * 8)
+                                              : make_uint4(0, 0, 0, 0);
+                            raw4[hh][c * 4] = u.x;
+                            raw4[hh][c * 4 + 1] = u.y;
+                            raw4[hh][c * 4 + 2] = u.z;
+                            raw4[hh][c * 4 + 3] = u.w;
+                        }
+#pragma unroll
+                    for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float2 f = unpack_bf16x2(raw4[hh][c]);
+                            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                    const int ex = max((__float_as_int(amax) >> 23) - 127, -100);
+                    const float down = __int_as_float((127 + 14 - ex) << 23);
+                    row_scale[h] = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23);
+#pragma unroll
+                    for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const float2 f = unpack_bf16x2(raw4[hh][j * 2 + c]);
+                                qf[hh * 4 + j][h + 2 * c] = pack_f16x2(f.x * down, f.y * down);
+                            }
+                }
+            }
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            float mv[2] = {-INFINITY, -INFINITY};  // 8-bit cache: reference of the weights 2^x vs
+            float o[D / 8][4];
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][e] = 0.0f;
+
+            for (int i = 0; i < seg; ++i, ++n) {
+                if (C::WPB < NW && (n & 1) != warp / C::WPB) continue;
+                const int st = n % NST;
+                ok = ok && mbar_wait(full0 + 8 * st, (n / NST) & 1, abort_flag, p.status, p.timeout_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) continue;
+                const uint32_t sk = base + st * C::STAGE, sv = sk + C::TILE;
+                const int key0 = (w.kb + i) * KB + wk * 16;
+                float s[2][4] = {};
+                if constexpr (!E4M3) {
+                    // Matrices (keys 0-7, 8-15) x (d 0-7, 8-15) of a step: lanes 0-7 and 16-23 address keys
+                    // 0-7 and 8-15 of the step's first eight d, lanes 8-15 and 24-31 of its second eight.
+                    const uint32_t kr = wk * 16 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        uint32_t b[4];
+                        ldsm4(sk + (ks >> 2) * (KB * 128) + swz<128>(kr, (ks & 3) * 2 + kc), b);
+                        mma<false>(s[0], qf[ks], b[0], b[1]);
+                        mma<false>(s[1], qf[ks], b[2], b[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int hh = 0; hh < D / 64; ++hh) {
+                            const uint4 u = ld_shared_v4(sk + swz<C::SEG>(wk * 16 + nt * 8 + r0, hh * 4 + t));
+                            const uint32_t c[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mma<true>(s[nt], qf[hh * 4 + j], e4m3x2_f16x2(c[j]), e4m3x2_f16x2(c[j] >> 16));
+                        }
+                }
+                // Scores in the exp2 domain, masked; lane t has keys 2t, 2t + 1 of each eight.
+                float lv[2][2] = {};
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    float ks[2] = {1.0f, 1.0f};
+                    if constexpr (E4M3) {
+                        const float* sc = reinterpret_cast<const float*>(gbase + C::SC_OFF + st * C::SCALES) + wk * 16 +
+                                          nt * 8 + 2 * t;
+                        const float2 k2 = *reinterpret_cast<const float2*>(sc);
+                        const float2 v2 = *reinterpret_cast<const float2*>(sc + KB);
+                        ks[0] = k2.x;
+                        ks[1] = k2.y;
+                        lv[nt][0] = __log2f(v2.x);
+                        lv[nt][1] = __log2f(v2.y);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + nt * 8 + 2 * t + (e & 1);
+                        const float x = s[nt][e] * (ks[e & 1] * row_scale[e >> 1]);
+                        s[nt][e] = key < lim[e >> 1] ? x : -INFINITY;
+                    }
+                }
+                uint32_t pa[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[4] = {s[0][2 * h], s[0][2 * h + 1], s[1][2 * h], s[1][2 * h + 1]};
+                    float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    bool move = mx > m[h] + RESCALE;
+                    float alpha = 1.0f;
+                    if (move) {
+                        alpha = ex2(m[h] - mx);
+                        m[h] = mx;
+                    }
+                    const float ref = m[h] == -INFINITY ? 0.0f : m[h];
+                    float pr[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) pr[e] = ex2(x[e] - ref);
+                    l[h] = l[h] * alpha + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
+                    if constexpr (E4M3) {
+                        // Weights 2^(x + log2 vs) against their own largest, which stands for 2^15: fp16's range
+                        // whatever the scales.  A weight is rounded to 2^-11 of itself, or to 2^-25 where
+                        // it is below fp16's normal range, 2^-40 of the largest.
+                        float y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = x[e] == -INFINITY ? -INFINITY : x[e] + lv[e >> 1][e & 1];
+                        float my = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                        my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 1));
+                        my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 2));
+                        move = my > mv[h];
+                        alpha = 1.0f;
+                        if (move) {
+                            alpha = ex2(mv[h] - my);
+                            mv[h] = my;
+                        }
+                        const float rv = (mv[h] == -INFINITY ? 0.0f : mv[h]) - 15.0f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) pr[e] = ex2(y[e] - rv);
+                    }
+                    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            o[c][2 * h] *= alpha;
+                            o[c][2 * h + 1] *= alpha;
+                        }
+                    }
+                    if constexpr (E4M3) {
+                        pa[h] = pack_f16x2(pr[0], pr[1]);
+                        pa[h + 2] = pack_f16x2(pr[2], pr[3]);
+                    } else {
+                        pa[h] = pack_bf16x2(pr[0], pr[1]);
+                        pa[h + 2] = pack_bf16x2(pr[2], pr[3]);
+                    }
+                }
+                // O += P V.  Rows of V past the sequence's keys are whatever the page holds: cleared, since
+                // 0 * NaN is NaN.  `live` masks the halves of a register that holds keys 2t, 2t + 1 (+ 8).
+                uint32_t live[2] = {0xffffffffu, 0xffffffffu};
+                const bool tail = key0 + 16 > w.keys;
+                if (tail) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = key0 + h * 8 + 2 * t;
+                        live[h] = (key < w.keys ? 0xffffu : 0u) | (key + 1 < w.keys ? 0xffff0000u : 0u);
+                    }
+                }
+                // Matrices (keys 0-7, 8-15) x two neighbouring eights of 16-bit columns.
+                const uint32_t vr = wk * 16 + (lane & 15), vc = lane >> 4;
+                if constexpr (!E4M3) {
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t b[4];
+                        ldsm4_t(sv + (c >> 2) * (KB * 128) + swz<128>(vr, (c & 3) * 2 + vc), b);
+                        if (tail) {
+                            b[0] &= live[0];
+                            b[1] &= live[1];
+                            b[2] &= live[0];
+                            b[3] &= live[1];
+                        }
+                        mma<false>(o[2 * c], pa, b[0], b[1]);
+                        mma<false>(o[2 * c + 1], pa, b[2], b[3]);
+                    }
+                } else {
+                    // A 16-bit column is two codes, d and d + 1: a register holds them for two keys.  Even and
+                    // odd d go to two products: o[2 c'] has the even d of 16, o[2 c' + 1] the odd.
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t b[4];
+                        ldsm4_t(sv + swz<C::SEG>(vr, c * 2 + vc), b);
+                        if (tail) {
+                            b[0] &= live[0];
+                            b[1] &= live[1];
+                            b[2] &= live[0];
+                            b[3] &= live[1];
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = b[2 * h], y = b[2 * h + 1];
+                            mma<true>(o[4 * c + 2 * h], pa, e4m3x2_f16x2(__byte_perm(x, 0, 0x0020)),
+                                      e4m3x2_f16x2(__byte_perm(y, 0, 0x0020)));
+                            mma<true>(o[4 * c + 2 * h + 1], pa, e4m3x2_f16x2(__byte_perm(x, 0, 0x0031)),
+                                      e4m3x2_f16x2(__byte_perm(y, 0, 0x0031)));
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty0 + 8 * st);
+            }
+
+            // ---- merge the eight warps' sums over their keys
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                if (t == 0) xm[warp * R + r0 + 8 * h] = m[h];
+            }
+            named_bar_sync(1, 32 * NW);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = r0 + 8 * h;
+                float mm = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < NW; ++x) mm = fmaxf(mm, xm[x * R + i]);
+                // 2^(own reference - common one); the 8-bit cache's weights have a reference of their own.
+                const float f = m[h] == -INFINITY ? 0.0f : ex2(m[h] - mm);
+                float fo = f;
+                if constexpr (E4M3) fo = mv[h] == -INFINITY ? 0.0f : ex2(mv[h] - 15.0f - mm);
+                if (t == 0) xl[warp * R + i] = l[h] * f;
+                if (i < rows) {
+                    float* dst = acc_s + (warp * R + i) * C::LD_ACC;
+                    if constexpr (!E4M3) {
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<float2*>(dst + c * 8 + 2 * t) =
+                                make_float2(o[c][2 * h] * fo, o[c][2 * h + 1] * fo);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c)
+                            *reinterpret_cast<float4*>(dst + c * 16 + 4 * t) =
+                                make_float4(o[2 * c][2 * h] * fo, o[2 * c + 1][2 * h] * fo, o[2 * c][2 * h + 1] * fo,
+                                            o[2 * c + 1][2 * h + 1] * fo);
+                    }
+                }
+            }
+            named_bar_sync(1, 32 * NW);
+            const bool begins = w.kb == 0, ends = w.kb + seg == w.nkb;
+            const int slot = begins ? 1 : 0;
+            if (ok) {
+                for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * NW) {
+                    const int i = x / (D / 4), c = (x % (D / 4)) * 4;
+                    float4 a = make_float4(0, 0, 0, 0);
+                    float lt = 0.0f, mm = -INFINITY;
+#pragma unroll
+                    for (int y = 0; y < NW; ++y) {
+                        const float4 b = *reinterpret_cast<const float4*>(acc_s + (y * R + i) * C::LD_ACC + c);
+                        a.x += b.x;
+                        a.y += b.y;
+                        a.z += b.z;
+                        a.w += b.w;
+                        lt += xl[y * R + i];
+                        mm = fmaxf(mm, xm[y * R + i]);
+                    }
+                    if (begins && ends) {
+                        const float inv = lt != 0.0f ? 1.0f / lt : 0.0f;  // nothing seen: zeros
+                        const long long r = static_cast<long long>(w.tile) * R + i;
+                        __nv_bfloat16* y = p.o + ((w.q.row0 + r / p.group) * p.heads + w.g * p.group + r % p.group) * D + c;
+                        *reinterpret_cast<uint2*>(y) =
+                            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+                    } else {
+                        const long long at = (static_cast<long long>(blockIdx.x) * 2 + slot) * R + i;
+                        *reinterpret_cast<float4*>(p.part_o + at * D + c) = a;
+                        if (c == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mm, lt);
+                    }
+                }
+                if (begins && !ends && threadIdx.x == 0) {
+                    // The tile's last block is in CTA (first block + blocks - 1) / per.
+                    const long long at = share.begin + share.count - seg;
+                    const int last = static_cast<int>((at + w.nkb - 1) / share.per);
+                    p.desc[blockIdx.x] = make_int4(w.s, w.g, w.tile, last - static_cast<int>(blockIdx.x) + 1);
+                }
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// Joins the parts of the tile that begins in slot 1 of CTA blockIdx.x and goes
+// on in slot 0 of the next ones: O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i,
+// in the order of the keys.  One warp per row, blockIdx.y rows apart.
+// zero_rest: also clears the rows of O that no sequence owns.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, int heads, const float* part_o,
+                                                        const float* part_ml, const int4* desc, __nv_bfloat16* o,
+                                                        int zero_rest) {
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (zero_rest) {
+        const long long a = v.n_seqs ? pmin(pmax(v.q_start[0], 0), v.rows) : 0;
+        const long long b = v.n_seqs ? pmin(pmax(v.q_start[v.n_seqs], a), v.rows) : 0;
+        const long long per = static_cast<long long>(heads) * D / 8;
+        const long long threads = static_cast<long long>(gridDim.x) * gridDim.y * 256;
+        const long long me = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+        uint4* y = reinterpret_cast<uint4*>(o);
+        for (long long i = me; i < a * per; i += threads) y[i] = make_uint4(0, 0, 0, 0);
+        for (long long i = b * per + me; i < v.rows * per; i += threads) y[i] = make_uint4(0, 0, 0, 0);
+    }
+    const int4 x = desc[blockIdx.x];
+    if (x.w == 0) return;
+    const PagedSeq q = paged_seq(v, x.x);
+    const long long total = static_cast<long long>(q.n) * group - static_cast<long long>(x.z) * ROWS;
+    const int rows = static_cast<int>(pmin(ROWS, total));
+    constexpr int E = D / 32;
+    for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
+        // Slot 1 of the first CTA is followed in memory by slot 0 of the next; then every second slot.
+        auto slot = [&](int k) { return (static_cast<long long>(blockIdx.x) * 2 + (k == 0 ? 1 : 2 * k)) * ROWS + i; };
+        float m = -INFINITY;
+        for (int k = lane; k < x.w; k += 32) m = fmaxf(m, part_ml[slot(k) * 2]);
+        for (int f = 16; f > 0; f >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, f));
+        float a[E] = {}, l = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < x.w; ++k) {
+            const long long at = slot(k);
+            const float2 ml = *reinterpret_cast<const float2*>(part_ml + at * 2);
+            const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+            l += ml.y * f;
+            if constexpr (E == 4) {
+                const float4 b = *reinterpret_cast<const float4*>(part_o + at * D + lane * 4);
+                a[0] += b.x * f;
+                a[1] += b.y * f;
+                a[2] += b.z * f;
+                a[3] += b.w * f;
+            } else {
+                const float2 b = *reinterpret_cast<const float2*>(part_o + at * D + lane * 2);
+                a[0] += b.x * f;
+                a[1] += b.y * f;
+            }
+        }
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        const long long r = static_cast<long long>(x.z) * ROWS + i;
+        __nv_bfloat16* y = o + ((q.row0 + r / group) * heads + x.y * group + r % group) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(y + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
     }
 }
 
-}  // namespace
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-namespace tpi {
-
-size_t attn_paged_scratch_bytes(int head_dim) {
-    (void)head_dim;
-    return 0;
+EncodeTiledFn encode_fn(std::string* err) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
+        qr != cudaDriverEntryPointSuccess || !f) {
+        if (err) *err = "cuTensorMapEncodeTiled is not available from the driver";
+        return nullptr;
+    }
+    return reinterpret_cast<EncodeTiledFn>(f);
 }
 
-int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest, cudaStream_t stream,
-                      std::string* err) {
-    (void)scratch;
-    PagedAttnParams p{};
-    p.v = paged_view(a);
-    p.K = a.K;
-    p.V = a.V;
+// The cache as {d, page, k, n_pages} with boxes of one row span by box_rows.
+int encode_cache(CUtensorMap* map, const tpi::PagedArgs& a, const void* base, int span, int box_rows, std::string* err) {
+    EncodeTiledFn encode = encode_fn(err);
+    if (!encode) return TP_ERR_CUDA;
+    const cuuint64_t elem = a.e4m3 ? 1 : 2;
+    const cuuint64_t d = static_cast<cuuint64_t>(a.head_dim), pg = static_cast<cuuint64_t>(a.page_size);
+    const cuuint64_t dims[4] = {d, pg, static_cast<cuuint64_t>(a.kv_heads), static_cast<cuuint64_t>(a.n_pages)};
+    const cuuint64_t strides[3] = {d * elem, d * pg * elem, d * pg * a.kv_heads * elem};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(span / elem), static_cast<cuuint32_t>(box_rows), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        if (err) *err = "cuTensorMapEncodeTiled (cache) failed: " + std::to_string(static_cast<int>(r));
+        return TP_ERR_CUDA;
+    }
+    return TP_OK;
+}
+
+int launched(const char* what, cudaError_t e, std::string* err) {
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess) return TP_OK;
+    if (err) *err = std::string(what) + ": " + cudaGetErrorString(e);
+    return TP_ERR_CUDA;
+}
+
+// Scratch of a launch: partial results of `rows` x D, their statistics, descriptors.
+struct Scratch {
+    size_t o, ml, desc, total;
+};
+Scratch scratch_of(int grid, int rows, int D) {
+    Scratch s;
+    s.o = 0;
+    s.ml = s.o + static_cast<size_t>(grid) * 2 * rows * D * 4;
+    s.desc = s.ml + static_cast<size_t>(grid) * 2 * rows * 2 * 4;
+    s.total = s.desc + static_cast<size_t>(grid) * 16;
+    return s;
+}
+
+template <class C>
+int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cudaStream_t stream, std::string* err) {
+    Params p;
+    memset(&p, 0, sizeof(p));
+    const int grid = tpi::device_sm_count();
+    p.box_rows = a.page_size < C::KB ? a.page_size : C::KB;
+    int rc;
+    if ((rc = encode_cache(&p.map_k, a, a.K, C::SEG, p.box_rows, err)) ||
+        (rc = encode_cache(&p.map_v, a, a.V, C::SEG, p.box_rows, err)))
+        return rc;
+    p.v = tpi::paged_view(a);
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
     p.qkv = static_cast<const __nv_bfloat16*>(a.QKV);
@@ -131,24 +771,49 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
     p.heads_per_shard = a.heads / a.t;
     p.shard_w = static_cast<int>(a.shard_w);
     p.group = a.heads / a.kv_heads;
-    p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.head_dim));
-    p.zero_rest = zero_rest ? 1 : 0;
+    p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(C::D));
+    const Scratch s = scratch_of(grid, R, C::D);
+    uint8_t* w = static_cast<uint8_t*>(scratch);
+    p.part_o = reinterpret_cast<float*>(w + s.o);
+    p.part_ml = reinterpret_cast<float*>(w + s.ml);
+    p.desc = reinterpret_cast<int4*>(w + s.desc);
     p.status = a.status;
-    const long long need = (a.tokens * a.heads + 7) / 8, most = static_cast<long long>(device_sm_count()) * 8;
-    const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(256);
-    cudaError_t e;
-    if (a.head_dim == 128)
-        e = a.e4m3 ? launch_pdl(attn_paged_simple_kernel<128, true>, grid, block, 0, stream, p)
-                   : launch_pdl(attn_paged_simple_kernel<128, false>, grid, block, 0, stream, p);
-    else
-        e = a.e4m3 ? launch_pdl(attn_paged_simple_kernel<64, true>, grid, block, 0, stream, p)
-                   : launch_pdl(attn_paged_simple_kernel<64, false>, grid, block, 0, stream, p);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) {
-        if (err) *err = std::string("paged attention launch: ") + cudaGetErrorString(e);
-        return TP_ERR_CUDA;
+    p.timeout_ns = a.timeout_ns;
+    static bool configured[64] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && !configured[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(attn_few_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return launched("cudaFuncSetAttribute(paged attention)", e, err);
+        configured[dev] = true;
     }
-    return TP_OK;
+    rc = launched("paged attention launch",
+                  tpi::launch_pdl(attn_few_kernel<C>, dim3(grid), dim3(NT), C::SMEM, stream, p), err);
+    if (rc) return rc;
+    return launched("paged attention join launch",
+                    tpi::launch_pdl(attn_join_kernel<C::D, R>, dim3(grid, 1), dim3(256), 0, stream, p.v, p.group,
+                                    p.heads, p.part_o, p.part_ml, p.desc, p.o, zero_rest ? 1 : 0),
+                    err);
+}
+
+}  // namespace
+
+namespace tpi {
+
+size_t attn_paged_scratch_bytes(int head_dim) { return scratch_of(device_sm_count(), R, head_dim).total; }
+
+int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest, cudaStream_t stream,
+                      std::string* err) {
+    if (a.n_seqs == 0) {
+        if (!zero_rest) return TP_OK;
+        return launched("output reset",
+                        cudaMemsetAsync(O, 0, static_cast<size_t>(a.tokens) * a.heads * a.head_dim * 2, stream), err);
+    }
+    if (a.head_dim == 128)
+        return a.e4m3 ? launch_few<Cfg<128, true, 8, 4>>(a, O, scratch, zero_rest, stream, err)
+                      : launch_few<Cfg<128, false, 4, 4>>(a, O, scratch, zero_rest, stream, err);
+    return a.e4m3 ? launch_few<Cfg<64, true, 8, 6>>(a, O, scratch, zero_rest, stream, err)
+                  : launch_few<Cfg<64, false, 8, 4>>(a, O, scratch, zero_rest, stream, err);
 }
 
 }  // namespace tpi

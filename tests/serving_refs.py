@@ -159,13 +159,15 @@ class Paged:
         return out
 
     def attention(self):
-        """(O, A) [rows][a][d]: the outputs (zeros where no sequence owns the row or nothing is seen) and
-        sum p |v|, the size that roundings of the probabilities act on."""
+        """(O, A, E) [rows][a][d]: the outputs (zeros where no sequence owns the row or nothing is seen),
+        sum p |v|, the size that roundings of the probabilities act on, and for an 8-bit cache
+        max (p vs) sum |code|, the size that the smallest weights' absolute rounding acts on."""
         Q = self.projected("Q")
         O = np.zeros((self.rows, self.a, self.d))
-        A = np.zeros_like(O)
+        A, E = np.zeros_like(O), np.zeros_like(O)
         for s in range(self.n_seqs):
             K, V = self.cached("K", s), self.cached("V", s)
+            vs = np.abs(V).max(axis=2, keepdims=True) / 448 + 1e-300  # at most the scale
             for i in range(self.new[s]):
                 n = self.position(s, i) + 1
                 if n <= 0:
@@ -178,7 +180,9 @@ class Paged:
                     p /= p.sum()
                     O[r, j] = p @ V[:n, g]
                     A[r, j] = p @ np.abs(V[:n, g])
-        return O, A
+                    if self.kv != "bf16":
+                        E[r, j] = (p * vs[:n, g, 0]).max() * (np.abs(V[:n, g]) / vs[:n, g]).sum(axis=0)
+        return O, A, E
 
     def owned(self):
         m = np.zeros(self.rows, dtype=bool)
@@ -186,14 +190,17 @@ class Paged:
         return m
 
 
-def attention_tolerance(O, A):
+def attention_tolerance(O, A, E):
     """Elementwise bound on a bf16 attention output's error.  Each probability is rounded to bf16 (half
     a step, 2^-8 of its value) before the product with V: at most 2^-8 A with A = sum p |v|.  The output
     is rounded to bf16 once: 2^-8 |O|.  A score is an fp32 sum of d exact products, off by at most
     (d + 2) 2^-24 sum |q k| / sqrt d <= 130 * 2^-24 * 12 < 2^-13 for standard normal Q and K at d <= 128
     (sum |q k| / sqrt d is about 7 there), which moves a probability by that share and the sum of
-    probabilities by no more: 2^-12 A.  exp2's 2^-22 and fp32 accumulation stay below what that leaves."""
-    return 2.0 ** -8 * (A + np.abs(O)) + 2.0 ** -12 * A
+    probabilities by no more: 2^-12 A.  exp2's 2^-22 and fp32 accumulation stay below what that leaves.
+    With 8-bit V the weights p vs are rounded to fp16 with the largest at 2^15: to 2^-11 of themselves, or
+    by at most 2^-25, 2^-40 of the largest, where they fall below fp16's normal range; times the codes
+    that is 2^-40 E (one power of two more for E's scales, which are at most the true ones)."""
+    return 2.0 ** -8 * (A + np.abs(O)) + 2.0 ** -12 * A + 2.0 ** -39 * E
 
 
 def softmax64(x, T):

@@ -91,12 +91,12 @@ def attend(x, max_new=None, plan_cache=None):
 
 
 def check_attention(x, O):
-    want, A = x.attention()
+    want, A, E = x.attention()
     got = host64(O).reshape(x.rows, x.a, x.d)
     own = x.owned()
     assert (got[~own] == 7).all()
     err = np.abs(got - want)[own]
-    tol = attention_tolerance(want, A)[own]
+    tol = attention_tolerance(want, A, E)[own]
     assert np.isfinite(got[own]).all()
     assert (err <= tol).all(), f"worst {np.max(err / np.maximum(tol, 1e-30)):.2f} of the tolerance"
 
@@ -137,11 +137,12 @@ def test_attention_large_scores(kv):
     x = Paged(8, 2, 64, 2, 16, [(1, 400), (20, 260)], kv, seed=10, scale=6.0)
     plan, O = attend(x)
     sync_ok(plan)
-    want, A = x.attention()
+    want, A, E = x.attention()
     got = host64(O).reshape(x.rows, x.a, x.d)
     # sum |q k| / sqrt d is up to about 40 times that of standard normal values here, and with it the
     # scores' share of the tolerance: 2^-12 * 2^6.
-    assert (np.abs(got - want) <= attention_tolerance(want, A) + 2.0 ** -6 * A).all()
+    worst = (np.abs(got - want) / (attention_tolerance(want, A, E) + 2.0 ** -6 * A + 1e-300)).max()
+    assert worst <= 1, worst
 
 
 def test_attention_repeats_bit_for_bit():

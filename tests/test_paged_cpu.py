@@ -135,6 +135,45 @@ void seq(const int* q, const int* len, long long rows, int n, int s, long long* 
 long long page(const int* table, long long pages, int maxp, int log2, int s, int pos) {
     return paged_page(view(table, 0, 0, pages, 0, 0, maxp, log2, 1), s, pos);
 }
+// The shares of a grid: for each block of work, in order, (sequence, g, tile, kb) into out, with the CTA
+// and the slot its segment would be written to; desc as the kernel writes it.  Returns the total.
+long long walk(const int* q, const int* len, long long rows, int n, int maxp, int log2, int k, int R, int KB, int G,
+               int grid, int* out, long long cap, int* desc) {
+    PagedView v = view(0, q, len, 1, rows, n, maxp, log2, k);
+    Tiling t = {R, KB, G};
+    long long total = 0, done = 0;
+    for (int s = 0; s < n; ++s) total += seq_blocks(v, paged_seq(v, s), t) * k;
+    const long long per = (total + grid - 1) / grid;
+    for (int c = 0; c < grid; ++c) {
+        desc[4 * c + 3] = 0;
+        const long long begin = pmin(c * per, total), count = pmin(per, total - begin);
+        int s = 0;
+        long long at = 0;
+        if (count > 0)
+            for (;; ++s) {
+                const long long m = seq_blocks(v, paged_seq(v, s), t) * k;
+                if (begin < at + m) break;
+                at += m;
+            }
+        TileWalk w;
+        w.start(v, t, s, begin - at, count);
+        for (; w.left > 0; w.next(v, t)) {
+            const int seg = w.segment();
+            const bool b = w.kb == 0, e = w.kb + seg == w.nkb;
+            for (int i = 0; i < seg; ++i, ++done) {
+                if (done >= cap) return -1;
+                int* o = out + 6 * done;
+                o[0] = w.s; o[1] = w.g; o[2] = w.tile; o[3] = w.kb + i; o[4] = c; o[5] = b && e ? -1 : b ? 1 : 0;
+            }
+            if (b && !e) {
+                const long long first = begin + count - seg;
+                desc[4 * c] = w.s; desc[4 * c + 1] = w.g; desc[4 * c + 2] = w.tile;
+                desc[4 * c + 3] = (int)((first + w.nkb - 1) / per) - c + 1;
+            }
+        }
+    }
+    return done == total ? total : -2;
+}
 long long row(int k, int log2, long long page, int g, int pos) {
     return paged_row(view(0, 0, 0, 0, 0, 0, 0, log2, k), page, g, pos);
 }
@@ -153,6 +192,8 @@ def host(tmp_path_factory):
     L.page.argtypes = [C.c_void_p, C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int]
     L.row.argtypes = [C.c_int, C.c_int, C.c_longlong, C.c_int, C.c_int]
     L.owner.argtypes = [C.c_void_p, C.c_int, C.c_longlong]
+    L.walk.restype = C.c_longlong
+    L.walk.argtypes = [C.c_void_p, C.c_void_p, C.c_longlong] + [C.c_int] * 8 + [C.c_void_p, C.c_longlong, C.c_void_p]
     L.seq.argtypes = [C.c_void_p, C.c_void_p, C.c_longlong, C.c_int, C.c_int, C.c_void_p]
     return L
 
@@ -194,6 +235,48 @@ def test_bad_pages_are_never_an_address(host):
 def test_cache_rows_pass_32_bits(host):
     assert host.row(8, 7, 2 ** 31 - 1, 7, 131) == ((2 ** 31 - 1) * 8 + 7) * 128 + 3
     assert host.row(2, 4, 5, 1, 35) == (5 * 2 + 1) * 16 + 3
+
+
+@pytest.mark.parametrize("R,KB", [(16, 64), (16, 128), (128, 128)])
+def test_shares_cover_all_work_once(host, R, KB):
+    rng = np.random.default_rng(R + KB)
+    for trial in range(60):
+        n, k, G = int(rng.integers(1, 9)), int(rng.choice([1, 2, 3])), int(rng.choice([1, 3, 4, 8]))
+        new, keep = rng.integers(0, 90, n), rng.integers(0, 900, n)
+        if trial % 3 == 0:
+            new = rng.integers(0, 3, n)
+        length = i32(np.maximum(new + keep - (trial % 4 == 0) * 300, 0))   # some with more new than kept
+        q, maxp = i32(np.cumsum([0, *new])), int(rng.integers(1, 80))
+        grid = int(rng.choice([1, 2, 7, 152]))
+        want = []
+        for s in range(n):
+            keys = min(int(length[s]), maxp * 16)
+            for g in range(k):
+                for tile in range(-(-int(new[s]) * G // R)):
+                    last = min((tile + 1) * R, int(new[s]) * G) - 1
+                    seen = min(int(length[s]) - int(new[s]) + last // G + 1, keys)
+                    want += [(s, g, tile, b) for b in range(max(1, -(-seen // KB)))]
+        out, desc = np.zeros((len(want) + 1, 6), dtype=np.int32), np.zeros((grid, 4), dtype=np.int32)
+        got = host.walk(q.ctypes.data, length.ctypes.data, int(q[-1]), n, maxp, 4, k, R, KB, G, grid, out.ctypes.data,
+                        len(want), desc.ctypes.data)
+        assert got == len(want)
+        out = out[:got]
+        assert [tuple(x) for x in out[:, :4].tolist()] == want
+        # Parts: a tile cut by a share's border is in slot 1 of one CTA and slot 0 of the next ones.
+        slots = {}
+        for s, g, tile, b, cta, slot in out.tolist():
+            slots.setdefault((s, g, tile), []).append((cta, slot))
+        parts = 0
+        for key, places in slots.items():
+            places = sorted(set(places))
+            if places[0][1] == -1:
+                assert len(places) == 1
+                continue
+            c = places[0][0]
+            assert places == [(c, 1)] + [(c + i, 0) for i in range(1, len(places))]
+            assert desc[c].tolist() == [*key, len(places)]
+            parts += 1
+        assert (desc[:, 3] > 0).sum() == parts
 
 
 def test_problems_own_their_rows():
