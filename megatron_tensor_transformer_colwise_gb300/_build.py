@@ -22,7 +22,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libtp.so")
 
 SOURCES = ["tp_api.cu", "tp_gemm.cu", "tp_elementwise.cu", "tp_attn.cu", "tp_attn_bwd.cu", "tp_vocab.cu",
-           "tp_kv.cu", "tp_attn_paged.cu", "tp_verify.cu"]
+           "tp_kv.cu", "tp_attn_paged.cu", "tp_attn_chunk.cu", "tp_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -31,13 +31,13 @@
 #include <cstring>
 #include <string>
 
-#include "tp_device.cuh"
-#include "tp_internal.h"
-#include "tp_paged.cuh"
+#include "tp_attn_paged.cuh"
 
 namespace {
 
 using namespace tpk;
+using tpi::launched;
+using tpi::Scratch;
 
 constexpr int R = 16;        // query rows of a tile
 constexpr int NW = 8;        // consumer warps
@@ -84,12 +84,6 @@ struct Params {
     unsigned long long timeout_ns;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -131,22 +125,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
-                                            int32_t c2, int32_t c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
-
-// Contiguous copy to shared memory; addresses and size multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
 // Byte offset of 16-byte piece c of row r in a box of SEG-byte rows written
 // by TMA with the swizzle of that span: 128 bytes XOR the row's 8 with the
 // piece, 64 bytes two rows to a 128-byte line.
@@ -154,63 +132,6 @@ template <int SEG>
 __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) {
     if constexpr (SEG == 128) return r * 128 + ((c ^ (r & 7)) << 4);
     else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
-
-// The share of CTA blockIdx.x: its first sequence, block there, and number of
-// blocks; the same in all threads.  Every thread sums the blocks of a run of
-// sequences, and a scan of the sums finds the share's beginning.
-struct Share {
-    long long begin, count, per, seq_begin;  // seq_begin: number of the first sequence's first block
-    int s;
-};
-template <class C>
-__device__ __forceinline__ Share find_share(const Params& p, const Tiling& t, uint8_t* scratch) {
-    long long* sums = reinterpret_cast<long long*>(scratch);
-    long long* found = sums + NT / 32;
-    int* found_s = reinterpret_cast<int*>(found + 1);
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int run = (p.v.n_seqs + NT - 1) / NT;
-    const int s0 = min(tid * run, p.v.n_seqs), s1 = min(s0 + run, p.v.n_seqs);
-    long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += seq_blocks(p.v, paged_seq(p.v, s), t) * p.v.kv_heads;
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    if (lane == 31) sums[tid >> 5] = inc;
-    __syncthreads();
-    long long before = inc - mine, total = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < (tid >> 5)) before += sums[w];
-        total += sums[w];
-    }
-    Share x;
-    x.per = (total + gridDim.x - 1) / gridDim.x;
-    x.begin = pmin(static_cast<long long>(blockIdx.x) * x.per, total);
-    x.count = pmin(x.per, total - x.begin);
-    if (x.count > 0 && x.begin >= before && x.begin < before + mine) {
-        long long at = before;
-        int s = s0;
-        for (; s < s1; ++s) {
-            const long long n = seq_blocks(p.v, paged_seq(p.v, s), t) * p.v.kv_heads;
-            if (x.begin < at + n) break;
-            at += n;
-        }
-        *found = at;
-        *found_s = s;
-    }
-    __syncthreads();
-    x.seq_begin = *found;
-    x.s = x.count > 0 ? *found_s : 0;
-    return x;
-}
-
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > 200000000ull) break;  // 200 ms
 }
 
 template <class C>
@@ -239,7 +160,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
     }
     pdl_trigger();
     pdl_wait();
-    const Share share = find_share<C>(p, tiling, gbase + C::SCAN_OFF);  // its barriers cover the set-up above
+    const Share share = find_share<NT>(p.v, tiling, gbase + C::SCAN_OFF);  // its barriers cover the set-up above
     TileWalk w;
     w.start(p.v, tiling, share.s, share.begin - share.seq_begin, share.count);
 
@@ -639,8 +560,9 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
 // on in slot 0 of the next ones: O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i,
 // in the order of the keys.  One warp per row, blockIdx.y rows apart.
 // zero_rest: also clears the rows of O that no sequence owns.
+// A tile has tile_rows rows, a slot room for ROWS.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, int heads, const float* part_o,
+__global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, int tile_rows, int heads, const float* part_o,
                                                         const float* part_ml, const int4* desc, __nv_bfloat16* o,
                                                         int zero_rest) {
     pdl_trigger();
@@ -659,8 +581,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, 
     const int4 x = desc[blockIdx.x];
     if (x.w == 0) return;
     const PagedSeq q = paged_seq(v, x.x);
-    const long long total = static_cast<long long>(q.n) * group - static_cast<long long>(x.z) * ROWS;
-    const int rows = static_cast<int>(pmin(ROWS, total));
+    const long long total = static_cast<long long>(q.n) * group - static_cast<long long>(x.z) * tile_rows;
+    const int rows = static_cast<int>(pmin(tile_rows, total));
     constexpr int E = D / 32;
     for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
         // Slot 1 of the first CTA is followed in memory by slot 0 of the next; then every second slot.
@@ -688,67 +610,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, 
             }
         }
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-        const long long r = static_cast<long long>(x.z) * ROWS + i;
+        const long long r = static_cast<long long>(x.z) * tile_rows + i;
         __nv_bfloat16* y = o + ((q.row0 + r / group) * heads + x.y * group + r % group) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(y + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
     }
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn(std::string* err) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
-        qr != cudaDriverEntryPointSuccess || !f) {
-        if (err) *err = "cuTensorMapEncodeTiled is not available from the driver";
-        return nullptr;
-    }
-    return reinterpret_cast<EncodeTiledFn>(f);
-}
-
-// The cache as {d, page, k, n_pages} with boxes of one row span by box_rows.
-int encode_cache(CUtensorMap* map, const tpi::PagedArgs& a, const void* base, int span, int box_rows, std::string* err) {
-    EncodeTiledFn encode = encode_fn(err);
-    if (!encode) return TP_ERR_CUDA;
-    const cuuint64_t elem = a.e4m3 ? 1 : 2;
-    const cuuint64_t d = static_cast<cuuint64_t>(a.head_dim), pg = static_cast<cuuint64_t>(a.page_size);
-    const cuuint64_t dims[4] = {d, pg, static_cast<cuuint64_t>(a.kv_heads), static_cast<cuuint64_t>(a.n_pages)};
-    const cuuint64_t strides[3] = {d * elem, d * pg * elem, d * pg * a.kv_heads * elem};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(span / elem), static_cast<cuuint32_t>(box_rows), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    const CUresult r = encode(map, a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        if (err) *err = "cuTensorMapEncodeTiled (cache) failed: " + std::to_string(static_cast<int>(r));
-        return TP_ERR_CUDA;
-    }
-    return TP_OK;
-}
-
-int launched(const char* what, cudaError_t e, std::string* err) {
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e == cudaSuccess) return TP_OK;
-    if (err) *err = std::string(what) + ": " + cudaGetErrorString(e);
-    return TP_ERR_CUDA;
-}
-
-// Scratch of a launch: partial results of `rows` x D, their statistics, descriptors.
-struct Scratch {
-    size_t o, ml, desc, total;
-};
-Scratch scratch_of(int grid, int rows, int D) {
-    Scratch s;
-    s.o = 0;
-    s.ml = s.o + static_cast<size_t>(grid) * 2 * rows * D * 4;
-    s.desc = s.ml + static_cast<size_t>(grid) * 2 * rows * 2 * 4;
-    s.total = s.desc + static_cast<size_t>(grid) * 16;
-    return s;
 }
 
 template <class C>
@@ -758,8 +624,8 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     const int grid = tpi::device_sm_count();
     p.box_rows = a.page_size < C::KB ? a.page_size : C::KB;
     int rc;
-    if ((rc = encode_cache(&p.map_k, a, a.K, C::SEG, p.box_rows, err)) ||
-        (rc = encode_cache(&p.map_v, a, a.V, C::SEG, p.box_rows, err)))
+    if ((rc = tpi::encode_cache(&p.map_k, a, a.K, C::SEG, p.box_rows, err)) ||
+        (rc = tpi::encode_cache(&p.map_v, a, a.V, C::SEG, p.box_rows, err)))
         return rc;
     p.v = tpi::paged_view(a);
     p.k_scale = a.k_scale;
@@ -772,7 +638,7 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     p.shard_w = static_cast<int>(a.shard_w);
     p.group = a.heads / a.kv_heads;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(C::D));
-    const Scratch s = scratch_of(grid, R, C::D);
+    const Scratch s = tpi::scratch_of(grid, R, C::D);
     uint8_t* w = static_cast<uint8_t*>(scratch);
     p.part_o = reinterpret_cast<float*>(w + s.o);
     p.part_ml = reinterpret_cast<float*>(w + s.ml);
@@ -790,17 +656,36 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     rc = launched("paged attention launch",
                   tpi::launch_pdl(attn_few_kernel<C>, dim3(grid), dim3(NT), C::SMEM, stream, p), err);
     if (rc) return rc;
-    return launched("paged attention join launch",
-                    tpi::launch_pdl(attn_join_kernel<C::D, R>, dim3(grid, 1), dim3(256), 0, stream, p.v, p.group,
-                                    p.heads, p.part_o, p.part_ml, p.desc, p.o, zero_rest ? 1 : 0),
-                    err);
+    return tpi::attn_join_launch(a, R, R, O, w, s, grid, zero_rest, stream, err);
+}
+
+template <int D, int ROWS>
+cudaError_t join(const tpi::PagedArgs& a, int tile_rows, void* O, uint8_t* w, const Scratch& s, int grid, bool zero_rest,
+                 cudaStream_t stream) {
+    return tpi::launch_pdl(attn_join_kernel<D, ROWS>, dim3(grid, (ROWS + 7) / 8), dim3(256), 0, stream,
+                           tpi::paged_view(a), a.heads / a.kv_heads, tile_rows, a.heads,
+                           reinterpret_cast<const float*>(w + s.o), reinterpret_cast<const float*>(w + s.ml),
+                           reinterpret_cast<const int4*>(w + s.desc), static_cast<__nv_bfloat16*>(O), zero_rest ? 1 : 0);
 }
 
 }  // namespace
 
 namespace tpi {
 
-size_t attn_paged_scratch_bytes(int head_dim) { return scratch_of(device_sm_count(), R, head_dim).total; }
+// The kernel for many rows has the larger tiles.
+size_t attn_paged_scratch_bytes(int head_dim) { return scratch_of(device_sm_count(), 128, head_dim).total; }
+
+int attn_join_launch(const PagedArgs& a, int tile_rows, int slot_rows, void* O, uint8_t* w, const Scratch& s, int grid,
+                     bool zero_rest, cudaStream_t stream, std::string* err) {
+    cudaError_t e;
+    if (a.head_dim == 128)
+        e = slot_rows == R ? join<128, R>(a, tile_rows, O, w, s, grid, zero_rest, stream)
+                           : join<128, 128>(a, tile_rows, O, w, s, grid, zero_rest, stream);
+    else
+        e = slot_rows == R ? join<64, R>(a, tile_rows, O, w, s, grid, zero_rest, stream)
+                           : join<64, 128>(a, tile_rows, O, w, s, grid, zero_rest, stream);
+    return launched("paged attention join launch", e, err);
+}
 
 int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest, cudaStream_t stream,
                       std::string* err) {
@@ -809,6 +694,11 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
         return launched("output reset",
                         cudaMemsetAsync(O, 0, static_cast<size_t>(a.tokens) * a.heads * a.head_dim * 2, stream), err);
     }
+    // Few rows a sequence and KV head (the caller's bound on its new tokens, or all rows of the call): one tile
+    // of 16.  More: tiles of 128 on tcgen05.
+    const int64_t most = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
+    if (most * (a.heads / a.kv_heads) > R && !a.e4m3)
+        return attn_chunk_launch(a, O, scratch, zero_rest, stream, err);
     if (a.head_dim == 128)
         return a.e4m3 ? launch_few<Cfg<128, true, 8, 4>>(a, O, scratch, zero_rest, stream, err)
                       : launch_few<Cfg<128, false, 4, 4>>(a, O, scratch, zero_rest, stream, err);

@@ -1,0 +1,165 @@
+// tp_attn_paged.cuh -- what the two kernels of attention over a paged cache
+// share: a CTA's share of the work, the cache's tensor maps, and the scratch of
+// split tiles.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <string>
+
+#include "tp_device.cuh"
+#include "tp_internal.h"
+#include "tp_paged.cuh"
+
+namespace tpk {
+
+// 2^x (PTX ex2.approx.ftz: relative error about 2^-22, -inf -> +0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// Contiguous copy to shared memory; addresses and size multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// The share of CTA blockIdx.x: its first sequence, block there, and number of
+// blocks; the same in all threads.  Every thread sums the blocks of a run of
+// sequences, and a scan of the sums finds the share's beginning.
+struct Share {
+    long long begin, count, per, seq_begin;  // seq_begin: number of the first sequence's first block
+    int s;
+};
+// scratch: 8 (NT / 32) + 16 bytes of shared memory.
+template <int NT>
+__device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t, uint8_t* scratch) {
+    long long* sums = reinterpret_cast<long long*>(scratch);
+    long long* found = sums + NT / 32;
+    int* found_s = reinterpret_cast<int*>(found + 1);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int run = (v.n_seqs + NT - 1) / NT;
+    const int s0 = min(tid * run, v.n_seqs), s1 = min(s0 + run, v.n_seqs);
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) mine += seq_blocks(v, paged_seq(v, s), t) * v.kv_heads;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) sums[tid >> 5] = inc;
+    __syncthreads();
+    long long before = inc - mine, total = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < (tid >> 5)) before += sums[w];
+        total += sums[w];
+    }
+    Share x;
+    x.per = (total + gridDim.x - 1) / gridDim.x;
+    x.begin = pmin(static_cast<long long>(blockIdx.x) * x.per, total);
+    x.count = pmin(x.per, total - x.begin);
+    if (x.count > 0 && x.begin >= before && x.begin < before + mine) {
+        long long at = before;
+        int s = s0;
+        for (; s < s1; ++s) {
+            const long long n = seq_blocks(v, paged_seq(v, s), t) * v.kv_heads;
+            if (x.begin < at + n) break;
+            at += n;
+        }
+        *found = at;
+        *found_s = s;
+    }
+    __syncthreads();
+    x.seq_begin = *found;
+    x.s = x.count > 0 ? *found_s : 0;
+    return x;
+}
+
+// Wait for copies in flight when a role gives up.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > 200000000ull) break;  // 200 ms
+}
+
+}  // namespace tpk
+
+namespace tpi {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn encode_fn(std::string* err) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
+        qr != cudaDriverEntryPointSuccess || !f) {
+        if (err) *err = "cuTensorMapEncodeTiled is not available from the driver";
+        return nullptr;
+    }
+    return reinterpret_cast<EncodeTiledFn>(f);
+}
+
+// The cache as {d, page, k, n_pages} with boxes of one row span by box_rows.
+inline int encode_cache(CUtensorMap* map, const PagedArgs& a, const void* base, int span, int box_rows, std::string* err) {
+    EncodeTiledFn encode = encode_fn(err);
+    if (!encode) return TP_ERR_CUDA;
+    const cuuint64_t elem = a.e4m3 ? 1 : 2;
+    const cuuint64_t d = static_cast<cuuint64_t>(a.head_dim), pg = static_cast<cuuint64_t>(a.page_size);
+    const cuuint64_t dims[4] = {d, pg, static_cast<cuuint64_t>(a.kv_heads), static_cast<cuuint64_t>(a.n_pages)};
+    const cuuint64_t strides[3] = {d * elem, d * pg * elem, d * pg * a.kv_heads * elem};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(span / elem), static_cast<cuuint32_t>(box_rows), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        if (err) *err = "cuTensorMapEncodeTiled (cache) failed: " + std::to_string(static_cast<int>(r));
+        return TP_ERR_CUDA;
+    }
+    return TP_OK;
+}
+
+inline int launched(const char* what, cudaError_t e, std::string* err) {
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess) return TP_OK;
+    if (err) *err = std::string(what) + ": " + cudaGetErrorString(e);
+    return TP_ERR_CUDA;
+}
+
+// Scratch of a launch: partial results of `rows` x D, their statistics, descriptors.
+struct Scratch {
+    size_t o, ml, desc, total;
+};
+inline Scratch scratch_of(int grid, int rows, int D) {
+    Scratch s;
+    s.o = 0;
+    s.ml = s.o + static_cast<size_t>(grid) * 2 * rows * D * 4;
+    s.desc = s.ml + static_cast<size_t>(grid) * 2 * rows * 2 * 4;
+    s.total = s.desc + static_cast<size_t>(grid) * 16;
+    return s;
+}
+
+// Attention of many rows a sequence (tp_attn_chunk.cu), and the joining of the
+// tiles that its shares, or those of the kernel for few rows, cut.
+int attn_chunk_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest, cudaStream_t stream, std::string* err);
+int attn_join_launch(const PagedArgs& a, int tile_rows, int slot_rows, void* O, uint8_t* scratch, const Scratch& s, int grid,
+                     bool zero_rest, cudaStream_t stream, std::string* err);
+
+}  // namespace tpi
