@@ -8,9 +8,12 @@
 // once serves all of them; 4 * 128 * d operations a key against 4 d bytes: the
 // tensor cores bound it as soon as a tile is full.  The work is cut into equal
 // shares of 128-key blocks (tp_paged_index.h), one persistent CTA an SM:
-//   warp 0      TMA: Q of a tile as one box {64, heads, shards, tokens}, K and
-//               V blocks as one box a page, all lanes issuing; page numbers
-//               are read 32 at a time, a window ahead.
+//   warp 0      TMA: Q of a tile as one box {64, heads, shards, tokens}, K blocks
+//               as one box a page and 64 columns.
+//   warp 11     TMA: V blocks.  A copy takes its issuing thread about 150
+//               cycles here (its operands go to uniform registers one by one),
+//               so K and V have a thread each; page numbers are read 32 at a
+//               time, a window ahead.
 //   warp 1      TMEM owner and S issuer: S = Q K^T (tcgen05, fp32) into three
 //               TMEM buffers.
 //   warp 2      PV issuer: O += P V, P from tensor memory.
@@ -34,7 +37,7 @@ using namespace tpk;
 constexpr int QB = 128;          // TMEM lanes: rows of a tile, at most
 constexpr int KB = 128;          // keys of a block
 constexpr int NS = 3;            // S buffers in TMEM
-constexpr int NT = 352;          // threads
+constexpr int NT = 384;          // threads
 constexpr int BOX = 128 * 128;   // 128 rows of one swizzle span (64 bf16)
 constexpr float RESCALE = 8.0f;  // log2 of the growth of P before O is rescaled
 
@@ -54,6 +57,11 @@ enum {
     NUM_BARS = B_DRAIN + 2
 };
 
+// What the epilogue of a segment needs once its walk has moved on.
+struct Done {
+    int row0, g, rows, where;  // row0: the tile's first token's row; where: -1 the output, else the CTA's slot
+};
+
 template <int D_>
 struct Lay {
     static constexpr int D = D_;
@@ -65,13 +73,16 @@ struct Lay {
     static constexpr int DC = D / 2;         // O columns of a softmax warp
     static constexpr int STG_ROW = DC * 2;   // bytes of a staged row
     static constexpr int STG_OFF = V_OFF + 2 * TILE;
-    static constexpr int XCH_OFF = STG_OFF + 8 * 32 * STG_ROW;  // [3][2][128] fp32
-    static constexpr int BAR_OFF = XCH_OFF + 3 * 2 * QB * 4;
+    static constexpr int XCH_OFF = STG_OFF + 8 * 32 * STG_ROW;  // [7][128] fp32: maxima x 2 x 2, sums x 2, references
+    static constexpr int BAR_OFF = XCH_OFF + 7 * QB * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * NUM_BARS + 16;
-    static constexpr int DATA = SCAN_OFF + 8 * (NT / 32) + 16;
+    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NT / 32 + 1);  // the share's beginning, then one walk a warp
+    static constexpr int DONE_OFF = WALK_OFF + (NT / 32 + 1) * sizeof(TileWalk);
+    static constexpr int PAGE_OFF = (DONE_OFF + 8 * sizeof(Done) + 15) / 16 * 16;  // page numbers of the two producers
+    static constexpr int DATA = PAGE_OFF + 2 * 64 * 4;
     static constexpr int SMEM = DATA + 1024;
     static constexpr int O_COL = NS * KB;
-    static_assert(O_COL + D <= 512 && SMEM <= 232448 && SCAN_OFF % 8 == 0, "configuration");
+    static_assert(O_COL + D <= 512 && SMEM <= 232448 && SCAN_OFF % 8 == 0 && sizeof(TileWalk) % 8 == 0, "configuration");
 };
 
 struct Params {
@@ -79,7 +90,7 @@ struct Params {
     CUtensorMap map_k, map_v;  // the cache as {d, page, k, n_pages}
     PagedView v;
     __nv_bfloat16* o;
-    int heads, group, tile_rows, box_rows;
+    int heads, group, tile_tok, box_rows;
     int kv_per_shard;        // KV heads of a shard, 0 if shards share them
     int shards_per_kv;       // shards that share a KV head (1 if they have their own)
     float scale_log2;
@@ -88,14 +99,6 @@ struct Params {
     int4* desc;
     unsigned* status;
     unsigned long long timeout_ns;
-};
-
-// What the epilogue of a segment needs once its walk has moved on.
-struct Done {
-    long long row0;  // first row of the sequence
-    int g, tile, rows, where;  // where: -1 the output, else the CTA's slot
-    float m, l;
-    bool bad;
 };
 
 template <class L>
@@ -110,7 +113,8 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::BAR_OFF + 8 * NUM_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Tiling tiling = {p.tile_rows, KB, p.group};
+    const Tiling tiling = {p.tile_tok, p.group, 7};
+    const Waiter wait = {abort_flag, p.status, p.timeout_ns};
 
     if (threadIdx.x == 0) {
         mbar_init(bar(B_Q_FULL), 1);
@@ -143,99 +147,88 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
     tc_fence_before();
     pdl_trigger();
     pdl_wait();
-    const Share share = find_share<NT>(p.v, tiling, gbase + L::SCAN_OFF);  // its barriers cover the set-up above
+    TileWalk* walks = reinterpret_cast<TileWalk*>(gbase + L::WALK_OFF);
+    const Share share =  // its barriers cover the set-up above
+        find_share<NT>(p.v, tiling, reinterpret_cast<long long*>(gbase + L::SCAN_OFF), walks);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    TileWalk w;
-    w.start(p.v, tiling, share.s, share.begin - share.seq_begin, share.count);
+    // Each warp walks on its own, in shared memory; lane 0 moves.
+    TileWalk& w = walks[1 + warp];
+    if (lane == 0) w = walks[0];
+    __syncwarp();
+    auto move_on = [&] {
+        __syncwarp();
+        if (lane == 0) w.next(p.v, tiling);
+        __syncwarp();
+    };
 
-    if (warp == 0) {
-        // ---------------------------------------------------------- TMA producer
-        // Order of a segment's loads: for each block i, K(i + 1) then V(i); in
-        // place of the K behind the last come the next segment's Q and first K.
-        bool ok = true;
-        uint32_t q_issued = 0, kn = 0, vn = 0;  // loads issued
+    if (warp == 0 || warp == 11) {
+        // ---------------------------------------------------------- TMA producers
+        const bool is_v = warp == 11;
         const int log2 = p.v.page_log2, per_block = KB / p.box_rows;
-        // Page numbers of a sequence, one a lane: [win, win + 32) and the 32 behind them.
-        struct Pages {
-            int win, cur, nxt;
-        };
-        auto page_at = [&](const TileWalk& x, int i) -> int {
-            if ((static_cast<long long>(i) << log2) >= x.keys) return -1;
-            const int pg = p.v.table[static_cast<long long>(x.s) * p.v.max_pages + i];
-            if (pg >= 0 && pg < p.v.n_pages) return pg;
-            if (p.status) atomicOr(p.status, kStatusPage);
-            return -1;
-        };
-        auto open = [&](const TileWalk& x) -> Pages {
-            const int win = (x.kb * KB) >> log2;
-            return Pages{win, page_at(x, win + lane), page_at(x, win + 32 + lane)};
-        };
-        // K or V of the segment's block i.  A box past the sequence's keys or on no page of the cache has page -1:
-        // TMA fills it with zeros.
-        auto load_kv = [&](const TileWalk& x, Pages& pg, int i, bool is_v) -> bool {
-            uint32_t& n = is_v ? vn : kn;
-            const int st = n & 1;
-            const uint32_t full = bar((is_v ? B_V_FULL : B_K_FULL) + st), empty = bar((is_v ? B_V_EMPTY : B_K_EMPTY) + st);
-            const int key0 = (x.kb + i) * KB, first = key0 >> log2;
-            if (first + per_block > pg.win + 32) {  // 32 is a multiple of a block's pages: whole windows
-                pg.win += 32;
-                pg.cur = pg.nxt;
-                pg.nxt = page_at(x, pg.win + 32 + lane);
-            }
-            bool got = mbar_wait(empty, ((n >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns);
-            if (!__all_sync(0xffffffffu, got)) return false;
-            const int b = lane % per_block, seg = lane / per_block;
-            const int key = key0 + b * p.box_rows;
-            int page = __shfl_sync(0xffffffffu, pg.cur, ((key >> log2) - pg.win) & 31);
-            if (key >= x.keys) page = -1;
-            if (lane == 0) mbar_arrive_expect_tx(full, L::TILE);
+        // Page numbers of two windows of 32 pages: page i of the sequence at ring[i - first page of the segment, mod 64].
+        int* ring = reinterpret_cast<int*>(gbase + L::PAGE_OFF) + (is_v ? 64 : 0);
+        const CUtensorMap* map = is_v ? &p.map_v : &p.map_k;
+        const uint32_t dst0 = is_v ? sV : sK, full0 = bar(is_v ? B_V_FULL : B_K_FULL), empty0 = bar(is_v ? B_V_EMPTY : B_K_EMPTY);
+        int4 cut = make_int4(0, 0, 0, 0);  // the tile that begins here and goes on in the next CTAs
+        uint32_t n = 0, li = 0;            // blocks and segments issued
+        bool ok = true;
+        for (; w.left > 0 && ok; move_on(), ++li) {
+            const int seg = w.segment(), keys = w.keys, g = w.g, page0 = (w.kb * KB) >> log2;
+            const int32_t* table = p.v.table + static_cast<long long>(w.s) * p.v.max_pages;
+            auto page_at = [&](int i) -> int {  // -1: past the sequence's keys, or on no page of the cache
+                if ((static_cast<long long>(i) << log2) >= keys) return -1;
+                const int pg = table[i];
+                if (pg >= 0 && pg < p.v.n_pages) return pg;
+                if (p.status) atomicOr(p.status, kStatusPage);
+                return -1;
+            };
+            ring[lane] = page_at(page0 + lane);
+            int next = page_at(page0 + 32 + lane);
             __syncwarp();
-            if (seg < NSEG)
-                tma_load_4d((is_v ? sV : sK) + st * L::TILE + seg * BOX + b * p.box_rows * 128, is_v ? &p.map_v : &p.map_k,
-                            full, seg * 64, key & ((1 << log2) - 1), x.g, page);
-            __syncwarp();
-            ++n;
-            return true;
-        };
-        auto load_q = [&](const TileWalk& x) -> bool {
-            bool got = q_issued == 0 || mbar_wait(bar(B_Q_EMPTY), (q_issued - 1) & 1u, abort_flag, p.status, p.timeout_ns);
-            if (!__all_sync(0xffffffffu, got)) return false;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(B_Q_FULL), p.tile_rows * D * 2);
-                const int head = p.kv_per_shard ? (x.g % p.kv_per_shard) * p.group : 0;
-                const int shard = p.kv_per_shard ? x.g / p.kv_per_shard : x.g * p.shards_per_kv;
-                const int token = static_cast<int>(x.q.row0) + x.tile * (p.tile_rows / p.group);
-#pragma unroll
-                for (int c = 0; c < NSEG; ++c)
-                    tma_load_4d(sQ + c * BOX, &p.map_q, bar(B_Q_FULL), 64 * c, head, shard, token);
-            }
-            __syncwarp();
-            ++q_issued;
-            return true;
-        };
-        if (w.left > 0) {
-            Pages kp = open(w);
-            ok = load_q(w) && load_kv(w, kp, 0, false);
-            while (ok && w.left > 0) {
-                const int seg = w.segment();
-                TileWalk y = w;
-                y.next(p.v, tiling);
-                Pages vp = open(w), yp{0, -1, -1};
-                if (y.left > 0) yp = open(y);
-                for (int i = 0; i < seg && ok; ++i) {
-                    if (i + 1 < seg) ok = load_kv(w, kp, i + 1, false);
-                    else if (y.left > 0) ok = load_q(y) && load_kv(y, yp, 0, false);
-                    if (ok) ok = load_kv(w, vp, i, true);
+            if (!is_v) {
+                if (w.kb == 0 && seg < w.nkb) {
+                    const long long at = share.begin + share.count - seg;  // the segment is the share's last
+                    cut = make_int4(w.s, g, w.tile, share_of(at + w.nkb - 1, share.per) - static_cast<int>(blockIdx.x) + 1);
                 }
-                w = y;
-                kp = yp;
+                ok = __all_sync(0xffffffffu, li == 0 || wait(bar(B_Q_EMPTY), (li - 1) & 1u));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(B_Q_FULL), p.tile_tok * p.group * D * 2);
+                    const int head = p.kv_per_shard ? (g % p.kv_per_shard) * p.group : 0;
+                    const int shard = p.kv_per_shard ? g / p.kv_per_shard : g * p.shards_per_kv;
+#pragma unroll
+                    for (int c = 0; c < NSEG; ++c)
+                        tma_load_4d(sQ + c * BOX, &p.map_q, bar(B_Q_FULL), 64 * c, head, shard, w.q.row0 + w.tile * p.tile_tok);
+                }
+            }
+            for (int i = 0, at = 0; i < seg; ++i, ++n, at += per_block) {
+                if ((at & 31) == 0) {  // a window begins: the one behind it takes the other half of the ring
+                    ring[(at + 32 + lane) & 63] = next;
+                    next = page_at(page0 + at + 64 + lane);
+                    __syncwarp();
+                }
+                const uint32_t st = n & 1;
+                ok = __all_sync(0xffffffffu, wait(empty0 + 8 * st, ((n >> 1) & 1u) ^ 1u));
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t full = full0 + 8 * st, dst = dst0 + st * L::TILE;
+                    mbar_arrive_expect_tx(full, L::TILE);
+#pragma unroll 2
+                    for (int b = 0; b < per_block; ++b) {
+                        const int page = ring[(at + b) & 63];  // -1: TMA fills the box with zeros and reads nothing
+#pragma unroll
+                        for (int c = 0; c < NSEG; ++c)
+                            tma_load_4d(dst + c * BOX + b * p.box_rows * 128, map, full, c * 64, 0, g, page);
+                    }
+                }
+                __syncwarp();
             }
         }
+        if (!is_v && lane == 0) p.desc[blockIdx.x] = cut;
         // No copy may be in flight when the CTA's shared memory goes.
-        if (q_issued) drain(bar(B_Q_FULL), (q_issued - 1) & 1u);
-        for (uint32_t i = kn > 2 ? kn - 2 : 0; i < kn; ++i) drain(bar(B_K_FULL + (i & 1)), (i >> 1) & 1u);
-        for (uint32_t i = vn > 2 ? vn - 2 : 0; i < vn; ++i) drain(bar(B_V_FULL + (i & 1)), (i >> 1) & 1u);
+        if (!is_v && li) drain(bar(B_Q_FULL), (li - 1) & 1u);
+        for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i) drain(full0 + 8 * (i & 1), (i >> 1) & 1u);
     } else if (warp == 1) {
         // ---------------------------------------------------------- S issuer
         if (lane == 0) {
@@ -245,13 +238,12 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
             uint32_t gb = 0, li = 0;
             for (; w.left > 0 && ok; w.next(p.v, tiling), ++li) {
                 const int seg = w.segment();
-                ok = mbar_wait(bar(B_Q_FULL), li & 1u, abort_flag, p.status, p.timeout_ns);
+                ok = wait(bar(B_Q_FULL), li & 1u);
                 for (int i = 0; i < seg && ok; ++i, ++gb) {
                     const uint32_t st = gb & 1u, sb = gb % NS;
                     // Buffer sb held P of block gb - NS: its PV must have read it.
-                    ok = (gb < NS || mbar_wait(bar(B_PV_DONE + sb), ((gb - NS) / NS) & 1u, abort_flag, p.status,
-                                               p.timeout_ns)) &&
-                         mbar_wait(bar(B_K_FULL + st), (gb >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
+                    ok = (gb < NS || wait(bar(B_PV_DONE + sb), ((gb - NS) / NS) & 1u)) &&
+                         wait(bar(B_K_FULL + st), (gb >> 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t kdesc = kdesc0 + (st * L::TILE) / 16;
@@ -280,11 +272,11 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                 const int seg = w.segment();
                 for (int i = 0; i < seg && ok; ++i, ++gb) {
                     const uint32_t st = gb & 1u, pb = gb % NS;
-                    ok = mbar_wait(bar(B_P_FULL + pb), (gb / NS) & 1u, abort_flag, p.status, p.timeout_ns) &&
-                         mbar_wait(bar(B_V_FULL + st), (gb >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
+                    ok = wait(bar(B_P_FULL + pb), (gb / NS) & 1u) &&
+                         wait(bar(B_V_FULL + st), (gb >> 1) & 1u);
                     // The first PV of a segment overwrites O: the previous epilogue must have read it.
                     if (ok && i == 0 && li > 0)
-                        ok = mbar_wait(bar(B_O_EMPTY), (li - 1) & 1u, abort_flag, p.status, p.timeout_ns);
+                        ok = wait(bar(B_O_EMPTY), (li - 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t vdesc = vdesc0 + (st * L::TILE) / 16;
@@ -309,14 +301,14 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
         const int r = q * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
         float* xch = reinterpret_cast<float*>(gbase + L::XCH_OFF);
-        if (threadIdx.x == 96) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+        Done* done = reinterpret_cast<Done*>(gbase + L::DONE_OFF) + (warp - 3);
         // Failures pass through here before the warps act on them, so the two halves of a quadrant leave together.
         auto pair_all = [&](bool v) -> bool { return named_bar_and(1u + static_cast<uint32_t>(q), 64u, v); };
+        bool bad = false;  // a wait gave up: acted on at the next pair_all, with the other half
         // Outputs of a finished segment: O / l as bf16, or O, m and l to the CTA's slot.
-        auto epilogue = [&](const Done& e, uint32_t eli) -> bool {
-            bool got = !e.bad && mbar_wait(bar(B_O_FULL), eli & 1u, abort_flag, p.status, p.timeout_ns);
+        auto epilogue = [&](uint32_t eli) -> bool {
+            bool got = !bad && wait(bar(B_O_FULL), eli & 1u);
             got = __all_sync(0xffffffffu, got);
-            xch[4 * QB + hf * QB + r] = e.l;
             if (!pair_all(got)) return false;
             tc_fence_after();
             const float l = xch[4 * QB + r] + xch[5 * QB + r];
@@ -328,6 +320,7 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_O_EMPTY));
+            const Done e = *done;
             if (q * 32 >= e.rows) return true;
             if (e.where >= 0) {
                 if (r < e.rows) {
@@ -337,7 +330,7 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                     for (int c = 0; c < DC / 4; ++c)
                         dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
                                              __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
-                    if (hf == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(e.m, l);
+                    if (hf == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(xch[6 * QB + r], l);
                 }
                 return true;
             }
@@ -360,54 +353,45 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
             }
             __syncwarp();
             constexpr int STEP = 32 / PIECES;
-#pragma unroll
-            for (int i = 0; i < 32 / STEP; ++i) {
-                const int row = i * STEP + lane / PIECES, u = lane % PIECES;
-                const uint4 x = ld_shared_v4(at(row, u));
-                if (q * 32 + row < e.rows) {
-                    const unsigned rr = static_cast<unsigned>(e.tile * p.tile_rows + q * 32 + row), grp = p.group;
-                    const long long token = e.row0 + rr / grp;
-                    __nv_bfloat16* y = p.o + (token * p.heads + e.g * p.group + rr % grp) * D + hf * DC + u * 8;
-                    *reinterpret_cast<uint4*>(y) = x;
-                }
+            const int u = lane % PIECES;
+#pragma unroll 1
+            for (int row = lane / PIECES; row < 32; row += STEP) {
+                const int x = q * 32 + row;
+                if (x >= e.rows) break;
+                const int tok = x / p.group;
+                __nv_bfloat16* y = p.o + (static_cast<long long>(e.row0 + tok) * p.heads + e.g * p.group + x - tok * p.group) * D +
+                                   hf * DC + u * 8;
+                *reinterpret_cast<uint4*>(y) = ld_shared_v4(at(row, u));
             }
             return true;
         };
         bool ok = true, pending = false;
-        Done pd{};
         uint32_t gb = 0, li = 0;
-        for (; w.left > 0; w.next(p.v, tiling), ++li) {
-            const int seg = w.segment();
-            Done cur;
-            cur.row0 = w.q.row0;
-            cur.g = w.g;
-            cur.tile = w.tile;
-            cur.rows = static_cast<int>(pmin(p.tile_rows, static_cast<long long>(w.q.n) * p.group -
-                                                              static_cast<long long>(w.tile) * p.tile_rows));
-            const bool begins = w.kb == 0, ends = w.kb + seg == w.nkb;
-            cur.where = begins && ends ? -1 : begins ? 1 : 0;
-            if (begins && !ends && threadIdx.x == 96) {
-                const long long first = share.begin + share.count - seg;
-                const int last = static_cast<int>((first + w.nkb - 1) / share.per);
-                p.desc[blockIdx.x] = make_int4(w.s, w.g, w.tile, last - static_cast<int>(blockIdx.x) + 1);
-            }
-            const bool active = q * 32 < cur.rows;  // some row of the quadrant is the tile's
-            const int seen = r < cur.rows ? row_keys(w.q, w.keys, static_cast<long long>(w.tile) * p.tile_rows + r, p.group) : 0;
+        // One turn a segment, and one more for the last one's outputs, so that the epilogue's code is there once.
+        for (;; ++li) {
+            const bool have = w.left > 0;
+            if (!have && !pending) break;
+            const int seg = have ? w.segment() : 1;
+            const int rows = have ? tile_tokens(w.q, tiling, w.tile) * p.group : 0;
+            const bool active = q * 32 < rows;  // some row of the quadrant is the tile's
+            // Keys behind the current block's first (lim: that this row sees, from this half's first on; left: that exist).
+            int lim = (r < rows ? token_keys(w.q, w.keys, w.tile * p.tile_tok + r / p.group) : 0) - w.kb * KB - hf * KC;
+            int left = w.keys - w.kb * KB;
             float m_ref = -INFINITY, l_sum = 0.0f;
-            bool bad = false;
-            for (int i = 0; i < seg; ++i, ++gb) {
+#pragma unroll 1
+            for (int i = 0; i < seg; ++i) {
+              if (have) {
                 const uint32_t st = gb % NS;
-                const int key0 = (w.kb + i) * KB;
-                bool got = !bad && mbar_wait(bar(B_S_FULL + st), (gb / NS) & 1u, abort_flag, p.status, p.timeout_ns);
+                bool got = !bad && wait(bar(B_S_FULL + st), (gb / NS) & 1u);
                 // The block with the sequence's last key: rows of V behind it are whatever the page holds, and
                 // 0 * NaN is NaN.  They are cleared before P is announced.
-                if (got && key0 + KB > w.keys && key0 < w.keys) {
+                if (got && left < KB && left > 0) {
                     const uint32_t vs = gb & 1u;
-                    got = mbar_wait(bar(B_V_FULL + vs), (gb >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
+                    got = wait(bar(B_V_FULL + vs), (gb >> 1) & 1u);
                     if (got) {
-                        const int from = w.keys - key0;
-                        for (int x = static_cast<int>(threadIdx.x) - 96; x < (KB - from) * NSEG * 8; x += 256) {
-                            const int row = from + x / (NSEG * 8), c = x % (NSEG * 8);
+                        #pragma unroll 1
+                        for (int x = static_cast<int>(threadIdx.x) - 96; x < (KB - left) * NSEG * 8; x += 256) {
+                            const int row = left + x / (NSEG * 8), c = x % (NSEG * 8);
                             st_shared_v4(sV + vs * L::TILE + (c >> 3) * BOX + row * 128 + (c & 7) * 16, 0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
@@ -422,7 +406,6 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                     for (int c = 0; c < KC / 32; ++c)
                         tmem_ld32(tmem + lane_off + st * KB + hf * KC + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
                     tmem_ld_wait();
-                    const int lim = seen - (key0 + hf * KC);  // columns that the row sees
                     if (lim < KC) {
 #pragma unroll
                         for (int c = 0; c < KC; ++c)
@@ -477,10 +460,10 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                     if (__any_sync(0xffffffffu, rescale)) {
                         // O is rescaled in place: the PV of the previous block must be done.
                         const uint32_t pb = gb - 1;
-                        const bool got2 = mbar_wait(bar(B_PV_DONE + pb % NS), (pb / NS) & 1u, abort_flag, p.status, p.timeout_ns);
+                        const bool got2 = wait(bar(B_PV_DONE + pb % NS), (pb / NS) & 1u);
                         __syncwarp();
                         if (!__all_sync(0xffffffffu, got2)) {
-                            bad = true;  // acted on at the next pair_all, with the other half
+                            bad = true;
                         } else {
                             tc_fence_after();
 #pragma unroll 1
@@ -503,22 +486,29 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_P_FULL + st));
+                ++gb;
+                lim -= KB;
+                left -= KB;
+              }
                 if (i == 0 && pending) {
-                    if (!epilogue(pd, li - 1)) {
+                    if (!epilogue(li - 1)) {
                         ok = false;
                         break;
                     }
                     pending = false;
                 }
             }
-            if (!ok) break;
-            cur.m = m_ref;
-            cur.l = l_sum;
-            cur.bad = bad;
-            pd = cur;
+            if (!ok || !have) break;
+            xch[(4 + hf) * QB + r] = l_sum;  // the epilogue's pair_all comes before either half reads
+            if (hf == 0) xch[6 * QB + r] = m_ref;
             pending = true;
+            __syncwarp();
+            if (lane == 0) {
+                const bool begins = w.kb == 0, ends = w.kb + seg == w.nkb;
+                *done = Done{w.q.row0 + w.tile * p.tile_tok, w.g, rows, begins && ends ? -1 : begins ? 1 : 0};
+            }
+            move_on();
         }
-        if (ok && pending) epilogue(pd, li - 1);
     }
     __syncwarp();
     tc_fence_before();
@@ -541,7 +531,7 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
     p.o = static_cast<__nv_bfloat16*>(O);
     p.heads = a.heads;
     p.group = a.heads / a.kv_heads;
-    p.tile_rows = QB / p.group * p.group;
+    p.tile_tok = QB / p.group;
     p.kv_per_shard = a.kv_heads / a.t;
     p.shards_per_kv = p.kv_per_shard ? 1 : a.t / a.kv_heads;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(L::D));
@@ -555,7 +545,7 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
         const cuuint64_t strides[3] = {static_cast<cuuint64_t>(L::D) * 2, static_cast<cuuint64_t>(a.shard_w) * 2,
                                        static_cast<cuuint64_t>(a.ld_qkv) * 2};
         const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.group / p.shards_per_kv),
-                                   static_cast<cuuint32_t>(p.shards_per_kv), static_cast<cuuint32_t>(QB / p.group)};
+                                   static_cast<cuuint32_t>(p.shards_per_kv), static_cast<cuuint32_t>(p.tile_tok)};
         const cuuint32_t estr[4] = {1, 1, 1, 1};
         const CUresult r = encode(&p.map_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.QKV), dims, strides,
                                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -583,7 +573,7 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
     rc = tpi::launched("chunk attention launch",
                        tpi::launch_pdl(attn_chunk_kernel<L>, dim3(grid), dim3(NT), L::SMEM, stream, p), err);
     if (rc) return rc;
-    return tpi::attn_join_launch(a, p.tile_rows, QB, O, w, s, grid, zero_rest, stream, err);
+    return tpi::attn_join_launch(a, p.tile_tok, QB, O, w, s, grid, zero_rest, stream, err);
 }
 
 }  // namespace

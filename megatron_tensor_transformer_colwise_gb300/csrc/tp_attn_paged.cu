@@ -39,7 +39,7 @@ using namespace tpk;
 using tpi::launched;
 using tpi::Scratch;
 
-constexpr int R = 16;        // query rows of a tile
+constexpr int R = 16;        // query rows of a tile, at most
 constexpr int NW = 8;        // consumer warps
 constexpr int NT = 32 * (NW + 1);
 constexpr float RESCALE = 8.0f;  // log2 of the growth of a weight before the sums are rescaled
@@ -50,7 +50,9 @@ template <int D_, bool E4M3_, int WPB_, int NST_>
 struct Cfg {
     static constexpr int D = D_, WPB = WPB_, NST = NST_;
     static constexpr bool E4M3 = E4M3_;
-    static constexpr int KB = 16 * WPB;
+    static constexpr int LOG2_KB = WPB == 8 ? 7 : 6;
+    static constexpr int KB = 1 << LOG2_KB;
+    static_assert(KB == 16 * WPB, "keys of a block");
     static constexpr int ROW = E4M3 ? D : 2 * D;       // bytes of a cached row
     static constexpr int SEG = ROW < 128 ? ROW : 128;  // bytes of a TMA box row (one swizzle span)
     static constexpr int NSEG = ROW / SEG;
@@ -63,7 +65,8 @@ struct Cfg {
     static constexpr int XM_OFF = ACC_OFF + NW * R * LD_ACC * 4;
     static constexpr int BAR_OFF = XM_OFF + 2 * NW * R * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * 2 * NST;
-    static constexpr int DATA = SCAN_OFF + 8 * (NW + 1) + 32;
+    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NW + 2);  // the share's beginning, then one walk a warp
+    static constexpr int DATA = WALK_OFF + (NW + 2) * sizeof(TileWalk);
     static constexpr int SMEM = DATA + 1024;
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -75,7 +78,7 @@ struct Params {
     const __nv_bfloat16* qkv;
     long long ld_qkv;
     __nv_bfloat16* o;
-    int heads, heads_per_shard, shard_w, group, box_rows;
+    int heads, heads_per_shard, shard_w, group, tile_tok, box_rows;
     float scale_log2;
     float* part_o;   // [grid][2][R][D]
     float* part_ml;  // [grid][2][R][2]
@@ -146,7 +149,8 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
     const uint32_t full0 = base + C::BAR_OFF, empty0 = full0 + 8 * NST;
     volatile int* abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Tiling tiling = {R, KB, p.group};
+    const Tiling tiling = {p.tile_tok, p.group, C::LOG2_KB};
+    const Waiter wait = {abort_flag, p.status, p.timeout_ns};
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
@@ -160,52 +164,62 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
     }
     pdl_trigger();
     pdl_wait();
-    const Share share = find_share<NT>(p.v, tiling, gbase + C::SCAN_OFF);  // its barriers cover the set-up above
-    TileWalk w;
-    w.start(p.v, tiling, share.s, share.begin - share.seq_begin, share.count);
+    TileWalk* walks = reinterpret_cast<TileWalk*>(gbase + C::WALK_OFF);
+    const Share share =  // its barriers cover the set-up above
+        find_share<NT>(p.v, tiling, reinterpret_cast<long long*>(gbase + C::SCAN_OFF), walks);
+    // Each warp walks on its own, in shared memory; lane 0 moves.
+    TileWalk& w = walks[1 + warp];
+    if (lane == 0) w = walks[0];
+    __syncwarp();
+    auto move_on = [&] {
+        __syncwarp();
+        if (lane == 0) w.next(p.v, tiling);
+        __syncwarp();
+    };
 
     if (warp == NW) {
         // ------------------------------------------------------ producer
         bool ok = true;
         int n = 0;  // blocks issued
-        for (; w.left > 0 && ok; w.next(p.v, tiling)) {
-            const int seg = w.segment();
+        for (; w.left > 0 && ok; move_on()) {
+            const int seg = w.segment(), kb0 = w.kb, keys = w.keys, g = w.g;
+            const int32_t* table = p.v.table + static_cast<long long>(w.s) * p.v.max_pages;
             const int page_rows = 1 << p.v.page_log2;
             const int per_block = KB / p.box_rows;  // boxes (pages, or parts of one) of a block
             int window = -32, held = -1;            // pages [window, window + 32) of the sequence, one a lane
             for (int i = 0; i < seg && ok; ++i, ++n) {
                 const int st = n % NST;
                 const uint32_t full = full0 + 8 * st;
-                const int key0 = (w.kb + i) * KB;
+                const int key0 = (kb0 + i) * KB;
                 const int first = key0 >> p.v.page_log2;
                 if (first + per_block > window + 32 || first < window) {
                     window = first;
                     const int pg = window + lane;
                     held = -1;
-                    if (pg * static_cast<long long>(page_rows) < w.keys) {
-                        held = p.v.table[static_cast<long long>(w.s) * p.v.max_pages + pg];
+                    if (pg * static_cast<long long>(page_rows) < keys) {
+                        held = table[pg];
                         if (held < 0 || held >= p.v.n_pages) {
                             held = -1;
                             if (p.status) atomicOr(p.status, kStatusPage);
                         }
                     }
                 }
-                ok = mbar_wait(empty0 + 8 * st, ((n / NST) & 1) ^ 1, abort_flag, p.status, p.timeout_ns);
+                ok = wait(empty0 + 8 * st, ((n / NST) & 1) ^ 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 // Box b of the block: keys key0 + b * box_rows.  A box past the
                 // sequence's keys, or on a page outside the cache, is loaded
                 // from page -1: TMA fills it with zeros and reads nothing.
-                const int b = lane % per_block, seg_i = lane / per_block;  // lanes: boxes x spans of a row
-                const int k_box = key0 + b * p.box_rows;
-                int page = __shfl_sync(0xffffffffu, held, (k_box >> p.v.page_log2) - window);
-                if (k_box >= w.keys) page = -1;
-                const int off = k_box & (page_rows - 1);
                 if constexpr (E4M3) {
-                    const bool mine = seg_i == 0;
-                    const uint32_t sc = base + C::SC_OFF + st * C::SCALES + b * p.box_rows * 4;
+                    // Scales, a lane a box; those of no page are zeros.
+                    const int k_box = key0 + lane * p.box_rows;
+                    int page = __shfl_sync(0xffffffffu, held, (first - window + lane) & 31);
+                    if (k_box >= keys) page = -1;
+                    const bool mine = lane < per_block;
+                    const uint32_t sc = base + C::SC_OFF + st * C::SCALES + lane * p.box_rows * 4;
                     const unsigned scaled = __ballot_sync(0xffffffffu, mine && page >= 0);
-                    if (mine && page < 0) {  // scales of no page: zeros
+                    if (mine && page < 0) {
+#pragma unroll 1
                         for (int x = 0; x < p.box_rows; x += 4) {
                             st_shared_v4(sc + x * 4, 0, 0, 0, 0);
                             st_shared_v4(sc + KB * 4 + x * 4, 0, 0, 0, 0);
@@ -214,21 +228,29 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(full, 2 * C::TILE + 8u * p.box_rows * __popc(scaled));
-                    __syncwarp();
-                    if (mine && page >= 0) {
-                        const long long at = paged_row(p.v, page, w.g, off);
-                        bulk_load(sc, p.k_scale + at, p.box_rows * 4, full);
-                        bulk_load(sc + KB * 4, p.v_scale + at, p.box_rows * 4, full);
-                    }
                 } else {
                     if (lane == 0) mbar_arrive_expect_tx(full, 2 * C::TILE);
-                    __syncwarp();
                 }
-                if (seg_i < C::NSEG) {
-                    const uint32_t dst = base + st * C::STAGE + seg_i * (KB * C::SEG) + b * p.box_rows * C::SEG;
-                    const int c0 = seg_i * (E4M3 ? 128 : 64);
-                    tma_load_4d(dst, &p.map_k, full, c0, off, w.g, page);
-                    tma_load_4d(dst + C::TILE, &p.map_v, full, c0, off, w.g, page);
+                // One lane issues: a copy's operands are uniform registers, so lanes would take turns.
+#pragma unroll 1
+                for (int b = 0; b < per_block; ++b) {
+                    const int k_box = key0 + b * p.box_rows, off = k_box & (page_rows - 1);
+                    int page = __shfl_sync(0xffffffffu, held, ((k_box >> p.v.page_log2) - window) & 31);
+                    if (k_box >= keys) page = -1;
+                    if (lane == 0) {
+                        const uint32_t dst = base + st * C::STAGE + b * p.box_rows * C::SEG;
+#pragma unroll
+                        for (int c = 0; c < C::NSEG; ++c) {
+                            tma_load_4d(dst + c * (KB * C::SEG), &p.map_k, full, c * (E4M3 ? 128 : 64), off, g, page);
+                            tma_load_4d(dst + C::TILE + c * (KB * C::SEG), &p.map_v, full, c * (E4M3 ? 128 : 64), off, g, page);
+                        }
+                        if (E4M3 && page >= 0) {
+                            const uint32_t sc = base + C::SC_OFF + st * C::SCALES + b * p.box_rows * 4;
+                            const long long at = paged_row(p.v, page, g, off);
+                            bulk_load(sc, p.k_scale + at, p.box_rows * 4, full);
+                            bulk_load(sc + KB * 4, p.v_scale + at, p.box_rows * 4, full);
+                        }
+                    }
                 }
                 __syncwarp();
             }
@@ -245,14 +267,15 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
         bool ok = true;
         int n = 0;
         if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-        for (; w.left > 0; w.next(p.v, tiling)) {
-            const int seg = w.segment();
-            const int rows = static_cast<int>(pmin(R, static_cast<long long>(w.q.n) * p.group - static_cast<long long>(w.tile) * R));
+        for (; w.left > 0; move_on()) {
+            const int seg = w.segment(), kb0 = w.kb, keys = w.keys, g = w.g;
+            const PagedSeq q = w.q;
+            const int tok0 = w.tile * p.tile_tok;  // first token of the tile
+            const int rows = tile_tokens(q, tiling, w.tile) * p.group;
             // Row i of the tile: its query head's row of the buffer, and the keys it sees.
             auto q_row = [&](int i) -> const __nv_bfloat16* {
-                const long long r = static_cast<long long>(w.tile) * R + i;
-                const int j = w.g * p.group + static_cast<int>(r % p.group);
-                return p.qkv + (w.q.row0 + r / p.group) * p.ld_qkv +
+                const int tok = i / p.group, j = g * p.group + i - tok * p.group;
+                return p.qkv + static_cast<long long>(q.row0 + tok0 + tok) * p.ld_qkv +
                        static_cast<long long>(j / p.heads_per_shard) * p.shard_w + (j % p.heads_per_shard) * D;
             };
             int lim[2];
@@ -261,7 +284,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int i = r0 + 8 * h;
-                lim[h] = i < rows ? row_keys(w.q, w.keys, static_cast<long long>(w.tile) * R + i, p.group) : 0;
+                lim[h] = i < rows ? token_keys(q, keys, tok0 + i / p.group) : 0;
                 const __nv_bfloat16* x = i < rows ? q_row(i) : nullptr;
                 if constexpr (!E4M3) {
 #pragma unroll
@@ -321,11 +344,11 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
             for (int i = 0; i < seg; ++i, ++n) {
                 if (C::WPB < NW && (n & 1) != warp / C::WPB) continue;
                 const int st = n % NST;
-                ok = ok && mbar_wait(full0 + 8 * st, (n / NST) & 1, abort_flag, p.status, p.timeout_ns);
+                ok = ok && wait(full0 + 8 * st, (n / NST) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 const uint32_t sk = base + st * C::STAGE, sv = sk + C::TILE;
-                const int key0 = (w.kb + i) * KB + wk * 16;
+                const int key0 = (kb0 + i) * KB + wk * 16;
                 float s[2][4] = {};
                 if constexpr (!E4M3) {
                     // Matrices (keys 0-7, 8-15) x (d 0-7, 8-15) of a step: lanes 0-7 and 16-23 address keys
@@ -428,12 +451,12 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                 // O += P V.  Rows of V past the sequence's keys are whatever the page holds: cleared, since
                 // 0 * NaN is NaN.  `live` masks the halves of a register that holds keys 2t, 2t + 1 (+ 8).
                 uint32_t live[2] = {0xffffffffu, 0xffffffffu};
-                const bool tail = key0 + 16 > w.keys;
+                const bool tail = key0 + 16 > keys;
                 if (tail) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int key = key0 + h * 8 + 2 * t;
-                        live[h] = (key < w.keys ? 0xffffu : 0u) | (key + 1 < w.keys ? 0xffff0000u : 0u);
+                        live[h] = (key < keys ? 0xffffu : 0u) | (key + 1 < keys ? 0xffff0000u : 0u);
                     }
                 }
                 // Matrices (keys 0-7, 8-15) x two neighbouring eights of 16-bit columns.
@@ -515,7 +538,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                 }
             }
             named_bar_sync(1, 32 * NW);
-            const bool begins = w.kb == 0, ends = w.kb + seg == w.nkb;
+            const bool begins = kb0 == 0, ends = kb0 + seg == w.nkb;
             const int slot = begins ? 1 : 0;
             if (ok) {
                 for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * NW) {
@@ -534,8 +557,9 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                     }
                     if (begins && ends) {
                         const float inv = lt != 0.0f ? 1.0f / lt : 0.0f;  // nothing seen: zeros
-                        const long long r = static_cast<long long>(w.tile) * R + i;
-                        __nv_bfloat16* y = p.o + ((w.q.row0 + r / p.group) * p.heads + w.g * p.group + r % p.group) * D + c;
+                        const int tok = i / p.group;
+                        __nv_bfloat16* y = p.o +
+                            (static_cast<long long>(q.row0 + tok0 + tok) * p.heads + g * p.group + i - tok * p.group) * D + c;
                         *reinterpret_cast<uint2*>(y) =
                             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
                     } else {
@@ -547,8 +571,8 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                 if (begins && !ends && threadIdx.x == 0) {
                     // The tile's last block is in CTA (first block + blocks - 1) / per.
                     const long long at = share.begin + share.count - seg;
-                    const int last = static_cast<int>((at + w.nkb - 1) / share.per);
-                    p.desc[blockIdx.x] = make_int4(w.s, w.g, w.tile, last - static_cast<int>(blockIdx.x) + 1);
+                    const int last = share_of(at + w.nkb - 1, share.per);
+                    p.desc[blockIdx.x] = make_int4(w.s, g, w.tile, last - static_cast<int>(blockIdx.x) + 1);
                 }
             }
         }
@@ -560,17 +584,16 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
 // on in slot 0 of the next ones: O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i,
 // in the order of the keys.  One warp per row, blockIdx.y rows apart.
 // zero_rest: also clears the rows of O that no sequence owns.
-// A tile has tile_rows rows, a slot room for ROWS.
+// A tile has tile_tok tokens of `group` rows, a slot room for ROWS rows.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, int tile_rows, int heads, const float* part_o,
+__global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, int tile_tok, int heads, const float* part_o,
                                                         const float* part_ml, const int4* desc, __nv_bfloat16* o,
                                                         int zero_rest) {
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (zero_rest) {
-        const long long a = v.n_seqs ? pmin(pmax(v.q_start[0], 0), v.rows) : 0;
-        const long long b = v.n_seqs ? pmin(pmax(v.q_start[v.n_seqs], a), v.rows) : 0;
+        const int a = imin(imax(v.q_start[0], 0), v.rows), b = imin(imax(v.q_start[v.n_seqs], a), v.rows);
         const long long per = static_cast<long long>(heads) * D / 8;
         const long long threads = static_cast<long long>(gridDim.x) * gridDim.y * 256;
         const long long me = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
@@ -581,8 +604,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, 
     const int4 x = desc[blockIdx.x];
     if (x.w == 0) return;
     const PagedSeq q = paged_seq(v, x.x);
-    const long long total = static_cast<long long>(q.n) * group - static_cast<long long>(x.z) * tile_rows;
-    const int rows = static_cast<int>(pmin(tile_rows, total));
+    const int rows = tile_tokens(q, Tiling{tile_tok, group, 0}, x.z) * group;
     constexpr int E = D / 32;
     for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
         // Slot 1 of the first CTA is followed in memory by slot 0 of the next; then every second slot.
@@ -610,8 +632,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, 
             }
         }
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-        const long long r = static_cast<long long>(x.z) * tile_rows + i;
-        __nv_bfloat16* y = o + ((q.row0 + r / group) * heads + x.y * group + r % group) * D + lane * E;
+        const int tok = i / group;
+        __nv_bfloat16* y =
+            o + (static_cast<long long>(q.row0 + x.z * tile_tok + tok) * heads + x.y * group + i - tok * group) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(y + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
     }
@@ -637,6 +660,7 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     p.heads_per_shard = a.heads / a.t;
     p.shard_w = static_cast<int>(a.shard_w);
     p.group = a.heads / a.kv_heads;
+    p.tile_tok = R / p.group;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(C::D));
     const Scratch s = tpi::scratch_of(grid, R, C::D);
     uint8_t* w = static_cast<uint8_t*>(scratch);
@@ -656,14 +680,14 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     rc = launched("paged attention launch",
                   tpi::launch_pdl(attn_few_kernel<C>, dim3(grid), dim3(NT), C::SMEM, stream, p), err);
     if (rc) return rc;
-    return tpi::attn_join_launch(a, R, R, O, w, s, grid, zero_rest, stream, err);
+    return tpi::attn_join_launch(a, p.tile_tok, R, O, w, s, grid, zero_rest, stream, err);
 }
 
 template <int D, int ROWS>
-cudaError_t join(const tpi::PagedArgs& a, int tile_rows, void* O, uint8_t* w, const Scratch& s, int grid, bool zero_rest,
+cudaError_t join(const tpi::PagedArgs& a, int tile_tok, void* O, uint8_t* w, const Scratch& s, int grid, bool zero_rest,
                  cudaStream_t stream) {
     return tpi::launch_pdl(attn_join_kernel<D, ROWS>, dim3(grid, (ROWS + 7) / 8), dim3(256), 0, stream,
-                           tpi::paged_view(a), a.heads / a.kv_heads, tile_rows, a.heads,
+                           tpi::paged_view(a), a.heads / a.kv_heads, tile_tok, a.heads,
                            reinterpret_cast<const float*>(w + s.o), reinterpret_cast<const float*>(w + s.ml),
                            reinterpret_cast<const int4*>(w + s.desc), static_cast<__nv_bfloat16*>(O), zero_rest ? 1 : 0);
 }
@@ -675,15 +699,15 @@ namespace tpi {
 // The kernel for many rows has the larger tiles.
 size_t attn_paged_scratch_bytes(int head_dim) { return scratch_of(device_sm_count(), 128, head_dim).total; }
 
-int attn_join_launch(const PagedArgs& a, int tile_rows, int slot_rows, void* O, uint8_t* w, const Scratch& s, int grid,
+int attn_join_launch(const PagedArgs& a, int tile_tok, int slot_rows, void* O, uint8_t* w, const Scratch& s, int grid,
                      bool zero_rest, cudaStream_t stream, std::string* err) {
     cudaError_t e;
     if (a.head_dim == 128)
-        e = slot_rows == R ? join<128, R>(a, tile_rows, O, w, s, grid, zero_rest, stream)
-                           : join<128, 128>(a, tile_rows, O, w, s, grid, zero_rest, stream);
+        e = slot_rows == R ? join<128, R>(a, tile_tok, O, w, s, grid, zero_rest, stream)
+                           : join<128, 128>(a, tile_tok, O, w, s, grid, zero_rest, stream);
     else
-        e = slot_rows == R ? join<64, R>(a, tile_rows, O, w, s, grid, zero_rest, stream)
-                           : join<64, 128>(a, tile_rows, O, w, s, grid, zero_rest, stream);
+        e = slot_rows == R ? join<64, R>(a, tile_tok, O, w, s, grid, zero_rest, stream)
+                           : join<64, 128>(a, tile_tok, O, w, s, grid, zero_rest, stream);
     return launched("paged attention join launch", e, err);
 }
 
@@ -696,8 +720,9 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
     }
     // Few rows a sequence and KV head (the caller's bound on its new tokens, or all rows of the call): one tile
     // of 16.  More: tiles of 128 on tcgen05.
+    const int group = a.heads / a.kv_heads;
     const int64_t most = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
-    if (most * (a.heads / a.kv_heads) > R && !a.e4m3)
+    if (group > R || (most * group > R && !a.e4m3))
         return attn_chunk_launch(a, O, scratch, zero_rest, stream, err);
     if (a.head_dim == 128)
         return a.e4m3 ? launch_few<Cfg<128, true, 8, 4>>(a, O, scratch, zero_rest, stream, err)

@@ -37,55 +37,84 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// The share of CTA blockIdx.x: its first sequence, block there, and number of
-// blocks; the same in all threads.  Every thread sums the blocks of a run of
-// sequences, and a scan of the sums finds the share's beginning.
-struct Share {
-    long long begin, count, per, seq_begin;  // seq_begin: number of the first sequence's first block
-    int s;
+// mbar_wait with its loop out of line: the waits of a kernel's roles, inlined
+// with it, took more of the instruction cache than the work between them.
+__device__ __noinline__ inline bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
+                                                  uint64_t timeout_ns) {
+    return mbar_wait(bar, parity, abort_flag, status, timeout_ns);
+}
+struct Waiter {
+    volatile int* abort_flag;
+    unsigned* status;
+    uint64_t timeout_ns;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        return mbar_try_wait(bar, parity) || bar_wait_slow(bar, parity, abort_flag, status, timeout_ns);
+    }
 };
-// scratch: 8 (NT / 32) + 16 bytes of shared memory.
+
+// total / grid rounded up, without a 64-bit division: an approximate quotient,
+// corrected by the remainder (below 2^31 for total < 2^50).
+__device__ __forceinline__ long long share_size(long long total, int grid) {
+    const long long q = static_cast<long long>(__ll2float_rn(total) / static_cast<float>(grid));
+    const int rem = static_cast<int>(total - q * grid);
+    const int more = rem >= 0 ? (rem + grid - 1) / grid : -(-rem / grid);
+    return q + more;
+}
+
+// The CTA whose share holds block `at`: at / per, the same way.
+__device__ __forceinline__ int share_of(long long at, long long per) {
+    long long q = static_cast<long long>(__ll2float_rn(at) / __ll2float_rn(per));
+    while (q * per > at) --q;
+    while ((q + 1) * per <= at) ++q;
+    return static_cast<int>(q);
+}
+
+// The share of CTA blockIdx.x: its first block, their number, every CTA's
+// number; *walk0 gets the walk's beginning.  Every thread sums the blocks of a
+// run of sequences, a scan of the sums finds the share's beginning, and the
+// thread that holds it starts the walk.  sums: NT / 32 + 1 words of 8 bytes of
+// shared memory.  Ends with __syncthreads.
+struct Share {
+    long long begin, count, per;
+};
 template <int NT>
-__device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t, uint8_t* scratch) {
-    long long* sums = reinterpret_cast<long long*>(scratch);
-    long long* found = sums + NT / 32;
-    int* found_s = reinterpret_cast<int*>(found + 1);
+__device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t, long long* sums, TileWalk* walk0) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int run = (v.n_seqs + NT - 1) / NT;
     const int s0 = min(tid * run, v.n_seqs), s1 = min(s0 + run, v.n_seqs);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += seq_blocks(v, paged_seq(v, s), t) * v.kv_heads;
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s) mine += seq_blocks(v, paged_seq(v, s), t);
     long long inc = mine;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
     }
     if (lane == 31) sums[tid >> 5] = inc;
+    if (tid == 0) walk0->left = 0;
     __syncthreads();
     long long before = inc - mine, total = 0;
+#pragma unroll 1
     for (int w = 0; w < NT / 32; ++w) {
         if (w < (tid >> 5)) before += sums[w];
         total += sums[w];
     }
     Share x;
-    x.per = (total + gridDim.x - 1) / gridDim.x;
+    x.per = share_size(total, static_cast<int>(gridDim.x));
     x.begin = pmin(static_cast<long long>(blockIdx.x) * x.per, total);
     x.count = pmin(x.per, total - x.begin);
     if (x.count > 0 && x.begin >= before && x.begin < before + mine) {
-        long long at = before;
         int s = s0;
-        for (; s < s1; ++s) {
-            const long long n = seq_blocks(v, paged_seq(v, s), t) * v.kv_heads;
-            if (x.begin < at + n) break;
-            at += n;
+#pragma unroll 1
+        for (; s < s1 - 1; ++s) {
+            const long long n = seq_blocks(v, paged_seq(v, s), t);
+            if (x.begin < before + n) break;
+            before += n;
         }
-        *found = at;
-        *found_s = s;
+        walk0->start(v, t, s, x.begin - before, x.count);
     }
     __syncthreads();
-    x.seq_begin = *found;
-    x.s = x.count > 0 ? *found_s : 0;
     return x;
 }
 
@@ -159,7 +188,7 @@ inline Scratch scratch_of(int grid, int rows, int D) {
 // Attention of many rows a sequence (tp_attn_chunk.cu), and the joining of the
 // tiles that its shares, or those of the kernel for few rows, cut.
 int attn_chunk_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest, cudaStream_t stream, std::string* err);
-int attn_join_launch(const PagedArgs& a, int tile_rows, int slot_rows, void* O, uint8_t* scratch, const Scratch& s, int grid,
+int attn_join_launch(const PagedArgs& a, int tile_tok, int slot_rows, void* O, uint8_t* scratch, const Scratch& s, int grid,
                      bool zero_rest, cudaStream_t stream, std::string* err);
 
 }  // namespace tpi

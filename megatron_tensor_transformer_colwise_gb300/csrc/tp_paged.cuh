@@ -25,7 +25,7 @@ inline tpk::PagedView paged_view(const PagedArgs& a) {
     v.q_start = a.q_start;
     v.kv_len = a.kv_len;
     v.n_pages = a.n_pages;
-    v.rows = a.tokens;
+    v.rows = static_cast<int>(a.tokens);
     v.n_seqs = a.n_seqs;
     v.max_pages = a.max_pages;
     while ((1 << v.page_log2) < a.page_size) ++v.page_log2;

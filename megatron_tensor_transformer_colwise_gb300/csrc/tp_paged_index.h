@@ -9,14 +9,21 @@
 
 #ifdef __CUDACC__
 #define TP_HD __host__ __device__ __forceinline__
+// Run once a tile or less, and kept out of line: inlined into every role of a
+// kernel they outgrew the instruction cache.
+#define TP_HD_CALL __host__ __device__ __noinline__ inline
 #else
 #define TP_HD inline
+#define TP_HD_CALL inline
 #endif
 
 namespace tpk {
 
 TP_HD long long pmin(long long a, long long b) { return a < b ? a : b; }
 TP_HD long long pmax(long long a, long long b) { return a > b ? a : b; }
+
+TP_HD int imin(int a, int b) { return a < b ? a : b; }
+TP_HD int imax(int a, int b) { return a > b ? a : b; }
 
 // Longest sequence: positions and their block ends stay in 32 bits.
 constexpr int kMaxLen = 1 << 30;
@@ -26,7 +33,7 @@ struct PagedView {
     const int32_t* q_start;  // [n_seqs + 1]
     const int32_t* kv_len;   // [n_seqs]
     long long n_pages;
-    long long rows;          // M
+    int rows;                // M
     int n_seqs, max_pages, page_log2;
     int kv_heads, d;
 };
@@ -34,18 +41,15 @@ struct PagedView {
 // A sequence's rows and lengths, clamped to what exists: the i-th of its n new
 // tokens is row row0 + i, at position len - n + i (negative: sees nothing).
 struct PagedSeq {
-    long long row0;
-    int n;
-    int len;
+    int row0, n, len;
 };
 
 TP_HD PagedSeq paged_seq(const PagedView& v, int s) {
-    const long long a = pmin(pmax(v.q_start[s], 0), v.rows);
-    const long long b = pmin(pmax(v.q_start[s + 1], a), v.rows);
+    const int a = imin(imax(v.q_start[s], 0), v.rows), b = imin(imax(v.q_start[s + 1], a), v.rows);
     PagedSeq x;
     x.row0 = a;
-    x.n = static_cast<int>(b - a);
-    x.len = static_cast<int>(pmin(pmax(v.kv_len[s], 0), kMaxLen));
+    x.n = b - a;
+    x.len = imin(imax(v.kv_len[s], 0), kMaxLen);
     return x;
 }
 
@@ -78,50 +82,91 @@ TP_HD int paged_owner(const PagedView& v, long long row) {
 
 // ------------------------------------------------------------ attention's work
 //
-// A tile is R query rows of one sequence and KV head g: row r of the sequence's
-// n * G (G query heads per KV head) is token r / G and query head g G + r % G,
-// so that the heads that read the same keys share a tile.  Its work is the
-// blocks of KB keys up to the last key that its last row sees, one at least (a
-// tile that sees nothing still writes its zeros).  All tiles' blocks in the
-// order (sequence, g, tile) are numbered 0 .. total - 1, and CTA c of a grid
-// takes `per` of them from c * per on: equal shares whatever the lengths, and
-// a long sequence spreads over the CTAs.  A tile cut by a share's border is
-// written as partial results: by the CTA where it begins in that CTA's slot 1,
-// by those that continue it in their slot 0.
+// A tile is `tok` new tokens of one sequence with the G = a/k query heads of
+// one KV head g: row r is token r / G and query head g G + r % G, so that the
+// heads that read the same keys share a tile.  Its work is the blocks of KB
+// keys up to the last key that its last token sees, one at least (a tile that
+// sees nothing still writes its zeros).  All tiles' blocks in the order
+// (sequence, g, tile) are numbered 0 .. total - 1, and CTA c of a grid takes
+// `per` of them from c * per on: equal shares whatever the lengths, and a long
+// sequence spreads over the CTAs.  A tile cut by a share's border is written as
+// partial results: by the CTA where it begins in that CTA's slot 1, by those
+// that continue it in their slot 0.
 
 struct Tiling {
-    int rows, keys;  // R, KB
-    int group;       // G
+    int tok, group;  // tokens of a tile, G
+    int log2_keys;   // KB = 2^log2_keys
 };
 
 // Keys of sequence q that exist: its length, at most what the page table holds.
 TP_HD int paged_keys(const PagedView& v, const PagedSeq& q) {
-    const long long cap = static_cast<long long>(v.max_pages) << v.page_log2;
-    return static_cast<int>(pmin(q.len, cap));
+    return static_cast<int>(pmin(q.len, static_cast<long long>(v.max_pages) << v.page_log2));
 }
 
-// Keys that row r of the sequence sees (none or fewer than none: nothing).
-TP_HD int row_keys(const PagedSeq& q, int keys, long long r, int group) {
-    const long long seen = q.len - q.n + r / group + 1;
-    return static_cast<int>(seen < keys ? seen : keys);
+// Keys that token i of the sequence sees (none or fewer than none: nothing).
+TP_HD int token_keys(const PagedSeq& q, int keys, int i) {
+    const int seen = q.len - q.n + i + 1;
+    return seen < keys ? seen : keys;
 }
 
-TP_HD int seq_tiles(const PagedSeq& q, const Tiling& t) {
-    return static_cast<int>((static_cast<long long>(q.n) * t.group + t.rows - 1) / t.rows);
+TP_HD int seq_tiles(const PagedSeq& q, const Tiling& t) { return static_cast<int>((static_cast<unsigned>(q.n) + t.tok - 1u) / static_cast<unsigned>(t.tok)); }
+
+// Tokens of a tile that are the sequence's.
+TP_HD int tile_tokens(const PagedSeq& q, const Tiling& t, int tile) {
+    const int left = q.n - tile * t.tok;
+    return left < t.tok ? left : t.tok;
 }
 
 TP_HD int tile_blocks(const PagedSeq& q, int keys, const Tiling& t, int tile) {
-    const long long last = pmin((tile + 1ll) * t.rows, static_cast<long long>(q.n) * t.group) - 1;
-    const int seen = row_keys(q, keys, last, t.group);
-    return seen <= 0 ? 1 : (seen - 1) / t.keys + 1;
+    const int seen = token_keys(q, keys, tile * t.tok + tile_tokens(q, t, tile) - 1);
+    return seen <= 0 ? 1 : ((seen - 1) >> t.log2_keys) + 1;
 }
 
-// Blocks of one KV head of a sequence.
-TP_HD long long seq_blocks(const PagedView& v, const PagedSeq& q, const Tiling& t) {
-    const int keys = paged_keys(v, q), nt = seq_tiles(q, t);
+// sum_{x < n} floor((a x + b) / m), by Euclid's algorithm on (m, a).  a n + b
+// stays below 2^32 here: it starts at the sequence's tokens and a block of
+// keys, and never grows.
+TP_HD long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
     long long sum = 0;
-    for (int i = 0; i < nt; ++i) sum += tile_blocks(q, keys, t, i);
+    while (n > 0) {
+        sum += static_cast<long long>(n) * (n - 1) / 2 * (a / m) + static_cast<long long>(n) * (b / m);
+        a %= m;
+        const unsigned top = a * n + b % m;
+        n = top / m;
+        b = top % m;
+        const unsigned x = m;
+        m = a;
+        a = x;
+        if (m == 0) break;
+    }
     return sum;
+}
+
+// Blocks of the first `count` tiles of one KV head of a sequence.
+TP_HD_CALL long long tiles_blocks(const PagedSeq& q, int keys, const Tiling& t, int count) {
+    if (count <= 0) return 0;
+    long long sum = 0;
+    if (count == seq_tiles(q, t)) sum += tile_blocks(q, keys, t, --count);  // the last tile may be short
+    // Tile j sees up to e_j = base + (j + 1) tok: one block while e_j <= KB, ceil(e_j / KB) while e_j < keys,
+    // then ceil(keys / KB).
+    const int base = q.len - q.n, kb = 1 << t.log2_keys;
+    const unsigned tok = static_cast<unsigned>(t.tok);
+    const unsigned one = kb < base ? 0u : static_cast<unsigned>(kb - base) / tok;
+    const unsigned full = keys <= base ? 0u : (static_cast<unsigned>(keys) - static_cast<unsigned>(base) - 1u) / tok;
+    const unsigned n = static_cast<unsigned>(count);
+    const unsigned c1 = one < n ? one : n;
+    const unsigned c2 = full < c1 ? c1 : full < n ? full : n;
+    sum += c1;
+    if (c2 > c1) sum += floor_sum(c2 - c1, 1u << t.log2_keys, tok, static_cast<unsigned>(base + kb - 1) + (c1 + 1) * tok);
+    const int most = keys <= 0 ? 1 : ((keys - 1) >> t.log2_keys) + 1;
+    return sum + static_cast<long long>(n - c2) * most;
+}
+
+// Blocks of a sequence, all KV heads.
+TP_HD long long seq_blocks(const PagedView& v, const PagedSeq& q, const Tiling& t) {
+    if (q.n <= 0) return 0;
+    const int keys = paged_keys(v, q);
+    return (q.n <= t.tok ? tile_blocks(q, keys, t, 0) : tiles_blocks(q, keys, t, seq_tiles(q, t))) *
+           static_cast<long long>(v.kv_heads);
 }
 
 // A CTA's walk over its share: segments of consecutive blocks of one tile.
@@ -132,29 +177,31 @@ struct TileWalk {
     int kb, nkb;     // next block of the tile, its number of blocks
 
     // Begin `count` blocks at block `off` of sequence s0 (all KV heads counted).
-    TP_HD void start(const PagedView& v, const Tiling& t, int s0, long long off, long long count) {
+    TP_HD_CALL void start(const PagedView& v, const Tiling& t, int s0, long long off, long long count) {
         left = count;
         s = s0;
         if (left <= 0) return;
         q = paged_seq(v, s);
         keys = paged_keys(v, q);
         tiles = seq_tiles(q, t);
-        const long long per_head = seq_blocks(v, q, t);
-        g = static_cast<int>(off / per_head);
-        off -= g * per_head;
+        const long long per_head = tiles_blocks(q, keys, t, tiles);
+        g = 0;
+        for (; off >= per_head; ++g) off -= per_head;
+        // The tile whose first block is the last at or before off.
+        int hi = tiles;
         tile = 0;
-        nkb = tile_blocks(q, keys, t, 0);
-        while (off >= nkb) {
-            off -= nkb;
-            ++tile;
-            nkb = tile_blocks(q, keys, t, tile);
+        while (hi - tile > 1) {
+            const int mid = (tile + hi) >> 1;
+            if (tiles_blocks(q, keys, t, mid) <= off) tile = mid;
+            else hi = mid;
         }
-        kb = static_cast<int>(off);
+        kb = static_cast<int>(off - tiles_blocks(q, keys, t, tile));
+        nkb = tile_blocks(q, keys, t, tile);
     }
     // Blocks of the current segment.
     TP_HD int segment() const { return static_cast<int>(pmin(left, nkb - kb)); }
     // Move past the current segment.
-    TP_HD void next(const PagedView& v, const Tiling& t) {
+    TP_HD_CALL void next(const PagedView& v, const Tiling& t) {
         const int n = segment();
         left -= n;
         kb += n;

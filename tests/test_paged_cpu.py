@@ -137,12 +137,12 @@ long long page(const int* table, long long pages, int maxp, int log2, int s, int
 }
 // The shares of a grid: for each block of work, in order, (sequence, g, tile, kb) into out, with the CTA
 // and the slot its segment would be written to; desc as the kernel writes it.  Returns the total.
-long long walk(const int* q, const int* len, long long rows, int n, int maxp, int log2, int k, int R, int KB, int G,
-               int grid, int* out, long long cap, int* desc) {
+long long walk(const int* q, const int* len, long long rows, int n, int maxp, int log2, int k, int tok, int log2_keys,
+               int G, int grid, int* out, long long cap, int* desc) {
     PagedView v = view(0, q, len, 1, rows, n, maxp, log2, k);
-    Tiling t = {R, KB, G};
+    Tiling t = {tok, G, log2_keys};
     long long total = 0, done = 0;
-    for (int s = 0; s < n; ++s) total += seq_blocks(v, paged_seq(v, s), t) * k;
+    for (int s = 0; s < n; ++s) total += seq_blocks(v, paged_seq(v, s), t);
     const long long per = (total + grid - 1) / grid;
     for (int c = 0; c < grid; ++c) {
         desc[4 * c + 3] = 0;
@@ -151,7 +151,7 @@ long long walk(const int* q, const int* len, long long rows, int n, int maxp, in
         long long at = 0;
         if (count > 0)
             for (;; ++s) {
-                const long long m = seq_blocks(v, paged_seq(v, s), t) * k;
+                const long long m = seq_blocks(v, paged_seq(v, s), t);
                 if (begin < at + m) break;
                 at += m;
             }
@@ -174,6 +174,11 @@ long long walk(const int* q, const int* len, long long rows, int n, int maxp, in
     }
     return done == total ? total : -2;
 }
+long long blocks(int n, int len, int maxp, int tok, int log2_keys) {
+    const int q[2] = {0, n};
+    PagedView v = view(0, q, &len, 1, n, 1, maxp, 4, 1);
+    return seq_blocks(v, paged_seq(v, 0), Tiling{tok, 1, log2_keys});
+}
 long long row(int k, int log2, long long page, int g, int pos) {
     return paged_row(view(0, 0, 0, 0, 0, 0, 0, log2, k), page, g, pos);
 }
@@ -192,7 +197,7 @@ def host(tmp_path_factory):
     L.page.argtypes = [C.c_void_p, C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int]
     L.row.argtypes = [C.c_int, C.c_int, C.c_longlong, C.c_int, C.c_int]
     L.owner.argtypes = [C.c_void_p, C.c_int, C.c_longlong]
-    L.walk.restype = C.c_longlong
+    L.walk.restype = L.blocks.restype = C.c_longlong
     L.walk.argtypes = [C.c_void_p, C.c_void_p, C.c_longlong] + [C.c_int] * 8 + [C.c_void_p, C.c_longlong, C.c_void_p]
     L.seq.argtypes = [C.c_void_p, C.c_void_p, C.c_longlong, C.c_int, C.c_int, C.c_void_p]
     return L
@@ -237,11 +242,12 @@ def test_cache_rows_pass_32_bits(host):
     assert host.row(2, 4, 5, 1, 35) == (5 * 2 + 1) * 16 + 3
 
 
-@pytest.mark.parametrize("R,KB", [(16, 64), (16, 128), (128, 128)])
-def test_shares_cover_all_work_once(host, R, KB):
-    rng = np.random.default_rng(R + KB)
-    for trial in range(60):
-        n, k, G = int(rng.integers(1, 9)), int(rng.choice([1, 2, 3])), int(rng.choice([1, 3, 4, 8]))
+@pytest.mark.parametrize("rows,log2_keys", [(16, 6), (16, 7), (128, 7)])
+def test_shares_cover_all_work_once(host, rows, log2_keys):
+    rng, KB = np.random.default_rng(rows + log2_keys), 1 << log2_keys
+    for trial in range(100):
+        n, k, G = int(rng.integers(1, 9)), int(rng.choice([1, 2, 3])), int(rng.choice([1, 3, 4, 5, 7, 8, 16]))
+        tok = rows // G
         new, keep = rng.integers(0, 90, n), rng.integers(0, 900, n)
         if trial % 3 == 0:
             new = rng.integers(0, 3, n)
@@ -252,12 +258,12 @@ def test_shares_cover_all_work_once(host, R, KB):
         for s in range(n):
             keys = min(int(length[s]), maxp * 16)
             for g in range(k):
-                for tile in range(-(-int(new[s]) * G // R)):
-                    last = min((tile + 1) * R, int(new[s]) * G) - 1
-                    seen = min(int(length[s]) - int(new[s]) + last // G + 1, keys)
+                for tile in range(-(-int(new[s]) // tok)):
+                    last = min((tile + 1) * tok, int(new[s])) - 1
+                    seen = min(int(length[s]) - int(new[s]) + last + 1, keys)
                     want += [(s, g, tile, b) for b in range(max(1, -(-seen // KB)))]
         out, desc = np.zeros((len(want) + 1, 6), dtype=np.int32), np.zeros((grid, 4), dtype=np.int32)
-        got = host.walk(q.ctypes.data, length.ctypes.data, int(q[-1]), n, maxp, 4, k, R, KB, G, grid, out.ctypes.data,
+        got = host.walk(q.ctypes.data, length.ctypes.data, int(q[-1]), n, maxp, 4, k, tok, log2_keys, G, grid, out.ctypes.data,
                         len(want), desc.ctypes.data)
         assert got == len(want)
         out = out[:got]
@@ -277,6 +283,21 @@ def test_shares_cover_all_work_once(host, R, KB):
             assert desc[c].tolist() == [*key, len(places)]
             parts += 1
         assert (desc[:, 3] > 0).sum() == parts
+
+
+def test_blocks_of_a_sequence_in_closed_form(host):
+    """The sum over a sequence's tiles, against the loop: long sequences, ends of the page table inside."""
+    rng = np.random.default_rng(5)
+    out = np.zeros(1, dtype=np.int64)
+    for _ in range(400):
+        new, keep, tok = int(rng.integers(1, 5000)), int(rng.integers(-3000, 9000)), int(rng.choice([1, 2, 3, 5, 16, 18, 32, 42, 128]))
+        length, maxp, log2_keys = max(new + keep, 0), int(rng.integers(1, 900)), int(rng.choice([6, 7]))
+        keys, want = min(length, 16 * maxp), 0
+        for tile in range(-(-new // tok)):
+            seen = min(length - new + min((tile + 1) * tok, new), keys)
+            want += max(1, -(-seen >> log2_keys) if seen <= 0 else ((seen - 1) >> log2_keys) + 1)
+        got = host.blocks(new, length, maxp, tok, log2_keys)
+        assert got == want
 
 
 def test_problems_own_their_rows():
