@@ -18,8 +18,7 @@
 //               TMEM buffers.
 //   warp 2      PV issuer: O += P V, P from tensor memory.
 //   warps 3..10 softmax, two warps a TMEM lane quadrant, half of a block's keys
-//               each; a tile's outputs leave after the next tile's first block,
-//               staged in shared memory for whole-line stores.
+//               each; a tile's outputs leave after the next tile's first block.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -71,12 +70,10 @@ struct Lay {
     static constexpr int K_OFF = TILE;
     static constexpr int V_OFF = K_OFF + 2 * TILE;
     static constexpr int DC = D / 2;         // O columns of a softmax warp
-    static constexpr int STG_ROW = DC * 2;   // bytes of a staged row
-    static constexpr int STG_OFF = V_OFF + 2 * TILE;
-    static constexpr int XCH_OFF = STG_OFF + 8 * 32 * STG_ROW;  // [7][128] fp32: maxima x 2 x 2, sums x 2, references
+    static constexpr int XCH_OFF = V_OFF + 2 * TILE;  // [7][128] fp32: maxima x 2 x 2, sums x 2, references
     static constexpr int BAR_OFF = XCH_OFF + 7 * QB * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * NUM_BARS + 16;
-    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NT / 32 + 1);  // the share's beginning, then one walk a warp
+    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NT / 32 + 2);  // the share's beginning, then one walk a warp
     static constexpr int DONE_OFF = WALK_OFF + (NT / 32 + 1) * sizeof(TileWalk);
     static constexpr int PAGE_OFF = (DONE_OFF + 8 * sizeof(Done) + 15) / 16 * 16;  // page numbers of the two producers
     static constexpr int DATA = PAGE_OFF + 2 * 64 * 4;
@@ -189,7 +186,8 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
             if (!is_v) {
                 if (w.kb == 0 && seg < w.nkb) {
                     const long long at = share.begin + share.count - seg;  // the segment is the share's last
-                    cut = make_int4(w.s, g, w.tile, share_of(at + w.nkb - 1, share.per) - static_cast<int>(blockIdx.x) + 1);
+                    cut = make_int4(w.q.row0 + w.tile * p.tile_tok, g, tile_tokens(w.q, tiling, w.tile) * p.group,
+                                    share_of(at + w.nkb - 1, share.per) - static_cast<int>(blockIdx.x) + 1);
                 }
                 ok = __all_sync(0xffffffffu, li == 0 || wait(bar(B_Q_EMPTY), (li - 1) & 1u));
                 if (!ok) break;
@@ -334,34 +332,18 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                 }
                 return true;
             }
-            // Rows through shared memory, so that neighbouring lanes store neighbouring pieces of a row.
-            const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
-            constexpr int PIECES = L::STG_ROW / 16;          // 8 or 4
-            const uint32_t stg = base + L::STG_OFF + static_cast<uint32_t>((warp - 3) * 32) * L::STG_ROW;
-            auto at = [&](uint32_t row, uint32_t u) {
-                const uint32_t x = PIECES == 8 ? row & 7u : (row >> 1) & 3u;
-                return stg + row * L::STG_ROW + ((u ^ x) << 4);
-            };
-            __syncwarp();
+            if (r < e.rows) {
+                const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
+                const int tok = r / p.group;
+                __nv_bfloat16* y = p.o + (static_cast<long long>(e.row0 + tok) * p.heads + e.g * p.group + r - tok * p.group) * D + hf * DC;
 #pragma unroll
-            for (int u = 0; u < PIECES; ++u) {
-                uint32_t wv[4];
+                for (int u = 0; u < DC / 8; ++u) {
+                    uint32_t wv[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    wv[x] = pack_bf16x2(__uint_as_float(o[u * 8 + 2 * x]) * inv, __uint_as_float(o[u * 8 + 2 * x + 1]) * inv);
-                st_shared_v4(at(lane, u), wv[0], wv[1], wv[2], wv[3]);
-            }
-            __syncwarp();
-            constexpr int STEP = 32 / PIECES;
-            const int u = lane % PIECES;
-#pragma unroll 1
-            for (int row = lane / PIECES; row < 32; row += STEP) {
-                const int x = q * 32 + row;
-                if (x >= e.rows) break;
-                const int tok = x / p.group;
-                __nv_bfloat16* y = p.o + (static_cast<long long>(e.row0 + tok) * p.heads + e.g * p.group + x - tok * p.group) * D +
-                                   hf * DC + u * 8;
-                *reinterpret_cast<uint4*>(y) = ld_shared_v4(at(row, u));
+                    for (int x = 0; x < 4; ++x)
+                        wv[x] = pack_bf16x2(__uint_as_float(o[u * 8 + 2 * x]) * inv, __uint_as_float(o[u * 8 + 2 * x + 1]) * inv);
+                    *reinterpret_cast<uint4*>(y + u * 8) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+                }
             }
             return true;
         };
@@ -573,7 +555,7 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
     rc = tpi::launched("chunk attention launch",
                        tpi::launch_pdl(attn_chunk_kernel<L>, dim3(grid), dim3(NT), L::SMEM, stream, p), err);
     if (rc) return rc;
-    return tpi::attn_join_launch(a, p.tile_tok, QB, O, w, s, grid, zero_rest, stream, err);
+    return tpi::attn_join_launch(a, QB, O, w, s, grid, zero_rest, stream, err);
 }
 
 }  // namespace

@@ -65,7 +65,7 @@ struct Cfg {
     static constexpr int XM_OFF = ACC_OFF + NW * R * LD_ACC * 4;
     static constexpr int BAR_OFF = XM_OFF + 2 * NW * R * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * 2 * NST;
-    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NW + 2);  // the share's beginning, then one walk a warp
+    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NW + 3);  // the share's beginning, then one walk a warp
     static constexpr int DATA = WALK_OFF + (NW + 2) * sizeof(TileWalk);
     static constexpr int SMEM = DATA + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -82,7 +82,7 @@ struct Params {
     float scale_log2;
     float* part_o;   // [grid][2][R][D]
     float* part_ml;  // [grid][2][R][2]
-    int4* desc;      // [grid]: sequence, KV head, tile, parts of the tile that begins in a CTA's slot 1
+    int4* desc;      // [grid]: first row, KV head, rows, parts of the tile that begins in a CTA's slot 1
     unsigned* status;
     unsigned long long timeout_ns;
 };
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                     // The tile's last block is in CTA (first block + blocks - 1) / per.
                     const long long at = share.begin + share.count - seg;
                     const int last = share_of(at + w.nkb - 1, share.per);
-                    p.desc[blockIdx.x] = make_int4(w.s, g, w.tile, last - static_cast<int>(blockIdx.x) + 1);
+                    p.desc[blockIdx.x] = make_int4(q.row0 + tok0, g, rows, last - static_cast<int>(blockIdx.x) + 1);
                 }
             }
         }
@@ -582,61 +582,49 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
 
 // Joins the parts of the tile that begins in slot 1 of CTA blockIdx.x and goes
 // on in slot 0 of the next ones: O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i,
-// in the order of the keys.  One warp per row, blockIdx.y rows apart.
-// zero_rest: also clears the rows of O that no sequence owns.
-// A tile has tile_tok tokens of `group` rows, a slot room for ROWS rows.
+// in the order of the keys.  A warp takes 128 / D rows at a time, 16 bytes a
+// lane.  zero_rest: also clears the rows of O that no sequence owns.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) attn_join_kernel(PagedView v, int group, int tile_tok, int heads, const float* part_o,
-                                                        const float* part_ml, const int4* desc, __nv_bfloat16* o,
-                                                        int zero_rest) {
+__global__ void __launch_bounds__(ROWS == R ? 256 : 1024) attn_join_kernel(PagedView v, int group, int heads, const float* part_o,
+                                                                           const float* part_ml, const int4* desc,
+                                                                           __nv_bfloat16* o, int zero_rest) {
     pdl_trigger();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int LANES = D / 4, PER_WARP = 32 / LANES;
+    const int4 x = desc[blockIdx.x];  // the tile's first row, KV head, rows, parts
     if (zero_rest) {
         const int a = imin(imax(v.q_start[0], 0), v.rows), b = imin(imax(v.q_start[v.n_seqs], a), v.rows);
         const long long per = static_cast<long long>(heads) * D / 8;
-        const long long threads = static_cast<long long>(gridDim.x) * gridDim.y * 256;
-        const long long me = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+        const long long threads = static_cast<long long>(gridDim.x) * blockDim.x;
+        const long long me = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
         uint4* y = reinterpret_cast<uint4*>(o);
         for (long long i = me; i < a * per; i += threads) y[i] = make_uint4(0, 0, 0, 0);
         for (long long i = b * per + me; i < v.rows * per; i += threads) y[i] = make_uint4(0, 0, 0, 0);
     }
-    const int4 x = desc[blockIdx.x];
-    if (x.w == 0) return;
-    const PagedSeq q = paged_seq(v, x.x);
-    const int rows = tile_tokens(q, Tiling{tile_tok, group, 0}, x.z) * group;
-    constexpr int E = D / 32;
-    for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
+    const int c = (threadIdx.x % LANES) * 4;
+    for (int i = threadIdx.x / LANES; i < x.z; i += (blockDim.x / 32) * PER_WARP) {
+        if (x.w == 0) return;
         // Slot 1 of the first CTA is followed in memory by slot 0 of the next; then every second slot.
         auto slot = [&](int k) { return (static_cast<long long>(blockIdx.x) * 2 + (k == 0 ? 1 : 2 * k)) * ROWS + i; };
-        float m = -INFINITY;
-        for (int k = lane; k < x.w; k += 32) m = fmaxf(m, part_ml[slot(k) * 2]);
-        for (int f = 16; f > 0; f >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, f));
-        float a[E] = {}, l = 0.0f;
+        float m = -INFINITY, l = 0.0f;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
         for (int k = 0; k < x.w; ++k) {
-            const long long at = slot(k);
-            const float2 ml = *reinterpret_cast<const float2*>(part_ml + at * 2);
-            const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
-            l += ml.y * f;
-            if constexpr (E == 4) {
-                const float4 b = *reinterpret_cast<const float4*>(part_o + at * D + lane * 4);
-                a[0] += b.x * f;
-                a[1] += b.y * f;
-                a[2] += b.z * f;
-                a[3] += b.w * f;
-            } else {
-                const float2 b = *reinterpret_cast<const float2*>(part_o + at * D + lane * 2);
-                a[0] += b.x * f;
-                a[1] += b.y * f;
-            }
+            const float2 ml = *reinterpret_cast<const float2*>(part_ml + slot(k) * 2);
+            const float4 b = *reinterpret_cast<const float4*>(part_o + slot(k) * D + c);
+            const float mm = fmaxf(m, ml.x), base = mm == -INFINITY ? 0.0f : mm;
+            const float f = ex2(m - base), e = ex2(ml.x - base);  // 2^-inf = 0: nothing before, nothing seen
+            m = mm;
+            l = l * f + ml.y * e;
+            a.x = a.x * f + b.x * e;
+            a.y = a.y * f + b.y * e;
+            a.z = a.z * f + b.z * e;
+            a.w = a.w * f + b.w * e;
         }
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         const int tok = i / group;
-        __nv_bfloat16* y =
-            o + (static_cast<long long>(q.row0 + x.z * tile_tok + tok) * heads + x.y * group + i - tok * group) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(y + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
+        __nv_bfloat16* y = o + (static_cast<long long>(x.x + tok) * heads + x.y * group + i - tok * group) * D + c;
+        *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     }
 }
 
@@ -680,14 +668,14 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     rc = launched("paged attention launch",
                   tpi::launch_pdl(attn_few_kernel<C>, dim3(grid), dim3(NT), C::SMEM, stream, p), err);
     if (rc) return rc;
-    return tpi::attn_join_launch(a, p.tile_tok, R, O, w, s, grid, zero_rest, stream, err);
+    return tpi::attn_join_launch(a, R, O, w, s, grid, zero_rest, stream, err);
 }
 
 template <int D, int ROWS>
-cudaError_t join(const tpi::PagedArgs& a, int tile_tok, void* O, uint8_t* w, const Scratch& s, int grid, bool zero_rest,
+cudaError_t join(const tpi::PagedArgs& a, void* O, uint8_t* w, const Scratch& s, int grid, bool zero_rest,
                  cudaStream_t stream) {
-    return tpi::launch_pdl(attn_join_kernel<D, ROWS>, dim3(grid, (ROWS + 7) / 8), dim3(256), 0, stream,
-                           tpi::paged_view(a), a.heads / a.kv_heads, tile_tok, a.heads,
+    return tpi::launch_pdl(attn_join_kernel<D, ROWS>, dim3(grid), dim3(ROWS == R ? 256 : 1024), 0, stream,
+                           tpi::paged_view(a), a.heads / a.kv_heads, a.heads,
                            reinterpret_cast<const float*>(w + s.o), reinterpret_cast<const float*>(w + s.ml),
                            reinterpret_cast<const int4*>(w + s.desc), static_cast<__nv_bfloat16*>(O), zero_rest ? 1 : 0);
 }
@@ -699,15 +687,15 @@ namespace tpi {
 // The kernel for many rows has the larger tiles.
 size_t attn_paged_scratch_bytes(int head_dim) { return scratch_of(device_sm_count(), 128, head_dim).total; }
 
-int attn_join_launch(const PagedArgs& a, int tile_tok, int slot_rows, void* O, uint8_t* w, const Scratch& s, int grid,
+int attn_join_launch(const PagedArgs& a, int slot_rows, void* O, uint8_t* w, const Scratch& s, int grid,
                      bool zero_rest, cudaStream_t stream, std::string* err) {
     cudaError_t e;
     if (a.head_dim == 128)
-        e = slot_rows == R ? join<128, R>(a, tile_tok, O, w, s, grid, zero_rest, stream)
-                           : join<128, 128>(a, tile_tok, O, w, s, grid, zero_rest, stream);
+        e = slot_rows == R ? join<128, R>(a, O, w, s, grid, zero_rest, stream)
+                           : join<128, 128>(a, O, w, s, grid, zero_rest, stream);
     else
-        e = slot_rows == R ? join<64, R>(a, tile_tok, O, w, s, grid, zero_rest, stream)
-                           : join<64, 128>(a, tile_tok, O, w, s, grid, zero_rest, stream);
+        e = slot_rows == R ? join<64, R>(a, O, w, s, grid, zero_rest, stream)
+                           : join<64, 128>(a, O, w, s, grid, zero_rest, stream);
     return launched("paged attention join launch", e, err);
 }
 

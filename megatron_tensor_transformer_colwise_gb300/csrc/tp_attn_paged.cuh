@@ -71,15 +71,17 @@ __device__ __forceinline__ int share_of(long long at, long long per) {
 
 // The share of CTA blockIdx.x: its first block, their number, every CTA's
 // number; *walk0 gets the walk's beginning.  Every thread sums the blocks of a
-// run of sequences, a scan of the sums finds the share's beginning, and the
-// thread that holds it starts the walk.  sums: NT / 32 + 1 words of 8 bytes of
-// shared memory.  Ends with __syncthreads.
+// run of sequences, and a scan of the sums finds the sequence where the share
+// begins; warp 0 then looks for the tile, 32 at a time.  sums: NT / 32 + 2 words
+// of 8 bytes of shared memory.  Ends with __syncthreads.
 struct Share {
     long long begin, count, per;
 };
 template <int NT>
 __device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t, long long* sums, TileWalk* walk0) {
     const int tid = threadIdx.x, lane = tid & 31;
+    long long* found_off = sums + NT / 32;
+    int* found_s = reinterpret_cast<int*>(found_off + 1);
     const int run = (v.n_seqs + NT - 1) / NT;
     const int s0 = min(tid * run, v.n_seqs), s1 = min(s0 + run, v.n_seqs);
     long long mine = 0;
@@ -112,7 +114,31 @@ __device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t,
             if (x.begin < before + n) break;
             before += n;
         }
-        walk0->start(v, t, s, x.begin - before, x.count);
+        *found_off = x.begin - before;
+        *found_s = s;
+    }
+    __syncthreads();
+    if (tid < 32 && x.count > 0) {
+        const int s = *found_s;
+        long long off = *found_off;
+        const PagedSeq q = paged_seq(v, s);
+        const int keys = paged_keys(v, q), tiles = seq_tiles(q, t);
+        const long long per_head = tiles == 1 ? tile_blocks(q, keys, t, 0) : tiles_blocks(q, keys, t, tiles);
+        int g = 0;
+#pragma unroll 1
+        for (; off >= per_head; ++g) off -= per_head;
+        // The last tile that begins at or before `off`: of [lo, lo + 32 step) by its 32 steps, then within one.
+        int lo = 0, step = 1;
+        while (step * 32 < tiles) step *= 32;
+#pragma unroll 1
+        for (; tiles > 1; step /= 32) {
+            const int at = lo + lane * step;
+            const bool before_off = at < tiles && tiles_blocks(q, keys, t, at) <= off;
+            lo += (__popc(__ballot_sync(0xffffffffu, before_off)) - 1) * step;
+            if (step == 1) break;
+        }
+        if (tiles > 1) off -= tiles_blocks(q, keys, t, lo);
+        if (lane == 0) walk0->start(v, t, s, g, lo, static_cast<int>(off), x.count);
     }
     __syncthreads();
     return x;
@@ -188,7 +214,7 @@ inline Scratch scratch_of(int grid, int rows, int D) {
 // Attention of many rows a sequence (tp_attn_chunk.cu), and the joining of the
 // tiles that its shares, or those of the kernel for few rows, cut.
 int attn_chunk_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest, cudaStream_t stream, std::string* err);
-int attn_join_launch(const PagedArgs& a, int tile_tok, int slot_rows, void* O, uint8_t* scratch, const Scratch& s, int grid,
+int attn_join_launch(const PagedArgs& a, int slot_rows, void* O, uint8_t* scratch, const Scratch& s, int grid,
                      bool zero_rest, cudaStream_t stream, std::string* err);
 
 }  // namespace tpi

@@ -176,26 +176,17 @@ struct TileWalk {
     int s, g, tile, tiles, keys;
     int kb, nkb;     // next block of the tile, its number of blocks
 
-    // Begin `count` blocks at block `off` of sequence s0 (all KV heads counted).
-    TP_HD_CALL void start(const PagedView& v, const Tiling& t, int s0, long long off, long long count) {
+    // Begin `count` blocks of sequence s0 in KV head g0, `off` blocks behind the first block of tile `first`
+    // (off within that tile).
+    TP_HD_CALL void start(const PagedView& v, const Tiling& t, int s0, int g0, int first, int off, long long count) {
         left = count;
         s = s0;
-        if (left <= 0) return;
+        g = g0;
+        tile = first;
         q = paged_seq(v, s);
         keys = paged_keys(v, q);
         tiles = seq_tiles(q, t);
-        const long long per_head = tiles_blocks(q, keys, t, tiles);
-        g = 0;
-        for (; off >= per_head; ++g) off -= per_head;
-        // The tile whose first block is the last at or before off.
-        int hi = tiles;
-        tile = 0;
-        while (hi - tile > 1) {
-            const int mid = (tile + hi) >> 1;
-            if (tiles_blocks(q, keys, t, mid) <= off) tile = mid;
-            else hi = mid;
-        }
-        kb = static_cast<int>(off - tiles_blocks(q, keys, t, tile));
+        kb = off;
         nkb = tile_blocks(q, keys, t, tile);
     }
     // Blocks of the current segment.

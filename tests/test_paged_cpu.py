@@ -156,7 +156,18 @@ long long walk(const int* q, const int* len, long long rows, int n, int maxp, in
                 at += m;
             }
         TileWalk w;
-        w.start(v, t, s, begin - at, count);
+        w.left = 0;
+        if (count > 0) {
+            // As the kernels find the tile, one at a time instead of 32.
+            const PagedSeq x = paged_seq(v, s);
+            const int keys = paged_keys(v, x), tiles = seq_tiles(x, t);
+            const long long per_head = tiles_blocks(x, keys, t, tiles);
+            long long off = begin - at;
+            int g = 0, tile = 0;
+            for (; off >= per_head; ++g) off -= per_head;
+            while (tile + 1 < tiles && tiles_blocks(x, keys, t, tile + 1) <= off) ++tile;
+            w.start(v, t, s, g, tile, (int)(off - tiles_blocks(x, keys, t, tile)), count);
+        }
         for (; w.left > 0; w.next(v, t)) {
             const int seg = w.segment();
             const bool b = w.kb == 0, e = w.kb + seg == w.nkb;
