@@ -70,11 +70,13 @@ struct Lay {
     static constexpr int K_OFF = TILE;
     static constexpr int V_OFF = K_OFF + 2 * TILE;
     static constexpr int DC = D / 2;         // O columns of a softmax warp
-    static constexpr int XCH_OFF = V_OFF + 2 * TILE;  // [7][128] fp32: maxima x 2 x 2, sums x 2, references
+    static constexpr int STG_ROW = DC * 2;            // bytes of a staged output row
+    static constexpr int STG_OFF = V_OFF + 2 * TILE;  // 32 rows a softmax warp
+    static constexpr int XCH_OFF = STG_OFF + 8 * 32 * STG_ROW;  // [7][128] fp32: maxima x 2 x 2, sums x 2, references
     static constexpr int BAR_OFF = XCH_OFF + 7 * QB * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * NUM_BARS + 16;
-    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NT / 32 + 2);  // the share's beginning, then one walk a warp
-    static constexpr int DONE_OFF = WALK_OFF + (NT / 32 + 1) * sizeof(TileWalk);
+    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NT / 32 + 2);  // the share's beginning, one walk a warp, the producers' walks ahead
+    static constexpr int DONE_OFF = WALK_OFF + (NT / 32 + 3) * sizeof(TileWalk);
     static constexpr int PAGE_OFF = (DONE_OFF + 8 * sizeof(Done) + 15) / 16 * 16;  // page numbers of the two producers
     static constexpr int DATA = PAGE_OFF + 2 * 64 * 4;
     static constexpr int SMEM = DATA + 1024;
@@ -85,9 +87,11 @@ struct Lay {
 struct Params {
     CUtensorMap map_q;         // the projection buffer as {d, heads a shard, shards, tokens}
     CUtensorMap map_k, map_v;  // the cache as {d, page, k, n_pages}
+    CUtensorMap map_o;         // O as {d, heads, tokens}, boxes of 32 rows of a KV head and half their columns
+    int o_boxes;               // 1: G divides 32, so that such a box is whole tokens
     PagedView v;
     __nv_bfloat16* o;
-    int heads, group, tile_tok, box_rows;
+    int heads, group, tile_tok, log2_tok, box_rows;
     int kv_per_shard;        // KV heads of a shard, 0 if shards share them
     int shards_per_kv;       // shards that share a KV head (1 if they have their own)
     float scale_log2;
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::BAR_OFF + 8 * NUM_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Tiling tiling = {p.tile_tok, p.group, 7};
+    const Tiling tiling = {p.tile_tok, p.group, 7, p.log2_tok};
     const Waiter wait = {abort_flag, p.status, p.timeout_ns};
 
     if (threadIdx.x == 0) {
@@ -168,42 +172,60 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
         const CUtensorMap* map = is_v ? &p.map_v : &p.map_k;
         const uint32_t dst0 = is_v ? sV : sK, full0 = bar(is_v ? B_V_FULL : B_K_FULL), empty0 = bar(is_v ? B_V_EMPTY : B_K_EMPTY);
         int4 cut = make_int4(0, 0, 0, 0);  // the tile that begins here and goes on in the next CTAs
-        uint32_t n = 0, li = 0;            // blocks and segments issued
+        uint32_t n = 0, li = 0;            // blocks and Q tiles issued
         bool ok = true;
-        for (; w.left > 0 && ok; move_on(), ++li) {
-            const int seg = w.segment(), keys = w.keys, g = w.g, page0 = (w.kb * KB) >> log2;
-            const int32_t* table = p.v.table + static_cast<long long>(w.s) * p.v.max_pages;
-            auto page_at = [&](int i) -> int {  // -1: past the sequence's keys, or on no page of the cache
-                if ((static_cast<long long>(i) << log2) >= keys) return -1;
-                const int pg = table[i];
-                if (pg >= 0 && pg < p.v.n_pages) return pg;
-                if (p.status) atomicOr(p.status, kStatusPage);
-                return -1;
-            };
-            ring[lane] = page_at(page0 + lane);
-            int next = page_at(page0 + 32 + lane);
+        // Page i of a segment's sequence; -1: past its keys, or on no page of the cache.
+        auto page_at = [&](const TileWalk& x, int i) -> int {
+            if ((static_cast<long long>(i) << log2) >= x.keys) return -1;
+            const int pg = p.v.table[static_cast<long long>(x.s) * p.v.max_pages + i];
+            if (pg >= 0 && pg < p.v.n_pages) return pg;
+            if (p.status) atomicOr(p.status, kStatusPage);
+            return -1;
+        };
+        // y walks a segment ahead: the first pages of the next segment are read, and its Q is brought to L2, in time.
+        TileWalk& y = walks[1 + NT / 32 + (is_v ? 1 : 0)];
+        if (lane == 0) y = w;
+        __syncwarp();
+        auto q_box = [&](const TileWalk& x, bool load) {
+            const int head = p.kv_per_shard ? (x.g % p.kv_per_shard) * p.group : 0;
+            const int shard = p.kv_per_shard ? x.g / p.kv_per_shard : x.g * p.shards_per_kv;
+            const int token = x.q.row0 + x.tile * p.tile_tok;
+#pragma unroll 1
+            for (int c = 0; c < NSEG; ++c) {
+                if (load) tma_load_4d(sQ + c * BOX, &p.map_q, bar(B_Q_FULL), 64 * c, head, shard, token);
+                else tma_prefetch_l2_4d(&p.map_q, 64 * c, head, shard, token);
+            }
+        };
+        int first = -1, behind = -1;
+        if (y.left > 0) {
+            first = page_at(y, ((y.kb * KB) >> log2) + lane);
+            behind = page_at(y, ((y.kb * KB) >> log2) + 32 + lane);
+        }
+        while (y.left > 0 && ok) {
             __syncwarp();
-            if (!is_v) {
-                if (w.kb == 0 && seg < w.nkb) {
-                    const long long at = share.begin + share.count - seg;  // the segment is the share's last
-                    cut = make_int4(w.q.row0 + w.tile * p.tile_tok, g, tile_tokens(w.q, tiling, w.tile) * p.group,
-                                    share_of(at + w.nkb - 1, share.per) - static_cast<int>(blockIdx.x) + 1);
-                }
-                ok = __all_sync(0xffffffffu, li == 0 || wait(bar(B_Q_EMPTY), (li - 1) & 1u));
-                if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(B_Q_FULL), p.tile_tok * p.group * D * 2);
-                    const int head = p.kv_per_shard ? (g % p.kv_per_shard) * p.group : 0;
-                    const int shard = p.kv_per_shard ? g / p.kv_per_shard : g * p.shards_per_kv;
-#pragma unroll
-                    for (int c = 0; c < NSEG; ++c)
-                        tma_load_4d(sQ + c * BOX, &p.map_q, bar(B_Q_FULL), 64 * c, head, shard, w.q.row0 + w.tile * p.tile_tok);
-                }
+            if (lane == 0) {
+                w = y;
+                y.next(p.v, tiling);
+            }
+            __syncwarp();
+            const int seg = w.segment(), g = w.g, page0 = (w.kb * KB) >> log2;
+            int next = behind;
+            ring[lane] = first;
+            __syncwarp();
+            if (y.left > 0) {
+                first = page_at(y, ((y.kb * KB) >> log2) + lane);
+                behind = page_at(y, ((y.kb * KB) >> log2) + 32 + lane);
+                if (!is_v && lane == 0) q_box(y, false);
+            }
+            if (w.kb == 0 && seg < w.nkb) {
+                const long long at = share.begin + share.count - seg;  // the segment is the share's last
+                cut = make_int4(w.q.row0 + w.tile * p.tile_tok, g, tile_tokens(w.q, tiling, w.tile) * p.group,
+                                share_of(at + w.nkb - 1, share.per) - static_cast<int>(blockIdx.x) + 1);
             }
             for (int i = 0, at = 0; i < seg; ++i, ++n, at += per_block) {
                 if ((at & 31) == 0) {  // a window begins: the one behind it takes the other half of the ring
                     ring[(at + 32 + lane) & 63] = next;
-                    next = page_at(page0 + at + 64 + lane);
+                    if (i + 32 / per_block < seg) next = page_at(w, page0 + at + 64 + lane);
                     __syncwarp();
                 }
                 const uint32_t st = n & 1;
@@ -221,6 +243,19 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                     }
                 }
                 __syncwarp();
+                if (!is_v && i == 0) {  // Q behind the first K: it waits for the previous segment's last S
+                    ok = __all_sync(0xffffffffu, li == 0 || wait(bar(B_Q_EMPTY), (li - 1) & 1u));
+                    if (!ok) {
+                        ++n;
+                        break;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(B_Q_FULL), p.tile_tok * p.group * D * 2);
+                        q_box(w, true);
+                    }
+                    ++li;
+                    __syncwarp();
+                }
             }
         }
         if (!is_v && lane == 0) p.desc[blockIdx.x] = cut;
@@ -332,17 +367,34 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                 }
                 return true;
             }
-            if (r < e.rows) {
-                const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
-                const int tok = r / p.group;
-                __nv_bfloat16* y = p.o + (static_cast<long long>(e.row0 + tok) * p.heads + e.g * p.group + r - tok * p.group) * D + hf * DC;
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
+            const int tok = r / p.group;
+            __nv_bfloat16* y = p.o + (static_cast<long long>(e.row0 + tok) * p.heads + e.g * p.group + r - tok * p.group) * D + hf * DC;
+            // A quadrant of whole tokens, all of them the sequence's, leaves by one TMA store through shared memory
+            // (a warp's own 16-byte stores touch 32 lines each); others row by row.
+            const bool boxed = p.o_boxes && q * 32 + 32 <= e.rows;
+            constexpr int PIECES = L::STG_ROW / 16;  // 8 or 4
+            const uint32_t stg = base + L::STG_OFF + static_cast<uint32_t>((warp - 3) * 32) * L::STG_ROW;
+            const uint32_t sw = PIECES == 8 ? lane & 7 : (lane >> 1) & 3;
+            if (boxed) {
+                if (lane == 0) bulk_wait_group_read0();  // the previous store has read the box
+                __syncwarp();
+            }
 #pragma unroll
-                for (int u = 0; u < DC / 8; ++u) {
-                    uint32_t wv[4];
+            for (int u = 0; u < PIECES; ++u) {
+                uint32_t wv[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        wv[x] = pack_bf16x2(__uint_as_float(o[u * 8 + 2 * x]) * inv, __uint_as_float(o[u * 8 + 2 * x + 1]) * inv);
-                    *reinterpret_cast<uint4*>(y + u * 8) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+                for (int x = 0; x < 4; ++x)
+                    wv[x] = pack_bf16x2(__uint_as_float(o[u * 8 + 2 * x]) * inv, __uint_as_float(o[u * 8 + 2 * x + 1]) * inv);
+                if (boxed) st_shared_v4(stg + lane * L::STG_ROW + ((u ^ sw) << 4), wv[0], wv[1], wv[2], wv[3]);
+                else if (r < e.rows) *reinterpret_cast<uint4*>(y + u * 8) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+            }
+            if (boxed) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&p.map_o, stg, hf * DC, e.g * p.group, e.row0 + tok);
+                    bulk_commit_group();
                 }
             }
             return true;
@@ -491,6 +543,7 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
             }
             move_on();
         }
+        if (lane == 0) bulk_wait_group0();  // the stores have left shared memory before the CTA does
     }
     __syncwarp();
     tc_fence_before();
@@ -514,6 +567,7 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
     p.heads = a.heads;
     p.group = a.heads / a.kv_heads;
     p.tile_tok = QB / p.group;
+    p.log2_tok = exact_log2(p.tile_tok);
     p.kv_per_shard = a.kv_heads / a.t;
     p.shards_per_kv = p.kv_per_shard ? 1 : a.t / a.kv_heads;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(L::D));
@@ -536,6 +590,23 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
             if (err) *err = "cuTensorMapEncodeTiled (queries) failed: " + std::to_string(static_cast<int>(r));
             return TP_ERR_CUDA;
         }
+    }
+    if (32 % p.group == 0) {
+        tpi::EncodeTiledFn encode = tpi::encode_fn(err);
+        if (!encode) return TP_ERR_CUDA;
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(L::D), static_cast<cuuint64_t>(a.heads), static_cast<cuuint64_t>(a.tokens)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(L::D) * 2, static_cast<cuuint64_t>(L::D) * 2 * a.heads};
+        const cuuint32_t box[3] = {static_cast<cuuint32_t>(L::DC), static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(32 / p.group)};
+        const cuuint32_t estr[3] = {1, 1, 1};
+        const CUresult r = encode(&p.map_o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, O, dims, strides, box, estr,
+                                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  L::STG_ROW == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) {
+            if (err) *err = "cuTensorMapEncodeTiled (outputs) failed: " + std::to_string(static_cast<int>(r));
+            return TP_ERR_CUDA;
+        }
+        p.o_boxes = 1;
     }
     const tpi::Scratch s = tpi::scratch_of(grid, QB, L::D);
     uint8_t* w = static_cast<uint8_t*>(scratch);

@@ -78,7 +78,7 @@ struct Params {
     const __nv_bfloat16* qkv;
     long long ld_qkv;
     __nv_bfloat16* o;
-    int heads, heads_per_shard, shard_w, group, tile_tok, box_rows;
+    int heads, heads_per_shard, shard_w, group, tile_tok, log2_tok, box_rows;
     float scale_log2;
     float* part_o;   // [grid][2][R][D]
     float* part_ml;  // [grid][2][R][2]
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
     const uint32_t full0 = base + C::BAR_OFF, empty0 = full0 + 8 * NST;
     volatile int* abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Tiling tiling = {p.tile_tok, p.group, C::LOG2_KB};
+    const Tiling tiling = {p.tile_tok, p.group, C::LOG2_KB, p.log2_tok};
     const Waiter wait = {abort_flag, p.status, p.timeout_ns};
 
     if (threadIdx.x == 0) {
@@ -649,6 +649,7 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     p.shard_w = static_cast<int>(a.shard_w);
     p.group = a.heads / a.kv_heads;
     p.tile_tok = R / p.group;
+    p.log2_tok = exact_log2(p.tile_tok);
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(C::D));
     const Scratch s = tpi::scratch_of(grid, R, C::D);
     uint8_t* w = static_cast<uint8_t*>(scratch);

@@ -96,7 +96,14 @@ TP_HD int paged_owner(const PagedView& v, long long row) {
 struct Tiling {
     int tok, group;  // tokens of a tile, G
     int log2_keys;   // KB = 2^log2_keys
+    int log2_tok;    // log2 of tok, -1 if that is not a power of two (at most KB)
 };
+
+inline int exact_log2(int x) {
+    int k = 0;
+    while ((1 << k) < x) ++k;
+    return (1 << k) == x ? k : -1;
+}
 
 // Keys of sequence q that exist: its length, at most what the page table holds.
 TP_HD int paged_keys(const PagedView& v, const PagedSeq& q) {
@@ -120,6 +127,12 @@ TP_HD int tile_tokens(const PagedSeq& q, const Tiling& t, int tile) {
 TP_HD int tile_blocks(const PagedSeq& q, int keys, const Tiling& t, int tile) {
     const int seen = token_keys(q, keys, tile * t.tok + tile_tokens(q, t, tile) - 1);
     return seen <= 0 ? 1 : ((seen - 1) >> t.log2_keys) + 1;
+}
+
+// sum_{x < n} floor(x / 2^k).
+TP_HD long long quotient_sum(unsigned n, int k) {
+    const long long q = n >> k, r = n & ((1u << k) - 1);
+    return ((q * (q - 1) / 2) << k) + r * q;
 }
 
 // sum_{x < n} floor((a x + b) / m), by Euclid's algorithm on (m, a).  a n + b
@@ -156,7 +169,15 @@ TP_HD_CALL long long tiles_blocks(const PagedSeq& q, int keys, const Tiling& t, 
     const unsigned c1 = one < n ? one : n;
     const unsigned c2 = full < c1 ? c1 : full < n ? full : n;
     sum += c1;
-    if (c2 > c1) sum += floor_sum(c2 - c1, 1u << t.log2_keys, tok, static_cast<unsigned>(base + kb - 1) + (c1 + 1) * tok);
+    if (c2 > c1) {
+        const unsigned b = static_cast<unsigned>(base + kb - 1) + (c1 + 1) * tok;
+        if (t.log2_tok >= 0) {  // floor((tok x + b) / KB) = floor((x + floor(b / tok)) / (KB / tok))
+            const unsigned y = b >> t.log2_tok;
+            sum += quotient_sum(c2 - c1 + y, t.log2_keys - t.log2_tok) - quotient_sum(y, t.log2_keys - t.log2_tok);
+        } else {
+            sum += floor_sum(c2 - c1, 1u << t.log2_keys, tok, b);
+        }
+    }
     const int most = keys <= 0 ? 1 : ((keys - 1) >> t.log2_keys) + 1;
     return sum + static_cast<long long>(n - c2) * most;
 }

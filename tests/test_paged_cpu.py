@@ -140,7 +140,7 @@ long long page(const int* table, long long pages, int maxp, int log2, int s, int
 long long walk(const int* q, const int* len, long long rows, int n, int maxp, int log2, int k, int tok, int log2_keys,
                int G, int grid, int* out, long long cap, int* desc) {
     PagedView v = view(0, q, len, 1, rows, n, maxp, log2, k);
-    Tiling t = {tok, G, log2_keys};
+    Tiling t = {tok, G, log2_keys, exact_log2(tok)};
     long long total = 0, done = 0;
     for (int s = 0; s < n; ++s) total += seq_blocks(v, paged_seq(v, s), t);
     const long long per = (total + grid - 1) / grid;
@@ -188,7 +188,7 @@ long long walk(const int* q, const int* len, long long rows, int n, int maxp, in
 long long blocks(int n, int len, int maxp, int tok, int log2_keys) {
     const int q[2] = {0, n};
     PagedView v = view(0, q, &len, 1, n, 1, maxp, 4, 1);
-    return seq_blocks(v, paged_seq(v, 0), Tiling{tok, 1, log2_keys});
+    return seq_blocks(v, paged_seq(v, 0), Tiling{tok, 1, log2_keys, exact_log2(tok)});
 }
 long long row(int k, int log2, long long page, int g, int pos) {
     return paged_row(view(0, 0, 0, 0, 0, 0, 0, log2, k), page, g, pos);
@@ -301,7 +301,7 @@ def test_blocks_of_a_sequence_in_closed_form(host):
     rng = np.random.default_rng(5)
     out = np.zeros(1, dtype=np.int64)
     for _ in range(400):
-        new, keep, tok = int(rng.integers(1, 5000)), int(rng.integers(-3000, 9000)), int(rng.choice([1, 2, 3, 5, 16, 18, 32, 42, 128]))
+        new, keep, tok = int(rng.integers(1, 5000)), int(rng.integers(-3000, 9000)), int(rng.choice([1, 2, 3, 5, 16, 18, 25, 32, 42, 64]))
         length, maxp, log2_keys = max(new + keep, 0), int(rng.integers(1, 900)), int(rng.choice([6, 7]))
         keys, want = min(length, 16 * maxp), 0
         for tile in range(-(-new // tok)):
