@@ -584,7 +584,7 @@ TP_API int tp_kv_cache_check(const tp_config* cfg, const tp_kv_cache* cache, int
  *   scale = amax / 448,  code_j = e4m3(x_j * (448 / amax))
  * with the quotients and the product rounded to fp32 and the code rounded to
  * nearest even, at most 448 in magnitude; NaN stays NaN.  Rows of QKV that no
- * sequence owns are not read, other cache rows are left as they are. */
+ * sequence owns go nowhere, other cache rows are left as they are. */
 TP_API int tp_kv_cache_write(tp_plan_t plan, const tp_kv_cache* cache, const tp_bf16* QKV, void* stream);
 
 /* Read back: K_out[s][p], V_out[s][p] = the cached key and value of position

@@ -9,10 +9,16 @@
 // 448.  The product with the rounded reciprocal is at most 448 (1 + 2^-23), so
 // the saturating conversion never changes a finite value by more than its
 // rounding.
+//
+// Both directions are bound by memory: every element is read and written once.
+// A row of d bf16 (128 or 256 bytes) is a group of d / 8 lanes, 16 bytes each,
+// so a warp moves 2 or 4 rows at a time, and a thread issues its loads of
+// several rows before the first is used.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <string>
 
 #include "tp_device.cuh"
@@ -26,6 +32,8 @@ using namespace tpk;
 constexpr float kE4M3Max = 448.0f;
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100
 constexpr float kAmaxCeil = 3.3895313892515355e38f;   // largest finite bf16
+constexpr int THREADS = 256;
+constexpr int STARTS = 1025;  // sequences' starts staged in shared memory, at most
 
 struct KvParams {
     PagedView v;
@@ -33,90 +41,175 @@ struct KvParams {
     float *k_scale, *v_scale;
     const __nv_bfloat16* qkv;
     long long ld_qkv;
-    int shard_w, q_w, kv_w, kv_per_shard, t;
+    int shard_w, q_w, kv_w, held, heads_step, t;  // held: KV heads of a shard; heads_step: shards that share one (k < t), else 0
     unsigned* status;
     // read back
     __nv_bfloat16 *k_out, *v_out;
     long long max_len;
+    int chunks;  // blocks of tokens of a sequence
 };
 
-// One warp per (new token, KV head, K or V).
-template <bool E4M3>
-__global__ void __launch_bounds__(256) kv_write_kernel(const KvParams p) {
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int k = p.v.kv_heads, d = p.v.d;
-    const long long n_items = p.v.rows * k * 2;
-    const long long warps = static_cast<long long>(gridDim.x) * 8;
-    for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < n_items; it += warps) {
-        const bool is_v = it & 1;
-        const int g = static_cast<int>((it >> 1) % k);
-        const long long row = (it >> 1) / k;
-        const int s = paged_owner(p.v, row);
-        if (s < 0) continue;
-        const PagedSeq q = paged_seq(p.v, s);
-        const int pos = q.len - q.n + static_cast<int>(row - q.row0);
-        const long long page = paged_page(p.v, s, pos);
-        if (page < 0) {
-            if (lane == 0 && pos >= 0 && p.status) atomicOr(p.status, kStatusPage);
-            continue;
+// Two fp32 as e4m3 (round to nearest even, at most 448, NaN stays NaN); lo in
+// the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_e4m3x2(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// 16 bytes of a bf16 row to the cache.  at: the cache's row.  The LANES lanes
+// of a row call together (amax is theirs).
+template <int D, bool E4M3>
+__device__ __forceinline__ void store_row(const KvParams& p, bool is_v, long long at, int c, uint4 u, bool live) {
+    constexpr int LANES = D / 8;
+    if constexpr (!E4M3) {
+        if (live) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.V : p.K) + at * D + c * 8) = u;
+    } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        float x[8], amax = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_bf16x2(w[e]);
+            x[2 * e] = f.x;
+            x[2 * e + 1] = f.y;
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));  // NaN is ignored
         }
-        // k >= t: shard g / (k/t) holds g; k < t: shard g t / k is the first with a replica.
-        const int shard = k >= p.t ? g / p.kv_per_shard : g * (p.t / k);
-        const int local = k >= p.t ? g % p.kv_per_shard : 0;
-        const __nv_bfloat16* x =
-            p.qkv + row * p.ld_qkv + shard * p.shard_w + p.q_w + (is_v ? p.kv_w : 0) + local * d;
-        const long long at = paged_row(p.v, page, g, pos);
-        if constexpr (!E4M3) {
-            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(is_v ? p.V : p.K) + at * d;
-            for (int c = lane; c < d; c += 32) y[c] = x[c];
-        } else {
-            float amax = 0.0f;
-            for (int c = lane; c < d; c += 32) amax = fmaxf(amax, fabsf(__bfloat162float(x[c])));
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            amax = fminf(fmaxf(amax, kAmaxFloor), kAmaxCeil);
-            const float inv = __fdiv_rn(kE4M3Max, amax);
-            uint8_t* y = static_cast<uint8_t*>(is_v ? p.V : p.K) + at * d;
-            for (int c = lane; c < d; c += 32)
-                y[c] = __nv_cvt_float_to_fp8(__fmul_rn(__bfloat162float(x[c]), inv), __NV_SATFINITE, __NV_E4M3);
-            if (lane == 0) (is_v ? p.v_scale : p.k_scale)[at] = __fdiv_rn(amax, kE4M3Max);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        amax = fminf(fmaxf(amax, kAmaxFloor), kAmaxCeil);
+        const float inv = __fdiv_rn(kE4M3Max, amax);
+        uint32_t r[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            r[e] = pack_e4m3x2(__fmul_rn(x[4 * e], inv), __fmul_rn(x[4 * e + 1], inv)) |
+                   pack_e4m3x2(__fmul_rn(x[4 * e + 2], inv), __fmul_rn(x[4 * e + 3], inv)) << 16;
+        if (live) {
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? p.V : p.K) + at * D + c * 8) = make_uint2(r[0], r[1]);
+            if (c == 0) (is_v ? p.v_scale : p.k_scale)[at] = __fdiv_rn(amax, kE4M3Max);
         }
     }
 }
 
-// One warp per (sequence, position, KV head, K or V).
-template <bool E4M3>
-__global__ void __launch_bounds__(256) kv_read_kernel(const KvParams p) {
+// Append.  A group of D / 8 lanes takes a (token, KV head) at a time, K and V
+// together: their loads are in flight while the token's place is looked up.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(THREADS) kv_write_kernel(const __grid_constant__ KvParams p) {
+    constexpr int LANES = D / 8;
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int k = p.v.kv_heads, d = p.v.d;
-    const long long n_items = static_cast<long long>(p.v.n_seqs) * p.max_len * k * 2;
-    const long long warps = static_cast<long long>(gridDim.x) * 8;
-    for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < n_items; it += warps) {
-        const bool is_v = it & 1;
-        const int g = static_cast<int>((it >> 1) % k);
-        const long long r = (it >> 1) / k;
-        const int s = static_cast<int>(r / p.max_len);
-        const long long pos = r % p.max_len;
-        if (pos >= p.v.kv_len[s]) continue;
-        const long long page = paged_page(p.v, s, static_cast<int>(pos));
-        if (page < 0 && lane == 0 && p.status) atomicOr(p.status, kStatusPage);
-        const long long at = page < 0 ? 0 : paged_row(p.v, page, g, static_cast<int>(pos));
-        __nv_bfloat16* y = (is_v ? p.v_out : p.k_out) + (r * k + g) * d;
-        for (int c = lane; c < d; c += 32) {
-            float x = 0.0f;
-            if (page >= 0) {
-                if constexpr (E4M3) {
-                    const uint8_t code = static_cast<const uint8_t*>(is_v ? p.V : p.K)[at * d + c];
-                    x = __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3))) *
-                        (is_v ? p.v_scale : p.k_scale)[at];
-                } else {
-                    x = __bfloat162float(static_cast<const __nv_bfloat16*>(is_v ? p.V : p.K)[at * d + c]);
-                }
+    // Every token's owner is looked up: in shared memory, when the sequences' starts fit.
+    __shared__ int32_t starts[STARTS];
+    const bool staged = p.v.n_seqs < STARTS;
+    if (staged) {
+        for (int i = threadIdx.x; i <= p.v.n_seqs; i += THREADS) starts[i] = p.v.q_start[i];
+        __syncthreads();
+    }
+    const int c = threadIdx.x % LANES, k = p.v.kv_heads;
+    const unsigned items = static_cast<unsigned>(p.v.rows) * static_cast<unsigned>(k);
+    const unsigned step = gridDim.x * (THREADS / LANES);
+    // Whole warps stay in the loop (a row's lanes exchange their maxima).
+    for (unsigned base = blockIdx.x * (THREADS / LANES); base < items; base += step) {
+        const unsigned it = base + threadIdx.x / LANES;
+        const bool in = it < items;
+        const int row = static_cast<int>((in ? it : 0) / static_cast<unsigned>(k));
+        const int g = static_cast<int>((in ? it : 0) - static_cast<unsigned>(row) * k);
+        // k >= t: shard g / held holds g; k < t: the first of the shards that share it.
+        const int shard = p.heads_step ? g * p.heads_step : g / p.held;
+        const int local = p.heads_step ? 0 : g - shard * p.held;
+        const __nv_bfloat16* x = p.qkv + row * p.ld_qkv + static_cast<long long>(shard) * p.shard_w + p.q_w + local * D + c * 8;
+        const uint4 kx = *reinterpret_cast<const uint4*>(x), vx = *reinterpret_cast<const uint4*>(x + p.kv_w);
+        const int s = in ? paged_owner(staged ? starts : p.v.q_start, p.v.n_seqs, row) : -1;
+        long long at = -1;
+        if (s >= 0) {
+            const PagedSeq q = paged_seq(p.v, s);
+            const int pos = q.len - q.n + (row - q.row0);
+            const long long page = paged_page(p.v, s, pos);
+            if (page >= 0) at = paged_row(p.v, page, g, pos);
+            else if (pos >= 0 && c == 0 && p.status) atomicOr(p.status, kStatusPage);
+        }
+        store_row<D, E4M3>(p, false, at, c, kx, at >= 0);
+        store_row<D, E4M3>(p, true, at, c, vx, at >= 0);
+    }
+}
+
+// Read back.  Block (chunk, sequence): 64 positions of a sequence, all heads.
+// A thread's turn is 16 bytes of K and of V of one (position, head), UNROLL
+// turns in flight.
+constexpr int READ_POS = 64;
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(THREADS) kv_read_kernel(const __grid_constant__ KvParams p) {
+    constexpr int LANES = D / 8, UNROLL = 4;
+    pdl_trigger();
+    pdl_wait();
+    const int s = blockIdx.x / p.chunks;
+    const long long first = static_cast<long long>(blockIdx.x - s * p.chunks) * READ_POS;
+    const long long len = pmin(p.v.kv_len[s], p.max_len);
+    const int n = static_cast<int>(pmin(READ_POS, len - first));
+    if (n <= 0) return;
+    const int c = threadIdx.x % LANES, k = p.v.kv_heads;
+    const int items = n * k, log2 = p.v.page_log2;
+    __shared__ long long pages[READ_POS / 16];  // of the block's positions, -1 outside the cache
+    if (threadIdx.x <= ((n - 1) >> log2)) {
+        pages[threadIdx.x] = paged_page(p.v, s, static_cast<int>(first) + (static_cast<int>(threadIdx.x) << log2));
+        if (pages[threadIdx.x] < 0 && p.status) atomicOr(p.status, kStatusPage);
+    }
+    __syncthreads();
+    // Items in the cache's order (position fastest within a page and head), so that neighbouring groups read
+    // neighbouring rows.
+    for (int i0 = threadIdx.x / LANES; i0 < items; i0 += UNROLL * (THREADS / LANES)) {
+        uint4 ku[UNROLL], vu[UNROLL];
+        float ks[UNROLL], vs[UNROLL];
+        long long to[UNROLL];
+#pragma unroll
+        for (int e = 0; e < UNROLL; ++e) {
+            const int i = i0 + e * (THREADS / LANES);
+            to[e] = -1;
+            if (i >= items) continue;
+            const int g = i / n, pos = i - g * n;
+            const int in_page = static_cast<int>(first) + pos;
+            const long long page = pages[((in_page >> log2) - (static_cast<int>(first) >> log2))];
+            to[e] = ((s * p.max_len + first + pos) * k + g) * D + c * 8;
+            ku[e] = vu[e] = make_uint4(0, 0, 0, 0);
+            ks[e] = vs[e] = 0.0f;
+            if (page < 0) continue;
+            const long long at = paged_row(p.v, page, g, in_page);
+            if constexpr (E4M3) {
+                const uint2 a = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.K) + at * D + c * 8));
+                const uint2 b = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.V) + at * D + c * 8));
+                ku[e].x = a.x;
+                ku[e].y = a.y;
+                vu[e].x = b.x;
+                vu[e].y = b.y;
+                ks[e] = p.k_scale[at];
+                vs[e] = p.v_scale[at];
+            } else {
+                ku[e] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.K) + at * D + c * 8));
+                vu[e] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.V) + at * D + c * 8));
             }
-            y[c] = __float2bfloat16_rn(x);
+        }
+#pragma unroll
+        for (int e = 0; e < UNROLL; ++e) {
+            if (to[e] < 0) continue;
+            if constexpr (E4M3) {
+                auto expand = [](uint4 u, float f) {
+                    uint32_t r[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float2 v = unpack_e4m3x2((x < 2 ? u.x : u.y) >> (16 * (x & 1)));
+                        r[x] = pack_bf16x2(v.x * f, v.y * f);
+                    }
+                    return make_uint4(r[0], r[1], r[2], r[3]);
+                };
+                ku[e] = expand(ku[e], ks[e]);
+                vu[e] = expand(vu[e], vs[e]);
+            }
+            __stcs(reinterpret_cast<uint4*>(p.k_out + to[e]), ku[e]);
+            __stcs(reinterpret_cast<uint4*>(p.v_out + to[e]), vu[e]);
         }
     }
 }
@@ -133,7 +226,8 @@ KvParams params_of(const tpi::PagedArgs& a) {
     p.shard_w = static_cast<int>(a.shard_w);
     p.q_w = static_cast<int>(a.q_w);
     p.kv_w = static_cast<int>(a.kv_w);
-    p.kv_per_shard = a.kv_heads / a.t;
+    p.held = a.kv_heads >= a.t ? a.kv_heads / a.t : 1;
+    p.heads_step = a.kv_heads >= a.t ? 0 : a.t / a.kv_heads;
     p.t = a.t;
     p.status = a.status;
     return p;
@@ -146,12 +240,6 @@ int launched(const char* what, cudaError_t e, std::string* err) {
     return TP_ERR_CUDA;
 }
 
-unsigned blocks_for(long long warps) {
-    const long long most = static_cast<long long>(tpi::device_sm_count()) * 8;
-    const long long need = (warps + 7) / 8;
-    return static_cast<unsigned>(need < most ? need : most);
-}
-
 }  // namespace
 
 namespace tpi {
@@ -159,9 +247,16 @@ namespace tpi {
 int kv_write_launch(const PagedArgs& a, cudaStream_t stream, std::string* err) {
     if (a.n_seqs == 0) return TP_OK;
     const KvParams p = params_of(a);
-    const unsigned grid = blocks_for(a.tokens * a.kv_heads * 2);
-    const cudaError_t e = a.e4m3 ? launch_pdl(kv_write_kernel<true>, dim3(grid), dim3(256), 0, stream, p)
-                                 : launch_pdl(kv_write_kernel<false>, dim3(grid), dim3(256), 0, stream, p);
+    const long long groups = THREADS / (a.head_dim / 8);
+    const long long need = (a.tokens * a.kv_heads + groups - 1) / groups;
+    const dim3 grid(static_cast<unsigned>(std::min<long long>(need, device_sm_count() * 8LL))), block(THREADS);
+    cudaError_t e;
+    if (a.head_dim == 128)
+        e = a.e4m3 ? launch_pdl(kv_write_kernel<128, true>, grid, block, 0, stream, p)
+                   : launch_pdl(kv_write_kernel<128, false>, grid, block, 0, stream, p);
+    else
+        e = a.e4m3 ? launch_pdl(kv_write_kernel<64, true>, grid, block, 0, stream, p)
+                   : launch_pdl(kv_write_kernel<64, false>, grid, block, 0, stream, p);
     return launched("cache write kernel", e, err);
 }
 
@@ -170,11 +265,22 @@ int kv_read_launch(const PagedArgs& a, int64_t max_len, void* k_out, void* v_out
     if (a.n_seqs == 0 || max_len == 0) return TP_OK;
     KvParams p = params_of(a);
     p.max_len = max_len;
+    p.chunks = static_cast<int>((max_len + READ_POS - 1) / READ_POS);
     p.k_out = static_cast<__nv_bfloat16*>(k_out);
     p.v_out = static_cast<__nv_bfloat16*>(v_out);
-    const unsigned grid = blocks_for(static_cast<long long>(a.n_seqs) * max_len * a.kv_heads * 2);
-    const cudaError_t e = a.e4m3 ? launch_pdl(kv_read_kernel<true>, dim3(grid), dim3(256), 0, stream, p)
-                                 : launch_pdl(kv_read_kernel<false>, dim3(grid), dim3(256), 0, stream, p);
+    const long long blocks = static_cast<long long>(a.n_seqs) * p.chunks;
+    if (blocks > 0x7fffffffll) {
+        if (err) *err = "n_seqs x max_len is too large for one read";
+        return TP_ERR_UNSUPPORTED;
+    }
+    const dim3 grid(static_cast<unsigned>(blocks)), block(THREADS);
+    cudaError_t e;
+    if (a.head_dim == 128)
+        e = a.e4m3 ? launch_pdl(kv_read_kernel<128, true>, grid, block, 0, stream, p)
+                   : launch_pdl(kv_read_kernel<128, false>, grid, block, 0, stream, p);
+    else
+        e = a.e4m3 ? launch_pdl(kv_read_kernel<64, true>, grid, block, 0, stream, p)
+                   : launch_pdl(kv_read_kernel<64, false>, grid, block, 0, stream, p);
     return launched("cache read kernel", e, err);
 }
 

@@ -69,12 +69,12 @@ TP_HD long long paged_row(const PagedView& v, long long page, int g, int pos) {
 
 // Sequence that owns `row`: the last s with q_start[s] <= row, if the row is
 // below q_start[s + 1]; -1 otherwise.
-TP_HD int paged_owner(const PagedView& v, long long row) {
-    int lo = 0, hi = v.n_seqs;  // invariant: q_start[lo] <= row (if any), q_start[hi] > row
-    if (v.n_seqs == 0 || row < v.q_start[0] || row >= v.q_start[v.n_seqs]) return -1;
+TP_HD int paged_owner(const int32_t* q_start, int n_seqs, int row) {
+    if (n_seqs == 0 || row < q_start[0] || row >= q_start[n_seqs]) return -1;
+    int lo = 0, hi = n_seqs;  // q_start[lo] <= row < q_start[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (v.q_start[mid] <= row) lo = mid;
+        if (q_start[mid] <= row) lo = mid;
         else hi = mid;
     }
     return lo;

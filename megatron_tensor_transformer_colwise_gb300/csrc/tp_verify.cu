@@ -8,6 +8,15 @@
 // exponential race: with E_v independent Exp(1), argmax_v w_v / E_v is v with
 // probability w_v / sum w, whatever the scale of w, so that neither the sum
 // nor a running sum over the vocabulary is needed.
+//
+// One launch: a cluster of 8 CTAs per sequence, an eighth of the vocabulary
+// each.  Up to 8 rows (16 rows of logits with the draft's) are summed at a
+// time, a group of warps each, with a running maximum; only the maxima and sums
+// are exchanged, through distributed shared memory, as the vocabulary-parallel
+// loss does between its shards.  Every CTA then decides by itself, and the race
+// runs over the one row where a draft was refused (its logits are read a second
+// time, from L2).  Bound by reading the logits once; rows behind a refused
+// draft are still read if they are among its 8.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -15,12 +24,16 @@
 
 #include "tp_device.cuh"
 #include "tp_internal.h"
+#include "tp_packed.cuh"
 
 namespace {
 
 using namespace tpk;
 
-constexpr int VT = 512;
+constexpr int CS = 8;      // CTAs of a cluster
+constexpr int WARPS = 16;
+constexpr int VT = WARPS * 32;
+constexpr int ROWS = 8;    // rows of a batch
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct VerifyParams {
@@ -29,8 +42,23 @@ struct VerifyParams {
     const int32_t *ids, *q_start;
     const float *temperature, *u, *noise;
     int32_t *accepted, *tokens;
-    int n_seqs;
 };
+
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// m = max x_v and s = sum 2^((x_v - m) it), it = log2(e) / T.
+struct Stat {
+    float m, s;
+};
+__device__ __forceinline__ Stat merge(Stat a, Stat b, float it) {
+    const float m = fmaxf(a.m, b.m);
+    if (m == -INFINITY) return {m, 0.0f};
+    return {m, a.s * ex2f((a.m - m) * it) + b.s * ex2f((b.m - m) * it)};
+}
 
 // Largest value and its lowest index.
 struct Best {
@@ -40,105 +68,239 @@ struct Best {
 __device__ __forceinline__ Best better(Best a, Best b) {
     return (b.v > a.v || (b.v == a.v && b.i < a.i)) ? b : a;
 }
-
-__device__ __forceinline__ Best block_best(Best a, Best* red) {
+__device__ __forceinline__ Best warp_best(Best a) {
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        Best b = {__shfl_xor_sync(0xffffffffu, a.v, o), __shfl_xor_sync(0xffffffffu, a.i, o)};
+        const Best b = {__shfl_xor_sync(0xffffffffu, a.v, o), __shfl_xor_sync(0xffffffffu, a.i, o)};
         a = better(a, b);
     }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
-    __syncthreads();
-    a = red[0];
-    for (int w = 1; w < VT / 32; ++w) a = better(a, red[w]);
     return a;
 }
 
-// m = max_v x_v and sum_v 2^((x_v - m) it), it = log2(e) / T: the difference
-// comes first, so that logits at the type's ends do not overflow.
-__device__ __forceinline__ float2 row_stats(const __nv_bfloat16* x, long long v, float it, float* red) {
-    float m = -INFINITY;
-    for (long long c = threadIdx.x; c < v; c += VT) m = fmaxf(m, __bfloat162float(x[c]));
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    for (int w = 0; w < VT / 32; ++w) m = fmaxf(m, red[w]);
-    float s = 0.0f;
-    if (m > -INFINITY)
-        for (long long c = threadIdx.x; c < v; c += VT) s += exp2f((__bfloat162float(x[c]) - m) * it);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = 0.0f;
-    for (int w = 0; w < VT / 32; ++w) s += red[w];
-    return make_float2(m, s);
+// 8 bytes to the same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ void store_cluster(uint32_t addr, int rank, uint32_t a, uint32_t b) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(mapa_shared(addr, static_cast<uint32_t>(rank))), "r"(a),
+                 "r"(b)
+                 : "memory");
 }
 
-__device__ __forceinline__ float prob(float x, float it, float2 st) {
-    return st.y > 0.0f ? exp2f((x - st.x) * it) / st.y : 0.0f;
+// Pieces of 8 logits (16 bytes): first, first + step, ... below end, four
+// loads in flight; f(values, index of the first).
+template <class F>
+__device__ __forceinline__ void for_pieces(const __nv_bfloat16* x, int first, int end, int step, F f) {
+    const uint4* src = reinterpret_cast<const uint4*>(x);
+    for (int c0 = first; c0 < end; c0 += 4 * step) {
+        uint4 u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c0 + e * step < end) u[e] = src[c0 + e * step];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (c0 + e * step >= end) break;
+            const uint32_t w[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 t = unpack_bf16x2(w[k]);
+                v[2 * k] = t.x;
+                v[2 * k + 1] = t.y;
+            }
+            f(v, (c0 + e * step) * 8);
+        }
+    }
 }
 
-// One CTA per sequence.
-__global__ void __launch_bounds__(VT) verify_simple_kernel(const VerifyParams p) {
+__device__ __forceinline__ float prob(float x, float it, Stat st) {
+    return st.s > 0.0f ? ex2f((x - st.m) * it) / st.s : 0.0f;
+}
+
+__global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT, 2) verify_kernel(const VerifyParams p) {
     pdl_trigger();
     pdl_wait();
-    __shared__ float red[VT / 32];
-    __shared__ Best bred[VT / 32];
-    const int s = blockIdx.x;
+    __shared__ Stat part[WARPS];           // a warp's statistics, or its largest logit
+    __shared__ Stat all[2][2 * ROWS][CS];  // by batch parity, row of logits and CTA
+    __shared__ Best race[WARPS][2], raced[CS][2];
+    const int rank = static_cast<int>(cluster_ctarank()), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = blockIdx.x / CS;
     const long long r0 = min(max(static_cast<long long>(p.q_start[s]), 0ll), p.rows);
     const long long r1 = min(max(static_cast<long long>(p.q_start[s + 1]), r0), p.rows);
     const int n = static_cast<int>(r1 - r0);
+    if (n == 0) {  // the whole cluster
+        if (rank == 0 && threadIdx.x == 0) p.accepted[s] = 0;
+        return;
+    }
     const float T = p.temperature ? p.temperature[s] : 1.0f;
     const bool greedy = !(T > 0.0f);
     const float it = fminf(LOG2E / T, 1e30f);  // finite, so that 0 * it is 0
-    int taken = 0, token = -1;
-    for (int i = 0; i < n; ++i) {
-        const __nv_bfloat16* z = p.z + (r0 + i) * p.v;
-        const __nv_bfloat16* y = (p.y && i + 1 < n) ? p.y + (r0 + i) * p.v : nullptr;
-        const long long x = i + 1 < n ? p.ids[r0 + i + 1] : -1;
-        const bool inside = x >= 0 && x < p.v;
-        Best b = {-INFINITY, 0x7fffffff};
-        if (greedy) {
-            for (long long c = threadIdx.x; c < p.v; c += VT)
-                b = better(b, Best{__bfloat162float(z[c]), static_cast<int>(c)});
-            b = block_best(b, bred);
-            token = b.v > -INFINITY ? b.i : -1;
-            if (i + 1 < n && inside && token == x) {
-                ++taken;
-                continue;
+    const int pieces = static_cast<int>(p.v / 8), mine = (pieces + CS - 1) / CS;
+    const int begin = min(rank * mine, pieces), end = min(begin + mine, pieces);
+
+    int taken = n - 1, token = -1;
+    Stat sp = {-INFINITY, 0.0f}, sq = {-INFINITY, 0.0f};
+    bool drafted = false;  // the row that stops has a draft distribution
+    for (int b0 = 0, parity = 0; b0 < n; b0 += ROWS, parity ^= 1) {
+        const int rows = min(ROWS, n - b0);
+        // Rows of logits: the target's, then the draft's (none behind the last draft).
+        const int drafts = greedy || !p.y ? 0 : min(rows, n - 1 - b0);
+        const int items = rows + drafts, per = WARPS / items;
+        const int item = warp / per, sub = warp % per;
+        if (item < items) {
+            const __nv_bfloat16* x = (item < rows ? p.z + (r0 + b0 + item) * p.v : p.y + (r0 + b0 + item - rows) * p.v);
+            const int first = begin + sub * 32 + lane, step = per * 32;
+            if (greedy) {
+                Best b = {-INFINITY, 0x7fffffff};
+                for_pieces(x, first, end, step, [&](const float (&v)[8], int i) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (v[k] > b.v) b = {v[k], i + k};  // indices ascend in a thread
+                });
+                b = warp_best(b);
+                if (lane == 0) part[warp] = {b.v, __int_as_float(b.i)};
+            } else {
+                Stat a = {-INFINITY, 0.0f};
+                for_pieces(x, first, end, step, [&](const float (&v)[8], int) {
+                    float bm = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+                    if (bm > a.m) {
+                        a.s *= ex2f((a.m - bm) * it);  // 0 * 0 at first
+                        a.m = bm;
+                    }
+                    if (a.m == -INFINITY) return;
+                    // The difference first, as everywhere: exact for near logits, and finite at the type's ends.
+                    const uint64_t minus = f2_pack(-a.m, -a.m), its = f2_pack(it, it);
+                    float e[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float x0, x1;
+                        f2_unpack(f2_mul(f2_add(f2_pack(v[2 * k], v[2 * k + 1]), minus), its), x0, x1);
+                        e[2 * k] = ex2f(x0);
+                        e[2 * k + 1] = ex2f(x1);
+                    }
+                    a.s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                });
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)};
+                    a = merge(a, b, it);
+                }
+                if (lane == 0) part[warp] = a;
             }
+        }
+        __syncthreads();
+        if (threadIdx.x < items * CS) {
+            const int i = threadIdx.x / CS, to = threadIdx.x % CS;
+            Stat a = part[i * per];
+            for (int k = 1; k < per; ++k) {
+                const Stat b = part[i * per + k];
+                if (greedy) {
+                    const Best c = better({a.m, __float_as_int(a.s)}, {b.m, __float_as_int(b.s)});
+                    a = {c.v, __int_as_float(c.i)};
+                } else {
+                    a = merge(a, b, it);
+                }
+            }
+            store_cluster(smem_u32(&all[parity][i][rank]), to, __float_as_uint(a.m), __float_as_uint(a.s));
+        }
+        // A batch's buffer is written again two batches on: behind the next batch's barrier, which every CTA
+        // reaches after it has read this one.
+        cluster_sync_all();
+        // Every warp decides, a lane a row.
+        bool take = false;
+        Stat tp_ = {-INFINITY, 0.0f}, tq = {-INFINITY, 0.0f};
+        if (lane < rows) {
+            const long long r = r0 + b0 + lane;
+            const bool last = b0 + lane + 1 == n;
+            const long long x = last ? -1 : p.ids[r + 1];
+            const bool inside = x >= 0 && x < p.v;
+            tp_ = all[parity][lane][0];
+            for (int k = 1; k < CS; ++k) {
+                const Stat b = all[parity][lane][k];
+                if (greedy) {
+                    const Best c = better({tp_.m, __float_as_int(tp_.s)}, {b.m, __float_as_int(b.s)});
+                    tp_ = {c.v, __int_as_float(c.i)};
+                } else {
+                    tp_ = merge(tp_, b, it);
+                }
+            }
+            if (greedy) {
+                take = inside && tp_.m > -INFINITY && __float_as_int(tp_.s) == static_cast<int>(x);
+            } else {
+                if (lane < drafts) {
+                    tq = all[parity][rows + lane][0];
+                    for (int k = 1; k < CS; ++k) tq = merge(tq, all[parity][rows + lane][k], it);
+                }
+                if (inside) {
+                    const float px = prob(__bfloat162float(p.z[r * p.v + x]), it, tp_);
+                    const float qx = lane < drafts ? prob(__bfloat162float(p.y[r * p.v + x]), it, tq) : 0.0f;
+                    take = p.u[r] * qx < px;
+                }
+            }
+        }
+        const unsigned kept = __ballot_sync(0xffffffffu, lane < rows && !take);
+        if (kept) {
+            const int i = __ffs(kept) - 1;
+            taken = b0 + i;
+            sp = {__shfl_sync(0xffffffffu, tp_.m, i), __shfl_sync(0xffffffffu, tp_.s, i)};
+            sq = {__shfl_sync(0xffffffffu, tq.m, i), __shfl_sync(0xffffffffu, tq.s, i)};
+            drafted = i < drafts;
             break;
         }
-        const float2 sp = row_stats(z, p.v, it, red);
-        float2 sq = make_float2(0.0f, 0.0f);
-        if (y) sq = row_stats(y, p.v, it, red);
-        if (inside) {
-            const float px = prob(__bfloat162float(z[x]), it, sp);
-            const float qx = y ? prob(__bfloat162float(y[x]), it, sq) : 0.0f;
-            if (p.u[r0 + i] * qx < px) {
-                ++taken;
-                continue;
+    }
+    if (greedy) {
+        token = sp.m > -INFINITY ? __float_as_int(sp.s) : -1;
+    } else {
+        // The race over w = max(0, p - q), and over p alone in case that leaves nothing.
+        Best b = {0.0f, 0x7fffffff}, f = b;
+        const uint4* z = reinterpret_cast<const uint4*>(p.z + (r0 + taken) * p.v);
+        const uint4* y = drafted ? reinterpret_cast<const uint4*>(p.y + (r0 + taken) * p.v) : nullptr;
+        const float4* e4 = p.noise ? reinterpret_cast<const float4*>(p.noise + s * p.v) : nullptr;
+        const float ip = sp.s > 0.0f ? 1.0f / sp.s : 0.0f, iq = sq.s > 0.0f ? 1.0f / sq.s : 0.0f;
+#pragma unroll 2
+        for (int c = begin + static_cast<int>(threadIdx.x); c < end; c += VT) {
+            const uint4 zu = z[c], yu = y ? y[c] : make_uint4(0, 0, 0, 0);
+            const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+            const float4 ea = e4 ? __ldcs(e4 + 2 * c) : one, eb = e4 ? __ldcs(e4 + 2 * c + 1) : one;
+            const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w}, yw[4] = {yu.x, yu.y, yu.z, yu.w};
+            const float e[8] = {ea.x, ea.y, ea.z, ea.w, eb.x, eb.y, eb.z, eb.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 zf = unpack_bf16x2(zw[k >> 1]), yf = unpack_bf16x2(yw[k >> 1]);
+                const float pv = ex2f((((k & 1) ? zf.y : zf.x) - sp.m) * it) * ip;
+                const float qv = y ? ex2f((((k & 1) ? yf.y : yf.x) - sq.m) * it) * iq : 0.0f;
+                // A probability of NaN, as from NaN or infinite logits, wins nothing.
+                const float rb = __fdividef(pv - (iq > 0.0f ? qv : 0.0f), e[k]), rf = __fdividef(pv, e[k]);
+                if (rb > b.v) b = {rb, c * 8 + k};
+                if (rf > f.v) f = {rf, c * 8 + k};
             }
         }
-        Best f = b;  // from p alone, where max(0, p - q) leaves nothing
-        for (long long c = threadIdx.x; c < p.v; c += VT) {
-            const float e = p.noise ? p.noise[s * p.v + c] : 1.0f;
-            const float pc = prob(__bfloat162float(z[c]), it, sp);
-            const float w = y ? pc - prob(__bfloat162float(y[c]), it, sq) : pc;
-            if (w > 0.0f) b = better(b, Best{w / e, static_cast<int>(c)});
-            if (pc > 0.0f) f = better(f, Best{pc / e, static_cast<int>(c)});
+        b = warp_best(b);
+        f = warp_best(f);
+        if (lane == 0) {
+            race[warp][0] = b;
+            race[warp][1] = f;
         }
-        b = block_best(b, bred);
-        f = block_best(f, bred);
-        if (!(b.v > 0.0f)) b = f;
-        token = b.v > 0.0f ? b.i : -1;
-        break;
+        __syncthreads();
+        if (threadIdx.x < 2) {
+            Best a = race[0][threadIdx.x];
+            for (int k = 1; k < WARPS; ++k) a = better(a, race[k][threadIdx.x]);
+            store_cluster(smem_u32(&raced[rank][threadIdx.x]), 0, __float_as_uint(a.v), static_cast<uint32_t>(a.i));
+        }
+        cluster_sync_all();
+        if (rank == 0) {
+            b = raced[0][0];
+            f = raced[0][1];
+            for (int k = 1; k < CS; ++k) {
+                b = better(b, raced[k][0]);
+                f = better(f, raced[k][1]);
+            }
+            if (!(b.v > 0.0f)) b = f;
+            token = b.v > 0.0f ? b.i : -1;
+        }
     }
-    if (threadIdx.x == 0) p.accepted[s] = taken;
-    for (int i = threadIdx.x; i < n; i += VT)
-        p.tokens[r0 + i] = i < taken ? p.ids[r0 + i + 1] : i == taken ? token : -1;
+    if (rank == 0) {
+        if (threadIdx.x == 0) p.accepted[s] = taken;
+        for (int i = threadIdx.x; i < n; i += VT)
+            p.tokens[r0 + i] = i < taken ? p.ids[r0 + i + 1] : i == taken ? token : -1;
+    }
 }
 
 }  // namespace
@@ -159,8 +321,7 @@ int verify_launch(const VerifyArgs& a, cudaStream_t stream, std::string* err) {
     p.noise = a.noise;
     p.accepted = a.accepted;
     p.tokens = a.tokens;
-    p.n_seqs = a.n_seqs;
-    cudaError_t e = launch_pdl(verify_simple_kernel, dim3(static_cast<unsigned>(a.n_seqs)), dim3(VT), 0, stream, p);
+    cudaError_t e = launch_pdl(verify_kernel, dim3(static_cast<unsigned>(a.n_seqs) * CS), dim3(VT), 0, stream, p);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         if (err) *err = std::string("verification kernel: ") + cudaGetErrorString(e);

@@ -127,7 +127,7 @@ static PagedView view(const int* table, const int* q, const int* len, long long 
     return v;
 }
 extern "C" {
-int owner(const int* q, int n, long long row) { return paged_owner(view(0, q, 0, 0, 0, n, 0, 0, 1), row); }
+int owner(const int* q, int n, long long row) { return paged_owner(q, n, (int)row); }
 void seq(const int* q, const int* len, long long rows, int n, int s, long long* out) {
     PagedSeq x = paged_seq(view(0, q, len, 0, rows, n, 0, 0, 1), s);
     out[0] = x.row0; out[1] = x.n; out[2] = x.len;
