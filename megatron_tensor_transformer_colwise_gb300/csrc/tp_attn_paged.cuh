@@ -168,6 +168,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 inline EncodeTiledFn encode_fn(std::string* err) {
+    static void* found = nullptr;  // the driver's entry point: one a process, the same whoever stores it
+    if (found) return reinterpret_cast<EncodeTiledFn>(found);
     void* f = nullptr;
     cudaDriverEntryPointQueryResult qr;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
@@ -175,6 +177,7 @@ inline EncodeTiledFn encode_fn(std::string* err) {
         if (err) *err = "cuTensorMapEncodeTiled is not available from the driver";
         return nullptr;
     }
+    found = f;
     return reinterpret_cast<EncodeTiledFn>(f);
 }
 

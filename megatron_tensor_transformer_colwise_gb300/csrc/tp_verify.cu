@@ -11,7 +11,8 @@
 //
 // One launch: a cluster of 8 CTAs per sequence, an eighth of the vocabulary
 // each.  Up to 8 rows (16 rows of logits with the draft's) are summed at a
-// time, a group of warps each, with a running maximum; only the maxima and sums
+// time, every thread its pieces of one row after the other with a running
+// maximum and loads in flight across rows; only the maxima and sums
 // are exchanged, through distributed shared memory, as the vocabulary-parallel
 // loss does between its shards.  Every CTA then decides by itself, and the race
 // runs over the one row where a draft was refused (its logits are read a second
@@ -31,9 +32,10 @@ namespace {
 using namespace tpk;
 
 constexpr int CS = 8;      // CTAs of a cluster
-constexpr int WARPS = 16;
+constexpr int WARPS = 8;   // small CTAs, four an SM: a batch of 64 sequences is one wave
 constexpr int VT = WARPS * 32;
 constexpr int ROWS = 8;    // rows of a batch
+constexpr int FLY = 4;     // 16-byte loads in flight a thread
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct VerifyParams {
@@ -84,40 +86,14 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, int rank, uint32_t 
                  : "memory");
 }
 
-// Pieces of 8 logits (16 bytes): first, first + step, ... below end, four
-// loads in flight; f(values, index of the first).
-template <class F>
-__device__ __forceinline__ void for_pieces(const __nv_bfloat16* x, int first, int end, int step, F f) {
-    const uint4* src = reinterpret_cast<const uint4*>(x);
-    for (int c0 = first; c0 < end; c0 += 4 * step) {
-        uint4 u[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c0 + e * step < end) u[e] = src[c0 + e * step];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (c0 + e * step >= end) break;
-            const uint32_t w[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
-            float v[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 t = unpack_bf16x2(w[k]);
-                v[2 * k] = t.x;
-                v[2 * k + 1] = t.y;
-            }
-            f(v, (c0 + e * step) * 8);
-        }
-    }
-}
-
 __device__ __forceinline__ float prob(float x, float it, Stat st) {
     return st.s > 0.0f ? ex2f((x - st.m) * it) / st.s : 0.0f;
 }
 
-__global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT, 2) verify_kernel(const VerifyParams p) {
+__global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT, 4) verify_kernel(const VerifyParams p) {
     pdl_trigger();
     pdl_wait();
-    __shared__ Stat part[WARPS];           // a warp's statistics, or its largest logit
+    __shared__ Stat part[2 * ROWS][VT];    // by row of logits: a thread's statistics, or its largest logit
     __shared__ Stat all[2][2 * ROWS][CS];  // by batch parity, row of logits and CTA
     __shared__ Best race[WARPS][2], raced[CS][2];
     const int rank = static_cast<int>(cluster_ctarank()), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -142,63 +118,94 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT, 2) verify_kerne
         const int rows = min(ROWS, n - b0);
         // Rows of logits: the target's, then the draft's (none behind the last draft).
         const int drafts = greedy || !p.y ? 0 : min(rows, n - 1 - b0);
-        const int items = rows + drafts, per = WARPS / items;
-        const int item = warp / per, sub = warp % per;
-        if (item < items) {
-            const __nv_bfloat16* x = (item < rows ? p.z + (r0 + b0 + item) * p.v : p.y + (r0 + b0 + item - rows) * p.v);
-            const int first = begin + sub * 32 + lane, step = per * 32;
-            if (greedy) {
-                Best b = {-INFINITY, 0x7fffffff};
-                for_pieces(x, first, end, step, [&](const float (&v)[8], int i) {
+        const int items = rows + drafts;
+        // Pieces of 8 logits (16 bytes): this thread's of a row are begin + threadIdx.x + j VT; one row after the
+        // other, FLY loads in flight.
+        const int turns = (end - begin + VT - 1) / VT;
+        auto row_of = [&](int i) {
+            return reinterpret_cast<const uint4*>(i < rows ? p.z + (r0 + b0 + i) * p.v : p.y + (r0 + b0 + i - rows) * p.v);
+        };
+        Stat a = {-INFINITY, 0.0f};
+        int li = 0, lj = 0;  // row and piece of the next load
+        int ui = 0, uj = 0;  // and of the next use
+        const int first = begin + static_cast<int>(threadIdx.x);
+        for (int k0 = 0; k0 < items * turns; k0 += FLY) {
+            uint4 u[FLY];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (v[k] > b.v) b = {v[k], i + k};  // indices ascend in a thread
-                });
-                b = warp_best(b);
-                if (lane == 0) part[warp] = {b.v, __int_as_float(b.i)};
-            } else {
-                Stat a = {-INFINITY, 0.0f};
-                for_pieces(x, first, end, step, [&](const float (&v)[8], int) {
-                    float bm = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-                    if (bm > a.m) {
-                        a.s *= ex2f((a.m - bm) * it);  // 0 * 0 at first
-                        a.m = bm;
-                    }
-                    if (a.m == -INFINITY) return;
-                    // The difference first, as everywhere: exact for near logits, and finite at the type's ends.
-                    const uint64_t minus = f2_pack(-a.m, -a.m), its = f2_pack(it, it);
-                    float e[8];
+            for (int e = 0; e < FLY; ++e) {
+                if (li < items && first + lj * VT < end) u[e] = row_of(li)[first + lj * VT];
+                if (++lj == turns) {
+                    lj = 0;
+                    ++li;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < FLY; ++e) {
+                if (ui == items) break;
+                const int piece = first + uj * VT;
+                if (piece < end) {
+                    const uint32_t w[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+                    float v[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float x0, x1;
-                        f2_unpack(f2_mul(f2_add(f2_pack(v[2 * k], v[2 * k + 1]), minus), its), x0, x1);
-                        e[2 * k] = ex2f(x0);
-                        e[2 * k + 1] = ex2f(x1);
+                        const float2 t = unpack_bf16x2(w[k]);
+                        v[2 * k] = t.x;
+                        v[2 * k + 1] = t.y;
                     }
-                    a.s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-                });
+                    if (greedy) {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)};
-                    a = merge(a, b, it);
+                        for (int k = 0; k < 8; ++k)
+                            if (v[k] > a.m) a = {v[k], __int_as_float(piece * 8 + k)};  // indices ascend in a thread
+                    } else {
+                        const float bm = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
+                        if (bm > a.m) {
+                            a.s *= ex2f((a.m - bm) * it);  // 0 * 0 at first
+                            a.m = bm;
+                        }
+                        if (a.m > -INFINITY) {
+                            // The difference first, as everywhere: exact for near logits, finite at the type's ends.
+                            const uint64_t minus = f2_pack(-a.m, -a.m), its = f2_pack(it, it);
+                            float x[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float x0, x1;
+                                f2_unpack(f2_mul(f2_add(f2_pack(v[2 * k], v[2 * k + 1]), minus), its), x0, x1);
+                                x[2 * k] = ex2f(x0);
+                                x[2 * k + 1] = ex2f(x1);
+                            }
+                            a.s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                        }
+                    }
                 }
-                if (lane == 0) part[warp] = a;
+                if (++uj == turns) {
+                    part[ui][threadIdx.x] = a;
+                    a = {-INFINITY, 0.0f};
+                    uj = 0;
+                    ++ui;
+                }
             }
         }
         __syncthreads();
-        if (threadIdx.x < items * CS) {
-            const int i = threadIdx.x / CS, to = threadIdx.x % CS;
-            Stat a = part[i * per];
-            for (int k = 1; k < per; ++k) {
-                const Stat b = part[i * per + k];
-                if (greedy) {
-                    const Best c = better({a.m, __float_as_int(a.s)}, {b.m, __float_as_int(b.s)});
-                    a = {c.v, __int_as_float(c.i)};
-                } else {
-                    a = merge(a, b, it);
+        // A warp a row: the CTA's statistics, to every CTA of the cluster.
+        for (int i = warp; i < items; i += WARPS) {
+            Stat b = {-INFINITY, 0.0f};
+            if (turns > 0) b = part[i][lane];
+            if (greedy) {
+                Best c = {b.m, b.m > -INFINITY ? __float_as_int(b.s) : 0x7fffffff};
+                for (int k = 32; turns > 0 && k < VT; k += 32) {
+                    const Stat d = part[i][lane + k];
+                    if (d.m > -INFINITY) c = better(c, {d.m, __float_as_int(d.s)});
                 }
+                c = warp_best(c);
+                b = {c.v, __int_as_float(c.i)};
+            } else {
+                for (int k = 32; turns > 0 && k < VT; k += 32) b = merge(b, part[i][lane + k], it);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    b = merge(b, {__shfl_xor_sync(0xffffffffu, b.m, o), __shfl_xor_sync(0xffffffffu, b.s, o)}, it);
             }
-            store_cluster(smem_u32(&all[parity][i][rank]), to, __float_as_uint(a.m), __float_as_uint(a.s));
+            if (lane < CS)
+                store_cluster(smem_u32(&all[parity][i][rank]), lane, __float_as_uint(b.m), __float_as_uint(b.s));
         }
         // A batch's buffer is written again two batches on: behind the next batch's barrier, which every CTA
         // reaches after it has read this one.
