@@ -167,18 +167,19 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-inline EncodeTiledFn encode_fn(std::string* err) {
-    static void* found = nullptr;  // the driver's entry point: one a process, the same whoever stores it
-    if (found) return reinterpret_cast<EncodeTiledFn>(found);
+inline EncodeTiledFn find_encode_fn() {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult qr;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
-        qr != cudaDriverEntryPointSuccess || !f) {
-        if (err) *err = "cuTensorMapEncodeTiled is not available from the driver";
+        qr != cudaDriverEntryPointSuccess)
         return nullptr;
-    }
-    found = f;
     return reinterpret_cast<EncodeTiledFn>(f);
+}
+// The driver's entry point, looked up once a process.
+inline EncodeTiledFn encode_fn(std::string* err) {
+    static const EncodeTiledFn found = find_encode_fn();
+    if (!found && err) *err = "cuTensorMapEncodeTiled is not available from the driver";
+    return found;
 }
 
 // The cache as {d, page, k, n_pages} with boxes of one row span by box_rows.
