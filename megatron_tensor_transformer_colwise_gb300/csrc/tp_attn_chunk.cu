@@ -10,15 +10,20 @@
 // shares of 128-key blocks (tp_paged_index.h), one persistent CTA an SM:
 //   warp 0      TMA: Q of a tile as one box {64, heads, shards, tokens}, K blocks
 //               as one box a page and 64 columns.
-//   warp 11     TMA: V blocks.  A copy takes its issuing thread about 150
-//               cycles here (its operands go to uniform registers one by one),
-//               so K and V have a thread each; page numbers are read 32 at a
-//               time, a window ahead.
 //   warp 1      TMEM owner and S issuer: S = Q K^T (tcgen05, fp32) into three
 //               TMEM buffers.
 //   warp 2      PV issuer: O += P V, P from tensor memory.
-//   warps 3..10 softmax, two warps a TMEM lane quadrant, half of a block's keys
+//   warp 3      TMA: V blocks.  A copy takes its issuing thread about 150
+//               cycles here (its operands go to uniform registers one by one),
+//               so K and V have a thread each; page numbers are read 32 at a
+//               time, a window ahead.
+//   warps 4..11 softmax, two warps a TMEM lane quadrant, half of a block's keys
 //               each; a tile's outputs leave after the next tile's first block.
+// From an 8-bit cache the codes of K and V come through a ring of their own
+// (warp 0 loads both), and warps 12..15 write them out as bf16, which holds
+// every code, in the layout the products read.  The scales stay outside the
+// products, as in tp_attn_paged.cu: K's multiplies S's columns, V's the columns
+// of P before P is rounded to bf16.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,7 +41,6 @@ using namespace tpk;
 constexpr int QB = 128;          // TMEM lanes: rows of a tile, at most
 constexpr int KB = 128;          // keys of a block
 constexpr int NS = 3;            // S buffers in TMEM
-constexpr int NT = 384;          // threads
 constexpr int BOX = 128 * 128;   // 128 rows of one swizzle span (64 bf16)
 constexpr float RESCALE = 8.0f;  // log2 of the growth of P before O is rescaled
 
@@ -53,17 +57,28 @@ enum {
     B_O_FULL = B_P_FULL + NS,
     B_O_EMPTY = B_O_FULL + 1,
     B_DRAIN = B_O_EMPTY + 1,     // x2
-    NUM_BARS = B_DRAIN + 2
+    B_R_FULL = B_DRAIN + 2,      // x NRAW: codes of a K or V block
+    B_R_EMPTY = B_R_FULL + 3,
+    B_SC_FULL = B_R_EMPTY + 3,   // x NSC: scales of a block
+    NUM_BARS = B_SC_FULL + 4
 };
+constexpr int NRAW = 3;  // stages of the ring of codes
+constexpr int NSC = 4;   // blocks whose scales are held (a block's codes are loaded once PV of the fourth before it is done)
 
 // What the epilogue of a segment needs once its walk has moved on.
 struct Done {
     int row0, g, rows, where;  // row0: the tile's first token's row; where: -1 the output, else the CTA's slot
 };
 
-template <int D_>
+template <int D_, bool E4M3_>
 struct Lay {
     static constexpr int D = D_;
+    static constexpr bool E4M3 = E4M3_;
+    static constexpr int NT = E4M3 ? 512 : 384;
+    static constexpr int KRING = E4M3 ? NRAW : 2;   // stages that the producers fill
+    static constexpr int FULL = E4M3 ? 4 : 1;       // arrivals that fill an operand stage: converting warps, or the copy
+    static constexpr int CODES = KB * D;            // bytes of a block's codes
+    static constexpr int RAW = E4M3 ? CODES + 2 * KB * 4 : 0;  // and, behind K's, the block's scales of K and V
     static constexpr int NSEG = D / 64;
     static constexpr int TILE = KB * D * 2;  // Q, K or V
     static constexpr int Q_OFF = 0;
@@ -72,7 +87,9 @@ struct Lay {
     static constexpr int DC = D / 2;         // O columns of a softmax warp
     static constexpr int STG_ROW = DC * 2;            // bytes of a staged output row
     static constexpr int STG_OFF = V_OFF + 2 * TILE;  // 32 rows a softmax warp
-    static constexpr int XCH_OFF = STG_OFF + 8 * 32 * STG_ROW;  // [7][128] fp32: maxima x 2 x 2, sums x 2, references
+    static constexpr int RAW_OFF = STG_OFF + (E4M3 ? 0 : 8 * 32 * STG_ROW);  // no room for staged outputs beside the codes
+    static constexpr int SC_OFF = RAW_OFF + NRAW * RAW;
+    static constexpr int XCH_OFF = SC_OFF + (E4M3 ? NSC * 2 * KB * 4 : 0);  // [7][128] fp32: maxima x 2 x 2, sums x 2, references
     static constexpr int BAR_OFF = XCH_OFF + 7 * QB * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * NUM_BARS + 16;
     static constexpr int WALK_OFF = SCAN_OFF + 8 * (NT / 32 + 2);  // the share's beginning, one walk a warp, the producers' walks ahead
@@ -85,6 +102,7 @@ struct Lay {
 };
 
 struct Params {
+    const float *k_scale, *v_scale;
     CUtensorMap map_q;         // the projection buffer as {d, heads a shard, shards, tokens}
     CUtensorMap map_k, map_v;  // the cache as {d, page, k, n_pages}
     CUtensorMap map_o;         // O as {d, heads, tokens}, boxes of 32 rows of a KV head and half their columns
@@ -103,8 +121,9 @@ struct Params {
 };
 
 template <class L>
-__global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant__ Params p) {
-    constexpr int D = L::D, NSEG = L::NSEG;
+__global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_constant__ Params p) {
+    constexpr int D = L::D, NSEG = L::NSEG, NT = L::NT;
+    constexpr bool E4M3 = L::E4M3;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -121,9 +140,9 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
         mbar_init(bar(B_Q_FULL), 1);
         mbar_init(bar(B_Q_EMPTY), 1);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar(B_K_FULL + s), 1);
+            mbar_init(bar(B_K_FULL + s), L::FULL);
             mbar_init(bar(B_K_EMPTY + s), 1);
-            mbar_init(bar(B_V_FULL + s), 1);
+            mbar_init(bar(B_V_FULL + s), L::FULL);
             mbar_init(bar(B_V_EMPTY + s), 1);
         }
         for (int s = 0; s < NS; ++s) {
@@ -135,6 +154,11 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
         mbar_init(bar(B_O_EMPTY), 8);
         mbar_init(bar(B_DRAIN), 1);
         mbar_init(bar(B_DRAIN + 1), 1);
+        for (int s = 0; s < NRAW; ++s) {
+            mbar_init(bar(B_R_FULL + s), 1);
+            mbar_init(bar(B_R_EMPTY + s), 4);
+        }
+        for (int s = 0; s < NSC; ++s) mbar_init(bar(B_SC_FULL + s), 4);
         *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_desc(&p.map_q);
@@ -163,14 +187,15 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
         __syncwarp();
     };
 
-    if (warp == 0 || warp == 11) {
+    if (warp == 0 || (warp == 3 && !E4M3)) {
         // ---------------------------------------------------------- TMA producers
-        const bool is_v = warp == 11;
+        const bool is_v = warp == 3;
         const int log2 = p.v.page_log2, per_block = KB / p.box_rows;
         // Page numbers of two windows of 32 pages: page i of the sequence at ring[i - first page of the segment, mod 64].
         int* ring = reinterpret_cast<int*>(gbase + L::PAGE_OFF) + (is_v ? 64 : 0);
-        const CUtensorMap* map = is_v ? &p.map_v : &p.map_k;
-        const uint32_t dst0 = is_v ? sV : sK, full0 = bar(is_v ? B_V_FULL : B_K_FULL), empty0 = bar(is_v ? B_V_EMPTY : B_K_EMPTY);
+        const uint32_t dst0 = E4M3 ? base + L::RAW_OFF : is_v ? sV : sK;
+        const uint32_t full0 = bar(E4M3 ? B_R_FULL : is_v ? B_V_FULL : B_K_FULL);
+        const uint32_t empty0 = bar(E4M3 ? B_R_EMPTY : is_v ? B_V_EMPTY : B_K_EMPTY);
         int4 cut = make_int4(0, 0, 0, 0);  // the tile that begins here and goes on in the next CTAs
         uint32_t n = 0, li = 0;            // blocks and Q tiles issued
         bool ok = true;
@@ -222,46 +247,83 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                 cut = make_int4(w.q.row0 + w.tile * p.tile_tok, g, tile_tokens(w.q, tiling, w.tile) * p.group,
                                 share_of(at + w.nkb - 1, share.per) - static_cast<int>(blockIdx.x) + 1);
             }
-            for (int i = 0, at = 0; i < seg; ++i, ++n, at += per_block) {
+            for (int i = 0, at = 0; i < seg && ok; ++i, at += per_block) {
                 if ((at & 31) == 0) {  // a window begins: the one behind it takes the other half of the ring
                     ring[(at + 32 + lane) & 63] = next;
                     if (i + 32 / per_block < seg) next = page_at(w, page0 + at + 64 + lane);
                     __syncwarp();
                 }
-                const uint32_t st = n & 1;
-                ok = __all_sync(0xffffffffu, wait(empty0 + 8 * st, ((n >> 1) & 1u) ^ 1u));
-                if (!ok) break;
-                if (lane == 0) {
-                    const uint32_t full = full0 + 8 * st, dst = dst0 + st * L::TILE;
-                    mbar_arrive_expect_tx(full, L::TILE);
+#pragma unroll 1
+                for (int kind = 0; kind < (E4M3 ? 2 : 1); ++kind, ++n) {  // 8 bits: K, then V
+                    const uint32_t st = n % L::KRING;
+                    ok = __all_sync(0xffffffffu, wait(empty0 + 8 * st, ((n / L::KRING) & 1u) ^ 1u));
+                    if (!ok) break;
+                    const uint32_t full = full0 + 8 * st;
+                    if constexpr (E4M3) {
+                        const uint32_t dst = dst0 + st * L::RAW;
+                        int scaled = 0;
+                        if (kind == 0) {  // the block's scales, a lane a box; those of no page are zeros
+                            const int page = lane < per_block ? ring[(at + lane) & 63] : -1;
+                            const uint32_t sc = dst + L::CODES + lane * p.box_rows * 4;
+                            scaled = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                            if (lane < per_block && page < 0) {
+#pragma unroll 1
+                                for (int x = 0; x < p.box_rows; x += 4) {
+                                    st_shared_v4(sc + x * 4, 0, 0, 0, 0);
+                                    st_shared_v4(sc + KB * 4 + x * 4, 0, 0, 0, 0);
+                                }
+                                fence_proxy_async_smem();
+                            }
+                            __syncwarp();
+                        }
+                        if (lane == 0) {
+                            const CUtensorMap* map = kind ? &p.map_v : &p.map_k;
+                            mbar_arrive_expect_tx(full, L::CODES + 8u * p.box_rows * scaled);
+#pragma unroll 1
+                            for (int b = 0; b < per_block; ++b) {
+                                const int page = ring[(at + b) & 63];
+                                tma_load_4d(dst + b * p.box_rows * D, map, full, 0, 0, g, page);
+                                if (kind == 0 && page >= 0) {
+                                    const long long row = paged_row(p.v, page, g, 0);
+                                    const uint32_t sc = dst + L::CODES + b * p.box_rows * 4;
+                                    bulk_load(sc, p.k_scale + row, p.box_rows * 4, full);
+                                    bulk_load(sc + KB * 4, p.v_scale + row, p.box_rows * 4, full);
+                                }
+                            }
+                        }
+                    } else if (lane == 0) {
+                        const uint32_t dst = dst0 + st * L::TILE;
+                        const CUtensorMap* map = is_v ? &p.map_v : &p.map_k;
+                        mbar_arrive_expect_tx(full, L::TILE);
 #pragma unroll 2
-                    for (int b = 0; b < per_block; ++b) {
-                        const int page = ring[(at + b) & 63];  // -1: TMA fills the box with zeros and reads nothing
+                        for (int b = 0; b < per_block; ++b) {
+                            const int page = ring[(at + b) & 63];  // -1: TMA fills the box with zeros and reads nothing
 #pragma unroll
-                        for (int c = 0; c < NSEG; ++c)
-                            tma_load_4d(dst + c * BOX + b * p.box_rows * 128, map, full, c * 64, 0, g, page);
+                            for (int c = 0; c < NSEG; ++c)
+                                tma_load_4d(dst + c * BOX + b * p.box_rows * 128, map, full, c * 64, 0, g, page);
+                        }
                     }
-                }
-                __syncwarp();
-                if (!is_v && i == 0) {  // Q behind the first K: it waits for the previous segment's last S
-                    ok = __all_sync(0xffffffffu, li == 0 || wait(bar(B_Q_EMPTY), (li - 1) & 1u));
-                    if (!ok) {
-                        ++n;
-                        break;
-                    }
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar(B_Q_FULL), p.tile_tok * p.group * D * 2);
-                        q_box(w, true);
-                    }
-                    ++li;
                     __syncwarp();
+                    if (!is_v && i == 0 && kind == 0) {  // Q behind the first K: it waits for the previous segment's last S
+                        ok = __all_sync(0xffffffffu, li == 0 || wait(bar(B_Q_EMPTY), (li - 1) & 1u));
+                        if (!ok) {
+                            ++n;
+                            break;
+                        }
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar(B_Q_FULL), p.tile_tok * p.group * D * 2);
+                            q_box(w, true);
+                        }
+                        ++li;
+                        __syncwarp();
+                    }
                 }
             }
         }
         if (!is_v && lane == 0) p.desc[blockIdx.x] = cut;
         // No copy may be in flight when the CTA's shared memory goes.
         if (!is_v && li) drain(bar(B_Q_FULL), (li - 1) & 1u);
-        for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i) drain(full0 + 8 * (i & 1), (i >> 1) & 1u);
+        for (uint32_t i = n > L::KRING ? n - L::KRING : 0; i < n; ++i) drain(full0 + 8 * (i % L::KRING), (i / L::KRING) & 1u);
     } else if (warp == 1) {
         // ---------------------------------------------------------- S issuer
         if (lane == 0) {
@@ -325,16 +387,74 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
             umma_commit(bar(B_DRAIN + 1));
             drain(bar(B_DRAIN + 1), 0);
         }
-    } else {
+    } else if (E4M3 && warp >= 12) {
+        // ---------------------------------------------------------- codes to bf16
+        // Warp wc takes 32 keys of a block.  A lane's turn is 16 codes of a key, 16 bytes read and 32 written.  The
+        // lanes of a quarter-warp take two keys, one its lower four turns and the other its upper four: reads (rows
+        // of 128 bytes) and writes (rows of 128 bytes, 16-byte pieces XOR the key's low bits) then meet no bank twice.
+        const int wc = warp - 12;
+        bool ok = true;
+        uint32_t n = 0, gb = 0;
+        for (; w.left > 0 && ok; move_on()) {
+            const int seg = w.segment();
+            int left = w.keys - w.kb * KB;  // keys behind the block's first that exist
+            for (int i = 0; i < seg && ok; ++i, ++gb, left -= KB) {
+#pragma unroll 1
+                for (int kind = 0; kind < 2 && ok; ++kind, ++n) {  // K, then V
+                    const uint32_t st = n % NRAW, to = gb & 1u;
+                    ok = wait(bar(B_R_FULL + st), (n / NRAW) & 1u) &&
+                         wait(bar((kind ? B_V_EMPTY : B_K_EMPTY) + to), ((gb >> 1) & 1u) ^ 1u);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t src = base + L::RAW_OFF + st * L::RAW, dst = (kind ? sV : sK) + to * L::TILE;
+                    constexpr int TURNS = D / 16;  // of a key
+#pragma unroll 2
+                    for (int x = 0; x < TURNS; ++x) {
+                        const int row = wc * 32 + (D == 128 ? (x >> 1) * 8 : x * 8) + (lane >> 2);
+                        const int c = D == 128 ? (lane & 3) + 4 * (((lane >> 2) ^ x) & 1) : lane & 3;
+                        const uint4 u = ld_shared_v4(src + row * D + c * 16);
+                        const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t out[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 f = e4m3x2_float2(in[e >> 1] >> (16 * (e & 1)));
+                            out[e] = pack_bf16x2(f.x, f.y);
+                        }
+                        // Keys of V past the sequence's end are whatever the page holds, and 0 * NaN is NaN.
+                        if (kind && row >= left)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) out[e] = 0;
+                        const uint32_t at = dst + (c >> 2) * BOX + row * 128, piece = (c & 3) * 2, sw = row & 7;
+                        st_shared_v4(at + ((piece ^ sw) << 4), out[0], out[1], out[2], out[3]);
+                        st_shared_v4(at + (((piece + 1) ^ sw) << 4), out[4], out[5], out[6], out[7]);
+                    }
+                    if (kind == 0) {  // 2 x 32 scales a warp; zeros past the sequence's end, where P is 0
+                        const bool in = wc * 32 + lane < left;
+                        const uint32_t sc = base + L::SC_OFF + (gb % NSC) * (2 * KB * 4) + (wc * 32 + lane) * 4;
+                        const uint32_t from = src + L::CODES + (wc * 32 + lane) * 4;
+                        st_shared_f32(sc, in ? ld_shared_f32(from) : 0.0f);
+                        st_shared_f32(sc + KB * 4, in ? ld_shared_f32(from + KB * 4) : 0.0f);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(B_R_EMPTY + st));
+                        if (kind == 0) mbar_arrive(bar(B_SC_FULL + gb % NSC));
+                        mbar_arrive(bar((kind ? B_V_FULL : B_K_FULL) + to));
+                    }
+                }
+            }
+        }
+    } else if (warp >= 4) {
         // ---------------------------------------------------------- softmax / epilogue
         // Two warps share a TMEM lane quadrant: half hf takes keys [64 hf, 64 hf + 64) of a block and O columns
         // [hf D / 2, + D / 2).  They agree on a row's maximum through shared memory once a block.
         constexpr int KC = KB / 2, DC = L::DC;
-        const int q = warp & 3, hf = (warp - 3) >> 2;
+        const int q = warp & 3, hf = (warp - 4) >> 2;
         const int r = q * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
         float* xch = reinterpret_cast<float*>(gbase + L::XCH_OFF);
-        Done* done = reinterpret_cast<Done*>(gbase + L::DONE_OFF) + (warp - 3);
+        Done* done = reinterpret_cast<Done*>(gbase + L::DONE_OFF) + (warp - 4);
         // Failures pass through here before the warps act on them, so the two halves of a quadrant leave together.
         auto pair_all = [&](bool v) -> bool { return named_bar_and(1u + static_cast<uint32_t>(q), 64u, v); };
         bool bad = false;  // a wait gave up: acted on at the next pair_all, with the other half
@@ -372,9 +492,9 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
             __nv_bfloat16* y = p.o + (static_cast<long long>(e.row0 + tok) * p.heads + e.g * p.group + r - tok * p.group) * D + hf * DC;
             // A quadrant of whole tokens, all of them the sequence's, leaves by one TMA store through shared memory
             // (a warp's own 16-byte stores touch 32 lines each); others row by row.
-            const bool boxed = p.o_boxes && q * 32 + 32 <= e.rows;
+            const bool boxed = !E4M3 && p.o_boxes && q * 32 + 32 <= e.rows;
             constexpr int PIECES = L::STG_ROW / 16;  // 8 or 4
-            const uint32_t stg = base + L::STG_OFF + static_cast<uint32_t>((warp - 3) * 32) * L::STG_ROW;
+            const uint32_t stg = base + L::STG_OFF + static_cast<uint32_t>((warp - 4) * 32) * L::STG_ROW;
             const uint32_t sw = PIECES == 8 ? lane & 7 : (lane >> 1) & 3;
             if (boxed) {
                 if (lane == 0) bulk_wait_group_read0();  // the previous store has read the box
@@ -419,18 +539,19 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                 bool got = !bad && wait(bar(B_S_FULL + st), (gb / NS) & 1u);
                 // The block with the sequence's last key: rows of V behind it are whatever the page holds, and
                 // 0 * NaN is NaN.  They are cleared before P is announced.
-                if (got && left < KB && left > 0) {
+                if (!E4M3 && got && left < KB && left > 0) {
                     const uint32_t vs = gb & 1u;
                     got = wait(bar(B_V_FULL + vs), (gb >> 1) & 1u);
                     if (got) {
                         #pragma unroll 1
-                        for (int x = static_cast<int>(threadIdx.x) - 96; x < (KB - left) * NSEG * 8; x += 256) {
+                        for (int x = static_cast<int>(threadIdx.x) - 128; x < (KB - left) * NSEG * 8; x += 256) {
                             const int row = left + x / (NSEG * 8), c = x % (NSEG * 8);
                             st_shared_v4(sV + vs * L::TILE + (c >> 3) * BOX + row * 128 + (c & 7) * 16, 0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
                     }
                 }
+                if constexpr (E4M3) got = got && wait(bar(B_SC_FULL + gb % NSC), (gb / NSC) & 1u);
                 got = __all_sync(0xffffffffu, got);
                 uint32_t s[KC];
                 float mxp = -INFINITY;
@@ -440,6 +561,24 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
                     for (int c = 0; c < KC / 32; ++c)
                         tmem_ld32(tmem + lane_off + st * KB + hf * KC + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
                     tmem_ld_wait();
+                    if constexpr (E4M3) {  // the codes' products times their keys' scales
+                        const uint32_t sc = base + L::SC_OFF + (gb % NSC) * (2 * KB * 4) + hf * KC * 4;
+#pragma unroll
+                        for (int c = 0; c < KC; c += 4) {
+                            const uint4 f = ld_shared_v4(sc + c * 4);
+                            const uint64_t a = f2_mul(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                                      f2_pack(__uint_as_float(f.x), __uint_as_float(f.y)));
+                            const uint64_t b = f2_mul(f2_pack(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                                      f2_pack(__uint_as_float(f.z), __uint_as_float(f.w)));
+                            float x0, x1, x2, x3;
+                            f2_unpack(a, x0, x1);
+                            f2_unpack(b, x2, x3);
+                            s[c] = __float_as_uint(x0);
+                            s[c + 1] = __float_as_uint(x1);
+                            s[c + 2] = __float_as_uint(x2);
+                            s[c + 3] = __float_as_uint(x3);
+                        }
+                    }
                     if (lim < KC) {
 #pragma unroll
                         for (int c = 0; c < KC; ++c)
@@ -479,13 +618,22 @@ __global__ void __launch_bounds__(NT, 1) attn_chunk_kernel(const __grid_constant
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[e] = f2_pack(0.0f, 0.0f);
                     uint32_t pk[KC / 2];
+                    const uint32_t vsc = base + L::SC_OFF + (gb % NSC) * (2 * KB * 4) + (KB + hf * KC) * 4;
 #pragma unroll
-                    for (int c = 0; c < KC / 2; ++c) {
-                        float x0, x1;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), x0, x1);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        acc[c & 3] = f2_add(acc[c & 3], f2_pack(p0, p1));
-                        pk[c] = pack_bf16x2(p0, p1);
+                    for (int c = 0; c < KC / 2; c += 2) {
+                        uint4 vf = make_uint4(0, 0, 0, 0);
+                        if constexpr (E4M3) vf = ld_shared_v4(vsc + c * 8);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float x0, x1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * (c + h)]), __uint_as_float(s[2 * (c + h) + 1])), scale2, neg2), x0, x1);
+                            uint64_t pp = f2_pack(ex2(x0), ex2(x1));
+                            acc[(c + h) & 3] = f2_add(acc[(c + h) & 3], pp);
+                            if constexpr (E4M3)  // times V's scales
+                                pp = f2_mul(pp, f2_pack(__uint_as_float(h ? vf.z : vf.x), __uint_as_float(h ? vf.w : vf.y)));
+                            f2_unpack(pp, x0, x1);
+                            pk[c + h] = pack_bf16x2(x0, x1);
+                        }
                     }
                     float sum8[8];
 #pragma unroll
@@ -559,10 +707,12 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
     const int grid = tpi::device_sm_count();
     p.box_rows = a.page_size;
     int rc;
-    if ((rc = tpi::encode_cache(&p.map_k, a, a.K, 128, p.box_rows, err)) ||
-        (rc = tpi::encode_cache(&p.map_v, a, a.V, 128, p.box_rows, err)))
+    if ((rc = tpi::encode_cache(&p.map_k, a, a.K, L::E4M3 ? 0 : 128, p.box_rows, err)) ||
+        (rc = tpi::encode_cache(&p.map_v, a, a.V, L::E4M3 ? 0 : 128, p.box_rows, err)))
         return rc;
     p.v = tpi::paged_view(a);
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
     p.o = static_cast<__nv_bfloat16*>(O);
     p.heads = a.heads;
     p.group = a.heads / a.kv_heads;
@@ -624,7 +774,7 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
         configured[dev] = true;
     }
     rc = tpi::launched("chunk attention launch",
-                       tpi::launch_pdl(attn_chunk_kernel<L>, dim3(grid), dim3(NT), L::SMEM, stream, p), err);
+                       tpi::launch_pdl(attn_chunk_kernel<L>, dim3(grid), dim3(L::NT), L::SMEM, stream, p), err);
     if (rc) return rc;
     return tpi::attn_join_launch(a, QB, O, w, s, grid, zero_rest, stream, err);
 }
@@ -634,8 +784,11 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
 namespace tpi {
 
 int attn_chunk_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest, cudaStream_t stream, std::string* err) {
-    return a.head_dim == 128 ? launch<Lay<128>>(a, O, scratch, zero_rest, stream, err)
-                             : launch<Lay<64>>(a, O, scratch, zero_rest, stream, err);
+    if (a.head_dim == 128)
+        return a.e4m3 ? launch<Lay<128, true>>(a, O, scratch, zero_rest, stream, err)
+                      : launch<Lay<128, false>>(a, O, scratch, zero_rest, stream, err);
+    return a.e4m3 ? launch<Lay<64, true>>(a, O, scratch, zero_rest, stream, err)
+                  : launch<Lay<64, false>>(a, O, scratch, zero_rest, stream, err);
 }
 
 }  // namespace tpi

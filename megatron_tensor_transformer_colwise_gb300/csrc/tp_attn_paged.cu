@@ -116,13 +116,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes (low 16 bits) as two fp16: exact, NaN stays NaN.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -711,7 +704,7 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
     // of 16.  More: tiles of 128 on tcgen05.
     const int group = a.heads / a.kv_heads;
     const int64_t most = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
-    if (group > R || (most * group > R && !a.e4m3))
+    if (most * group > R)
         return attn_chunk_launch(a, O, scratch, zero_rest, stream, err);
     if (a.head_dim == 128)
         return a.e4m3 ? launch_few<Cfg<128, true, 8, 4>>(a, O, scratch, zero_rest, stream, err)

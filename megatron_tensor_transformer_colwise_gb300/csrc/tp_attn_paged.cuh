@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <string>
@@ -36,6 +37,23 @@ __device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* map, int32
                      reinterpret_cast<uint64_t>(map)),
                  "r"(c0), "r"(c1), "r"(c2), "r"(c3)
                  : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Two e4m3 codes (low 16 bits), exactly; NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3x2_float2(uint32_t codes) {
+    const uint32_t h = e4m3x2_f16x2(codes);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // Contiguous copy to shared memory; addresses and size multiples of 16 bytes.
@@ -182,7 +200,8 @@ inline EncodeTiledFn encode_fn(std::string* err) {
     return found;
 }
 
-// The cache as {d, page, k, n_pages} with boxes of one row span by box_rows.
+// The cache as {d, page, k, n_pages} with boxes of `span` bytes of a row (swizzled over that span) by box_rows;
+// span 0: whole rows, as they are.
 inline int encode_cache(CUtensorMap* map, const PagedArgs& a, const void* base, int span, int box_rows, std::string* err) {
     EncodeTiledFn encode = encode_fn(err);
     if (!encode) return TP_ERR_CUDA;
@@ -190,11 +209,13 @@ inline int encode_cache(CUtensorMap* map, const PagedArgs& a, const void* base, 
     const cuuint64_t d = static_cast<cuuint64_t>(a.head_dim), pg = static_cast<cuuint64_t>(a.page_size);
     const cuuint64_t dims[4] = {d, pg, static_cast<cuuint64_t>(a.kv_heads), static_cast<cuuint64_t>(a.n_pages)};
     const cuuint64_t strides[3] = {d * elem, d * pg * elem, d * pg * a.kv_heads * elem};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(span / elem), static_cast<cuuint32_t>(box_rows), 1, 1};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(span ? span / elem : d), static_cast<cuuint32_t>(box_rows), 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUresult r = encode(map, a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              span == 0    ? CU_TENSOR_MAP_SWIZZLE_NONE
+                              : span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                            : CU_TENSOR_MAP_SWIZZLE_64B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         if (err) *err = "cuTensorMapEncodeTiled (cache) failed: " + std::to_string(static_cast<int>(r));
