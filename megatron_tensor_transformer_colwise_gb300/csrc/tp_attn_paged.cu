@@ -17,7 +17,7 @@
 // persistent CTA an SM:
 //   warp 8      producer: TMA boxes of one page each into a ring of key
 //               blocks; the page numbers of 32 pages are read at a time.
-//   warps 0..7  consumers, 16 keys of a block each: S = Q K^T and O += P V by
+//   warps 0..7  consumers, 16 or 32 keys of a block each: S = Q K^T and O += P V by
 //               mma.sync m16n8k16 (rows = the tile's 16 query rows, P straight
 //               from S's registers), a running maximum of their own; at a
 //               tile's end the eight are merged in shared memory.
@@ -44,15 +44,16 @@ constexpr int NW = 8;        // consumer warps
 constexpr int NT = 32 * (NW + 1);
 constexpr float RESCALE = 8.0f;  // log2 of the growth of a weight before the sums are rescaled
 
-// Head dimension, element type, warps that share a key block (16 keys each;
-// with 4 the two halves of the warps take alternate blocks), ring stages.
-template <int D_, bool E4M3_, int WPB_, int NST_>
+// Head dimension, element type, warps that share a key block (with 4 the two
+// halves of the warps take alternate blocks), groups of 16 keys that a warp
+// takes of a block, ring stages.
+template <int D_, bool E4M3_, int WPB_, int NG_, int NST_>
 struct Cfg {
-    static constexpr int D = D_, WPB = WPB_, NST = NST_;
+    static constexpr int D = D_, WPB = WPB_, NG = NG_, NST = NST_;
     static constexpr bool E4M3 = E4M3_;
-    static constexpr int LOG2_KB = WPB == 8 ? 7 : 6;
+    static constexpr int LOG2_KB = WPB * NG == 8 ? 7 : 6;
     static constexpr int KB = 1 << LOG2_KB;
-    static_assert(KB == 16 * WPB, "keys of a block");
+    static_assert(KB == 16 * WPB * NG, "keys of a block");
     static constexpr int ROW = E4M3 ? D : 2 * D;       // bytes of a cached row
     static constexpr int SEG = ROW < 128 ? ROW : 128;  // bytes of a TMA box row (one swizzle span)
     static constexpr int NSEG = ROW / SEG;
@@ -132,7 +133,7 @@ __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) {
 
 template <class C>
 __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__ Params p) {
-    constexpr int D = C::D, KB = C::KB, NST = C::NST;
+    constexpr int D = C::D, KB = C::KB, NST = C::NST, NG = C::NG;
     constexpr bool E4M3 = C::E4M3;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_word;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
     } else {
         // ------------------------------------------------------ consumers
         const int r0 = lane >> 2, t = lane & 3;  // fragment rows r0 and r0 + 8, column pair t
-        const int wk = warp % C::WPB;            // the warp's 16 keys of a block
+        const int wk = warp % C::WPB;            // the warp's part of a block's keys
         float* xm = reinterpret_cast<float*>(gbase + C::XM_OFF);
         float* xl = xm + NW * R;
         float* acc_s = reinterpret_cast<float*>(gbase + C::ACC_OFF);
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                 return p.qkv + static_cast<long long>(q.row0 + tok0 + tok) * p.ld_qkv +
                        static_cast<long long>(j / p.heads_per_shard) * p.shard_w + (j % p.heads_per_shard) * D;
             };
+            const bool upper = rows > 8;
             int lim[2];
             uint32_t qf[D / 16][4];
             float row_scale[2] = {p.scale_log2, p.scale_log2};
@@ -341,58 +343,69 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 const uint32_t sk = base + st * C::STAGE, sv = sk + C::TILE;
-                const int key0 = (kb0 + i) * KB + wk * 16;
-                float s[2][4] = {};
-                if constexpr (!E4M3) {
-                    // Matrices (keys 0-7, 8-15) x (d 0-7, 8-15) of a step: lanes 0-7 and 16-23 address keys
-                    // 0-7 and 8-15 of the step's first eight d, lanes 8-15 and 24-31 of its second eight.
-                    const uint32_t kr = wk * 16 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+                const int wk0 = wk * (16 * NG), key0 = (kb0 + i) * KB + wk0;  // the warp's keys of the block
+                float s[NG][2][4] = {};
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        uint32_t b[4];
-                        ldsm4(sk + (ks >> 2) * (KB * 128) + swz<128>(kr, (ks & 3) * 2 + kc), b);
-                        mma<false>(s[0], qf[ks], b[0], b[1]);
-                        mma<false>(s[1], qf[ks], b[2], b[3]);
-                    }
-                } else {
+                for (int gr = 0; gr < NG; ++gr) {
+                    if constexpr (!E4M3) {
+                        // Matrices (keys 0-7, 8-15) x (d 0-7, 8-15) of a step: lanes 0-7 and 16-23 address keys
+                        // 0-7 and 8-15 of the step's first eight d, lanes 8-15 and 24-31 of its second eight.
+                        const uint32_t kr = wk0 + gr * 16 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                        for (int hh = 0; hh < D / 64; ++hh) {
-                            const uint4 u = ld_shared_v4(sk + swz<C::SEG>(wk * 16 + nt * 8 + r0, hh * 4 + t));
-                            const uint32_t c[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                mma<true>(s[nt], qf[hh * 4 + j], e4m3x2_f16x2(c[j]), e4m3x2_f16x2(c[j] >> 16));
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            uint32_t b[4];
+                            ldsm4(sk + (ks >> 2) * (KB * 128) + swz<128>(kr, (ks & 3) * 2 + kc), b);
+                            mma<false>(s[gr][0], qf[ks], b[0], b[1]);
+                            mma<false>(s[gr][1], qf[ks], b[2], b[3]);
                         }
+                    } else {
+#pragma unroll
+                        for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+                            for (int nt = 0; nt < 2; ++nt) {
+                                const uint4 u = ld_shared_v4(sk + swz<C::SEG>(wk0 + gr * 16 + nt * 8 + r0, hh * 4 + t));
+                                const uint32_t c[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    mma<true>(s[gr][nt], qf[hh * 4 + j], e4m3x2_f16x2(c[j]), e4m3x2_f16x2(c[j] >> 16));
+                            }
+                    }
                 }
                 // Scores in the exp2 domain, masked; lane t has keys 2t, 2t + 1 of each eight.
-                float lv[2][2] = {};
+                float lv[NG][2][2] = {};
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    float ks[2] = {1.0f, 1.0f};
-                    if constexpr (E4M3) {
-                        const float* sc = reinterpret_cast<const float*>(gbase + C::SC_OFF + st * C::SCALES) + wk * 16 +
-                                          nt * 8 + 2 * t;
-                        const float2 k2 = *reinterpret_cast<const float2*>(sc);
-                        const float2 v2 = *reinterpret_cast<const float2*>(sc + KB);
-                        ks[0] = k2.x;
-                        ks[1] = k2.y;
-                        lv[nt][0] = __log2f(v2.x);
-                        lv[nt][1] = __log2f(v2.y);
-                    }
+                for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + nt * 8 + 2 * t + (e & 1);
-                        const float x = s[nt][e] * (ks[e & 1] * row_scale[e >> 1]);
-                        s[nt][e] = key < lim[e >> 1] ? x : -INFINITY;
+                    for (int nt = 0; nt < 2; ++nt) {
+                        float ks[2] = {1.0f, 1.0f};
+                        if constexpr (E4M3) {
+                            const float* sc = reinterpret_cast<const float*>(gbase + C::SC_OFF + st * C::SCALES) + wk0 +
+                                              gr * 16 + nt * 8 + 2 * t;
+                            const float2 k2 = *reinterpret_cast<const float2*>(sc);
+                            const float2 v2 = *reinterpret_cast<const float2*>(sc + KB);
+                            ks[0] = k2.x;
+                            ks[1] = k2.y;
+                            lv[gr][nt][0] = __log2f(v2.x);
+                            lv[gr][nt][1] = __log2f(v2.y);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + gr * 16 + nt * 8 + 2 * t + (e & 1);
+                            const float x = s[gr][nt][e] * (ks[e & 1] * row_scale[e >> 1]);
+                            s[gr][nt][e] = key < lim[e >> 1] ? x : -INFINITY;
+                        }
                     }
-                }
-                uint32_t pa[4];
+                uint32_t pa[NG][4] = {};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float x[4] = {s[0][2 * h], s[0][2 * h + 1], s[1][2 * h], s[1][2 * h + 1]};
-                    float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                    if (h == 1 && !upper) break;  // no query in the tile's rows 8..15
+                    constexpr int NX = 4 * NG;
+                    float x[NX];
+#pragma unroll
+                    for (int e = 0; e < NX; ++e) x[e] = s[e >> 2][(e >> 1) & 1][2 * h + (e & 1)];
+                    float mx = x[0];
+#pragma unroll
+                    for (int e = 1; e < NX; ++e) mx = fmaxf(mx, x[e]);
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     bool move = mx > m[h] + RESCALE;
@@ -402,18 +415,23 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                         m[h] = mx;
                     }
                     const float ref = m[h] == -INFINITY ? 0.0f : m[h];
-                    float pr[4];
+                    float pr[NX], sum = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) pr[e] = ex2(x[e] - ref);
-                    l[h] = l[h] * alpha + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
+                    for (int e = 0; e < NX; ++e) {
+                        pr[e] = ex2(x[e] - ref);
+                        sum += pr[e];
+                    }
+                    l[h] = l[h] * alpha + sum;
                     if constexpr (E4M3) {
                         // Weights 2^(x + log2 vs) against their own largest, which stands for 2^15: fp16's range
                         // whatever the scales.  A weight is rounded to 2^-11 of itself, or to 2^-25 where
                         // it is below fp16's normal range, 2^-40 of the largest.
-                        float y[4];
+                        float y[NX];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = x[e] == -INFINITY ? -INFINITY : x[e] + lv[e >> 1][e & 1];
-                        float my = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                        for (int e = 0; e < NX; ++e) y[e] = x[e] == -INFINITY ? -INFINITY : x[e] + lv[e >> 2][(e >> 1) & 1][e & 1];
+                        float my = y[0];
+#pragma unroll
+                        for (int e = 1; e < NX; ++e) my = fmaxf(my, y[e]);
                         my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 1));
                         my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 2));
                         move = my > mv[h];
@@ -424,7 +442,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                         }
                         const float rv = (mv[h] == -INFINITY ? 0.0f : mv[h]) - 15.0f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) pr[e] = ex2(y[e] - rv);
+                        for (int e = 0; e < NX; ++e) pr[e] = ex2(y[e] - rv);
                     }
                     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -433,61 +451,63 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                             o[c][2 * h + 1] *= alpha;
                         }
                     }
-                    if constexpr (E4M3) {
-                        pa[h] = pack_f16x2(pr[0], pr[1]);
-                        pa[h + 2] = pack_f16x2(pr[2], pr[3]);
-                    } else {
-                        pa[h] = pack_bf16x2(pr[0], pr[1]);
-                        pa[h + 2] = pack_bf16x2(pr[2], pr[3]);
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) {
+                        pa[gr][h] = E4M3 ? pack_f16x2(pr[4 * gr], pr[4 * gr + 1]) : pack_bf16x2(pr[4 * gr], pr[4 * gr + 1]);
+                        pa[gr][h + 2] = E4M3 ? pack_f16x2(pr[4 * gr + 2], pr[4 * gr + 3]) : pack_bf16x2(pr[4 * gr + 2], pr[4 * gr + 3]);
                     }
                 }
                 // O += P V.  Rows of V past the sequence's keys are whatever the page holds: cleared, since
                 // 0 * NaN is NaN.  `live` masks the halves of a register that holds keys 2t, 2t + 1 (+ 8).
-                uint32_t live[2] = {0xffffffffu, 0xffffffffu};
-                const bool tail = key0 + 16 > keys;
-                if (tail) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int key = key0 + h * 8 + 2 * t;
-                        live[h] = (key < keys ? 0xffffu : 0u) | (key + 1 < keys ? 0xffff0000u : 0u);
-                    }
-                }
-                // Matrices (keys 0-7, 8-15) x two neighbouring eights of 16-bit columns.
-                const uint32_t vr = wk * 16 + (lane & 15), vc = lane >> 4;
-                if constexpr (!E4M3) {
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t b[4];
-                        ldsm4_t(sv + (c >> 2) * (KB * 128) + swz<128>(vr, (c & 3) * 2 + vc), b);
-                        if (tail) {
-                            b[0] &= live[0];
-                            b[1] &= live[1];
-                            b[2] &= live[0];
-                            b[3] &= live[1];
-                        }
-                        mma<false>(o[2 * c], pa, b[0], b[1]);
-                        mma<false>(o[2 * c + 1], pa, b[2], b[3]);
-                    }
-                } else {
-                    // A 16-bit column is two codes, d and d + 1: a register holds them for two keys.  Even and
-                    // odd d go to two products: o[2 c'] has the even d of 16, o[2 c' + 1] the odd.
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t b[4];
-                        ldsm4_t(sv + swz<C::SEG>(vr, c * 2 + vc), b);
-                        if (tail) {
-                            b[0] &= live[0];
-                            b[1] &= live[1];
-                            b[2] &= live[0];
-                            b[3] &= live[1];
-                        }
+                for (int gr = 0; gr < NG; ++gr) {
+                    const int kg = key0 + gr * 16;
+                    uint32_t live[2] = {0xffffffffu, 0xffffffffu};
+                    const bool tail = kg + 16 > keys;
+                    if (tail) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t x = b[2 * h], y = b[2 * h + 1];
-                            mma<true>(o[4 * c + 2 * h], pa, e4m3x2_f16x2(__byte_perm(x, 0, 0x0020)),
-                                      e4m3x2_f16x2(__byte_perm(y, 0, 0x0020)));
-                            mma<true>(o[4 * c + 2 * h + 1], pa, e4m3x2_f16x2(__byte_perm(x, 0, 0x0031)),
-                                      e4m3x2_f16x2(__byte_perm(y, 0, 0x0031)));
+                            const int key = kg + h * 8 + 2 * t;
+                            live[h] = (key < keys ? 0xffffu : 0u) | (key + 1 < keys ? 0xffff0000u : 0u);
+                        }
+                    }
+                    // Matrices (keys 0-7, 8-15) x two neighbouring eights of 16-bit columns.
+                    const uint32_t vr = wk0 + gr * 16 + (lane & 15), vc = lane >> 4;
+                    if constexpr (!E4M3) {
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t b[4];
+                            ldsm4_t(sv + (c >> 2) * (KB * 128) + swz<128>(vr, (c & 3) * 2 + vc), b);
+                            if (tail) {
+                                b[0] &= live[0];
+                                b[1] &= live[1];
+                                b[2] &= live[0];
+                                b[3] &= live[1];
+                            }
+                            mma<false>(o[2 * c], pa[gr], b[0], b[1]);
+                            mma<false>(o[2 * c + 1], pa[gr], b[2], b[3]);
+                        }
+                    } else {
+                        // A 16-bit column is two codes, d and d + 1: a register holds them for two keys.  Even and
+                        // odd d go to two products: o[2 c'] has the even d of 16, o[2 c' + 1] the odd.
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t b[4];
+                            ldsm4_t(sv + swz<C::SEG>(vr, c * 2 + vc), b);
+                            if (tail) {
+                                b[0] &= live[0];
+                                b[1] &= live[1];
+                                b[2] &= live[0];
+                                b[3] &= live[1];
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t x = b[2 * h], y = b[2 * h + 1];
+                                mma<true>(o[4 * c + 2 * h], pa[gr], e4m3x2_f16x2(__byte_perm(x, 0, 0x0020)),
+                                          e4m3x2_f16x2(__byte_perm(y, 0, 0x0020)));
+                                mma<true>(o[4 * c + 2 * h + 1], pa[gr], e4m3x2_f16x2(__byte_perm(x, 0, 0x0031)),
+                                          e4m3x2_f16x2(__byte_perm(y, 0, 0x0031)));
+                            }
                         }
                     }
                 }
@@ -707,10 +727,10 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
     if (most * group > R)
         return attn_chunk_launch(a, O, scratch, zero_rest, stream, err);
     if (a.head_dim == 128)
-        return a.e4m3 ? launch_few<Cfg<128, true, 8, 4>>(a, O, scratch, zero_rest, stream, err)
-                      : launch_few<Cfg<128, false, 4, 4>>(a, O, scratch, zero_rest, stream, err);
-    return a.e4m3 ? launch_few<Cfg<64, true, 8, 6>>(a, O, scratch, zero_rest, stream, err)
-                  : launch_few<Cfg<64, false, 8, 4>>(a, O, scratch, zero_rest, stream, err);
+        return a.e4m3 ? launch_few<Cfg<128, true, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
+                      : launch_few<Cfg<128, false, 4, 1, 4>>(a, O, scratch, zero_rest, stream, err);
+    return a.e4m3 ? launch_few<Cfg<64, true, 4, 2, 6>>(a, O, scratch, zero_rest, stream, err)
+                  : launch_few<Cfg<64, false, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
 }
 
 }  // namespace tpi
