@@ -17,12 +17,15 @@
 // persistent CTA an SM:
 //   warp 8      producer: TMA boxes of one page each into a ring of key
 //               blocks; the page numbers of 32 pages are read at a time.
-//   warps 0..7  consumers, 16 or 32 keys of a block each: S = Q K^T and O += P V by
-//               mma.sync m16n8k16 (rows = the tile's 16 query rows, P straight
-//               from S's registers), a running maximum of their own; at a
-//               tile's end the eight are merged in shared memory.
-// mma.sync rather than tcgen05: the tile has 16 rows, tcgen05's least is 64,
-// and P would make a round trip through tensor memory.
+//   warps 0..7  consumers, 16 or 32 keys of a block each: S^T = K Q^T and
+//               O^T += V^T P^T by mma.sync m16n8k16, a running maximum of their
+//               own; at a tile's end the eight are merged in shared memory.
+// The keys (and d) are the products' 16 rows and the query rows their 8 columns:
+// single tokens of 8 heads or fewer then waste no half of a product, which
+// matters at mma.sync's 1000 multiply-adds a clock and SM.  P^T goes from S^T's
+// registers to the second product's operand by movmatrix.  mma.sync rather than
+// tcgen05, whose tile has 64 rows at least and whose P makes a round trip
+// through tensor memory.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,17 +42,16 @@ using namespace tpk;
 using tpi::launched;
 using tpi::Scratch;
 
-constexpr int R = 16;        // query rows of a tile, at most
-constexpr int NW = 8;        // consumer warps
-constexpr int NT = 32 * (NW + 1);
+constexpr int R = 16;        // query rows of a tile, at most (8 for NB = 1): rows of a slot
 constexpr float RESCALE = 8.0f;  // log2 of the growth of a weight before the sums are rescaled
 
-// Head dimension, element type, warps that share a key block (with 4 the two
-// halves of the warps take alternate blocks), groups of 16 keys that a warp
+// Head dimension, element type, eights of query rows, consumer warps, those that share a key block
+// (the NW / WPB sets of warps take blocks in turn), groups of 16 keys that a warp
 // takes of a block, ring stages.
-template <int D_, bool E4M3_, int WPB_, int NG_, int NST_>
+template <int D_, bool E4M3_, int NB_, int NW_, int WPB_, int NG_, int NST_>
 struct Cfg {
-    static constexpr int D = D_, WPB = WPB_, NG = NG_, NST = NST_;
+    static constexpr int D = D_, NB = NB_, NW = NW_, WPB = WPB_, NG = NG_, NST = NST_;
+    static constexpr int NT = 32 * (NW + 1);
     static constexpr bool E4M3 = E4M3_;
     static constexpr int LOG2_KB = WPB * NG == 8 ? 7 : 6;
     static constexpr int KB = 1 << LOG2_KB;
@@ -63,13 +65,16 @@ struct Cfg {
     static constexpr int SC_OFF = NST * STAGE;
     static constexpr int ACC_OFF = SC_OFF + NST * SCALES;
     static constexpr int LD_ACC = D + 4;               // floats; 16-byte rows, shifted banks
-    static constexpr int XM_OFF = ACC_OFF + NW * R * LD_ACC * 4;
-    static constexpr int BAR_OFF = XM_OFF + 2 * NW * R * 4;
+    static constexpr int XM_OFF = ACC_OFF + NW * 8 * LD_ACC * 4;  // 8 rows of a tile at a time
+    static constexpr int BAR_OFF = XM_OFF + 3 * NW * R * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * 2 * NST;
     static constexpr int WALK_OFF = SCAN_OFF + 8 * (NW + 3);  // the share's beginning, then one walk a warp
     static constexpr int DATA = WALK_OFF + (NW + 2) * sizeof(TileWalk);
     static constexpr int SMEM = DATA + 1024;
     static_assert(SMEM <= 232448, "shared memory");
+    // A set of warps that met a stage every second time only could find its barrier two phases behind, which
+    // reads as done.
+    static_assert(NST % (NW / WPB) == 0, "every stage belongs to one set of warps");
 };
 
 struct Params {
@@ -104,17 +109,24 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
 template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (F16)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit elements, two neighbours of a row a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -132,8 +144,8 @@ __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__ Params p) {
-    constexpr int D = C::D, KB = C::KB, NST = C::NST, NG = C::NG;
+__global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constant__ Params p) {
+    constexpr int D = C::D, KB = C::KB, NST = C::NST, NG = C::NG, NW = C::NW, NB = C::NB;
     constexpr bool E4M3 = C::E4M3;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_word;
@@ -160,7 +172,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
     pdl_wait();
     TileWalk* walks = reinterpret_cast<TileWalk*>(gbase + C::WALK_OFF);
     const Share share =  // its barriers cover the set-up above
-        find_share<NT>(p.v, tiling, reinterpret_cast<long long*>(gbase + C::SCAN_OFF), walks);
+        find_share<C::NT>(p.v, tiling, reinterpret_cast<long long*>(gbase + C::SCAN_OFF), walks);
     // Each warp walks on its own, in shared memory; lane 0 moves.
     TileWalk& w = walks[1 + warp];
     if (lane == 0) w = walks[0];
@@ -253,10 +265,13 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
         for (int i = max(0, n - NST); i < n; ++i) drain(full0 + 8 * (i % NST), (i / NST) & 1);
     } else {
         // ------------------------------------------------------ consumers
-        const int r0 = lane >> 2, t = lane & 3;  // fragment rows r0 and r0 + 8, column pair t
+        // Fragments: r0 is a key (or d) of eight, and the query row of the operand Q^T; 2t, 2t + 1 are the query
+        // rows of S^T, P^T and O^T that the lane holds.
+        const int r0 = lane >> 2, t = lane & 3;
         const int wk = warp % C::WPB;            // the warp's part of a block's keys
+        // Maxima in two buffers in turn: a warp may be at its next tile while others still read this one's.
         float* xm = reinterpret_cast<float*>(gbase + C::XM_OFF);
-        float* xl = xm + NW * R;
+        float* xl = xm + 2 * NW * R;
         float* acc_s = reinterpret_cast<float*>(gbase + C::ACC_OFF);
         bool ok = true;
         int n = 0;
@@ -266,26 +281,25 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
             const PagedSeq q = w.q;
             const int tok0 = w.tile * p.tile_tok;  // first token of the tile
             const int rows = tile_tokens(q, tiling, w.tile) * p.group;
-            // Row i of the tile: its query head's row of the buffer, and the keys it sees.
+            // Row i of the tile: its query head's row of the buffer.
             auto q_row = [&](int i) -> const __nv_bfloat16* {
                 const int tok = i / p.group, j = g * p.group + i - tok * p.group;
                 return p.qkv + static_cast<long long>(q.row0 + tok0 + tok) * p.ld_qkv +
                        static_cast<long long>(j / p.heads_per_shard) * p.shard_w + (j % p.heads_per_shard) * D;
             };
-            const bool upper = rows > 8;
-            int lim[2];
-            uint32_t qf[D / 16][4];
-            float row_scale[2] = {p.scale_log2, p.scale_log2};
+            int lim[NB][2];  // keys that row 8 nb + 2t + e sees
+            uint32_t qf[NB][D / 16][2];
+            float row_scale[NB][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = r0 + 8 * h;
-                lim[h] = i < rows ? token_keys(q, keys, tok0 + i / p.group) : 0;
+            for (int nb = 0; nb < NB; ++nb) {
+                const int i = nb * 8 + r0;
                 const __nv_bfloat16* x = i < rows ? q_row(i) : nullptr;
+                float scale = p.scale_log2;
                 if constexpr (!E4M3) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        qf[ks][h] = x ? *reinterpret_cast<const uint32_t*>(x + ks * 16 + 2 * t) : 0u;
-                        qf[ks][h + 2] = x ? *reinterpret_cast<const uint32_t*>(x + ks * 16 + 8 + 2 * t) : 0u;
+                        qf[nb][ks][0] = x ? *reinterpret_cast<const uint32_t*>(x + ks * 16 + 2 * t) : 0u;
+                        qf[nb][ks][1] = x ? *reinterpret_cast<const uint32_t*>(x + ks * 16 + 8 + 2 * t) : 0u;
                     }
                 } else {
                     // A product may take d in any order that Q and K share: lane t has the 16 codes
@@ -316,7 +330,7 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                     const int ex = max((__float_as_int(amax) >> 23) - 127, -100);
                     const float down = __int_as_float((127 + 14 - ex) << 23);
-                    row_scale[h] = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23);
+                    scale = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23);
 #pragma unroll
                     for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
@@ -324,140 +338,175 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 const float2 f = unpack_bf16x2(raw4[hh][j * 2 + c]);
-                                qf[hh * 4 + j][h + 2 * c] = pack_f16x2(f.x * down, f.y * down);
+                                qf[nb][hh * 4 + j][c] = pack_f16x2(f.x * down, f.y * down);
                             }
                 }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = nb * 8 + 2 * t + e;
+                    lim[nb][e] = r < rows ? token_keys(q, keys, tok0 + r / p.group) : 0;
+                    row_scale[nb][e] = __shfl_sync(0xffffffffu, scale, (2 * t + e) * 4);
+                }
             }
-            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-            float mv[2] = {-INFINITY, -INFINITY};  // 8-bit cache: reference of the weights 2^x vs
-            float o[D / 8][4];
+            // By row: reference and sum; for 8 bits the reference of the weights 2^x vs.
+            float m[NB][2], l[NB][2], mv[NB][2], o[NB][D / 16][4];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
+            for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[c][e] = 0.0f;
+                for (int e = 0; e < 2; ++e) {
+                    m[nb][e] = mv[nb][e] = -INFINITY;
+                    l[nb][e] = 0.0f;
+                }
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[nb][c][e] = 0.0f;
+            }
 
             for (int i = 0; i < seg; ++i, ++n) {
-                if (C::WPB < NW && (n & 1) != warp / C::WPB) continue;
+                if (C::WPB < NW && n % (NW / C::WPB) != warp / C::WPB) continue;
                 const int st = n % NST;
                 ok = ok && wait(full0 + 8 * st, (n / NST) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 const uint32_t sk = base + st * C::STAGE, sv = sk + C::TILE;
                 const int wk0 = wk * (16 * NG), key0 = (kb0 + i) * KB + wk0;  // the warp's keys of the block
-                float s[NG][2][4] = {};
+                // S^T.  A warp issues in order and a product waits for its accumulator, so neighbouring products go to
+                // different ones: CH accumulators of D / CH steps each where there are few keys and rows.
+                constexpr int CH = NG * NB >= 4 ? 1 : 4 / (NG * NB) < D / 32 ? 4 / (NG * NB) : D / 32;
+                float s[NG][NB][CH][4] = {};
+                if constexpr (!E4M3) {
 #pragma unroll
-                for (int gr = 0; gr < NG; ++gr) {
-                    if constexpr (!E4M3) {
-                        // Matrices (keys 0-7, 8-15) x (d 0-7, 8-15) of a step: lanes 0-7 and 16-23 address keys
-                        // 0-7 and 8-15 of the step's first eight d, lanes 8-15 and 24-31 of its second eight.
-                        const uint32_t kr = wk0 + gr * 16 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+                    for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            uint32_t b[4];
-                            ldsm4(sk + (ks >> 2) * (KB * 128) + swz<128>(kr, (ks & 3) * 2 + kc), b);
-                            mma<false>(s[gr][0], qf[ks], b[0], b[1]);
-                            mma<false>(s[gr][1], qf[ks], b[2], b[3]);
+                        for (int gr = 0; gr < NG; ++gr) {
+                            // Matrices (keys 0-7, 8-15) x (d 0-7, then 8-15) of a step.
+                            uint32_t a[4];
+                            ldsm4(sk + (ks >> 2) * (KB * 128) + swz<128>(wk0 + gr * 16 + (lane & 15), (ks & 3) * 2 + (lane >> 4)), a);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) mma<false>(s[gr][nb][ks % CH], a, qf[nb][ks][0], qf[nb][ks][1]);
                         }
-                    } else {
+                } else {
 #pragma unroll
-                        for (int hh = 0; hh < D / 64; ++hh)
+                    for (int hh = 0; hh < D / 64; ++hh) {
+                        uint32_t c[NG][2][4];  // codes of keys r0 and r0 + 8
 #pragma unroll
-                            for (int nt = 0; nt < 2; ++nt) {
-                                const uint4 u = ld_shared_v4(sk + swz<C::SEG>(wk0 + gr * 16 + nt * 8 + r0, hh * 4 + t));
-                                const uint32_t c[4] = {u.x, u.y, u.z, u.w};
+                        for (int x = 0; x < 2 * NG; ++x) {
+                            const uint4 u = ld_shared_v4(sk + swz<C::SEG>(wk0 + x * 8 + r0, hh * 4 + t));
+                            c[x >> 1][x & 1][0] = u.x;
+                            c[x >> 1][x & 1][1] = u.y;
+                            c[x >> 1][x & 1][2] = u.z;
+                            c[x >> 1][x & 1][3] = u.w;
+                        }
 #pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    mma<true>(s[gr][nt], qf[hh * 4 + j], e4m3x2_f16x2(c[j]), e4m3x2_f16x2(c[j] >> 16));
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int gr = 0; gr < NG; ++gr) {
+                                const uint32_t a[4] = {e4m3x2_f16x2(c[gr][0][j]), e4m3x2_f16x2(c[gr][1][j]),
+                                                       e4m3x2_f16x2(c[gr][0][j] >> 16), e4m3x2_f16x2(c[gr][1][j] >> 16)};
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb)
+                                    mma<true>(s[gr][nb][j % CH], a, qf[nb][hh * 4 + j][0], qf[nb][hh * 4 + j][1]);
                             }
                     }
                 }
-                // Scores in the exp2 domain, masked; lane t has keys 2t, 2t + 1 of each eight.
-                float lv[NG][2][2] = {};
+                // Scores in the exp2 domain, masked: x[..][2 hk + e] of key r0 + 8 hk and row 2t + e.
+                float x[NG][NB][4], lv[NG][2] = {};
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        float ks[2] = {1.0f, 1.0f};
+                    for (int hk = 0; hk < 2; ++hk) {
+                        float ks = 1.0f;
                         if constexpr (E4M3) {
-                            const float* sc = reinterpret_cast<const float*>(gbase + C::SC_OFF + st * C::SCALES) + wk0 +
-                                              gr * 16 + nt * 8 + 2 * t;
-                            const float2 k2 = *reinterpret_cast<const float2*>(sc);
-                            const float2 v2 = *reinterpret_cast<const float2*>(sc + KB);
-                            ks[0] = k2.x;
-                            ks[1] = k2.y;
-                            lv[gr][nt][0] = __log2f(v2.x);
-                            lv[gr][nt][1] = __log2f(v2.y);
+                            const float* sc = reinterpret_cast<const float*>(gbase + C::SC_OFF + st * C::SCALES) + wk0 + gr * 16 + hk * 8 + r0;
+                            ks = sc[0];
+                            lv[gr][hk] = __log2f(sc[KB]);
                         }
+                        const int key = key0 + gr * 16 + hk * 8 + r0;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = key0 + gr * 16 + nt * 8 + 2 * t + (e & 1);
-                            const float x = s[gr][nt][e] * (ks[e & 1] * row_scale[e >> 1]);
-                            s[gr][nt][e] = key < lim[e >> 1] ? x : -INFINITY;
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float sum = s[gr][nb][0][2 * hk + e];
+#pragma unroll
+                                for (int ch = 1; ch < CH; ++ch) sum += s[gr][nb][ch][2 * hk + e];
+                                x[gr][nb][2 * hk + e] = key < lim[nb][e] ? sum * (ks * row_scale[nb][e]) : -INFINITY;
+                            }
+                    }
+                uint32_t pb[NG][NB][2];  // P^T as the second product's operand
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    float pr[NG][4], alpha[2];
+                    bool move = false;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int gr = 0; gr < NG; ++gr) mx = fmaxf(mx, fmaxf(x[gr][nb][e], x[gr][nb][2 + e]));
+#pragma unroll
+                        for (int f = 4; f < 32; f <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, f));
+                        alpha[e] = 1.0f;
+                        if (mx > m[nb][e] + RESCALE) {
+                            alpha[e] = ex2(m[nb][e] - mx);
+                            m[nb][e] = mx;
+                            move = true;
                         }
+                        const float ref = m[nb][e] == -INFINITY ? 0.0f : m[nb][e];
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                            for (int hk = 0; hk < 2; ++hk) {
+                                pr[gr][2 * hk + e] = ex2(x[gr][nb][2 * hk + e] - ref);
+                                sum += pr[gr][2 * hk + e];
+                            }
+                        l[nb][e] = l[nb][e] * alpha[e] + sum;
                     }
-                uint32_t pa[NG][4] = {};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1 && !upper) break;  // no query in the tile's rows 8..15
-                    constexpr int NX = 4 * NG;
-                    float x[NX];
-#pragma unroll
-                    for (int e = 0; e < NX; ++e) x[e] = s[e >> 2][(e >> 1) & 1][2 * h + (e & 1)];
-                    float mx = x[0];
-#pragma unroll
-                    for (int e = 1; e < NX; ++e) mx = fmaxf(mx, x[e]);
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    bool move = mx > m[h] + RESCALE;
-                    float alpha = 1.0f;
-                    if (move) {
-                        alpha = ex2(m[h] - mx);
-                        m[h] = mx;
-                    }
-                    const float ref = m[h] == -INFINITY ? 0.0f : m[h];
-                    float pr[NX], sum = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < NX; ++e) {
-                        pr[e] = ex2(x[e] - ref);
-                        sum += pr[e];
-                    }
-                    l[h] = l[h] * alpha + sum;
                     if constexpr (E4M3) {
                         // Weights 2^(x + log2 vs) against their own largest, which stands for 2^15: fp16's range
                         // whatever the scales.  A weight is rounded to 2^-11 of itself, or to 2^-25 where
                         // it is below fp16's normal range, 2^-40 of the largest.
-                        float y[NX];
+                        move = false;
 #pragma unroll
-                        for (int e = 0; e < NX; ++e) y[e] = x[e] == -INFINITY ? -INFINITY : x[e] + lv[e >> 2][(e >> 1) & 1][e & 1];
-                        float my = y[0];
+                        for (int e = 0; e < 2; ++e) {
+                            float y[NG][2], my = -INFINITY;
 #pragma unroll
-                        for (int e = 1; e < NX; ++e) my = fmaxf(my, y[e]);
-                        my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 1));
-                        my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 2));
-                        move = my > mv[h];
-                        alpha = 1.0f;
-                        if (move) {
-                            alpha = ex2(mv[h] - my);
-                            mv[h] = my;
+                            for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                                for (int hk = 0; hk < 2; ++hk) {
+                                    const float v = x[gr][nb][2 * hk + e];
+                                    y[gr][hk] = v == -INFINITY ? v : v + lv[gr][hk];
+                                    my = fmaxf(my, y[gr][hk]);
+                                }
+#pragma unroll
+                            for (int f = 4; f < 32; f <<= 1) my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, f));
+                            alpha[e] = 1.0f;
+                            if (my > mv[nb][e]) {
+                                alpha[e] = ex2(mv[nb][e] - my);
+                                mv[nb][e] = my;
+                                move = true;
+                            }
+                            const float rv = (mv[nb][e] == -INFINITY ? 0.0f : mv[nb][e]) - 15.0f;
+#pragma unroll
+                            for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                                for (int hk = 0; hk < 2; ++hk) pr[gr][2 * hk + e] = ex2(y[gr][hk] - rv);
                         }
-                        const float rv = (mv[h] == -INFINITY ? 0.0f : mv[h]) - 15.0f;
-#pragma unroll
-                        for (int e = 0; e < NX; ++e) pr[e] = ex2(y[e] - rv);
                     }
                     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-                        for (int c = 0; c < D / 8; ++c) {
-                            o[c][2 * h] *= alpha;
-                            o[c][2 * h + 1] *= alpha;
-                        }
+                        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[nb][c][e] *= alpha[e & 1];
                     }
 #pragma unroll
-                    for (int gr = 0; gr < NG; ++gr) {
-                        pa[gr][h] = E4M3 ? pack_f16x2(pr[4 * gr], pr[4 * gr + 1]) : pack_bf16x2(pr[4 * gr], pr[4 * gr + 1]);
-                        pa[gr][h + 2] = E4M3 ? pack_f16x2(pr[4 * gr + 2], pr[4 * gr + 3]) : pack_bf16x2(pr[4 * gr + 2], pr[4 * gr + 3]);
-                    }
+                    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                        for (int hk = 0; hk < 2; ++hk)
+                            pb[gr][nb][hk] = transpose8(E4M3 ? pack_f16x2(pr[gr][2 * hk], pr[gr][2 * hk + 1])
+                                                             : pack_bf16x2(pr[gr][2 * hk], pr[gr][2 * hk + 1]));
                 }
-                // O += P V.  Rows of V past the sequence's keys are whatever the page holds: cleared, since
+                // O^T += V^T P^T.  Rows of V past the sequence's keys are whatever the page holds: cleared, since
                 // 0 * NaN is NaN.  `live` masks the halves of a register that holds keys 2t, 2t + 1 (+ 8).
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
@@ -471,42 +520,41 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                             live[h] = (key < keys ? 0xffffu : 0u) | (key + 1 < keys ? 0xffff0000u : 0u);
                         }
                     }
-                    // Matrices (keys 0-7, 8-15) x two neighbouring eights of 16-bit columns.
-                    const uint32_t vr = wk0 + gr * 16 + (lane & 15), vc = lane >> 4;
-                    if constexpr (!E4M3) {
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t b[4];
-                            ldsm4_t(sv + (c >> 2) * (KB * 128) + swz<128>(vr, (c & 3) * 2 + vc), b);
+                    for (int c0 = 0; c0 < C::ROW / 32; c0 += 2) {
+                        // 32 bytes of 16 keys' rows: (keys 0-7, 8-15) x two 16-byte columns, transposed.
+                        uint32_t b[2][4];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int c = c0 + y;
+                            if constexpr (!E4M3)  // keys 0-7: columns 0, 1; keys 8-15: columns 0, 1
+                                ldsm4_t(sv + (c >> 2) * (KB * 128) +
+                                            swz<128>(wk0 + gr * 16 + (lane & 7) + ((lane >> 4) << 3), (c & 3) * 2 + ((lane >> 3) & 1)), b[y]);
+                            else                  // column 0: keys 0-7, 8-15; column 1
+                                ldsm4_t(sv + swz<C::SEG>(wk0 + gr * 16 + (lane & 15), c * 2 + (lane >> 4)), b[y]);
                             if (tail) {
-                                b[0] &= live[0];
-                                b[1] &= live[1];
-                                b[2] &= live[0];
-                                b[3] &= live[1];
+                                b[y][0] &= live[0];
+                                b[y][1] &= live[E4M3 ? 1 : 0];
+                                b[y][2] &= live[E4M3 ? 0 : 1];
+                                b[y][3] &= live[1];
                             }
-                            mma<false>(o[2 * c], pa[gr], b[0], b[1]);
-                            mma<false>(o[2 * c + 1], pa[gr], b[2], b[3]);
                         }
-                    } else {
-                        // A 16-bit column is two codes, d and d + 1: a register holds them for two keys.  Even and
-                        // odd d go to two products: o[2 c'] has the even d of 16, o[2 c' + 1] the odd.
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t b[4];
-                            ldsm4_t(sv + swz<C::SEG>(vr, c * 2 + vc), b);
-                            if (tail) {
-                                b[0] &= live[0];
-                                b[1] &= live[1];
-                                b[2] &= live[0];
-                                b[3] &= live[1];
-                            }
+                        for (int y = 0; y < 2; ++y) {
+                            if constexpr (!E4M3) {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t x = b[2 * h], y = b[2 * h + 1];
-                                mma<true>(o[4 * c + 2 * h], pa[gr], e4m3x2_f16x2(__byte_perm(x, 0, 0x0020)),
-                                          e4m3x2_f16x2(__byte_perm(y, 0, 0x0020)));
-                                mma<true>(o[4 * c + 2 * h + 1], pa[gr], e4m3x2_f16x2(__byte_perm(x, 0, 0x0031)),
-                                          e4m3x2_f16x2(__byte_perm(y, 0, 0x0031)));
+                                for (int nb = 0; nb < NB; ++nb) mma<false>(o[nb][c0 + y], b[y], pb[gr][nb][0], pb[gr][nb][1]);
+                            } else {
+                                // A 16-bit column is two codes, d and d + 1, a register's halves two keys: even d are
+                                // the product's rows 0..7, odd d its rows 8..15.
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint32_t lo = b[y][2 * h], hi = b[y][2 * h + 1];
+                                    const uint32_t a[4] = {e4m3x2_f16x2(__byte_perm(lo, 0, 0x0020)), e4m3x2_f16x2(__byte_perm(lo, 0, 0x0031)),
+                                                           e4m3x2_f16x2(__byte_perm(hi, 0, 0x0020)), e4m3x2_f16x2(__byte_perm(hi, 0, 0x0031))};
+#pragma unroll
+                                    for (int nb = 0; nb < NB; ++nb) mma<true>(o[nb][2 * (c0 + y) + h], a, pb[gr][nb][0], pb[gr][nb][1]);
+                                }
                             }
                         }
                     }
@@ -515,58 +563,62 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                 if (lane == 0) mbar_arrive(empty0 + 8 * st);
             }
 
-            // ---- merge the eight warps' sums over their keys
+            // ---- merge the warps' sums over their keys, 8 rows at a time
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-                if (t == 0) xm[warp * R + r0 + 8 * h] = m[h];
-            }
-            named_bar_sync(1, 32 * NW);
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = r0 + 8 * h;
-                float mm = -INFINITY;
+                for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                for (int x = 0; x < NW; ++x) mm = fmaxf(mm, xm[x * R + i]);
-                // 2^(own reference - common one); the 8-bit cache's weights have a reference of their own.
-                const float f = m[h] == -INFINITY ? 0.0f : ex2(m[h] - mm);
-                float fo = f;
-                if constexpr (E4M3) fo = mv[h] == -INFINITY ? 0.0f : ex2(mv[h] - 15.0f - mm);
-                if (t == 0) xl[warp * R + i] = l[h] * f;
-                if (i < rows) {
-                    float* dst = acc_s + (warp * R + i) * C::LD_ACC;
-                    if constexpr (!E4M3) {
-#pragma unroll
-                        for (int c = 0; c < D / 8; ++c)
-                            *reinterpret_cast<float2*>(dst + c * 8 + 2 * t) =
-                                make_float2(o[c][2 * h] * fo, o[c][2 * h + 1] * fo);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c)
-                            *reinterpret_cast<float4*>(dst + c * 16 + 4 * t) =
-                                make_float4(o[2 * c][2 * h] * fo, o[2 * c + 1][2 * h] * fo, o[2 * c][2 * h + 1] * fo,
-                                            o[2 * c + 1][2 * h + 1] * fo);
-                    }
+                    for (int f = 4; f < 32; f <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], f);
+                    if (r0 == 0) xm[warp * R + nb * 8 + 2 * t + e] = m[nb][e];
                 }
-            }
-            named_bar_sync(1, 32 * NW);
             const bool begins = kb0 == 0, ends = kb0 + seg == w.nkb;
             const int slot = begins ? 1 : 0;
-            if (ok) {
-                for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * NW) {
-                    const int i = x / (D / 4), c = (x % (D / 4)) * 4;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                if (nb * 8 >= rows) break;
+                named_bar_sync(1, 32 * NW);  // the maxima are there, and the previous sums have been read
+                float fo[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = nb * 8 + 2 * t + e;
+                    float mm = -INFINITY;
+#pragma unroll
+                    for (int y = 0; y < NW; ++y) mm = fmaxf(mm, xm[y * R + r]);
+                    // 2^(own reference - common one); the 8-bit cache's weights have a reference of their own.
+                    const float f = m[nb][e] == -INFINITY ? 0.0f : ex2(m[nb][e] - mm);
+                    fo[e] = f;
+                    if constexpr (E4M3) fo[e] = mv[nb][e] == -INFINITY ? 0.0f : ex2(mv[nb][e] - 15.0f - mm);
+                    if (r0 == 0) xl[warp * R + r] = l[nb][e] * f;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float* dst = acc_s + (warp * 8 + 2 * t + e) * C::LD_ACC;
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        if constexpr (!E4M3) {
+                            dst[c * 16 + r0] = o[nb][c][e] * fo[e];
+                            dst[c * 16 + 8 + r0] = o[nb][c][2 + e] * fo[e];
+                        } else {
+                            *reinterpret_cast<float2*>(dst + c * 16 + 2 * r0) = make_float2(o[nb][c][e] * fo[e], o[nb][c][2 + e] * fo[e]);
+                        }
+                    }
+                }
+                named_bar_sync(1, 32 * NW);
+                if (!ok) continue;
+                for (int z = threadIdx.x; z < min(rows - 8 * nb, 8) * (D / 4); z += 32 * NW) {
+                    const int ir = z / (D / 4), i = ir + 8 * nb, c = (z % (D / 4)) * 4;
                     float4 a = make_float4(0, 0, 0, 0);
-                    float lt = 0.0f, mm = -INFINITY;
+                    float lt = 0.0f, mt = -INFINITY;
 #pragma unroll
                     for (int y = 0; y < NW; ++y) {
-                        const float4 b = *reinterpret_cast<const float4*>(acc_s + (y * R + i) * C::LD_ACC + c);
+                        const float4 b = *reinterpret_cast<const float4*>(acc_s + (y * 8 + ir) * C::LD_ACC + c);
                         a.x += b.x;
                         a.y += b.y;
                         a.z += b.z;
                         a.w += b.w;
                         lt += xl[y * R + i];
-                        mm = fmaxf(mm, xm[y * R + i]);
+                        mt = fmaxf(mt, xm[y * R + i]);
                     }
                     if (begins && ends) {
                         const float inv = lt != 0.0f ? 1.0f / lt : 0.0f;  // nothing seen: zeros
@@ -578,16 +630,17 @@ __global__ void __launch_bounds__(NT, 1) attn_few_kernel(const __grid_constant__
                     } else {
                         const long long at = (static_cast<long long>(blockIdx.x) * 2 + slot) * R + i;
                         *reinterpret_cast<float4*>(p.part_o + at * D + c) = a;
-                        if (c == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mm, lt);
+                        if (c == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mt, lt);
                     }
                 }
-                if (begins && !ends && threadIdx.x == 0) {
-                    // The tile's last block is in CTA (first block + blocks - 1) / per.
-                    const long long at = share.begin + share.count - seg;
-                    const int last = share_of(at + w.nkb - 1, share.per);
-                    p.desc[blockIdx.x] = make_int4(q.row0 + tok0, g, rows, last - static_cast<int>(blockIdx.x) + 1);
-                }
             }
+            if (begins && !ends && threadIdx.x == 0) {
+                // The tile's last block is in CTA (first block + blocks - 1) / per.
+                const long long at = share.begin + share.count - seg;
+                const int last = share_of(at + w.nkb - 1, share.per);
+                p.desc[blockIdx.x] = make_int4(q.row0 + tok0, g, rows, last - static_cast<int>(blockIdx.x) + 1);
+            }
+            xm = reinterpret_cast<float*>(gbase + C::XM_OFF) + (xm == reinterpret_cast<float*>(gbase + C::XM_OFF) ? NW * R : 0);
         }
     }
     __syncthreads();
@@ -661,7 +714,7 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     p.heads_per_shard = a.heads / a.t;
     p.shard_w = static_cast<int>(a.shard_w);
     p.group = a.heads / a.kv_heads;
-    p.tile_tok = R / p.group;
+    p.tile_tok = 8 * C::NB / p.group;
     p.log2_tok = exact_log2(p.tile_tok);
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(C::D));
     const Scratch s = tpi::scratch_of(grid, R, C::D);
@@ -680,7 +733,7 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
         configured[dev] = true;
     }
     rc = launched("paged attention launch",
-                  tpi::launch_pdl(attn_few_kernel<C>, dim3(grid), dim3(NT), C::SMEM, stream, p), err);
+                  tpi::launch_pdl(attn_few_kernel<C>, dim3(grid), dim3(C::NT), C::SMEM, stream, p), err);
     if (rc) return rc;
     return tpi::attn_join_launch(a, R, O, w, s, grid, zero_rest, stream, err);
 }
@@ -721,16 +774,22 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
                         cudaMemsetAsync(O, 0, static_cast<size_t>(a.tokens) * a.heads * a.head_dim * 2, stream), err);
     }
     // Few rows a sequence and KV head (the caller's bound on its new tokens, or all rows of the call): one tile
-    // of 16.  More: tiles of 128 on tcgen05.
+    // of 8 or 16.  More: tiles of 128 on tcgen05.
     const int group = a.heads / a.kv_heads;
     const int64_t most = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
-    if (most * group > R)
-        return attn_chunk_launch(a, O, scratch, zero_rest, stream, err);
+    if (most * group > R) return attn_chunk_launch(a, O, scratch, zero_rest, stream, err);
+    if (most * group <= 8) {
+        if (a.head_dim == 128)
+            return a.e4m3 ? launch_few<Cfg<128, true, 1, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
+                          : launch_few<Cfg<128, false, 1, 8, 4, 1, 4>>(a, O, scratch, zero_rest, stream, err);
+        return a.e4m3 ? launch_few<Cfg<64, true, 1, 8, 4, 2, 8>>(a, O, scratch, zero_rest, stream, err)
+                      : launch_few<Cfg<64, false, 1, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
+    }
     if (a.head_dim == 128)
-        return a.e4m3 ? launch_few<Cfg<128, true, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
-                      : launch_few<Cfg<128, false, 4, 1, 4>>(a, O, scratch, zero_rest, stream, err);
-    return a.e4m3 ? launch_few<Cfg<64, true, 4, 2, 6>>(a, O, scratch, zero_rest, stream, err)
-                  : launch_few<Cfg<64, false, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
+        return a.e4m3 ? launch_few<Cfg<128, true, 2, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
+                      : launch_few<Cfg<128, false, 2, 8, 4, 1, 4>>(a, O, scratch, zero_rest, stream, err);
+    return a.e4m3 ? launch_few<Cfg<64, true, 2, 8, 4, 2, 8>>(a, O, scratch, zero_rest, stream, err)
+                  : launch_few<Cfg<64, false, 2, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
 }
 
 }  // namespace tpi
