@@ -15,8 +15,8 @@
 // tile: 16 multiply-adds a byte, a few per cent of the tensor cores' rate).
 // The work is cut into equal shares of key blocks (tp_paged_index.h), one
 // persistent CTA an SM:
-//   warp 8      producer: TMA boxes of one page each into a ring of key
-//               blocks; the page numbers of 32 pages are read at a time.
+//   warps 8, 9  producers of K and of V: TMA boxes of one page each into a ring
+//               of key blocks; page numbers are read 32 at a time and ahead.
 //   warps 0..7  consumers, 16 or 32 keys of a block each: S^T = K Q^T and
 //               O^T += V^T P^T by mma.sync m16n8k16, a running maximum of their
 //               own; at a tile's end the eight are merged in shared memory.
@@ -51,7 +51,7 @@ constexpr float RESCALE = 8.0f;  // log2 of the growth of a weight before the su
 template <int D_, bool E4M3_, int NB_, int NW_, int WPB_, int NG_, int NST_>
 struct Cfg {
     static constexpr int D = D_, NB = NB_, NW = NW_, WPB = WPB_, NG = NG_, NST = NST_;
-    static constexpr int NT = 32 * (NW + 1);
+    static constexpr int NT = 32 * (NW + 2);
     static constexpr bool E4M3 = E4M3_;
     static constexpr int LOG2_KB = WPB * NG == 8 ? 7 : 6;
     static constexpr int KB = 1 << LOG2_KB;
@@ -68,8 +68,9 @@ struct Cfg {
     static constexpr int XM_OFF = ACC_OFF + NW * 8 * LD_ACC * 4;  // 8 rows of a tile at a time
     static constexpr int BAR_OFF = XM_OFF + 3 * NW * R * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * 2 * NST;
-    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NW + 3);  // the share's beginning, then one walk a warp
-    static constexpr int DATA = WALK_OFF + (NW + 2) * sizeof(TileWalk);
+    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NW + 4);  // the share's beginning, one walk a warp, the producers' ahead
+    static constexpr int PAGE_OFF = WALK_OFF + (NW + 5) * sizeof(TileWalk);  // page numbers of the two producers
+    static constexpr int DATA = PAGE_OFF + 2 * 64 * 4;
     static constexpr int SMEM = DATA + 1024;
     static_assert(SMEM <= 232448, "shared memory");
     // A set of warps that met a stage every second time only could find its barrier two phases behind, which
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
-            mbar_init(full0 + 8 * i, 1);
+            mbar_init(full0 + 8 * i, 2);  // the two producers
             mbar_init(empty0 + 8 * i, C::WPB);
         }
         abort_word = 0;
@@ -183,79 +184,87 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
         __syncwarp();
     };
 
-    if (warp == NW) {
-        // ------------------------------------------------------ producer
+    if (warp >= NW) {
+        // ------------------------------------------------------ producers: K, V
+        const bool is_v = warp > NW;
+        const int log2 = p.v.page_log2, page_mask = (1 << log2) - 1, per_block = KB / p.box_rows;
+        const CUtensorMap* map = is_v ? &p.map_v : &p.map_k;
+        const float* scales = is_v ? p.v_scale : p.k_scale;
+        // Page numbers of two windows of 32 pages: page i of the sequence at ring[i - first page of the segment, mod 64].
+        int* ring = reinterpret_cast<int*>(gbase + C::PAGE_OFF) + (is_v ? 64 : 0);
+        // Page i of a segment's sequence; -1: past its keys, or on no page of the cache (TMA fills such a box with
+        // zeros and reads nothing).
+        auto page_at = [&](const TileWalk& x, int i) -> int {
+            if ((static_cast<long long>(i) << log2) >= x.keys) return -1;
+            const int pg = p.v.table[static_cast<long long>(x.s) * p.v.max_pages + i];
+            if (pg >= 0 && pg < p.v.n_pages) return pg;
+            if (p.status) atomicOr(p.status, kStatusPage);
+            return -1;
+        };
+        // y walks a segment ahead: the first pages of the next segment are read in time.
+        TileWalk& y = walks[1 + NW + 2 + (is_v ? 1 : 0)];
+        if (lane == 0) y = w;
+        __syncwarp();
+        int first = -1, behind = -1, n = 0;  // n: blocks issued
+        if (y.left > 0) {
+            first = page_at(y, ((y.kb * KB) >> log2) + lane);
+            behind = page_at(y, ((y.kb * KB) >> log2) + 32 + lane);
+        }
         bool ok = true;
-        int n = 0;  // blocks issued
-        for (; w.left > 0 && ok; move_on()) {
-            const int seg = w.segment(), kb0 = w.kb, keys = w.keys, g = w.g;
-            const int32_t* table = p.v.table + static_cast<long long>(w.s) * p.v.max_pages;
-            const int page_rows = 1 << p.v.page_log2;
-            const int per_block = KB / p.box_rows;  // boxes (pages, or parts of one) of a block
-            int window = -32, held = -1;            // pages [window, window + 32) of the sequence, one a lane
-            for (int i = 0; i < seg && ok; ++i, ++n) {
+        while (y.left > 0 && ok) {
+            __syncwarp();
+            if (lane == 0) {
+                w = y;
+                y.next(p.v, tiling);
+            }
+            __syncwarp();
+            const int seg = w.segment(), g = w.g, page0 = (w.kb * KB) >> log2;
+            int next = behind, key0 = w.kb * KB, done = 0;  // done: first page of the window's first block
+            ring[lane] = first;
+            __syncwarp();
+            if (y.left > 0) {
+                first = page_at(y, ((y.kb * KB) >> log2) + lane);
+                behind = page_at(y, ((y.kb * KB) >> log2) + 32 + lane);
+            }
+            ring[32 + lane] = next;
+            next = page_at(w, page0 + 64 + lane);
+            __syncwarp();
+            for (int i = 0; i < seg; ++i, ++n, key0 += KB) {
+                const int at = (key0 >> log2) - page0;  // the block's first page
+                if (at - done >= 32) {                  // a window is behind: the next but one takes its place
+                    done += 32;
+                    ring[(done + 32 + lane) & 63] = next;
+                    next = page_at(w, page0 + done + 64 + lane);
+                    __syncwarp();
+                }
                 const int st = n % NST;
                 const uint32_t full = full0 + 8 * st;
-                const int key0 = (kb0 + i) * KB;
-                const int first = key0 >> p.v.page_log2;
-                if (first + per_block > window + 32 || first < window) {
-                    window = first;
-                    const int pg = window + lane;
-                    held = -1;
-                    if (pg * static_cast<long long>(page_rows) < keys) {
-                        held = table[pg];
-                        if (held < 0 || held >= p.v.n_pages) {
-                            held = -1;
-                            if (p.status) atomicOr(p.status, kStatusPage);
-                        }
-                    }
-                }
-                ok = wait(empty0 + 8 * st, ((n / NST) & 1) ^ 1);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, wait(empty0 + 8 * st, ((n / NST) & 1) ^ 1));
                 if (!ok) break;
-                // Box b of the block: keys key0 + b * box_rows.  A box past the
-                // sequence's keys, or on a page outside the cache, is loaded
-                // from page -1: TMA fills it with zeros and reads nothing.
-                if constexpr (E4M3) {
-                    // Scales, a lane a box; those of no page are zeros.
-                    const int k_box = key0 + lane * p.box_rows;
-                    int page = __shfl_sync(0xffffffffu, held, (first - window + lane) & 31);
-                    if (k_box >= keys) page = -1;
-                    const bool mine = lane < per_block;
-                    const uint32_t sc = base + C::SC_OFF + st * C::SCALES + lane * p.box_rows * 4;
-                    const unsigned scaled = __ballot_sync(0xffffffffu, mine && page >= 0);
-                    if (mine && page < 0) {
+                const uint32_t dst = base + st * C::STAGE + (is_v ? C::TILE : 0);
+                const uint32_t sc = base + C::SC_OFF + st * C::SCALES + (is_v ? KB * 4 : 0);
+                int scaled = 0;
+                if constexpr (E4M3) {  // a lane a box; the scales of no page are zeros
+                    const int page = lane < per_block ? ring[(at + lane) & 63] : -1;
+                    scaled = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                    if (lane < per_block && page < 0) {
 #pragma unroll 1
-                        for (int x = 0; x < p.box_rows; x += 4) {
-                            st_shared_v4(sc + x * 4, 0, 0, 0, 0);
-                            st_shared_v4(sc + KB * 4 + x * 4, 0, 0, 0, 0);
-                        }
+                        for (int x = 0; x < p.box_rows; x += 4) st_shared_v4(sc + (lane * p.box_rows + x) * 4, 0, 0, 0, 0);
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(full, 2 * C::TILE + 8u * p.box_rows * __popc(scaled));
-                } else {
-                    if (lane == 0) mbar_arrive_expect_tx(full, 2 * C::TILE);
                 }
-                // One lane issues: a copy's operands are uniform registers, so lanes would take turns.
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full, C::TILE + 4u * p.box_rows * scaled);
+                    // One lane issues: a copy's operands are uniform registers, so lanes would take turns.
 #pragma unroll 1
-                for (int b = 0; b < per_block; ++b) {
-                    const int k_box = key0 + b * p.box_rows, off = k_box & (page_rows - 1);
-                    int page = __shfl_sync(0xffffffffu, held, ((k_box >> p.v.page_log2) - window) & 31);
-                    if (k_box >= keys) page = -1;
-                    if (lane == 0) {
-                        const uint32_t dst = base + st * C::STAGE + b * p.box_rows * C::SEG;
+                    for (int b = 0; b < per_block; ++b) {
+                        const int page = ring[(at + b) & 63], off = (key0 + b * p.box_rows) & page_mask;
 #pragma unroll
-                        for (int c = 0; c < C::NSEG; ++c) {
-                            tma_load_4d(dst + c * (KB * C::SEG), &p.map_k, full, c * (E4M3 ? 128 : 64), off, g, page);
-                            tma_load_4d(dst + C::TILE + c * (KB * C::SEG), &p.map_v, full, c * (E4M3 ? 128 : 64), off, g, page);
-                        }
-                        if (E4M3 && page >= 0) {
-                            const uint32_t sc = base + C::SC_OFF + st * C::SCALES + b * p.box_rows * 4;
-                            const long long at = paged_row(p.v, page, g, off);
-                            bulk_load(sc, p.k_scale + at, p.box_rows * 4, full);
-                            bulk_load(sc + KB * 4, p.v_scale + at, p.box_rows * 4, full);
-                        }
+                        for (int c = 0; c < C::NSEG; ++c)
+                            tma_load_4d(dst + c * (KB * C::SEG) + b * p.box_rows * C::SEG, map, full, c * (E4M3 ? 128 : 64), off, g, page);
+                        if (E4M3 && page >= 0)
+                            bulk_load(sc + b * p.box_rows * 4, scales + paged_row(p.v, page, g, off), p.box_rows * 4, full);
                     }
                 }
                 __syncwarp();
