@@ -92,8 +92,8 @@ struct Lay {
     static constexpr int XCH_OFF = SC_OFF + (E4M3 ? NSC * 2 * KB * 4 : 0);  // [7][128] fp32: maxima x 2 x 2, sums x 2, references
     static constexpr int BAR_OFF = XCH_OFF + 7 * QB * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * NUM_BARS + 16;
-    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NT / 32 + 2);  // the share's beginning, one walk a warp, the producers' walks ahead
-    static constexpr int DONE_OFF = WALK_OFF + (NT / 32 + 3) * sizeof(TileWalk);
+    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NT / 32 + 2);  // one walk a warp, and the producers' ahead
+    static constexpr int DONE_OFF = WALK_OFF + (NT / 32 + 2) * sizeof(TileWalk);
     static constexpr int PAGE_OFF = (DONE_OFF + 8 * sizeof(Done) + 15) / 16 * 16;  // page numbers of the two producers
     static constexpr int DATA = PAGE_OFF + 2 * 64 * 4;
     static constexpr int SMEM = DATA + 1024;
@@ -170,17 +170,14 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
         tmem_relinquish();
     }
     tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
     pdl_trigger();
     pdl_wait();
     TileWalk* walks = reinterpret_cast<TileWalk*>(gbase + L::WALK_OFF);
-    const Share share =  // its barriers cover the set-up above
-        find_share<NT>(p.v, tiling, reinterpret_cast<long long*>(gbase + L::SCAN_OFF), walks);
-    tc_fence_after();
+    TileWalk& w = walks[warp];  // each warp walks on its own, in shared memory; lane 0 moves
+    const Share share = find_share<L::NT>(p.v, tiling, reinterpret_cast<long long*>(gbase + L::SCAN_OFF), w);
     const uint32_t tmem = *tmem_slot;
-    // Each warp walks on its own, in shared memory; lane 0 moves.
-    TileWalk& w = walks[1 + warp];
-    if (lane == 0) w = walks[0];
-    __syncwarp();
     auto move_on = [&] {
         __syncwarp();
         if (lane == 0) w.next(p.v, tiling);
@@ -208,7 +205,7 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
             return -1;
         };
         // y walks a segment ahead: the first pages of the next segment are read, and its Q is brought to L2, in time.
-        TileWalk& y = walks[1 + NT / 32 + (is_v ? 1 : 0)];
+        TileWalk& y = walks[NT / 32 + (is_v ? 1 : 0)];
         if (lane == 0) y = w;
         __syncwarp();
         auto q_box = [&](const TileWalk& x, bool load) {

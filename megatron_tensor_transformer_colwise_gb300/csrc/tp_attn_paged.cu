@@ -68,8 +68,8 @@ struct Cfg {
     static constexpr int XM_OFF = ACC_OFF + NW * 8 * LD_ACC * 4;  // 8 rows of a tile at a time
     static constexpr int BAR_OFF = XM_OFF + 3 * NW * R * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * 2 * NST;
-    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NW + 4);  // the share's beginning, one walk a warp, the producers' ahead
-    static constexpr int PAGE_OFF = WALK_OFF + (NW + 5) * sizeof(TileWalk);  // page numbers of the two producers
+    static constexpr int WALK_OFF = SCAN_OFF + 8 * (NW + 4);  // one walk a warp, and the producers' ahead
+    static constexpr int PAGE_OFF = WALK_OFF + (NW + 4) * sizeof(TileWalk);  // page numbers of the two producers
     static constexpr int DATA = PAGE_OFF + 2 * 64 * 4;
     static constexpr int SMEM = DATA + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -169,15 +169,12 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
         tma_prefetch_desc(&p.map_k);
         tma_prefetch_desc(&p.map_v);
     }
+    __syncthreads();
     pdl_trigger();
     pdl_wait();
     TileWalk* walks = reinterpret_cast<TileWalk*>(gbase + C::WALK_OFF);
-    const Share share =  // its barriers cover the set-up above
-        find_share<C::NT>(p.v, tiling, reinterpret_cast<long long*>(gbase + C::SCAN_OFF), walks);
-    // Each warp walks on its own, in shared memory; lane 0 moves.
-    TileWalk& w = walks[1 + warp];
-    if (lane == 0) w = walks[0];
-    __syncwarp();
+    TileWalk& w = walks[warp];  // each warp walks on its own, in shared memory; lane 0 moves
+    const Share share = find_share<C::NT>(p.v, tiling, reinterpret_cast<long long*>(gbase + C::SCAN_OFF), w);
     auto move_on = [&] {
         __syncwarp();
         if (lane == 0) w.next(p.v, tiling);
@@ -202,7 +199,7 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
             return -1;
         };
         // y walks a segment ahead: the first pages of the next segment are read in time.
-        TileWalk& y = walks[1 + NW + 2 + (is_v ? 1 : 0)];
+        TileWalk& y = walks[NW + 2 + (is_v ? 1 : 0)];
         if (lane == 0) y = w;
         __syncwarp();
         int first = -1, behind = -1, n = 0;  // n: blocks issued

@@ -96,57 +96,71 @@ __device__ __forceinline__ int share_of(long long at, long long per) {
 }
 
 // The share of CTA blockIdx.x: its first block, their number, every CTA's
-// number; *walk0 gets the walk's beginning.  Every thread sums the blocks of a
-// run of sequences, and a scan of the sums finds the sequence where the share
-// begins; warp 0 then looks for the tile, 32 at a time.  sums: NT / 32 + 2 words
-// of 8 bytes of shared memory.  Ends with __syncthreads.
+// number; walk gets its beginning.  Called by every warp (walk: its own, in
+// shared memory).  Sequences are summed in runs, and a scan of the sums finds
+// the one where the share begins; the tile is then looked for 32 at a time.  Up
+// to 256 sequences every warp does that alone, a run a lane: two barriers of
+// the CTA less in front of its first load.  More: a run a thread.  sums: NT / 32
+// + 2 words of 8 bytes of shared memory.
 struct Share {
     long long begin, count, per;
 };
 template <int NT>
-__device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t, long long* sums, TileWalk* walk0) {
+__device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t, long long* sums, TileWalk& walk) {
     const int tid = threadIdx.x, lane = tid & 31;
-    long long* found_off = sums + NT / 32;
-    int* found_s = reinterpret_cast<int*>(found_off + 1);
-    const int run = (v.n_seqs + NT - 1) / NT;
-    const int s0 = min(tid * run, v.n_seqs), s1 = min(s0 + run, v.n_seqs);
+    const bool alone = v.n_seqs <= 256;
+    const int run = alone ? (v.n_seqs + 31) / 32 : (v.n_seqs + NT - 1) / NT;
+    const int s0 = min((alone ? lane : tid) * run, v.n_seqs), s1 = min(s0 + run, v.n_seqs);
     long long mine = 0;
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) mine += seq_blocks(v, paged_seq(v, s), t);
     long long inc = mine;
-#pragma unroll 1
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
     }
-    if (lane == 31) sums[tid >> 5] = inc;
-    if (tid == 0) walk0->left = 0;
-    __syncthreads();
-    long long before = inc - mine, total = 0;
+    long long before = inc - mine, total = __shfl_sync(0xffffffffu, inc, 31);
+    if (!alone) {
+        if (lane == 31) sums[tid >> 5] = inc;
+        __syncthreads();
+        total = 0;
 #pragma unroll 1
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < (tid >> 5)) before += sums[w];
-        total += sums[w];
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < (tid >> 5)) before += sums[w];
+            total += sums[w];
+        }
     }
     Share x;
     x.per = share_size(total, static_cast<int>(gridDim.x));
     x.begin = pmin(static_cast<long long>(blockIdx.x) * x.per, total);
     x.count = pmin(x.per, total - x.begin);
-    if (x.count > 0 && x.begin >= before && x.begin < before + mine) {
-        int s = s0;
+    const bool here = x.count > 0 && x.begin >= before && x.begin < before + mine;
+    int s = s0;
+    long long off = x.begin - before;
+    if (here) {
 #pragma unroll 1
         for (; s < s1 - 1; ++s) {
             const long long n = seq_blocks(v, paged_seq(v, s), t);
-            if (x.begin < before + n) break;
-            before += n;
+            if (off < n) break;
+            off -= n;
         }
-        *found_off = x.begin - before;
-        *found_s = s;
     }
-    __syncthreads();
-    if (tid < 32 && x.count > 0) {
-        const int s = *found_s;
-        long long off = *found_off;
+    if (alone) {
+        const unsigned who = __ballot_sync(0xffffffffu, here);
+        const int from = who ? __ffs(who) - 1 : 0;
+        s = __shfl_sync(0xffffffffu, s, from);
+        off = __shfl_sync(0xffffffffu, off, from);
+    } else {
+        if (here) {
+            sums[NT / 32] = off;
+            sums[NT / 32 + 1] = s;
+        }
+        __syncthreads();
+        off = sums[NT / 32];
+        s = static_cast<int>(sums[NT / 32 + 1]);
+    }
+    if (x.count > 0) {
         const PagedSeq q = paged_seq(v, s);
         const int keys = paged_keys(v, q), tiles = seq_tiles(q, t);
         const long long per_head = tiles == 1 ? tile_blocks(q, keys, t, 0) : tiles_blocks(q, keys, t, tiles);
@@ -155,18 +169,32 @@ __device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t,
         for (; off >= per_head; ++g) off -= per_head;
         // The last tile that begins at or before `off`: of [lo, lo + 32 step) by its 32 steps, then within one.
         int lo = 0, step = 1;
-        while (step * 32 < tiles) step *= 32;
+        if (tiles > 1) {
+            while (step * 32 < tiles) step *= 32;
 #pragma unroll 1
-        for (; tiles > 1; step /= 32) {
-            const int at = lo + lane * step;
-            const bool before_off = at < tiles && tiles_blocks(q, keys, t, at) <= off;
-            lo += (__popc(__ballot_sync(0xffffffffu, before_off)) - 1) * step;
-            if (step == 1) break;
+            for (;; step /= 32) {
+                const int at = lo + lane * step;
+                const bool before_off = at < tiles && tiles_blocks(q, keys, t, at) <= off;
+                lo += (__popc(__ballot_sync(0xffffffffu, before_off)) - 1) * step;
+                if (step == 1) break;
+            }
+            off -= tiles_blocks(q, keys, t, lo);
         }
-        if (tiles > 1) off -= tiles_blocks(q, keys, t, lo);
-        if (lane == 0) walk0->start(v, t, s, g, lo, static_cast<int>(off), x.count);
+        if (lane == 0) {
+            walk.q = q;
+            walk.left = x.count;
+            walk.s = s;
+            walk.g = g;
+            walk.tile = lo;
+            walk.tiles = tiles;
+            walk.keys = keys;
+            walk.kb = static_cast<int>(off);
+            walk.nkb = tile_blocks(q, keys, t, lo);
+        }
+    } else if (lane == 0) {
+        walk.left = 0;
     }
-    __syncthreads();
+    __syncwarp();
     return x;
 }
 

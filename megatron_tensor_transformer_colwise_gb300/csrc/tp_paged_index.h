@@ -197,19 +197,6 @@ struct TileWalk {
     int s, g, tile, tiles, keys;
     int kb, nkb;     // next block of the tile, its number of blocks
 
-    // Begin `count` blocks of sequence s0 in KV head g0, `off` blocks behind the first block of tile `first`
-    // (off within that tile).
-    TP_HD_CALL void start(const PagedView& v, const Tiling& t, int s0, int g0, int first, int off, long long count) {
-        left = count;
-        s = s0;
-        g = g0;
-        tile = first;
-        q = paged_seq(v, s);
-        keys = paged_keys(v, q);
-        tiles = seq_tiles(q, t);
-        kb = off;
-        nkb = tile_blocks(q, keys, t, tile);
-    }
     // Blocks of the current segment.
     TP_HD int segment() const { return static_cast<int>(pmin(left, nkb - kb)); }
     // Move past the current segment.

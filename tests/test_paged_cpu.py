@@ -166,7 +166,8 @@ long long walk(const int* q, const int* len, long long rows, int n, int maxp, in
             int g = 0, tile = 0;
             for (; off >= per_head; ++g) off -= per_head;
             while (tile + 1 < tiles && tiles_blocks(x, keys, t, tile + 1) <= off) ++tile;
-            w.start(v, t, s, g, tile, (int)(off - tiles_blocks(x, keys, t, tile)), count);
+            w.q = x; w.left = count; w.s = s; w.g = g; w.tile = tile; w.tiles = tiles; w.keys = keys;
+            w.kb = (int)(off - tiles_blocks(x, keys, t, tile)); w.nkb = tile_blocks(x, keys, t, tile);
         }
         for (; w.left > 0; w.next(v, t)) {
             const int seg = w.segment();
