@@ -652,51 +652,98 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
     __syncthreads();
 }
 
+// Clears the rows of O that no sequence owns.
+__device__ __forceinline__ void clear_rest(const PagedView& v, int row_bytes, __nv_bfloat16* o) {
+    const int a = imin(imax(v.q_start[0], 0), v.rows), b = imin(imax(v.q_start[v.n_seqs], a), v.rows);
+    const long long per = row_bytes / 16, threads = static_cast<long long>(gridDim.x) * blockDim.x;
+    const long long me = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    uint4* y = reinterpret_cast<uint4*>(o);
+    for (long long i = me; i < a * per; i += threads) y[i] = make_uint4(0, 0, 0, 0);
+    for (long long i = b * per + me; i < v.rows * per; i += threads) y[i] = make_uint4(0, 0, 0, 0);
+}
+
+// Running (m, l, a) with one more part: O = sum 2^(m_i - m) O_i, l likewise.
+// 2^-inf = 0: nothing before, or nothing seen.
+__device__ __forceinline__ void join_part(float& m, float& l, float4& a, float2 ml, const float4& b) {
+    const float mm = fmaxf(m, ml.x), base = mm == -INFINITY ? 0.0f : mm;
+    const float f = ex2(m - base), e = ex2(ml.x - base);
+    m = mm;
+    l = l * f + ml.y * e;
+    a.x = a.x * f + b.x * e;
+    a.y = a.y * f + b.y * e;
+    a.z = a.z * f + b.z * e;
+    a.w = a.w * f + b.w * e;
+}
+__device__ __forceinline__ uint2 joined(float l, const float4& a) {
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    return make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+}
+
 // Joins the parts of the tile that begins in slot 1 of CTA blockIdx.x and goes
-// on in slot 0 of the next ones: O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i,
-// in the order of the keys.  A warp takes 128 / D rows at a time, 16 bytes a
-// lane.  zero_rest: also clears the rows of O that no sequence owns.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(ROWS == R ? 256 : 1024) attn_join_kernel(PagedView v, int group, int heads, const float* part_o,
-                                                                           const float* part_ml, const int4* desc,
-                                                                           __nv_bfloat16* o, int zero_rest) {
+// on in slot 0 of the next ones, O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i,
+// in a fixed order.  Slot 1 of the first CTA is followed in memory by slot 0 of
+// the next; then comes every second slot.  D / 4 lanes take a row, 16 bytes each.
+// Tiles of many rows have few parts: a row's lanes take them one after the other.
+template <int D>
+__global__ void __launch_bounds__(1024) attn_join_rows_kernel(PagedView v, int group, int heads, const float* part_o,
+                                                              const float* part_ml, const int4* desc, __nv_bfloat16* o,
+                                                              int zero_rest) {
     pdl_trigger();
     pdl_wait();
-    constexpr int LANES = D / 4, PER_WARP = 32 / LANES;
+    constexpr int LANES = D / 4, ROWS = 128;
     const int4 x = desc[blockIdx.x];  // the tile's first row, KV head, rows, parts
-    if (zero_rest) {
-        const int a = imin(imax(v.q_start[0], 0), v.rows), b = imin(imax(v.q_start[v.n_seqs], a), v.rows);
-        const long long per = static_cast<long long>(heads) * D / 8;
-        const long long threads = static_cast<long long>(gridDim.x) * blockDim.x;
-        const long long me = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-        uint4* y = reinterpret_cast<uint4*>(o);
-        for (long long i = me; i < a * per; i += threads) y[i] = make_uint4(0, 0, 0, 0);
-        for (long long i = b * per + me; i < v.rows * per; i += threads) y[i] = make_uint4(0, 0, 0, 0);
-    }
+    if (zero_rest) clear_rest(v, heads * D * 2, o);
     const int c = (threadIdx.x % LANES) * 4;
-    for (int i = threadIdx.x / LANES; i < x.z; i += (blockDim.x / 32) * PER_WARP) {
-        if (x.w == 0) return;
-        // Slot 1 of the first CTA is followed in memory by slot 0 of the next; then every second slot.
+    for (int i = threadIdx.x / LANES; i < x.z; i += 1024 / LANES) {
         auto slot = [&](int k) { return (static_cast<long long>(blockIdx.x) * 2 + (k == 0 ? 1 : 2 * k)) * ROWS + i; };
         float m = -INFINITY, l = 0.0f;
         float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int k = 0; k < x.w; ++k) {
-            const float2 ml = *reinterpret_cast<const float2*>(part_ml + slot(k) * 2);
-            const float4 b = *reinterpret_cast<const float4*>(part_o + slot(k) * D + c);
-            const float mm = fmaxf(m, ml.x), base = mm == -INFINITY ? 0.0f : mm;
-            const float f = ex2(m - base), e = ex2(ml.x - base);  // 2^-inf = 0: nothing before, nothing seen
-            m = mm;
-            l = l * f + ml.y * e;
-            a.x = a.x * f + b.x * e;
-            a.y = a.y * f + b.y * e;
-            a.z = a.z * f + b.z * e;
-            a.w = a.w * f + b.w * e;
-        }
-        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        for (int k = 0; k < x.w; ++k)
+            join_part(m, l, a, *reinterpret_cast<const float2*>(part_ml + slot(k) * 2),
+                      *reinterpret_cast<const float4*>(part_o + slot(k) * D + c));
         const int tok = i / group;
-        __nv_bfloat16* y = o + (static_cast<long long>(x.x + tok) * heads + x.y * group + i - tok * group) * D + c;
-        *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        *reinterpret_cast<uint2*>(o + (static_cast<long long>(x.x + tok) * heads + x.y * group + i - tok * group) * D + c) = joined(l, a);
+    }
+}
+
+// Tiles of few rows may have a part in every CTA: JW groups of D / 4 lanes a row
+// take them in turn (every JW-th), so that one long sequence is not joined at a
+// part's latency each; the groups' sums are joined in order through shared memory.
+template <int D>
+__global__ void __launch_bounds__(1024) attn_join_parts_kernel(PagedView v, int group, int heads, const float* part_o,
+                                                               const float* part_ml, const int4* desc, __nv_bfloat16* o,
+                                                               int zero_rest) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr int LANES = D / 4, JW = 8, AT_ONCE = 1024 / LANES / JW;  // rows at once
+    __shared__ float4 sums[JW][AT_ONCE][LANES];
+    __shared__ float2 mls[JW][AT_ONCE];
+    const int4 x = desc[blockIdx.x];  // the tile's first row, KV head, rows, parts
+    if (zero_rest) clear_rest(v, heads * D * 2, o);
+    const int lane = threadIdx.x % LANES, jw = (threadIdx.x / LANES) % JW, ir = threadIdx.x / (LANES * JW);
+    for (int i0 = 0; i0 < x.z; i0 += AT_ONCE) {
+        const int i = i0 + ir;
+        float m = -INFINITY, l = 0.0f;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < x.z) {
+            auto slot = [&](int k) { return (static_cast<long long>(blockIdx.x) * 2 + (k == 0 ? 1 : 2 * k)) * R + i; };
+#pragma unroll 4
+            for (int k = jw; k < x.w; k += JW)
+                join_part(m, l, a, *reinterpret_cast<const float2*>(part_ml + slot(k) * 2),
+                          *reinterpret_cast<const float4*>(part_o + slot(k) * D + lane * 4));
+        }
+        sums[jw][ir][lane] = a;
+        if (lane == 0) mls[jw][ir] = make_float2(m, l);
+        __syncthreads();
+        if (jw == 0 && i < x.z) {
+#pragma unroll
+            for (int k = 1; k < JW; ++k) join_part(m, l, a, mls[k][ir], sums[k][ir][lane]);
+            const int tok = i / group;
+            *reinterpret_cast<uint2*>(o + (static_cast<long long>(x.x + tok) * heads + x.y * group + i - tok * group) * D + lane * 4) =
+                joined(l, a);
+        }
+        __syncthreads();
     }
 }
 
@@ -744,11 +791,10 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     return tpi::attn_join_launch(a, R, O, w, s, grid, zero_rest, stream, err);
 }
 
-template <int D, int ROWS>
-cudaError_t join(const tpi::PagedArgs& a, void* O, uint8_t* w, const Scratch& s, int grid, bool zero_rest,
+template <class Kernel>
+cudaError_t join(Kernel kernel, const tpi::PagedArgs& a, void* O, uint8_t* w, const Scratch& s, int grid, bool zero_rest,
                  cudaStream_t stream) {
-    return tpi::launch_pdl(attn_join_kernel<D, ROWS>, dim3(grid), dim3(ROWS == R ? 256 : 1024), 0, stream,
-                           tpi::paged_view(a), a.heads / a.kv_heads, a.heads,
+    return tpi::launch_pdl(kernel, dim3(grid), dim3(1024), 0, stream, tpi::paged_view(a), a.heads / a.kv_heads, a.heads,
                            reinterpret_cast<const float*>(w + s.o), reinterpret_cast<const float*>(w + s.ml),
                            reinterpret_cast<const int4*>(w + s.desc), static_cast<__nv_bfloat16*>(O), zero_rest ? 1 : 0);
 }
@@ -762,13 +808,9 @@ size_t attn_paged_scratch_bytes(int head_dim) { return scratch_of(device_sm_coun
 
 int attn_join_launch(const PagedArgs& a, int slot_rows, void* O, uint8_t* w, const Scratch& s, int grid,
                      bool zero_rest, cudaStream_t stream, std::string* err) {
-    cudaError_t e;
-    if (a.head_dim == 128)
-        e = slot_rows == R ? join<128, R>(a, O, w, s, grid, zero_rest, stream)
-                           : join<128, 128>(a, O, w, s, grid, zero_rest, stream);
-    else
-        e = slot_rows == R ? join<64, R>(a, O, w, s, grid, zero_rest, stream)
-                           : join<64, 128>(a, O, w, s, grid, zero_rest, stream);
+    auto kernel = a.head_dim == 128 ? (slot_rows == R ? attn_join_parts_kernel<128> : attn_join_rows_kernel<128>)
+                                    : (slot_rows == R ? attn_join_parts_kernel<64> : attn_join_rows_kernel<64>);
+    const cudaError_t e = join(kernel, a, O, w, s, grid, zero_rest, stream);
     return launched("paged attention join launch", e, err);
 }
 
