@@ -100,8 +100,10 @@ __device__ __forceinline__ int share_of(long long at, long long per) {
 // shared memory).  Sequences are summed in runs, and a scan of the sums finds
 // the one where the share begins; the tile is then looked for 32 at a time.  Up
 // to 256 sequences every warp does that alone, a run a lane: two barriers of
-// the CTA less in front of its first load.  More: a run a thread.  sums: NT / 32
-// + 2 words of 8 bytes of shared memory.
+// the CTA less in front of its first load.  More: a run a thread.  What a lane
+// found of its sequence goes to the others by shuffles: a second read of its
+// lengths, and a second count of its blocks, cost about 2000 cycles.  sums: NT /
+// 32 + 2 words of 8 bytes of shared memory.
 struct Share {
     long long begin, count, per;
 };
@@ -111,9 +113,14 @@ __device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t,
     const bool alone = v.n_seqs <= 256;
     const int run = alone ? (v.n_seqs + 31) / 32 : (v.n_seqs + NT - 1) / NT;
     const int s0 = min((alone ? lane : tid) * run, v.n_seqs), s1 = min(s0 + run, v.n_seqs);
-    long long mine = 0;
+    long long mine = 0, per_head = 0;
+    PagedSeq q = {0, 0, 0};
 #pragma unroll 1
-    for (int s = s0; s < s1; ++s) mine += seq_blocks(v, paged_seq(v, s), t);
+    for (int s = s0; s < s1; ++s) {
+        q = paged_seq(v, s);
+        per_head = head_blocks(v, q, t);
+        mine += per_head * v.kv_heads;
+    }
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -121,7 +128,7 @@ __device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t,
         if (lane >= o) inc += x;
     }
     long long before = inc - mine, total = __shfl_sync(0xffffffffu, inc, 31);
-    if (!alone) {
+    if (__builtin_expect(!alone, 0)) {
         if (lane == 31) sums[tid >> 5] = inc;
         __syncthreads();
         total = 0;
@@ -138,19 +145,24 @@ __device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t,
     const bool here = x.count > 0 && x.begin >= before && x.begin < before + mine;
     int s = s0;
     long long off = x.begin - before;
-    if (here) {
+    if (__builtin_expect(run > 1 && here, 0)) {
 #pragma unroll 1
-        for (; s < s1 - 1; ++s) {
-            const long long n = seq_blocks(v, paged_seq(v, s), t);
-            if (off < n) break;
-            off -= n;
+        for (;; ++s) {
+            q = paged_seq(v, s);
+            per_head = head_blocks(v, q, t);
+            if (s == s1 - 1 || off < per_head * v.kv_heads) break;
+            off -= per_head * v.kv_heads;
         }
     }
-    if (alone) {
+    if (__builtin_expect(alone, 1)) {
         const unsigned who = __ballot_sync(0xffffffffu, here);
         const int from = who ? __ffs(who) - 1 : 0;
         s = __shfl_sync(0xffffffffu, s, from);
         off = __shfl_sync(0xffffffffu, off, from);
+        per_head = __shfl_sync(0xffffffffu, per_head, from);
+        q.row0 = __shfl_sync(0xffffffffu, q.row0, from);
+        q.n = __shfl_sync(0xffffffffu, q.n, from);
+        q.len = __shfl_sync(0xffffffffu, q.len, from);
     } else {
         if (here) {
             sums[NT / 32] = off;
@@ -159,11 +171,13 @@ __device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t,
         __syncthreads();
         off = sums[NT / 32];
         s = static_cast<int>(sums[NT / 32 + 1]);
+        if (x.count > 0) {
+            q = paged_seq(v, s);
+            per_head = head_blocks(v, q, t);
+        }
     }
     if (x.count > 0) {
-        const PagedSeq q = paged_seq(v, s);
         const int keys = paged_keys(v, q), tiles = seq_tiles(q, t);
-        const long long per_head = tiles == 1 ? tile_blocks(q, keys, t, 0) : tiles_blocks(q, keys, t, tiles);
         int g = 0;
 #pragma unroll 1
         for (; off >= per_head; ++g) off -= per_head;
@@ -174,11 +188,14 @@ __device__ __forceinline__ Share find_share(const PagedView& v, const Tiling& t,
 #pragma unroll 1
             for (;; step /= 32) {
                 const int at = lo + lane * step;
-                const bool before_off = at < tiles && tiles_blocks(q, keys, t, at) <= off;
-                lo += (__popc(__ballot_sync(0xffffffffu, before_off)) - 1) * step;
-                if (step == 1) break;
+                const long long blocks = tiles_blocks(q, keys, t, at < tiles ? at : 0);
+                const int last = __popc(__ballot_sync(0xffffffffu, at < tiles && blocks <= off)) - 1;
+                lo += last * step;
+                if (step == 1) {
+                    off -= __shfl_sync(0xffffffffu, blocks, last);
+                    break;
+                }
             }
-            off -= tiles_blocks(q, keys, t, lo);
         }
         if (lane == 0) {
             walk.q = q;

@@ -116,7 +116,8 @@ TP_HD int token_keys(const PagedSeq& q, int keys, int i) {
     return seen < keys ? seen : keys;
 }
 
-TP_HD int seq_tiles(const PagedSeq& q, const Tiling& t) { return static_cast<int>((static_cast<unsigned>(q.n) + t.tok - 1u) / static_cast<unsigned>(t.tok)); }
+TP_HD unsigned by_tok(unsigned x, const Tiling& t) { return t.log2_tok >= 0 ? x >> t.log2_tok : x / static_cast<unsigned>(t.tok); }
+TP_HD int seq_tiles(const PagedSeq& q, const Tiling& t) { return static_cast<int>(by_tok(static_cast<unsigned>(q.n + t.tok - 1), t)); }
 
 // Tokens of a tile that are the sequence's.
 TP_HD int tile_tokens(const PagedSeq& q, const Tiling& t, int tile) {
@@ -131,8 +132,9 @@ TP_HD int tile_blocks(const PagedSeq& q, int keys, const Tiling& t, int tile) {
 
 // sum_{x < n} floor(x / 2^k).
 TP_HD long long quotient_sum(unsigned n, int k) {
-    const long long q = n >> k, r = n & ((1u << k) - 1);
-    return ((q * (q - 1) / 2) << k) + r * q;
+    const unsigned q = n >> k, r = n & ((1u << k) - 1);
+    if (n < 65536u) return static_cast<long long>(((q * (q - 1) / 2) << k) + r * q);  // below n^2
+    return ((static_cast<long long>(q) * (q - 1) / 2) << k) + static_cast<long long>(r) * q;
 }
 
 // sum_{x < n} floor((a x + b) / m), by Euclid's algorithm on (m, a).  a n + b
@@ -155,7 +157,7 @@ TP_HD long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
 }
 
 // Blocks of the first `count` tiles of one KV head of a sequence.
-TP_HD_CALL long long tiles_blocks(const PagedSeq& q, int keys, const Tiling& t, int count) {
+TP_HD_CALL long long tiles_blocks(const PagedSeq q, int keys, const Tiling t, int count) {
     if (count <= 0) return 0;
     long long sum = 0;
     if (count == seq_tiles(q, t)) sum += tile_blocks(q, keys, t, --count);  // the last tile may be short
@@ -163,8 +165,8 @@ TP_HD_CALL long long tiles_blocks(const PagedSeq& q, int keys, const Tiling& t, 
     // then ceil(keys / KB).
     const int base = q.len - q.n, kb = 1 << t.log2_keys;
     const unsigned tok = static_cast<unsigned>(t.tok);
-    const unsigned one = kb < base ? 0u : static_cast<unsigned>(kb - base) / tok;
-    const unsigned full = keys <= base ? 0u : (static_cast<unsigned>(keys) - static_cast<unsigned>(base) - 1u) / tok;
+    const unsigned one = kb < base ? 0u : by_tok(static_cast<unsigned>(kb - base), t);
+    const unsigned full = keys <= base ? 0u : by_tok(static_cast<unsigned>(keys) - static_cast<unsigned>(base) - 1u, t);
     const unsigned n = static_cast<unsigned>(count);
     const unsigned c1 = one < n ? one : n;
     const unsigned c2 = full < c1 ? c1 : full < n ? full : n;
@@ -182,12 +184,16 @@ TP_HD_CALL long long tiles_blocks(const PagedSeq& q, int keys, const Tiling& t, 
     return sum + static_cast<long long>(n - c2) * most;
 }
 
-// Blocks of a sequence, all KV heads.
-TP_HD long long seq_blocks(const PagedView& v, const PagedSeq& q, const Tiling& t) {
+// Blocks of a sequence, one KV head.
+TP_HD long long head_blocks(const PagedView& v, const PagedSeq& q, const Tiling& t) {
     if (q.n <= 0) return 0;
     const int keys = paged_keys(v, q);
-    return (q.n <= t.tok ? tile_blocks(q, keys, t, 0) : tiles_blocks(q, keys, t, seq_tiles(q, t))) *
-           static_cast<long long>(v.kv_heads);
+    return q.n <= t.tok ? tile_blocks(q, keys, t, 0) : tiles_blocks(q, keys, t, seq_tiles(q, t));
+}
+
+// Blocks of a sequence, all KV heads.
+TP_HD long long seq_blocks(const PagedView& v, const PagedSeq& q, const Tiling& t) {
+    return head_blocks(v, q, t) * static_cast<long long>(v.kv_heads);
 }
 
 // A CTA's walk over its share: segments of consecutive blocks of one tile.
