@@ -109,7 +109,7 @@ struct Params {
     int o_boxes;               // 1: G divides 32, so that such a box is whole tokens
     PagedView v;
     __nv_bfloat16* o;
-    int heads, group, tile_tok, log2_tok, box_rows;
+    int heads, group, tile_tok, log2_tok, box_rows, least, most;
     int kv_per_shard;        // KV heads of a shard, 0 if shards share them
     int shards_per_kv;       // shards that share a KV head (1 if they have their own)
     float scale_log2;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::BAR_OFF + 8 * NUM_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Tiling tiling = {p.tile_tok, p.group, 7, p.log2_tok};
+    const Tiling tiling = {p.tile_tok, p.group, 7, p.log2_tok, p.least, p.most};
     const Waiter wait = {abort_flag, p.status, p.timeout_ns};
 
     if (threadIdx.x == 0) {
@@ -715,6 +715,8 @@ int launch(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, cuda
     p.group = a.heads / a.kv_heads;
     p.tile_tok = QB / p.group;
     p.log2_tok = exact_log2(p.tile_tok);
+    p.least = a.least;
+    p.most = a.most;
     p.kv_per_shard = a.kv_heads / a.t;
     p.shards_per_kv = p.kv_per_shard ? 1 : a.t / a.kv_heads;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(L::D));

@@ -85,7 +85,7 @@ struct Params {
     const __nv_bfloat16* qkv;
     long long ld_qkv;
     __nv_bfloat16* o;
-    int heads, heads_per_shard, shard_w, group, tile_tok, log2_tok, box_rows;
+    int heads, heads_per_shard, shard_w, group, tile_tok, log2_tok, box_rows, least, most;
     float scale_log2;
     float* part_o;   // [grid][2][R][D]
     float* part_ml;  // [grid][2][R][2]
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
     const uint32_t full0 = base + C::BAR_OFF, empty0 = full0 + 8 * NST;
     volatile int* abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Tiling tiling = {p.tile_tok, p.group, C::LOG2_KB, p.log2_tok};
+    const Tiling tiling = {p.tile_tok, p.group, C::LOG2_KB, p.log2_tok, p.least, p.most};
     const Waiter wait = {abort_flag, p.status, p.timeout_ns};
 
     if (threadIdx.x == 0) {
@@ -769,6 +769,8 @@ int launch_few(const tpi::PagedArgs& a, void* O, void* scratch, bool zero_rest, 
     p.group = a.heads / a.kv_heads;
     p.tile_tok = 8 * C::NB / p.group;
     p.log2_tok = exact_log2(p.tile_tok);
+    p.least = a.least;
+    p.most = a.most;
     p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(C::D));
     const Scratch s = tpi::scratch_of(grid, R, C::D);
     uint8_t* w = static_cast<uint8_t*>(scratch);
@@ -799,6 +801,22 @@ cudaError_t join(Kernel kernel, const tpi::PagedArgs& a, void* O, uint8_t* w, co
                            reinterpret_cast<const int4*>(w + s.desc), static_cast<__nv_bfloat16*>(O), zero_rest ? 1 : 0);
 }
 
+// Tiles of 8 rows, or of 16.
+int few(const tpi::PagedArgs& a, int64_t rows, void* O, void* scratch, bool zero_rest, cudaStream_t stream, std::string* err) {
+    if (rows <= 8) {
+        if (a.head_dim == 128)
+            return a.e4m3 ? launch_few<Cfg<128, true, 1, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
+                          : launch_few<Cfg<128, false, 1, 8, 4, 1, 4>>(a, O, scratch, zero_rest, stream, err);
+        return a.e4m3 ? launch_few<Cfg<64, true, 1, 8, 4, 2, 8>>(a, O, scratch, zero_rest, stream, err)
+                      : launch_few<Cfg<64, false, 1, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
+    }
+    if (a.head_dim == 128)
+        return a.e4m3 ? launch_few<Cfg<128, true, 2, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
+                      : launch_few<Cfg<128, false, 2, 8, 4, 1, 4>>(a, O, scratch, zero_rest, stream, err);
+    return a.e4m3 ? launch_few<Cfg<64, true, 2, 8, 4, 2, 8>>(a, O, scratch, zero_rest, stream, err)
+                  : launch_few<Cfg<64, false, 2, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
+}
+
 }  // namespace
 
 namespace tpi {
@@ -825,19 +843,23 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
     // of 8 or 16.  More: tiles of 128 on tcgen05.
     const int group = a.heads / a.kv_heads;
     const int64_t most = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
-    if (most * group > R) return attn_chunk_launch(a, O, scratch, zero_rest, stream, err);
-    if (most * group <= 8) {
-        if (a.head_dim == 128)
-            return a.e4m3 ? launch_few<Cfg<128, true, 1, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
-                          : launch_few<Cfg<128, false, 1, 8, 4, 1, 4>>(a, O, scratch, zero_rest, stream, err);
-        return a.e4m3 ? launch_few<Cfg<64, true, 1, 8, 4, 2, 8>>(a, O, scratch, zero_rest, stream, err)
-                      : launch_few<Cfg<64, false, 1, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
+    if (most * group <= R) return few(a, most * group, O, scratch, zero_rest, stream, err);
+    // A mixture from an 8-bit cache: at most half of n_seqs x most tokens are there, so many sequences have few.
+    // Those go to the few-row kernel, which reads codes at the memory's rate, where the 128-row tiles take 2 us a
+    // block whatever their rows (one chunk of 500 tokens and 23 single ones over 8000 keys: 296 -> 211 us, over 2000:
+    // 100 -> 85; over 500: 49 either way, over 200: 39 -> 44).  From bf16 the one launch is faster (170 and 205 us over
+    // 8000).
+    if (a.e4m3 && group <= R && 2 * a.tokens <= a.n_seqs * most && static_cast<int64_t>(a.max_pages) * a.page_size >= 1024) {
+        const int rows = group <= 8 ? 8 : R;
+        PagedArgs part = a;
+        part.most = rows / group;
+        const int rc = few(part, rows, O, scratch, false, stream, err);
+        if (rc) return rc;
+        part = a;
+        part.least = rows / group + 1;
+        return attn_chunk_launch(part, O, scratch, zero_rest, stream, err);
     }
-    if (a.head_dim == 128)
-        return a.e4m3 ? launch_few<Cfg<128, true, 2, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
-                      : launch_few<Cfg<128, false, 2, 8, 4, 1, 4>>(a, O, scratch, zero_rest, stream, err);
-    return a.e4m3 ? launch_few<Cfg<64, true, 2, 8, 4, 2, 8>>(a, O, scratch, zero_rest, stream, err)
-                  : launch_few<Cfg<64, false, 2, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
+    return attn_chunk_launch(a, O, scratch, zero_rest, stream, err);
 }
 
 }  // namespace tpi

@@ -217,6 +217,7 @@ struct PagedArgs {
     const int32_t *page_table = nullptr, *q_start = nullptr, *kv_len = nullptr;
     int64_t n_pages = 0;
     int n_seqs = 0, max_pages = 0, page_size = 0, max_new = 0;
+    int least = 1, most = 0x7fffffff;        // attention: new tokens of the sequences that a launch takes
     const void* QKV = nullptr;               // [tokens][ld_qkv], shard-blocked
     int64_t tokens = 0, ld_qkv = 0;
     int64_t shard_w = 0, q_w = 0, kv_w = 0;  // column layout of one shard

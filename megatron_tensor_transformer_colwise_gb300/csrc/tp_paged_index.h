@@ -97,6 +97,7 @@ struct Tiling {
     int tok, group;  // tokens of a tile, G
     int log2_keys;   // KB = 2^log2_keys
     int log2_tok;    // log2 of tok, -1 if that is not a power of two (at most KB)
+    int least = 1, most = 0x7fffffff;  // new tokens of the sequences that are taken; the others are as if they had none
 };
 
 inline int exact_log2(int x) {
@@ -115,6 +116,8 @@ TP_HD int token_keys(const PagedSeq& q, int keys, int i) {
     const int seen = q.len - q.n + i + 1;
     return seen < keys ? seen : keys;
 }
+
+TP_HD bool taken(const PagedSeq& q, const Tiling& t) { return q.n >= t.least && q.n <= t.most; }
 
 TP_HD unsigned by_tok(unsigned x, const Tiling& t) { return t.log2_tok >= 0 ? x >> t.log2_tok : x / static_cast<unsigned>(t.tok); }
 TP_HD int seq_tiles(const PagedSeq& q, const Tiling& t) { return static_cast<int>(by_tok(static_cast<unsigned>(q.n + t.tok - 1), t)); }
@@ -186,7 +189,7 @@ TP_HD_CALL long long tiles_blocks(const PagedSeq q, int keys, const Tiling t, in
 
 // Blocks of a sequence, one KV head.
 TP_HD long long head_blocks(const PagedView& v, const PagedSeq& q, const Tiling& t) {
-    if (q.n <= 0) return 0;
+    if (!taken(q, t)) return 0;
     const int keys = paged_keys(v, q);
     return q.n <= t.tok ? tile_blocks(q, keys, t, 0) : tiles_blocks(q, keys, t, seq_tiles(q, t));
 }
@@ -222,7 +225,7 @@ struct TileWalk {
                         return;
                     }
                     q = paged_seq(v, s);
-                } while (q.n == 0);
+                } while (!taken(q, t));
                 keys = paged_keys(v, q);
                 tiles = seq_tiles(q, t);
             }

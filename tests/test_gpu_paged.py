@@ -122,6 +122,19 @@ def test_attention_split_over_long_sequences(kv, lens):
     check_attention(x, O)
 
 
+# Long sequences' chunks between single tokens: from 8 bits a launch for each, the sequences told apart on the GPU.
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("geo,page", [((8, 2, 128, 2), 64), ((16, 1, 64, 1), 16), ((6, 2, 64, 2), 128), ((32, 2, 128, 2), 32)])
+@pytest.mark.parametrize("lens", [[(1, 1200), (50, 300), (0, 40), (2, 700), (3, 2), (1, 1), (9, 9), (1, 64)],
+                                  [(1, 1100)] * 5 + [(33, 40)], [(40, 1050), (0, 0), (0, 9), (0, 3)],
+                                  [(0, 0)] + [(1, 30)] * 300 + [(17, 1030)]])
+def test_attention_of_a_mixture(geo, page, kv, lens):
+    x = Paged(*geo, page, lens, kv, seed=12, pad=3, first=2)
+    plan, O = attend(x)
+    sync_ok(plan)
+    check_attention(x, O)
+
+
 def test_attention_of_many_sequences():
     rng = np.random.default_rng(8)
     lens = [(int(n), int(n + c)) for n, c in zip(rng.integers(0, 3, 700), rng.integers(0, 40, 700))]
