@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
             const int rows = have ? tile_tokens(w.q, tiling, w.tile) * p.group : 0;
             const bool active = q * 32 < rows;  // some row of the quadrant is the tile's
             // Keys behind the current block's first (lim: that this row sees, from this half's first on; left: that exist).
-            int lim = (r < rows ? token_keys(w.q, w.keys, w.tile * p.tile_tok + r / p.group) : 0) - w.kb * KB - hf * KC;
+            int lim = token_keys(w.q, w.keys, w.tile * p.tile_tok + min(r, rows - 1) / p.group) - w.kb * KB - hf * KC;
             int left = w.keys - w.kb * KB;
             float m_ref = -INFINITY, l_sum = 0.0f;
 #pragma unroll 1

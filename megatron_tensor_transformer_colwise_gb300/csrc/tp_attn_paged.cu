@@ -801,7 +801,7 @@ cudaError_t join(Kernel kernel, const tpi::PagedArgs& a, void* O, uint8_t* w, co
                            reinterpret_cast<const int4*>(w + s.desc), static_cast<__nv_bfloat16*>(O), zero_rest ? 1 : 0);
 }
 
-// Tiles of 8 rows, or of 16.
+// Tiles of 8 rows, or of 16 (not for heads of 128 from bf16).
 int few(const tpi::PagedArgs& a, int64_t rows, void* O, void* scratch, bool zero_rest, cudaStream_t stream, std::string* err) {
     if (rows <= 8) {
         if (a.head_dim == 128)
@@ -810,9 +810,7 @@ int few(const tpi::PagedArgs& a, int64_t rows, void* O, void* scratch, bool zero
         return a.e4m3 ? launch_few<Cfg<64, true, 1, 8, 4, 2, 8>>(a, O, scratch, zero_rest, stream, err)
                       : launch_few<Cfg<64, false, 1, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
     }
-    if (a.head_dim == 128)
-        return a.e4m3 ? launch_few<Cfg<128, true, 2, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
-                      : launch_few<Cfg<128, false, 2, 8, 4, 1, 4>>(a, O, scratch, zero_rest, stream, err);
+    if (a.head_dim == 128) return launch_few<Cfg<128, true, 2, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
     return a.e4m3 ? launch_few<Cfg<64, true, 2, 8, 4, 2, 8>>(a, O, scratch, zero_rest, stream, err)
                   : launch_few<Cfg<64, false, 2, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err);
 }
@@ -840,10 +838,19 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
                         cudaMemsetAsync(O, 0, static_cast<size_t>(a.tokens) * a.heads * a.head_dim * 2, stream), err);
     }
     // Few rows a sequence and KV head (the caller's bound on its new tokens, or all rows of the call): one tile
-    // of 8 or 16.  More: tiles of 128 on tcgen05.
+    // of 8 or 16.  More: tiles of 128 on tcgen05.  32 sequences over 1000 / 8000 keys, 8 KV heads, in us:
+    //                  bf16 d = 64       e4m3 d = 64       bf16 d = 128      e4m3 d = 128
+    //   8 rows   8:    16.1 /  86        19.3 /  81        32.2 / 160        22.6 /  97
+    //           16:    18.3 /  88        21.0 /  89        34.7 / 165        30.0 / 134
+    //          128:    23.6 / 102        36.0 / 185        32.8 / 161        42.6 / 229
+    //  16 rows  16:    21.6 /  91        24.7 /  93        40.0 / 169        35.4 / 140
+    //          128:    23.7 / 102        36.2 / 186        32.9 / 163        43.3 / 230
+    //  24 rows  16:    31.0 / 165        36.5 / 171        54.1 / 318        55.0 / 260   (two tiles)
+    //          128:    23.8 / 102        36.5 / 186        33.7 / 164        44.2 / 231
     const int group = a.heads / a.kv_heads;
     const int64_t most = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
-    if (most * group <= R) return few(a, most * group, O, scratch, zero_rest, stream, err);
+    const int64_t bound = a.e4m3 || a.head_dim == 64 ? R : 8;
+    if (most * group <= bound) return few(a, most * group, O, scratch, zero_rest, stream, err);
     // A mixture from an 8-bit cache: at most half of n_seqs x most tokens are there, so many sequences have few.
     // Those go to the few-row kernel, which reads codes at the memory's rate, where the 128-row tiles take 2 us a
     // block whatever their rows (one chunk of 500 tokens and 23 single ones over 8000 keys: 296 -> 211 us, over 2000:
