@@ -529,7 +529,7 @@ TP_API int tp_layer_forward_traced(tp_plan_t plan, const tp_bf16* X, const tp_la
 /* Element type of a key/value cache.
  * BF16: the projections' values as they are.
  * E4M3: 8-bit codes (4 exponent and 3 fraction bits, largest 448) with one
- *       fp32 scale per token and KV head, value = code * scale. */
+ *       fp32 scale per token and KV head, not negative, value = code * scale. */
 enum { TP_KV_BF16 = 0, TP_KV_E4M3 = 1 };
 
 /* A cache of the keys and values of many sequences in pages of page_size

@@ -199,6 +199,23 @@ def test_pages_outside_the_cache(kv):
         assert torch.equal(out[0][s, :x.len[s]].cpu(), torch.from_numpy(x.cached("K", s)).float().to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[(1, 300), (1, 80), (2, 40)], [(20, 300), (20, 80), (33, 200)]])
+def test_scales_of_zero(d, lens):
+    # A row of an 8-bit cache may hold a scale of zero (its values are zeros, whatever the codes), and all the rows of a
+    # sequence may, or have no page.
+    x = Paged(8, 2, d, 2, 16, lens, "e4m3", seed=22)
+    g = torch.Generator().manual_seed(23)
+    for sc in (x.ks, x.vs):
+        sc[torch.rand(sc.shape, generator=g) < 0.3] = 0
+    x.vs[x.table[1, :5]] = 0
+    x.table[2] = -1
+    plan, O = attend(x)
+    torch.cuda.synchronize()
+    assert tp.tp_get_device_status(plan) == tp.TP_ERR_INVALID_ARG
+    check_attention(x, O)
+
+
 def test_positions_past_the_page_table():
     x = Paged(8, 2, 64, 2, 16, [(1, 30), (1, 20)], seed=14)
     plan, cache = x.upload()
@@ -239,6 +256,34 @@ def test_captured_call_follows_the_lengths():
         K, V = (torch.from_numpy(t).view(torch.bfloat16) for t in y.written()[:2])
         y.K, y.V = K, V
         check_attention(y, O)
+
+
+def test_two_graphs_at_once():
+    # Each with a workspace of its own, replayed on two streams: a mixture (two pairs of launches) and single tokens.
+    calls = []
+    for lens, seed in (([(1, 1100), (30, 400), (1, 900), (0, 0), (1, 30)], 24), ([(1, 700), (1, 1300), (1, 5)], 25)):
+        x = Paged(8, 2, 128, 2, 64, lens, "e4m3", seed=seed)
+        plan, cache = x.upload()
+        n = tp.tp_plan_workspace_bytes(plan, tp.TP_OP_ATTN_PAGED)
+        ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+        QKV, O = dev(x.QKV), torch.full((x.rows, x.a * x.d), 7.0, dtype=torch.bfloat16, device="cuda")
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        tp.tp_attn_paged_forward(plan, cache, QKV, O, ws, n)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            for _ in range(4):
+                tp.tp_attn_paged_forward(plan, cache, QKV, O, ws, n)
+        O.fill_(7.0)
+        calls.append((x, plan, O, graph, side, cache, QKV, ws))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _, _, _, graph, side, *_ in calls:
+            with torch.cuda.stream(side):
+                graph.replay()
+    torch.cuda.synchronize()
+    for x, plan, O, *_ in calls:
+        sync_ok(plan)
+        check_attention(x, O)
 
 
 def test_on_another_stream():
