@@ -26,6 +26,13 @@
 // registers to the second product's operand by movmatrix.  mma.sync rather than
 // tcgen05, whose tile has 64 rows at least and whose P makes a round trip
 // through tensor memory.
+//
+// Measured, 32 query heads on 8 KV heads of 128: 64 single tokens over 500 to
+// 16000 keys from bf16 (1.04 GB) 160 us, 6.5 TB/s or 0.96 of the copy rate; over
+// 1000 to 32000 keys from 8 bits (1.17 GB) 203 us, 5.7 TB/s or 0.85: the codes'
+// conversion to fp16 and twice the keys a byte keep the schedulers busy.  One token
+// over 4096 keys 10.9 us: two launches, the look-up of the shares and one block a
+// CTA, each at its latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -684,6 +691,8 @@ __device__ __forceinline__ uint2 joined(float l, const float4& a) {
 // in a fixed order.  Slot 1 of the first CTA is followed in memory by slot 0 of
 // the next; then comes every second slot.  D / 4 lanes take a row, 16 bytes each.
 // Tiles of many rows have few parts: a row's lanes take them one after the other.
+// It moves two partial tiles a CTA at most (20 MB of fp32, in L2) and takes about
+// 4 us, most of it the launch.
 template <int D>
 __global__ void __launch_bounds__(1024) attn_join_rows_kernel(PagedView v, int group, int heads, const float* part_o,
                                                               const float* part_ml, const int4* desc, __nv_bfloat16* o,
@@ -709,7 +718,8 @@ __global__ void __launch_bounds__(1024) attn_join_rows_kernel(PagedView v, int g
 
 // Tiles of few rows may have a part in every CTA: JW groups of D / 4 lanes a row
 // take them in turn (every JW-th), so that one long sequence is not joined at a
-// part's latency each; the groups' sums are joined in order through shared memory.
+// part's latency each (one token over 4096 keys, 32 parts: 13.3 -> 11.5 us for both
+// kernels); the groups' sums are joined in order through shared memory.
 template <int D>
 __global__ void __launch_bounds__(1024) attn_join_parts_kernel(PagedView v, int group, int heads, const float* part_o,
                                                                const float* part_ml, const int4* desc, __nv_bfloat16* o,
