@@ -101,8 +101,8 @@ struct Lay {
     static constexpr int STG_OFF = V_OFF + 2 * TILE;  // 32 rows a softmax warp
     static constexpr int RAW_OFF = STG_OFF + (E4M3 ? 0 : 8 * 32 * STG_ROW);  // no room for staged outputs beside the codes
     static constexpr int SC_OFF = RAW_OFF + NRAW * RAW;
-    static constexpr int XCH_OFF = SC_OFF + (E4M3 ? NSC * 2 * KB * 4 : 0);  // [7][128] fp32: maxima x 2 x 2, sums x 2, references
-    static constexpr int BAR_OFF = XCH_OFF + 7 * QB * 4;
+    static constexpr int XCH_OFF = SC_OFF + (E4M3 ? NSC * 2 * KB * 4 : 0);  // [9][128] fp32: maxima and sums, each by parity and half; references
+    static constexpr int BAR_OFF = XCH_OFF + 9 * QB * 4;
     static constexpr int SCAN_OFF = BAR_OFF + 8 * NUM_BARS + 16;
     static constexpr int WALK_OFF = SCAN_OFF + 8 * (NT / 32 + 2);  // one walk a warp, and the producers' ahead
     static constexpr int DONE_OFF = WALK_OFF + (NT / 32 + 2) * sizeof(TileWalk);
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
             got = __all_sync(0xffffffffu, got);
             if (!pair_all(got)) return false;
             tc_fence_after();
-            const float l = xch[4 * QB + r] + xch[5 * QB + r];
+            const float l = xch[(4 + (eli & 1) * 2) * QB + r] + xch[(5 + (eli & 1) * 2) * QB + r];
             uint32_t o[DC];
 #pragma unroll
             for (int c = 0; c < DC / 32; ++c)
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
                     for (int c = 0; c < DC / 4; ++c)
                         dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
                                              __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
-                    if (hf == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(xch[6 * QB + r], l);
+                    if (hf == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(xch[8 * QB + r], l);
                 }
                 return true;
             }
@@ -693,8 +693,10 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
                 }
             }
             if (!ok || !have) break;
-            xch[(4 + hf) * QB + r] = l_sum;  // the epilogue's pair_all comes before either half reads
-            if (hf == 0) xch[6 * QB + r] = m_ref;
+            // The epilogue's pair_all comes before either half reads; by parity, since a segment of one block ends while the
+            // other half may still be reading the previous one's.
+            xch[(4 + (li & 1) * 2 + hf) * QB + r] = l_sum;
+            if (hf == 0) xch[8 * QB + r] = m_ref;
             pending = true;
             __syncwarp();
             if (lane == 0) {
