@@ -11,9 +11,9 @@
 // rounding.
 //
 // Both directions are bound by memory: every element is read and written once.
-// A row of d bf16 (128 or 256 bytes) is a group of d / 8 lanes, 16 bytes each,
-// so a warp moves 2 or 4 rows at a time, and a thread issues its loads of
-// several rows before the first is used.
+// A row of d bf16 (128 or 256 bytes) is a group of d / 16 lanes, two pieces of 16
+// bytes each (pieces c and c + d / 16, so that each access of a group is contiguous):
+// a warp moves 4 or 8 rows at a time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,6 +42,7 @@ struct KvParams {
     const __nv_bfloat16* qkv;
     long long ld_qkv;
     int shard_w, q_w, kv_w, held, heads_step;  // held: KV heads of a shard; heads_step: shards that share one (k < t), else 0
+    int log2_k;  // of the KV heads, -1 if that is no power of two
     unsigned* status;
     // read back
     __nv_bfloat16 *k_out, *v_out;
@@ -62,18 +63,22 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t codes) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// 16 bytes of a bf16 row to the cache.  at: the cache's row.  The LANES lanes
-// of a row call together (amax is theirs).
+// Two 16-byte pieces of a bf16 row, pieces c and c + LANES of it, to the cache.  at: the cache's row.  The LANES
+// lanes of a row call together (amax is theirs).
 template <int D, bool E4M3>
-__device__ __forceinline__ void store_row(const KvParams& p, bool is_v, long long at, int c, uint4 u, bool live) {
-    constexpr int LANES = D / 8;
+__device__ __forceinline__ void store_row(const KvParams& p, bool is_v, long long at, int c, const uint4 (&u)[2], bool live) {
+    constexpr int LANES = D / 16;
     if constexpr (!E4M3) {
-        if (live) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.V : p.K) + at * D + c * 8) = u;
+        uint4* y = reinterpret_cast<uint4*>(is_v ? p.V : p.K) + at * (D / 8) + c;
+        if (live) {
+            y[0] = u[0];
+            y[LANES] = u[1];
+        }
     } else {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        float x[8], amax = 0.0f;
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+        float x[16], amax = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
             const float2 f = unpack_bf16x2(w[e]);
             x[2 * e] = f.x;
             x[2 * e + 1] = f.y;
@@ -83,28 +88,31 @@ __device__ __forceinline__ void store_row(const KvParams& p, bool is_v, long lon
         for (int o = LANES / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         amax = fminf(fmaxf(amax, kAmaxFloor), kAmaxCeil);
         const float inv = __fdiv_rn(kE4M3Max, amax);
-        uint32_t r[2];
+        uint32_t r[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 4; ++e)
             r[e] = pack_e4m3x2(__fmul_rn(x[4 * e], inv), __fmul_rn(x[4 * e + 1], inv)) |
                    pack_e4m3x2(__fmul_rn(x[4 * e + 2], inv), __fmul_rn(x[4 * e + 3], inv)) << 16;
         if (live) {
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? p.V : p.K) + at * D + c * 8) = make_uint2(r[0], r[1]);
+            uint2* y = reinterpret_cast<uint2*>(is_v ? p.V : p.K) + at * (D / 8) + c;
+            y[0] = make_uint2(r[0], r[1]);
+            y[LANES] = make_uint2(r[2], r[3]);
             if (c == 0) (is_v ? p.v_scale : p.k_scale)[at] = __fdiv_rn(amax, kE4M3Max);
         }
     }
 }
 
-// Append.  A group of D / 8 lanes takes a (token, KV head) at a time, K and V
+// Append.  A group of D / 16 lanes takes a (token, KV head) at a time, K and V
 // together: their loads are in flight while the token's place is looked up.  8
 // blocks an SM walk the items.  8192 tokens of 8 heads of 128 into 8 bits take
-// 13.1 us (50 MB at 3.8 TB/s, the launch included); a block for every few tokens
-// with 4, 2 or 1 rows in flight a thread and one look-up for all heads takes 14.7
-// to 19.9, as each block then begins with the whole chain of look-ups.  64 single
-// tokens take 2.4 us, a launch.
+// 8.2 us, the launch included (50 MB at 6.1 TB/s; 11.3 with inputs not in L2).  A
+// lane's 32 bytes make that: with 16, and a division by k, the look-ups and quotients
+// of twice the lanes kept the schedulers at 0.73 and took 13.1 us.  A block for every
+// few tokens with one look-up for all heads took 14.7 to 19.9, since each then
+// begins with the whole chain of look-ups.  64 single tokens take 2.5 us, a launch.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(THREADS) kv_write_kernel(const __grid_constant__ KvParams p) {
-    constexpr int LANES = D / 8;
+    constexpr int LANES = D / 16;
     pdl_trigger();
     pdl_wait();
     // Every token's owner is looked up: in shared memory, when the sequences' starts fit.
@@ -122,13 +130,14 @@ __global__ void __launch_bounds__(THREADS) kv_write_kernel(const __grid_constant
     for (unsigned base = blockIdx.x * (THREADS / LANES); base < items; base += step) {
         const unsigned it = base + threadIdx.x / LANES;
         const bool in = it < items;
-        const int row = static_cast<int>((in ? it : 0) / static_cast<unsigned>(k));
+        const int row = static_cast<int>(p.log2_k >= 0 ? (in ? it : 0) >> p.log2_k : (in ? it : 0) / static_cast<unsigned>(k));
         const int g = static_cast<int>((in ? it : 0) - static_cast<unsigned>(row) * k);
         // k >= t: shard g / held holds g; k < t: the first of the shards that share it.
-        const int shard = p.heads_step ? g * p.heads_step : g / p.held;
+        const int shard = p.heads_step ? g * p.heads_step : p.held == 1 ? g : g / p.held;
         const int local = p.heads_step ? 0 : g - shard * p.held;
-        const __nv_bfloat16* x = p.qkv + row * p.ld_qkv + static_cast<long long>(shard) * p.shard_w + p.q_w + local * D + c * 8;
-        const uint4 kx = *reinterpret_cast<const uint4*>(x), vx = *reinterpret_cast<const uint4*>(x + p.kv_w);
+        const uint4* x = reinterpret_cast<const uint4*>(p.qkv + row * p.ld_qkv + static_cast<long long>(shard) * p.shard_w +
+                                                        p.q_w + local * D) + c;
+        const uint4 kx[2] = {x[0], x[LANES]}, vx[2] = {x[p.kv_w / 8], x[p.kv_w / 8 + LANES]};
         const int s = in ? paged_owner(staged ? starts : p.v.q_start, p.v.n_seqs, row) : -1;
         long long at = -1;
         if (s >= 0) {
@@ -235,6 +244,7 @@ KvParams params_of(const tpi::PagedArgs& a) {
     p.kv_w = static_cast<int>(a.kv_w);
     p.held = a.kv_heads >= a.t ? a.kv_heads / a.t : 1;
     p.heads_step = a.kv_heads >= a.t ? 0 : a.t / a.kv_heads;
+    p.log2_k = exact_log2(a.kv_heads);
     p.status = a.status;
     return p;
 }
@@ -253,7 +263,7 @@ namespace tpi {
 int kv_write_launch(const PagedArgs& a, cudaStream_t stream, std::string* err) {
     if (a.n_seqs == 0) return TP_OK;
     const KvParams p = params_of(a);
-    const long long groups = THREADS / (a.head_dim / 8);
+    const long long groups = THREADS / (a.head_dim / 16);
     const long long need = (a.tokens * a.kv_heads + groups - 1) / groups;
     const dim3 grid(static_cast<unsigned>(std::min<long long>(need, device_sm_count() * 8LL))), block(THREADS);
     cudaError_t e;
