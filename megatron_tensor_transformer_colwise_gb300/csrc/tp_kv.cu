@@ -152,14 +152,15 @@ __global__ void __launch_bounds__(THREADS) kv_write_kernel(const __grid_constant
     }
 }
 
-// Read back.  Block (chunk, sequence): 64 positions of a sequence, all heads.
-// A thread's turn is 16 bytes of K and of V of one (position, head), UNROLL
-// turns in flight.  16 sequences of 2000 to 16000 positions from 8 bits: 98 us,
-// 6.1 TB/s; 8 of up to 1000 from bf16: 3.2 us, a launch and its chain of loads.
-constexpr int READ_POS = 64;
+// Read back.  Block (chunk, sequence): 16 positions of a sequence, all heads.
+// A thread's turn is 32 bytes of bf16 of K and of V of one (position, head), UNROLL
+// turns in flight.  16 sequences of 2000 to 16000 positions from 8 bits: 90 us, 6.6
+// TB/s; with 64 positions a block 94, with 16 bytes a turn 98.  8 sequences of up to
+// 1000 from bf16: 2.5 us, a launch and its chain of loads (3.1 with 64 positions).
+constexpr int READ_POS = 16;  // the smallest page: a block's positions share one
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(THREADS) kv_read_kernel(const __grid_constant__ KvParams p) {
-    constexpr int LANES = D / 8, UNROLL = 4;
+    constexpr int LANES = D / 16, UNROLL = E4M3 ? 4 : 2;
     pdl_trigger();
     pdl_wait();
     const int s = blockIdx.x / p.chunks;
@@ -168,17 +169,13 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(const __grid_constant_
     const int n = static_cast<int>(pmin(READ_POS, len - first));
     if (n <= 0) return;
     const int c = threadIdx.x % LANES, k = p.v.kv_heads;
-    const int items = n * k, log2 = p.v.page_log2;
-    __shared__ long long pages[READ_POS / 16];  // of the block's positions, -1 outside the cache
-    if (threadIdx.x <= ((n - 1) >> log2)) {
-        pages[threadIdx.x] = paged_page(p.v, s, static_cast<int>(first) + (static_cast<int>(threadIdx.x) << log2));
-        if (pages[threadIdx.x] < 0 && p.status) atomicOr(p.status, kStatusPage);
-    }
-    __syncthreads();
+    const int items = n * k;
+    const long long page = paged_page(p.v, s, static_cast<int>(first));
+    if (page < 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusPage);
     // Items in the cache's order (position fastest within a page and head), so that neighbouring groups read
     // neighbouring rows.
     for (int i0 = threadIdx.x / LANES; i0 < items; i0 += UNROLL * (THREADS / LANES)) {
-        uint4 ku[UNROLL], vu[UNROLL];
+        uint4 ku[UNROLL][2], vu[UNROLL][2];
         float ks[UNROLL], vs[UNROLL];
         long long to[UNROLL];
 #pragma unroll
@@ -187,45 +184,52 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(const __grid_constant_
             to[e] = -1;
             if (i >= items) continue;
             const int g = i / n, pos = i - g * n;
-            const int in_page = static_cast<int>(first) + pos;
-            const long long page = pages[((in_page >> log2) - (static_cast<int>(first) >> log2))];
-            to[e] = ((s * p.max_len + first + pos) * k + g) * D + c * 8;
-            ku[e] = vu[e] = make_uint4(0, 0, 0, 0);
+            to[e] = ((s * p.max_len + first + pos) * k + g) * (D / 8) + c;
             ks[e] = vs[e] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ku[e][h] = vu[e][h] = make_uint4(0, 0, 0, 0);
             if (page < 0) continue;
-            const long long at = paged_row(p.v, page, g, in_page);
+            const long long at = paged_row(p.v, page, g, static_cast<int>(first) + pos);
             if constexpr (E4M3) {
-                const uint2 a = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.K) + at * D + c * 8));
-                const uint2 b = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.V) + at * D + c * 8));
-                ku[e].x = a.x;
-                ku[e].y = a.y;
-                vu[e].x = b.x;
-                vu[e].y = b.y;
                 ks[e] = p.k_scale[at];
                 vs[e] = p.v_scale[at];
-            } else {
-                ku[e] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.K) + at * D + c * 8));
-                vu[e] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.V) + at * D + c * 8));
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const long long x = at * (D / 8) + c + h * LANES;
+                if constexpr (E4M3) {
+                    const uint2 a = __ldcs(static_cast<const uint2*>(p.K) + x), b = __ldcs(static_cast<const uint2*>(p.V) + x);
+                    ku[e][h].x = a.x;
+                    ku[e][h].y = a.y;
+                    vu[e][h].x = b.x;
+                    vu[e][h].y = b.y;
+                } else {
+                    ku[e][h] = __ldcs(static_cast<const uint4*>(p.K) + x);
+                    vu[e][h] = __ldcs(static_cast<const uint4*>(p.V) + x);
+                }
             }
         }
 #pragma unroll
         for (int e = 0; e < UNROLL; ++e) {
             if (to[e] < 0) continue;
-            if constexpr (E4M3) {
-                auto expand = [](uint4 u, float f) {
-                    uint32_t r[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float2 v = unpack_e4m3x2((x < 2 ? u.x : u.y) >> (16 * (x & 1)));
-                        r[x] = pack_bf16x2(v.x * f, v.y * f);
-                    }
-                    return make_uint4(r[0], r[1], r[2], r[3]);
-                };
-                ku[e] = expand(ku[e], ks[e]);
-                vu[e] = expand(vu[e], vs[e]);
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (E4M3) {
+                    auto expand = [](uint4 u, float f) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float2 v = unpack_e4m3x2((x < 2 ? u.x : u.y) >> (16 * (x & 1)));
+                            r[x] = pack_bf16x2(v.x * f, v.y * f);
+                        }
+                        return make_uint4(r[0], r[1], r[2], r[3]);
+                    };
+                    ku[e][h] = expand(ku[e][h], ks[e]);
+                    vu[e][h] = expand(vu[e][h], vs[e]);
+                }
+                __stcs(reinterpret_cast<uint4*>(p.k_out) + to[e] + h * LANES, ku[e][h]);
+                __stcs(reinterpret_cast<uint4*>(p.v_out) + to[e] + h * LANES, vu[e][h]);
             }
-            __stcs(reinterpret_cast<uint4*>(p.k_out + to[e]), ku[e]);
-            __stcs(reinterpret_cast<uint4*>(p.v_out + to[e]), vu[e]);
         }
     }
 }
