@@ -23,7 +23,7 @@
 // registers and are joined across lanes once for both rows.  Measured: 64
 // sequences of 2 to 5 drafts over 128256 words 43.7 us where the rows that are
 // needed take 24 at the memory's rate (issue, and each batch's exchange); 2
-// sequences of 3 drafts over 32768 words 11.7 us, all of it latency: a batch's
+// sequences of 3 drafts over 32768 words 11.3 us, all of it latency: a batch's
 // loads, sums and exchange take about 2.5 us, the race as much.  Four rows a batch
 // bring that to 10.3 but 64 sequences to 53 and a refused first draft from 4.4 to
 // 6.2; deeper rings and prefetches of later rows change nothing.
@@ -132,6 +132,18 @@ __device__ __forceinline__ float prob(float x, float it, Stat st) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// What few calls need stays out of line, and a batch's rows share one loop's code: less to fetch in a call that
+// runs it once (97 -> 64 KB; 2 sequences of 3 drafts 11.7 -> 11.3 us, 64 sequences as before).
+
+// sum_pieces where m's product with the logits may overflow: logits at the type's ends.  m: the new maximum.
+__device__ __noinline__ Stat sum_ends(Stat a, uint4 u1, uint4 u2, float it, float m) {
+    const uint32_t w[8] = {u1.x, u1.y, u1.z, u1.w, u2.x, u2.y, u2.z, u2.w};
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += ex2f(scaled(bf16_lo(w[k]), it) - m) + ex2f(scaled(bf16_hi(w[k]), it) - m);
+    return {m, fmaf(a.s, ex2f(a.m - m), sum)};
+}
+
 // Two pieces of logits into a running state (u2 only if both).
 __device__ __forceinline__ void sum_pieces(Stat& a, const uint4& u1, const uint4& u2, float it) {
     const uint32_t w[8] = {u1.x, u1.y, u1.z, u1.w, u2.x, u2.y, u2.z, u2.w};
@@ -145,16 +157,14 @@ __device__ __forceinline__ void sum_pieces(Stat& a, const uint4& u1, const uint4
 #pragma unroll
     for (int k = 0; k < 4; ++k) bm[k] = max3(fmaxf(v[k], v[k + 4]), v[k + 8], v[k + 12]);
     const float m = fmaxf(a.m, scaled(max3(fmaxf(bm[0], bm[1]), bm[2], bm[3]), it));
-    float x[16];
-    if (fabsf(m) < 1e30f) {
-        const uint64_t its = f2_pack(it, it), minus = f2_pack(-m, -m);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f2_unpack(f2_fma(f2_pack(v[2 * k], v[2 * k + 1]), its, minus), x[2 * k], x[2 * k + 1]);
-    } else {  // nothing but -inf so far, or logits at the type's ends
-        if (m == -INFINITY) return;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = scaled(v[k], it) - m;
+    if (!(fabsf(m) < 1e30f)) {  // nothing but -inf so far, or logits at the type's ends
+        if (m != -INFINITY) a = sum_ends(a, u1, u2, it, m);
+        return;
     }
+    float x[16];
+    const uint64_t its = f2_pack(it, it), minus = f2_pack(-m, -m);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f2_unpack(f2_fma(f2_pack(v[2 * k], v[2 * k + 1]), its, minus), x[2 * k], x[2 * k + 1]);
     uint64_t sum[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -166,19 +176,30 @@ __device__ __forceinline__ void sum_pieces(Stat& a, const uint4& u1, const uint4
 }
 
 // The first of the largest logits: m the value, s the index's bits.
-__device__ __forceinline__ void best_piece(Stat& a, const uint4& u, int index) {
+__device__ __noinline__ Stat best_piece(Stat a, uint4 u, int index) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const float v = (k & 1) ? bf16_hi(w[k >> 1]) : bf16_lo(w[k >> 1]);
         if (v > a.m) a = {v, __int_as_float(index + k)};  // indices ascend in a thread
     }
+    return a;
 }
 // Two logits' weights.
 __device__ __forceinline__ uint64_t weight2(uint32_t w, uint64_t its, uint64_t minus) {
     float x0, x1;
     f2_unpack(f2_fma(f2_pack(bf16_lo(w), bf16_hi(w)), its, minus), x0, x1);
     return f2_pack(ex2f(x0), ex2f(x1));
+}
+
+// The same two of p - r q where logits stand at the type's ends.
+__device__ __noinline__ uint64_t weight2_ends(uint32_t z, uint32_t y, float it, float zm, float ym, float r) {
+    float a0 = weight(bf16_lo(z), it, zm), a1 = weight(bf16_hi(z), it, zm);
+    if (r != 0.0f) {
+        a0 = fmaf(-r, weight(bf16_lo(y), it, ym), a0);
+        a1 = fmaf(-r, weight(bf16_hi(y), it, ym), a1);
+    }
+    return f2_pack(a0, a1);
 }
 
 __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_kernel(const VerifyParams p) {
@@ -290,9 +311,10 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         } else {
             Stat a[ITEMS];
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                a[i] = {-INFINITY, 0.0f};
-                if (i >= items) continue;
+            for (int i = 0; i < ITEMS; ++i) a[i] = {-INFINITY, 0.0f};
+#pragma unroll 1
+            for (int i = 0; i < items; ++i) {
+                Stat b = {-INFINITY, 0.0f};
                 for (int at = begin; at < end; at += PPT * VT) {
                     ok = ok && wait(full0 + 8 * st, phase);
                     if (ok) {
@@ -303,15 +325,18 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
                             if (left <= 0) break;
                             const uint4 u1 = ring[st][e * VT + tid], u2 = left > VT ? ring[st][(e + 1) * VT + tid] : none;
                             if (greedy) {
-                                best_piece(a[i], u1, (at + e * VT + tid) * 8);
-                                best_piece(a[i], u2, (at + (e + 1) * VT + tid) * 8);
+                                b = best_piece(b, u1, (at + e * VT + tid) * 8);
+                                b = best_piece(b, u2, (at + (e + 1) * VT + tid) * 8);
                             } else {
-                                sum_pieces(a[i], u1, u2, it);
+                                sum_pieces(b, u1, u2, it);
                             }
                         }
                     }
                     release();
                 }
+#pragma unroll
+                for (int k = 0; k < ITEMS; ++k)
+                    if (k == i) a[k] = b;
             }
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) a[i] = greedy ? best_lanes<32>(a[i]) : join_lanes<32>(a[i]);
@@ -392,14 +417,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
                             }
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                float a0 = weight(bf16_lo(zw[k]), it, sp.m), a1 = weight(bf16_hi(zw[k]), it, sp.m);
-                                if (y) {
-                                    a0 = fmaf(-r, weight(bf16_lo(yw[k]), it, sq.m), a0);
-                                    a1 = fmaf(-r, weight(bf16_hi(yw[k]), it, sq.m), a1);
-                                }
-                                w[h][k] = f2_pack(a0, a1);
-                            }
+                            for (int k = 0; k < 4; ++k) w[h][k] = weight2_ends(zw[k], yw[k], it, sp.m, sq.m, y ? r : 0.0f);
                         }
                     }
                     release();
