@@ -135,12 +135,14 @@ void seq(const int* q, const int* len, long long rows, int n, int s, long long* 
 long long page(const int* table, long long pages, int maxp, int log2, int s, int pos) {
     return paged_page(view(table, 0, 0, pages, 0, 0, maxp, log2, 1), s, pos);
 }
+int least = 1, most = 0x7fffffff;
+void take(int a, int b) { least = a; most = b; }
 // The shares of a grid: for each block of work, in order, (sequence, g, tile, kb) into out, with the CTA
 // and the slot its segment would be written to; desc as the kernel writes it.  Returns the total.
 long long walk(const int* q, const int* len, long long rows, int n, int maxp, int log2, int k, int tok, int log2_keys,
                int G, int grid, int* out, long long cap, int* desc) {
     PagedView v = view(0, q, len, 1, rows, n, maxp, log2, k);
-    Tiling t = {tok, G, log2_keys, exact_log2(tok)};
+    Tiling t = {tok, G, log2_keys, exact_log2(tok), least, most};
     long long total = 0, done = 0;
     for (int s = 0; s < n; ++s) total += seq_blocks(v, paged_seq(v, s), t);
     const long long per = (total + grid - 1) / grid;
@@ -295,6 +297,32 @@ def test_shares_cover_all_work_once(host, rows, log2_keys):
             assert desc[c].tolist() == [*key, len(places)]
             parts += 1
         assert (desc[:, 3] > 0).sum() == parts
+
+
+def test_shares_of_some_sequences(host):
+    # A launch that takes sequences of some numbers of new tokens alone: every block of those once, none of the others.
+    rng = np.random.default_rng(77)
+    try:
+        for trial in range(60):
+            n, k, bound = int(rng.integers(1, 12)), int(rng.choice([1, 3])), int(rng.choice([1, 2, 8]))
+            new = np.where(rng.random(n) < 0.6, rng.integers(0, 4, n), rng.integers(0, 70, n))
+            length = i32(new + rng.integers(0, 600, n))
+            q, grid, both = i32(np.cumsum([0, *new])), int(rng.choice([1, 5, 152])), 0
+            for least, most in ((1, bound), (bound + 1, 0x7fffffff)):
+                tok = 4 if most == bound else 32
+                want = [(s, g, tile, b) for s in range(n) if least <= new[s] <= most for g in range(k)
+                        for tile in range(-(-int(new[s]) // tok))
+                        for b in range(max(1, -(-(int(length[s]) - int(new[s]) + min((tile + 1) * tok, int(new[s]))) // 128)))]
+                host.take(least, most)
+                out, desc = np.zeros((len(want) + 1, 6), dtype=np.int32), np.zeros((grid, 4), dtype=np.int32)
+                got = host.walk(q.ctypes.data, length.ctypes.data, int(q[-1]), n, 64, 4, k, tok, 7, 4, grid, out.ctypes.data,
+                                len(want), desc.ctypes.data)
+                assert got == len(want)
+                assert [tuple(x) for x in out[:got, :4].tolist()] == want
+                both += len({x[0] for x in want})
+            assert both == (new > 0).sum()
+    finally:
+        host.take(1, 0x7fffffff)
 
 
 def test_blocks_of_a_sequence_in_closed_form(host):
