@@ -26,7 +26,7 @@
 // of P before P is rounded to bf16.
 //
 // Measured, 32 query heads on 8 KV heads of 128: 2048 tokens behind 8192 cached
-// ones 242 us, 1280 TFLOP/s of the keys that are seen, 0.69 of cuBLAS.  A block of
+// ones 237 us, 1300 TFLOP/s of the keys that are seen, 0.70 of cuBLAS.  A block of
 // 128 keys then takes 1900 cycles where its products need 1024: the softmax bounds
 // it (eight warps: maximum, 2^x, rounding and the way through tensor memory).
 // From 8 bits a block takes 2.1 us instead of 1.05: the converting warps share the
@@ -34,8 +34,8 @@
 // without the conversion ran 1.7 us a block, without the scales too 1.5).  fp16
 // instead of bf16 takes half the conversion's instructions, but Q has to become
 // fp16 once a tile and P's range has to be watched: 2.6 us a block as built.
-// A tile costs about 3 us besides its blocks (Q, first page, last output), which is
-// what short contexts pay.
+// A tile costs 1 to 3 us besides its blocks (Q, first page, last output) and a CTA's
+// first about 3, which is what short contexts pay.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -125,7 +125,7 @@ struct Params {
     int kv_per_shard;        // KV heads of a shard, 0 if shards share them
     int shards_per_kv;       // shards that share a KV head (1 if they have their own)
     float scale_log2;
-    float* part_o;
+    float* part_o;   // [grid][2] slots of 128 rows in 16-byte pieces, as the join reads them
     float* part_ml;
     int4* desc;
     unsigned* status;
@@ -487,10 +487,12 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
             if (e.where >= 0) {
                 if (r < e.rows) {
                     const long long at = (static_cast<long long>(blockIdx.x) * 2 + e.where) * QB + r;
-                    float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + hf * DC);
+                    // In pieces of 16 bytes, [half and quadrant][piece][row of the quadrant]: 512 bytes a store of the
+                    // warp (row by row, a part took 3 us more).
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + (at - r) * D) + (warp - 4) * (DC / 4) * 32 + lane;
 #pragma unroll
                     for (int c = 0; c < DC / 4; ++c)
-                        dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                        dst[c * 32] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
                                              __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
                     if (hf == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(xch[8 * QB + r], l);
                 }
