@@ -110,6 +110,7 @@ struct Lay {
     static constexpr int DATA = PAGE_OFF + 2 * 64 * 4;
     static constexpr int SMEM = DATA + 1024;
     static constexpr int O_COL = NS * KB;
+    static constexpr int P_HALF = E4M3 ? KB / 2 : KB / 4;  // columns between P's halves of a block's keys
     static_assert(O_COL + D <= 512 && SMEM <= 232448 && SCAN_OFF % 8 == 0 && sizeof(TileWalk) % 8 == 0, "configuration");
 };
 
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
                     const uint64_t vdesc = vdesc0 + (st * L::TILE) / 16;
 #pragma unroll
                     for (int ks = 0; ks < KB / 16; ++ks)
-                        umma_bf16_ts(tmem + L::O_COL, tmem + pb * KB + ks * 8, vdesc + (ks * 16 * 128) / 16, idesc,
+                        umma_bf16_ts(tmem + L::O_COL, tmem + pb * KB + (ks >> 2) * L::P_HALF + (ks & 3) * 8, vdesc + (ks * 16 * 128) / 16, idesc,
                                      ks > 0 || i > 0 ? 1u : 0u);
                     umma_commit(bar(B_V_EMPTY + st));
                     umma_commit(bar(B_PV_DONE + pb));
@@ -567,50 +568,57 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
                 }
                 if constexpr (E4M3) got = got && wait(bar(B_SC_FULL + gb % NSC), (gb / NSC) & 1u);
                 got = __all_sync(0xffffffffu, got);
-                uint32_t s[KC];
+                constexpr int W = E4M3 ? 32 : KC;  // columns of S in registers at a time
+                const uint32_t ts = tmem + lane_off + st * KB + hf * KC;
+                uint32_t s[W];
                 float mxp = -INFINITY;
                 if (got && active) {
                     tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < KC / 32; ++c)
-                        tmem_ld32(tmem + lane_off + st * KB + hf * KC + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
-                    tmem_ld_wait();
-                    if constexpr (E4M3) {  // the codes' products times their keys' scales
-                        const uint32_t sc = base + L::SC_OFF + (gb % NSC) * (2 * KB * 4) + hf * KC * 4;
-#pragma unroll
-                        for (int c = 0; c < KC; c += 4) {
-                            const uint4 f = ld_shared_v4(sc + c * 4);
-                            const uint64_t a = f2_mul(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-                                                      f2_pack(__uint_as_float(f.x), __uint_as_float(f.y)));
-                            const uint64_t b = f2_mul(f2_pack(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
-                                                      f2_pack(__uint_as_float(f.z), __uint_as_float(f.w)));
-                            float x0, x1, x2, x3;
-                            f2_unpack(a, x0, x1);
-                            f2_unpack(b, x2, x3);
-                            s[c] = __float_as_uint(x0);
-                            s[c + 1] = __float_as_uint(x1);
-                            s[c + 2] = __float_as_uint(x2);
-                            s[c + 3] = __float_as_uint(x3);
-                        }
-                    }
-                    if (lim < KC) {
-#pragma unroll
-                        for (int c = 0; c < KC; ++c)
-                            if (c >= lim) s[c] = __float_as_uint(-INFINITY);
-                    }
                     float mx8[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[8 + e]));
+                    for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
 #pragma unroll
-                    for (int c = 16; c < KC; c += 16)
+                    for (int c0 = 0; c0 < KC; c0 += W) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            mx8[e] = max3(mx8[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 8 + e]));
+                        for (int c = 0; c < W / 32; ++c) tmem_ld32(ts + c0 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
+                        tmem_ld_wait();
+                        if constexpr (E4M3) {  // the codes' products times their keys' scales
+                            const uint32_t sc = base + L::SC_OFF + (gb % NSC) * (2 * KB * 4) + (hf * KC + c0) * 4;
+#pragma unroll
+                            for (int c = 0; c < W; c += 4) {
+                                const uint4 f = ld_shared_v4(sc + c * 4);
+                                float x0, x1, x2, x3;
+                                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                                 f2_pack(__uint_as_float(f.x), __uint_as_float(f.y))), x0, x1);
+                                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                                 f2_pack(__uint_as_float(f.z), __uint_as_float(f.w))), x2, x3);
+                                s[c] = __float_as_uint(x0);
+                                s[c + 1] = __float_as_uint(x1);
+                                s[c + 2] = __float_as_uint(x2);
+                                s[c + 3] = __float_as_uint(x3);
+                            }
+                        }
+                        if (lim < c0 + W) {
+#pragma unroll
+                            for (int c = 0; c < W; ++c)
+                                if (c0 + c >= lim) s[c] = __float_as_uint(-INFINITY);
+                        }
+#pragma unroll
+                        for (int c = 0; c < W; c += 16)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                mx8[e] = max3(mx8[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 8 + e]));
+                        // 8 bits: half the columns at a time, back to tensor memory for the second pass (with all 64 in
+                        // its 128 registers the loop spilled: a mixture of chunks and single tokens took 107 us instead of 98).
+                        if constexpr (E4M3) tmem_st32(ts + c0, *reinterpret_cast<const uint32_t(*)[32]>(&s[0]));
+                    }
+                    if constexpr (E4M3) tmem_st_wait();
                     mxp = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
                     xch[((gb & 1) * 2 + hf) * QB + r] = mxp;
                     tc_fence_before();
                 }
-                // The other half's S is in its registers once this returns, so P may be written over it.
+                // The other half's S is in its registers once this returns, so P may be written over it (8 bits: each half's
+                // P goes over its own S).
                 if (!pair_all(got)) {
                     ok = false;
                     break;
@@ -634,19 +642,26 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
                     uint32_t pk[KC / 2];
                     const uint32_t vsc = base + L::SC_OFF + (gb % NSC) * (2 * KB * 4) + (KB + hf * KC) * 4;
 #pragma unroll
-                    for (int c = 0; c < KC / 2; c += 2) {
-                        uint4 vf = make_uint4(0, 0, 0, 0);
-                        if constexpr (E4M3) vf = ld_shared_v4(vsc + c * 8);
+                    for (int c0 = 0; c0 < KC; c0 += W) {
+                        if constexpr (E4M3) {
+                            tmem_ld32(ts + c0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                            tmem_ld_wait();
+                        }
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float x0, x1;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * (c + h)]), __uint_as_float(s[2 * (c + h) + 1])), scale2, neg2), x0, x1);
-                            uint64_t pp = f2_pack(ex2(x0), ex2(x1));
-                            acc[(c + h) & 3] = f2_add(acc[(c + h) & 3], pp);
-                            if constexpr (E4M3)  // times V's scales
-                                pp = f2_mul(pp, f2_pack(__uint_as_float(h ? vf.z : vf.x), __uint_as_float(h ? vf.w : vf.y)));
-                            f2_unpack(pp, x0, x1);
-                            pk[c + h] = pack_bf16x2(x0, x1);
+                        for (int c = 0; c < W / 2; c += 2) {
+                            uint4 vf = make_uint4(0, 0, 0, 0);
+                            if constexpr (E4M3) vf = ld_shared_v4(vsc + c0 * 4 + c * 8);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float x0, x1;
+                                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * (c + h)]), __uint_as_float(s[2 * (c + h) + 1])), scale2, neg2), x0, x1);
+                                uint64_t pp = f2_pack(ex2(x0), ex2(x1));
+                                acc[(c + h) & 3] = f2_add(acc[(c + h) & 3], pp);
+                                if constexpr (E4M3)  // times V's scales
+                                    pp = f2_mul(pp, f2_pack(__uint_as_float(h ? vf.z : vf.x), __uint_as_float(h ? vf.w : vf.y)));
+                                f2_unpack(pp, x0, x1);
+                                pk[c0 / 2 + c + h] = pack_bf16x2(x0, x1);
+                            }
                         }
                     }
                     float sum8[8];
@@ -676,7 +691,7 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
                         }
                     }
                     // P over the first half of its S buffer: 64 keys as 32 packed columns.
-                    tmem_st32(tmem + lane_off + st * KB + hf * (KC / 2), pk);
+                    tmem_st32(tmem + lane_off + st * KB + hf * L::P_HALF, pk);
                     tmem_st_wait();
                     tc_fence_before();
                 }
