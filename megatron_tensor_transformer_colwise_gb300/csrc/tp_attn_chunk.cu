@@ -417,26 +417,32 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const uint32_t src = base + L::RAW_OFF + st * L::RAW, dst = (kind ? sV : sK) + to * L::TILE;
-                    constexpr int TURNS = D / 16;  // of a key
-#pragma unroll 2
-                    for (int x = 0; x < TURNS; ++x) {
-                        const int row = wc * 32 + (D == 128 ? (x >> 1) * 8 : x * 8) + (lane >> 2);
-                        const int c = D == 128 ? (lane & 3) + 4 * (((lane >> 2) ^ x) & 1) : lane & 3;
-                        const uint4 u = ld_shared_v4(src + row * D + c * 16);
-                        const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-                        uint32_t out[8];
+                    constexpr int TURNS = D / 16, AT_ONCE = TURNS < 4 ? TURNS : 4;  // of a key, and in registers
+#pragma unroll 1
+                    for (int x0 = 0; x0 < TURNS; x0 += AT_ONCE) {
+                        uint4 u[AT_ONCE];
+                        auto row_of = [&](int x) { return wc * 32 + (D == 128 ? (x >> 1) * 8 : x * 8) + (lane >> 2); };
+                        auto piece_of = [&](int x) { return D == 128 ? (lane & 3) + 4 * (((lane >> 2) ^ x) & 1) : lane & 3; };
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 f = e4m3x2_float2(in[e >> 1] >> (16 * (e & 1)));
-                            out[e] = pack_bf16x2(f.x, f.y);
+                        for (int y = 0; y < AT_ONCE; ++y) u[y] = ld_shared_v4(src + row_of(x0 + y) * D + piece_of(x0 + y) * 16);
+#pragma unroll
+                        for (int y = 0; y < AT_ONCE; ++y) {
+                            const int row = row_of(x0 + y), c = piece_of(x0 + y);
+                            const uint32_t in[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
+                            uint32_t out[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 f = e4m3x2_float2(in[e >> 1] >> (16 * (e & 1)));
+                                out[e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);  // their upper halves: exact
+                            }
+                            // Keys of V past the sequence's end are whatever the page holds, and 0 * NaN is NaN.
+                            if (kind && row >= left)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) out[e] = 0;
+                            const uint32_t at = dst + (c >> 2) * BOX + row * 128, piece = (c & 3) * 2, sw = row & 7;
+                            st_shared_v4(at + ((piece ^ sw) << 4), out[0], out[1], out[2], out[3]);
+                            st_shared_v4(at + (((piece + 1) ^ sw) << 4), out[4], out[5], out[6], out[7]);
                         }
-                        // Keys of V past the sequence's end are whatever the page holds, and 0 * NaN is NaN.
-                        if (kind && row >= left)
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) out[e] = 0;
-                        const uint32_t at = dst + (c >> 2) * BOX + row * 128, piece = (c & 3) * 2, sw = row & 7;
-                        st_shared_v4(at + ((piece ^ sw) << 4), out[0], out[1], out[2], out[3]);
-                        st_shared_v4(at + (((piece + 1) ^ sw) << 4), out[4], out[5], out[6], out[7]);
                     }
                     if (kind == 0) {  // 2 x 32 scales a warp; zeros past the sequence's end, where P is 0
                         const bool in = wc * 32 + lane < left;
