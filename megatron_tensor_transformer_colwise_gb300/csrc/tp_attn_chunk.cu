@@ -29,11 +29,11 @@
 // ones 237 us, 1300 TFLOP/s of the keys that are seen, 0.70 of cuBLAS.  A block of
 // 128 keys then takes 1900 cycles where its products need 1024: the softmax bounds
 // it (eight warps: maximum, 2^x, rounding and the way through tensor memory).
-// From 8 bits a block takes 2.1 us instead of 1.05: the converting warps share the
-// schedulers with the softmax, whose scales come through shared memory (copies
-// without the conversion ran 1.7 us a block, without the scales too 1.5).  fp16
-// instead of bf16 takes half the conversion's instructions, but Q has to become
-// fp16 once a tile and P's range has to be watched: 2.6 us a block as built.
+// From 8 bits a block takes 1.7 us instead of 1.1: the converting warps share the
+// schedulers and shared memory with the softmax.  fp16 instead of bf16 would take
+// half the conversion's instructions, but Q has to become fp16 once a tile and P's
+// range has to be watched (2.6 us a block as built, where bf16 took 2.1).  With 512
+// threads the roles have 128 registers, and what spills costs more than arithmetic.
 // A tile costs 1 to 3 us besides its blocks (Q, first page, last output) and a CTA's
 // first about 3, which is what short contexts pay.
 #include <cuda.h>

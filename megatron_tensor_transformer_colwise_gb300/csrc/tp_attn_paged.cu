@@ -870,22 +870,22 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
     // Few rows a sequence and KV head (the caller's bound on its new tokens, or all rows of the call): one tile
     // of 8 or 16.  More: tiles of 128 on tcgen05.  32 sequences over 1000 / 8000 keys, 8 KV heads, in us:
     //                  bf16 d = 64       e4m3 d = 64       bf16 d = 128      e4m3 d = 128
-    //   8 rows   8:    16.1 /  86        19.3 /  81        32.2 / 160        22.6 /  97
-    //           16:    18.3 /  88        21.0 /  89        34.7 / 165        30.0 / 134
-    //          128:    23.6 / 102        36.0 / 185        32.8 / 161        42.6 / 229
-    //  16 rows  16:    21.6 /  91        24.7 /  93        40.0 / 169        35.4 / 140
-    //          128:    23.7 / 102        36.2 / 186        32.9 / 163        43.3 / 230
-    //  24 rows  16:    31.0 / 165        36.5 / 171        54.1 / 318        55.0 / 260   (two tiles)
-    //          128:    23.8 / 102        36.5 / 186        33.7 / 164        44.2 / 231
+    //   8 rows   8:    16.0 /  86        19.3 /  81        32.2 / 160        22.6 /  97
+    //           16:    18.3 /  88        21.0 /  89        34.6 / 165        30.0 / 134
+    //          128:    23.6 / 102        33.6 / 170        33.0 / 162        38.1 / 198
+    //  16 rows  16:    21.6 /  91        24.6 /  93        40.0 / 169        35.4 / 140
+    //          128:    23.6 / 102        33.7 / 170        33.2 / 164        38.2 / 198
+    //  24 rows  16:    30.9 / 165        36.6 / 171        54.2 / 318        55.0 / 260   (two tiles)
+    //          128:    23.8 / 103        33.7 / 170        33.7 / 165        38.6 / 199
     const int group = a.heads / a.kv_heads;
     const int64_t most = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
     const int64_t bound = a.e4m3 || a.head_dim == 64 ? R : 8;
     if (most * group <= bound) return few(a, most * group, O, scratch, zero_rest, stream, err);
     // A mixture from an 8-bit cache: at most half of n_seqs x most tokens are there, so many sequences have few.
-    // Those go to the few-row kernel, which reads codes at the memory's rate, where the 128-row tiles take 2 us a
-    // block whatever their rows (one chunk of 500 tokens and 23 single ones over 8000 keys: 296 -> 211 us, over 2000:
-    // 100 -> 85; over 500: 49 either way, over 200: 39 -> 44).  From bf16 the one launch is faster (170 and 205 us over
-    // 8000).
+    // Those go to the few-row kernel, which reads codes at the memory's rate, where the 128-row tiles take 1.7 us a
+    // block whatever their rows.  One chunk of 500 tokens and 23 single ones, one launch and two: over 8000 keys 240 and
+    // 183 us, over 2000 79 and 71, over 500 37 and 39 (a table of that size stays with one).  From bf16 one launch is
+    // faster: 149 and 184 us over 8000.
     if (a.e4m3 && group <= R && 2 * a.tokens <= a.n_seqs * most && static_cast<int64_t>(a.max_pages) * a.page_size >= 1024) {
         const int rows = group <= 8 ? 8 : R;
         PagedArgs part = a;
