@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
-            mbar_init(full0 + 8 * i, 2);  // the two producers
+            mbar_init(full0 + 8 * i, E4M3 ? 2 + 2 * (KB / 4) : 2);  // the two producers, and their lanes that copy scales
             mbar_init(empty0 + 8 * i, C::WPB);
         }
         abort_word = 0;
@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
         // ------------------------------------------------------ producers: K, V
         const bool is_v = warp > NW;
         const int log2 = p.v.page_log2, page_mask = (1 << log2) - 1, per_block = KB / p.box_rows;
+        const int box_log2 = log2 < C::LOG2_KB ? log2 : C::LOG2_KB;
         const CUtensorMap* map = is_v ? &p.map_v : &p.map_k;
         const float* scales = is_v ? p.v_scale : p.k_scale;
         // Page numbers of two windows of 32 pages: page i of the sequence at ring[i - first page of the segment, mod 64].
@@ -247,19 +248,22 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
                 if (!ok) break;
                 const uint32_t dst = base + st * C::STAGE + (is_v ? C::TILE : 0);
                 const uint32_t sc = base + C::SC_OFF + st * C::SCALES + (is_v ? KB * 4 : 0);
-                int scaled = 0;
-                if constexpr (E4M3) {  // a lane a box; the scales of no page are zeros
-                    const int page = lane < per_block ? ring[(at + lane) & 63] : -1;
-                    scaled = __popc(__ballot_sync(0xffffffffu, page >= 0));
-                    if (lane < per_block && page < 0) {
-#pragma unroll 1
-                        for (int x = 0; x < p.box_rows; x += 4) st_shared_v4(sc + (lane * p.box_rows + x) * 4, 0, 0, 0, 0);
-                        fence_proxy_async_smem();
+                if constexpr (E4M3) {
+                    // The block's scales, four keys a lane (of one page: it has 16 keys at least); those of no page are zeros.
+                    // A copy a page, by the thread that issues the boxes, cost 48 single tokens over 8000 keys 265 us
+                    // at 16 keys a page and 172 at 32, where this takes 173 and 138 (131 at 128).
+                    static_assert(KB == 128, "four keys a lane");
+                    const int page = ring[(at + (lane * 4 >> box_log2)) & 63];
+                    if (page >= 0) {
+                        copy16(sc + lane * 16, scales + paged_row(p.v, page, g, (key0 + lane * 4) & page_mask));
+                        copies_arrive(full);
+                    } else {
+                        st_shared_v4(sc + lane * 16, 0, 0, 0, 0);
+                        mbar_arrive(full);
                     }
-                    __syncwarp();
                 }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(full, C::TILE + 4u * p.box_rows * scaled);
+                    mbar_arrive_expect_tx(full, C::TILE);
                     // One lane issues: a copy's operands are uniform registers, so lanes would take turns.
 #pragma unroll 1
                     for (int b = 0; b < per_block; ++b) {
@@ -267,14 +271,13 @@ __global__ void __launch_bounds__(C::NT, 1) attn_few_kernel(const __grid_constan
 #pragma unroll
                         for (int c = 0; c < C::NSEG; ++c)
                             tma_load_4d(dst + c * (KB * C::SEG) + b * p.box_rows * C::SEG, map, full, c * (E4M3 ? 128 : 64), off, g, page);
-                        if (E4M3 && page >= 0)
-                            bulk_load(sc + b * p.box_rows * 4, scales + paged_row(p.v, page, g, off), p.box_rows * 4, full);
                     }
                 }
                 __syncwarp();
             }
         }
         // No copy may be in flight when the CTA's shared memory goes.
+        if constexpr (E4M3) copies_wait();
         for (int i = max(0, n - NST); i < n; ++i) drain(full0 + 8 * (i % NST), (i / NST) & 1);
     } else {
         // ------------------------------------------------------ consumers

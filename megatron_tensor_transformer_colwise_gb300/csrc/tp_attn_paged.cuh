@@ -56,6 +56,16 @@ __device__ __forceinline__ float2 e4m3x2_float2(uint32_t codes) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// 16 bytes to shared memory by this thread, and its arrival at a barrier once all such copies of its own are there
+// (the barrier counts that arrival from the start).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Contiguous copy to shared memory; addresses and size multiples of 16 bytes.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
