@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
         mbar_init(bar(B_DRAIN), 1);
         mbar_init(bar(B_DRAIN + 1), 1);
         for (int s = 0; s < NRAW; ++s) {
-            mbar_init(bar(B_R_FULL + s), 1);
+            mbar_init(bar(B_R_FULL + s), 1 + 32);  // the codes' copies, and the lanes that copy scales
             mbar_init(bar(B_R_EMPTY + s), 4);
         }
         for (int s = 0; s < NSC; ++s) mbar_init(bar(B_SC_FULL + s), 4);
@@ -271,34 +271,29 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
                     const uint32_t full = full0 + 8 * st;
                     if constexpr (E4M3) {
                         const uint32_t dst = dst0 + st * L::RAW;
-                        int scaled = 0;
-                        if (kind == 0) {  // the block's scales, a lane a box; those of no page are zeros
-                            const int page = lane < per_block ? ring[(at + lane) & 63] : -1;
-                            const uint32_t sc = dst + L::CODES + lane * p.box_rows * 4;
-                            scaled = __popc(__ballot_sync(0xffffffffu, page >= 0));
-                            if (lane < per_block && page < 0) {
-#pragma unroll 1
-                                for (int x = 0; x < p.box_rows; x += 4) {
-                                    st_shared_v4(sc + x * 4, 0, 0, 0, 0);
-                                    st_shared_v4(sc + KB * 4 + x * 4, 0, 0, 0, 0);
-                                }
-                                fence_proxy_async_smem();
+                        // The block's scales of K and V behind K's codes, four keys a lane (of one page: it has 16 keys at
+                        // least); those of no page are zeros.
+                        const int key = lane * 4, page = ring[(at + (key >> log2)) & 63];
+                        const uint32_t sc = dst + L::CODES + key * 4;
+                        if (kind == 0 && page >= 0) {
+                            const long long row = paged_row(p.v, page, g, key & ((1 << log2) - 1));
+                            copy16(sc, p.k_scale + row);
+                            copy16(sc + KB * 4, p.v_scale + row);
+                            copies_arrive(full);
+                        } else {
+                            if (kind == 0) {
+                                st_shared_v4(sc, 0, 0, 0, 0);
+                                st_shared_v4(sc + KB * 4, 0, 0, 0, 0);
                             }
-                            __syncwarp();
+                            mbar_arrive(full);
                         }
                         if (lane == 0) {
                             const CUtensorMap* map = kind ? &p.map_v : &p.map_k;
-                            mbar_arrive_expect_tx(full, L::CODES + 8u * p.box_rows * scaled);
+                            mbar_arrive_expect_tx(full, L::CODES);
 #pragma unroll 1
                             for (int b = 0; b < per_block; ++b) {
                                 const int page = ring[(at + b) & 63];
                                 tma_load_4d(dst + b * p.box_rows * D, map, full, 0, 0, g, page);
-                                if (kind == 0 && page >= 0) {
-                                    const long long row = paged_row(p.v, page, g, 0);
-                                    const uint32_t sc = dst + L::CODES + b * p.box_rows * 4;
-                                    bulk_load(sc, p.k_scale + row, p.box_rows * 4, full);
-                                    bulk_load(sc + KB * 4, p.v_scale + row, p.box_rows * 4, full);
-                                }
                             }
                         }
                     } else if (lane == 0) {
@@ -332,6 +327,7 @@ __global__ void __launch_bounds__(L::NT, 1) attn_chunk_kernel(const __grid_const
         }
         if (!is_v && lane == 0) p.desc[blockIdx.x] = cut;
         // No copy may be in flight when the CTA's shared memory goes.
+        if constexpr (E4M3) copies_wait();
         if (!is_v && li) drain(bar(B_Q_FULL), (li - 1) & 1u);
         for (uint32_t i = n > L::KRING ? n - L::KRING : 0; i < n; ++i) drain(full0 + 8 * (i % L::KRING), (i / L::KRING) & 1u);
     } else if (warp == 1) {
