@@ -454,10 +454,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
-// Every thread of both CTAs: release this CTA's prior writes, wait for the peer.
-__device__ __forceinline__ void cluster_sync_all() {
+// Every thread of every CTA: release this CTA's prior writes, wait for the others (also until they run).
+__device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    cluster_arrive();
+    cluster_wait();
 }
 
 // TMA load into this CTA's shared memory whose completion is signalled on

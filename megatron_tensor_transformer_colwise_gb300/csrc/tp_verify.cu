@@ -225,9 +225,11 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         abort_word = 0;
         fence_barrier_init();
     }
-    __syncthreads();
+    // Every CTA of the cluster runs, and its barriers are there, before one stores into another's shared memory.
+    cluster_arrive();
     pdl_trigger();
     pdl_wait();
+    cluster_wait();
     const long long r0 = min(max(static_cast<long long>(p.q_start[s]), 0ll), p.rows);
     const long long r1 = min(max(static_cast<long long>(p.q_start[s + 1]), r0), p.rows);
     const float T = p.temperature ? p.temperature[s] : 1.0f;

@@ -75,6 +75,16 @@ def test_against_the_definition(v, t, rows):
     Drafts(rows, v, seed=v + len(rows), pad=2, first=1).check(t=t, least_clear=0.5)
 
 
+@pytest.mark.parametrize("v", [8, 16, 56, 72])
+def test_words_for_some_blocks_of_a_cluster_alone(v):
+    # Blocks without words reach the exchange first, whatever the others do: every run gives the same, and right.
+    d = Drafts([3, 1, 4] * 150, v, seed=v)
+    d.check(least_clear=0.5)
+    first = d.run()
+    for _ in range(20):
+        assert all(np.array_equal(a, b) for a, b in zip(d.run(), first))
+
+
 def test_a_batch_takes_and_refuses():
     taken = Drafts([5] * 120, 1024, seed=5).check()
     assert 0 < taken.mean() < 4 and (taken == 4).any() and (taken == 0).any()
