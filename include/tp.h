@@ -666,6 +666,14 @@ TP_API int tp_vocab_verify_drafts(const tp_bf16* logits, const tp_bf16* draft_lo
  * the context stays usable; read it with tp_get_device_status. */
 TP_API int tp_selftest_wait_timeout(tp_plan_t plan, uint64_t timeout_ns, void* stream);
 
+/* Failure-detection check: tp_vocab_verify_drafts with t = 1, no draft
+ * distribution, temperature 1 and noise 1, whose waits for copied logits give
+ * up at once: where = 1 at the first rows, 2 at the draw.  The kernel lets its
+ * copies in flight arrive and returns normally, so the context stays usable. */
+TP_API int tp_selftest_verify_timeout(const tp_bf16* logits, int64_t M, int64_t v, const int32_t* ids,
+                                      const int32_t* q_start, int32_t n_seqs, const float* u, int32_t* accepted,
+                                      int32_t* tokens, int where, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

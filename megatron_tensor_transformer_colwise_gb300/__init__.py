@@ -30,7 +30,7 @@ __all__ = [
     "tp_plan_workspace_bytes", "tp_plan_shard_table", "tp_get_device_status", "tp_last_error",
     "tp_reduce_partials", "tp_rmsnorm", "tp_colwise_forward", "tp_rowwise_forward",
     "tp_mlp_forward", "tp_mlp_forward_noalloc", "tp_qkv_forward", "tp_attn_core_forward", "tp_attn_forward",
-    "tp_layer_forward", "tp_layer_forward_traced", "tp_selftest_wait_timeout",
+    "tp_layer_forward", "tp_layer_forward_traced", "tp_selftest_wait_timeout", "tp_selftest_verify_timeout",
     "tp_packed_shard_table", "tp_packed_colwise_forward", "tp_vocab_embedding_forward",
     "tp_vocab_logits_forward", "tp_vocab_parallel_cross_entropy", "tp_sp_all_gather",
     "tp_sp_reduce_scatter", "tp_mlp_forward_train", "tp_mlp_backward", "tp_plan_attn_saved_bytes",
@@ -147,6 +147,7 @@ _SIGS = {
     "tp_attn_paged_forward": [_VP, C.POINTER(TPKVCache), _VP, _VP, _VP, C.c_size_t, _VP],
     "tp_attn_cached_forward": [_VP, C.POINTER(TPKVCache)] + [_VP] * 9 + [C.c_size_t, _VP],
     "tp_vocab_verify_drafts": [_VP, _VP, C.c_int64, C.c_int64, C.c_int32, _VP, _VP, C.c_int32] + [_VP] * 6,
+    "tp_selftest_verify_timeout": [_VP, C.c_int64, C.c_int64, _VP, _VP, C.c_int32, _VP, _VP, _VP, C.c_int, _VP],
 }
 EXPORTED = tuple(sorted(list(_SIGS) + ["tp_last_error"]))
 
@@ -415,6 +416,13 @@ def tp_layer_forward_traced(plan: Plan, X, weights, Y, workspace, ws_bytes: int,
 
 def tp_selftest_wait_timeout(plan: Plan, timeout_ns: int, stream=None) -> None:
     _call("tp_selftest_wait_timeout", plan.handle, timeout_ns, _s(stream))
+
+
+def tp_selftest_verify_timeout(logits, M: int, v: int, ids, q_start, n_seqs: int, u, accepted, tokens, where: int,
+                               stream=None) -> None:
+    """tp_vocab_verify_drafts whose waits give up at the first rows (where = 1) or at the draw (2)."""
+    _call("tp_selftest_verify_timeout", _p(logits), M, v, _p(ids), _p(q_start), n_seqs, _p(u), _p(accepted), _p(tokens),
+          where, _s(stream))
 
 
 def _blocks(blocks):

@@ -1655,10 +1655,11 @@ extern "C" int tp_attn_cached_forward(tp_plan_t plan, const tp_kv_cache* cache, 
     return TP_OK;
 }
 
-extern "C" int tp_vocab_verify_drafts(const tp_bf16* logits, const tp_bf16* draft_logits, int64_t M, int64_t v,
-                                      int32_t t, const int32_t* ids, const int32_t* q_start, int32_t n_seqs,
-                                      const float* temperature, const float* u, const float* noise,
-                                      int32_t* accepted, int32_t* tokens, void* stream) {
+namespace {
+
+int verify_drafts(const tp_bf16* logits, const tp_bf16* draft_logits, int64_t M, int64_t v, int32_t t, const int32_t* ids,
+                  const int32_t* q_start, int32_t n_seqs, const float* temperature, const float* u, const float* noise,
+                  int32_t* accepted, int32_t* tokens, int give_up, void* stream) {
     int rc;
     if ((rc = need_ptr(logits, "logits")) || (rc = opt_ptr(draft_logits, "draft_logits")) ||
         (rc = need_ptr(ids, "ids")) || (rc = need_ptr(q_start, "q_start")) ||
@@ -1681,8 +1682,26 @@ extern "C" int tp_vocab_verify_drafts(const tp_bf16* logits, const tp_bf16* draf
     a.noise = noise;
     a.accepted = accepted;
     a.tokens = tokens;
+    a.give_up = give_up;
     std::string err;
     return run(tpi::verify_launch(a, as_stream(stream), &err), err);
+}
+
+}  // namespace
+
+extern "C" int tp_vocab_verify_drafts(const tp_bf16* logits, const tp_bf16* draft_logits, int64_t M, int64_t v,
+                                      int32_t t, const int32_t* ids, const int32_t* q_start, int32_t n_seqs,
+                                      const float* temperature, const float* u, const float* noise,
+                                      int32_t* accepted, int32_t* tokens, void* stream) {
+    return verify_drafts(logits, draft_logits, M, v, t, ids, q_start, n_seqs, temperature, u, noise, accepted, tokens, 0,
+                         stream);
+}
+
+extern "C" int tp_selftest_verify_timeout(const tp_bf16* logits, int64_t M, int64_t v, const int32_t* ids,
+                                          const int32_t* q_start, int32_t n_seqs, const float* u, int32_t* accepted,
+                                          int32_t* tokens, int where, void* stream) {
+    if (where < 1 || where > 2) return fail(TP_ERR_INVALID_ARG, "where must be 1 or 2 (got %d)", where);
+    return verify_drafts(logits, nullptr, M, v, 1, ids, q_start, n_seqs, nullptr, u, nullptr, accepted, tokens, where, stream);
 }
 
 // ---------------------------------------------------------------------------

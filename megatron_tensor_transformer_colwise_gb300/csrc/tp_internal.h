@@ -243,6 +243,7 @@ struct VerifyArgs {
     int n_seqs = 0;
     const float *temperature = nullptr, *u = nullptr, *noise = nullptr;
     int32_t *accepted = nullptr, *tokens = nullptr;
+    int give_up = 0;  // self test: where the waits give up, 0 nowhere
 };
 int verify_launch(const VerifyArgs& a, cudaStream_t stream, std::string* err);
 

@@ -57,6 +57,7 @@ struct VerifyParams {
     const int32_t *ids, *q_start;
     const float *temperature, *u, *noise;
     int32_t *accepted, *tokens;
+    int give_up;  // self test: 1 or 2, the summing warps' waits give up at the first batch, or at the race
 };
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -244,7 +245,15 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
     const int begin = min(rank * mine, pieces), end = min(begin + mine, pieces);
 
     const Waiter wait = {&abort_word, nullptr, 2000000000ull};
-    bool ok = true;  // a wait that gave up leaves an unspecified answer, and ends
+    bool ok = true;
+    // Self test: from here on no wait of the summing warps succeeds, while copies are on their way.
+    auto give_up = [&](int where) {
+        if (p.give_up == where && warp < WARPS) {
+            *reinterpret_cast<volatile int*>(&abort_word) = 1;
+            ok = false;
+        }
+    };
+    give_up(1);
     // Ring position, the same sequence in the producer and in those that sum.
     int st = 0, issued = 0;
     uint32_t phase = 0;
@@ -256,7 +265,9 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
     };
     // Producer: the next stage gets `bytes` from a at offset 0, and more from b at the stage's middle.
     auto produce = [&](const void* a, uint32_t bytes, const void* b, uint32_t more) {
-        if (!ok || !(ok = wait(empty0 + 8 * st, phase ^ 1))) return;
+        // Warps that gave up release their stages unread: a barrier whose copy has not arrived must not be armed again.
+        ok = ok && wait(empty0 + 8 * st, phase ^ 1) && !*reinterpret_cast<volatile int*>(&abort_word);
+        if (!ok) return;
         const uint32_t full = full0 + 8 * st;
         mbar_arrive_expect_tx(full, bytes + more);
         if (bytes) bulk_load(smem_u32(&ring[st][0]), a, bytes, full);
@@ -384,6 +395,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         token = sp.m > -INFINITY ? __float_as_int(sp.s) : -1;
     } else {
         // The race over w = max(0, p - q); where that leaves nothing, a second one over p.
+        give_up(2);
         const uint4* z = reinterpret_cast<const uint4*>(p.z + (r0 + taken) * p.v);
         const uint4* y = drafted && sq.s > 0.0f ? reinterpret_cast<const uint4*>(p.y + (r0 + taken) * p.v) : nullptr;
         const float4* noise = p.noise ? reinterpret_cast<const float4*>(p.noise + s * p.v) : nullptr;
@@ -469,7 +481,8 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
             y = nullptr;
         }
     }
-    if (!ok && tid == VT)  // no copy may be in flight when the CTA's shared memory goes
+    // No copy may be in flight when the CTA's shared memory goes, whichever warp gave up.
+    if (abort_word && tid == VT)
         for (int i = max(0, issued - NST); i < issued; ++i) drain(full0 + 8 * (i % NST), (i / NST) & 1);
     if (rank == 0) {
         if (tid == 0) p.accepted[s] = taken;
@@ -496,6 +509,7 @@ int verify_launch(const VerifyArgs& a, cudaStream_t stream, std::string* err) {
     p.noise = a.noise;
     p.accepted = a.accepted;
     p.tokens = a.tokens;
+    p.give_up = a.give_up;
     constexpr int SMEM = NST * PPT * VT * 16;
     static bool configured[64] = {false};
     int dev = 0;

@@ -168,6 +168,22 @@ def test_tokens_follow_the_target():
     assert chi < 45, chi
 
 
+@pytest.mark.parametrize("where", [1, 2])
+@pytest.mark.parametrize("v", [8, 1024, 128256])
+def test_waits_that_give_up_leave_the_context_usable(v, where):
+    # Waits that give up while copies are on their way: the kernel ends, and calls around it are right.
+    d = Drafts([3, 1, 0, 5] * 10, v, seed=30)
+    n, M = len(d.start) - 1, d.logits.shape[0]
+    before = d.run(draft=False, temperature=False, noise=False)
+    acc, tok = (torch.full((k,), -7, dtype=torch.int32, device="cuda") for k in (n, M))
+    x = [dev(t) for t in (d.logits, d.ids, torch.as_tensor(d.start, dtype=torch.int32), d.u)]
+    for _ in range(3):
+        tp.tp_selftest_verify_timeout(x[0], M, v, x[1], x[2], n, x[3], acc, tok, where)
+    sync_ok()
+    after = d.run(draft=False, temperature=False, noise=False)
+    assert all(np.array_equal(a, b) for a, b in zip(before, after))
+
+
 def test_captured_and_replayed_with_new_numbers():
     d = Drafts([3, 2], 256, seed=13)
     n, M = 2, d.logits.shape[0]

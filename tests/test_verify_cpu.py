@@ -21,3 +21,21 @@ def test_the_cluster_has_started_before_a_store_into_another_block():
     barrier = min(src.index(w) for w in ("cluster_wait()", "cluster_sync_all()") if w in src)
     assert barrier < src.index("store_cluster(")
     assert "return" not in src[:barrier]
+
+
+def test_the_self_test_refuses_places_that_are_not_there():
+    p = 1 << 20
+    for where in (-1, 0, 3):
+        assert tp.lib().tp_selftest_verify_timeout(p, 4, 64, p, p, 2, p, p, p, where, None) == tp.TP_ERR_INVALID_ARG
+    assert tp.lib().tp_selftest_verify_timeout(p, 4, 66, p, p, 2, p, p, p, 1, None) == tp.TP_ERR_INVALID_ARG
+
+
+def test_nothing_is_armed_or_left_behind_once_a_wait_gave_up():
+    # The producer looks at the word that every wait sets when it gives up, after the wait for a free stage and
+    # before it arms the stage's barrier again; and the copies in flight are waited for by that word too, not by
+    # what the producer itself met.
+    src = kernel_source()
+    produce = src[src.index("auto produce ="):]
+    produce = produce[:produce.index("advance();")]
+    assert produce.index("wait(empty0") < produce.index("abort_word") < produce.index("mbar_arrive_expect_tx")
+    assert re.search(r"if \(abort_word && tid == VT\)\s*for [^;]*;[^;]*;[^)]*\) drain\(", src)
