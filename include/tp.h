@@ -651,7 +651,9 @@ TP_API int tp_attn_cached_forward(tp_plan_t plan, const tp_kv_cache* cache, cons
  * rows).  tokens: device [M] int32: row q_start[s] + i holds the i-th settled
  * token, the taken drafts and then the drawn one; -1 behind them; rows that
  * no sequence owns are left as they are.  A row without any probability (all
- * logits -inf) draws -1.  (v / t) % 8 == 0. */
+ * logits -inf) draws -1.  A device-side wait that gives up (2 s) settles
+ * nothing: accepted[s] is -1 then, and so are the tokens of all rows of that
+ * sequence.  (v / t) % 8 == 0. */
 TP_API int tp_vocab_verify_drafts(const tp_bf16* logits, const tp_bf16* draft_logits, int64_t M, int64_t v,
                                   int32_t t, const int32_t* ids, const int32_t* q_start, int32_t n_seqs,
                                   const float* temperature, const float* u, const float* noise,
@@ -669,7 +671,8 @@ TP_API int tp_selftest_wait_timeout(tp_plan_t plan, uint64_t timeout_ns, void* s
 /* Failure-detection check: tp_vocab_verify_drafts with t = 1, no draft
  * distribution, temperature 1 and noise 1, whose waits for copied logits give
  * up at once: where = 1 at the first rows, 2 at the draw.  The kernel lets its
- * copies in flight arrive and returns normally, so the context stays usable. */
+ * copies in flight arrive and returns normally, so the context stays usable;
+ * sequences with rows get -1 in accepted and in their tokens. */
 TP_API int tp_selftest_verify_timeout(const tp_bf16* logits, int64_t M, int64_t v, const int32_t* ids,
                                       const int32_t* q_start, int32_t n_seqs, const float* u, int32_t* accepted,
                                       int32_t* tokens, int where, void* stream);

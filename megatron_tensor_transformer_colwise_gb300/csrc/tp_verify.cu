@@ -289,6 +289,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
     int taken = n - 1, token = -1;
     Stat sp = {-INFINITY, 0.0f}, sq = {-INFINITY, 0.0f};
     bool drafted = false;  // the row that stops has a draft distribution
+    bool failed = false;   // a wait of some CTA gave up: what was summed is not the rows' sums, and nothing is settled
     for (int b0 = 0, parity = 0; b0 < n; b0 += ROWS, parity ^= 1) {
         const int rows = min(ROWS, n - b0);
         // Rows of logits: the target's, then the draft's (none behind the last draft).
@@ -363,6 +364,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         if (warp == 0) {
             Stat b = part[lane / WARPS][lane % WARPS];
             b = greedy ? best_lanes<WARPS>(b) : join_lanes<WARPS>(b);  // in every lane of the row: one a CTA to tell
+            if (abort_word) b.m = NAN;  // no largest value is NaN: a wait of this CTA gave up
             store_cluster(smem_u32(&all[parity][lane / CS][rank]), lane % CS, __float_as_uint(b.m), __float_as_uint(b.s));
         }
         // A batch's buffer is written again two batches on: behind the next batch's barrier, which every CTA
@@ -370,6 +372,8 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         cluster_sync_all();
         // Every warp decides: the rows' statistics, 8 lanes each, then lane i row i.
         Stat b = all[parity][lane / CS][lane % CS];
+        failed = __any_sync(0xffffffffu, isnan(b.m));  // the same in every warp and CTA
+        if (failed) break;
         b = greedy ? best_lanes<CS>(b) : join_lanes<CS>(b);
         const int of_p = min(lane, rows - 1) * CS, of_q = min(rows + lane, ITEMS - 1) * CS;
         const Stat tp_ = {__shfl_sync(0xffffffffu, b.m, of_p), __shfl_sync(0xffffffffu, b.s, of_p)};
@@ -393,7 +397,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
     }
     if (greedy) {
         token = sp.m > -INFINITY ? __float_as_int(sp.s) : -1;
-    } else {
+    } else if (!failed) {
         // The race over w = max(0, p - q); where that leaves nothing, a second one over p.
         give_up(2);
         const uint4* z = reinterpret_cast<const uint4*>(p.z + (r0 + taken) * p.v);
@@ -470,12 +474,18 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
                 Best b = race[0];
 #pragma unroll
                 for (int k = 1; k < WARPS; ++k) b = better(b, race[k]);
+                if (abort_word) b.v = NAN;
                 store_cluster(smem_u32(&raced[attempt][rank]), tid, __float_as_uint(b.v), static_cast<uint32_t>(b.i));
             }
             cluster_sync_all();
             Best b = raced[attempt][0];
+            failed = isnan(b.v);
 #pragma unroll
-            for (int k = 1; k < CS; ++k) b = better(b, raced[attempt][k]);
+            for (int k = 1; k < CS; ++k) {
+                failed = failed || isnan(raced[attempt][k].v);
+                b = better(b, raced[attempt][k]);
+            }
+            if (failed) break;
             token = b.v > 0.0f && sp.s > 0.0f ? b.i : -1;
             if (token >= 0 || !y) break;  // the same in every CTA
             y = nullptr;
@@ -484,6 +494,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
     // No copy may be in flight when the CTA's shared memory goes, whichever warp gave up.
     if (abort_word && tid == VT)
         for (int i = max(0, issued - NST); i < issued; ++i) drain(full0 + 8 * (i % NST), (i / NST) & 1);
+    if (failed) taken = token = -1;
     if (rank == 0) {
         if (tid == 0) p.accepted[s] = taken;
         for (int i = tid; i < n; i += VT + 32)

@@ -184,6 +184,21 @@ def test_waits_that_give_up_leave_the_context_usable(v, where):
     assert all(np.array_equal(a, b) for a, b in zip(before, after))
 
 
+@pytest.mark.parametrize("where", [1, 2])
+@pytest.mark.parametrize("v", [8, 1024, 128256])
+def test_a_wait_that_gives_up_settles_nothing(v, where):
+    d = Drafts([3, 1, 0, 5, 40], v, seed=31, pad=2, first=1)
+    n, M = len(d.start) - 1, d.logits.shape[0]
+    acc, tok = (torch.full((k,), -7, dtype=torch.int32, device="cuda") for k in (n, M))
+    tp.tp_selftest_verify_timeout(dev(d.logits), M, v, dev(d.ids), dev(torch.as_tensor(d.start, dtype=torch.int32)), n,
+                                  dev(d.u), acc, tok, where)
+    sync_ok()
+    assert acc.tolist() == [-1, -1, 0, -1, -1]
+    own = slice(int(d.start[0]), int(d.start[-1]))
+    assert (tok[own] == -1).all()
+    assert tok[0] == -7 and (tok[own.stop:] == -7).all()
+
+
 def test_captured_and_replayed_with_new_numbers():
     d = Drafts([3, 2], 256, seed=13)
     n, M = 2, d.logits.shape[0]
