@@ -637,6 +637,7 @@ TP_API int tp_attn_cached_forward(tp_plan_t plan, const tp_kv_cache* cache, cons
  * distribution that is a draw from w; the tokens then follow the target's
  * distribution.  T <= 0 (or NaN) is greedy: a draft is taken if it is the
  * first of the row's largest logits, and that index is the token drawn.
+ * An infinite T is uniform over the words whose logits are above -inf.
  * A sequence without drafts is ordinary sampling from one row.
  *
  * logits, draft_logits: device [M][v] bf16, vocabulary-sharded like

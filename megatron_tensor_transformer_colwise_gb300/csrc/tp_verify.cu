@@ -240,7 +240,9 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         return;
     }
     const bool greedy = !(T > 0.0f);
-    const float it = fminf(LOG2E / T, 1e30f);
+    // Above zero also for an infinite T (the least number of fp32): a logit of -inf times it stays -inf, and every
+    // other one vanishes.
+    const float it = fminf(fmaxf(LOG2E / T, 1.4e-45f), 1e30f);
     const int pieces = static_cast<int>(p.v / 8), mine = (pieces + CS - 1) / CS;
     const int begin = min(rank * mine, pieces), end = min(begin + mine, pieces);
 

@@ -168,6 +168,26 @@ def test_tokens_follow_the_target():
     assert chi < 45, chi
 
 
+def test_infinite_temperature_is_uniform_over_what_is_left():
+    # p and q are uniform over the words that are not masked; 1e300 says the same in 64 bits.
+    d = Drafts([3, 1, 2, 4] * 20, 264, seed=32)
+    lo = float("-inf")
+    d.logits[::2, 40:] = lo
+    d.logits[1::3, :30] = lo
+    d.draft[::5, 100:200] = lo
+    d.logits[3], d.logits[6, 7], d.logits[6, 8] = lo, 3e38, -3e38
+    d.temperature[:] = float("inf")
+    acc, tok = d.run()
+    d.temperature = d.temperature.double()
+    d.temperature[:] = 1e300
+    a, k, margin = d.want()
+    clear = margin > MARGIN
+    assert clear.mean() > 0.5
+    for s in np.flatnonzero(clear):
+        assert acc[s] == a[s] and np.array_equal(tok[d.start[s]:d.start[s + 1]], k[d.start[s]:d.start[s + 1]]), s
+    assert 0 < a.sum() and (k >= 0).mean() > 0.3
+
+
 @pytest.mark.parametrize("where", [1, 2])
 @pytest.mark.parametrize("v", [8, 1024, 128256])
 def test_waits_that_give_up_leave_the_context_usable(v, where):
