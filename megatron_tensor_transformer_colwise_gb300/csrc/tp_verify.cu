@@ -68,18 +68,22 @@ __device__ __forceinline__ float ex2f(float x) {
 
 // m and s = sum 2^(x_v it - m), it = log2(e) / T, with m the largest x_v it of
 // those summed so far as it is rounded: every use of m takes that same number,
-// so its rounding cancels.  m = -inf: nothing yet.
+// so its rounding cancels, as long as 2^(its rounding) is an ordinary number: the
+// largest x_v it lies within 8 of an m below NEAR.  From there on the products are rounded
+// like m, so that the largest stands for 1; other bf16 logits lie 2^19 below it or more.
+// m = -inf: nothing yet.
 struct Stat {
     float m, s;
 };
+constexpr float NEAR = 268435456.0f;  // 2^28
 // x it, held to the finite numbers: a logit at the type's ends stays one, only
 // -inf is no probability.
 __device__ __forceinline__ float scaled(float x, float it) {
     return x == -INFINITY ? x : fminf(fmaxf(x * it, -3.4028234663852886e38f), 3.4028234663852886e38f);
 }
-// 2^(x it - m).  The product is not rounded by itself where it cannot overflow.
+// 2^(x it - m).  The product is not rounded by itself below NEAR.
 __device__ __forceinline__ float weight(float x, float it, float m) {
-    return fabsf(m) < 1e30f ? ex2f(fmaf(x, it, -m)) : ex2f(scaled(x, it) - m);
+    return fabsf(m) < NEAR ? ex2f(fmaf(x, it, -m)) : ex2f(scaled(x, it) - m);
 }
 
 // Largest value and its lowest index.
@@ -136,7 +140,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // What few calls need stays out of line, and a batch's rows share one loop's code: less to fetch in a call that
 // runs it once (97 -> 64 KB; 2 sequences of 3 drafts 11.7 -> 11.3 us, 64 sequences as before).
 
-// sum_pieces where m's product with the logits may overflow: logits at the type's ends.  m: the new maximum.
+// sum_pieces from NEAR on: low temperatures, logits at the type's ends.  m: the new maximum.
 __device__ __noinline__ Stat sum_ends(Stat a, uint4 u1, uint4 u2, float it, float m) {
     const uint32_t w[8] = {u1.x, u1.y, u1.z, u1.w, u2.x, u2.y, u2.z, u2.w};
     float sum = 0.0f;
@@ -158,7 +162,7 @@ __device__ __forceinline__ void sum_pieces(Stat& a, const uint4& u1, const uint4
 #pragma unroll
     for (int k = 0; k < 4; ++k) bm[k] = max3(fmaxf(v[k], v[k + 4]), v[k + 8], v[k + 12]);
     const float m = fmaxf(a.m, scaled(max3(fmaxf(bm[0], bm[1]), bm[2], bm[3]), it));
-    if (!(fabsf(m) < 1e30f)) {  // nothing but -inf so far, or logits at the type's ends
+    if (!(fabsf(m) < NEAR)) {  // nothing but -inf so far, or from NEAR on
         if (m != -INFINITY) a = sum_ends(a, u1, u2, it, m);
         return;
     }
@@ -193,7 +197,7 @@ __device__ __forceinline__ uint64_t weight2(uint32_t w, uint64_t its, uint64_t m
     return f2_pack(ex2f(x0), ex2f(x1));
 }
 
-// The same two of p - r q where logits stand at the type's ends.
+// The same two of p - r q from NEAR on.
 __device__ __noinline__ uint64_t weight2_ends(uint32_t z, uint32_t y, float it, float zm, float ym, float r) {
     float a0 = weight(bf16_lo(z), it, zm), a1 = weight(bf16_hi(z), it, zm);
     if (r != 0.0f) {
@@ -407,7 +411,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         const float4* noise = p.noise ? reinterpret_cast<const float4*>(p.noise + s * p.v) : nullptr;
         // p - q up to the factor 1 / p's sum.
         const float r = y ? sp.s / sq.s : 0.0f;
-        const bool plain = fabsf(sp.m) < 1e30f && (!y || fabsf(sq.m) < 1e30f);  // no logits at the type's ends
+        const bool plain = fabsf(sp.m) < NEAR && (!y || fabsf(sq.m) < NEAR);
         for (int attempt = 0; attempt < 2; ++attempt) {
             if (warp == WARPS) {
                 if (lane == 0)

@@ -188,6 +188,23 @@ def test_infinite_temperature_is_uniform_over_what_is_left():
     assert 0 < a.sum() and (k >= 0).mean() > 0.3
 
 
+@pytest.mark.parametrize("T", [1e-3, 1e-5, 1e-7, 1e-8, 3e-9, 1e-12, 1e-20, 1e-30, 1e-38])
+def test_low_temperatures(T):
+    # x / T goes up to 10^39: all but the largest logits vanish.  bf16 logits tie, so that drafts and draws among
+    # equals are left to u and the noise.  A probability is off by 2^-22 (x_max - x) / T log2 e, which is below
+    # 2 MARGIN where the probability itself is above 2^-80.
+    d = Drafts([3, 1, 4, 2] * 30, 264, seed=33, near=0.1)
+    g = torch.Generator().manual_seed(34)
+    for x in (d.logits, d.draft):
+        x += 20 * torch.randint(-1, 2, (x.shape[0], 1), generator=g)     # largest logits near 27, 7 and -13
+        best = x.float().amax(1, keepdim=True).to(torch.bfloat16)
+        x[:, 5:6] = x[:, 200:201] = best
+    d.ids[:] = torch.where(torch.rand(len(d.ids), generator=g) < 0.5, 200, 5).int()
+    d.temperature[:] = T
+    taken = d.check(least_clear=0.9)
+    assert taken.max() == 3 and taken.min() == 0
+
+
 @pytest.mark.parametrize("where", [1, 2])
 @pytest.mark.parametrize("v", [8, 1024, 128256])
 def test_waits_that_give_up_leave_the_context_usable(v, where):
