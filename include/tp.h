@@ -561,7 +561,7 @@ typedef struct {
                                    tp_kv_cache_read)                                  */
     const int32_t* kv_len;      /* [n_seqs], with this call's new tokens              */
     int64_t n_pages;            /* >= 1                                               */
-    int32_t n_seqs;             /* >= 0                                               */
+    int32_t n_seqs;             /* >= 0; page_table and kv_len may be NULL for 0      */
     int32_t max_pages;          /* row length of page_table, >= 1                     */
     int32_t page_size;          /* 16, 32, 64 or 128                                  */
     int32_t kv_dtype;           /* TP_KV_*                                            */
@@ -590,7 +590,8 @@ TP_API int tp_kv_cache_write(tp_plan_t plan, const tp_kv_cache* cache, const tp_
 /* Read back: K_out[s][p], V_out[s][p] = the cached key and value of position
  * p < min(kv_len[s], max_len) of sequence s, as bf16 (E4M3: code * scale in
  * fp32, rounded once).  K_out, V_out: device [n_seqs][max_len][k][d] bf16; rows
- * past a sequence's length are left as they are. */
+ * past a sequence's length are left as they are.  n_seqs = 0 or max_len = 0
+ * reads nothing (K_out and V_out may be NULL then). */
 TP_API int tp_kv_cache_read(tp_plan_t plan, const tp_kv_cache* cache, int64_t max_len, tp_bf16* K_out,
                             tp_bf16* V_out, void* stream);
 

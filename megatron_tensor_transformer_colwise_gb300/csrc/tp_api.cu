@@ -77,6 +77,9 @@ int opt_ptr(const void* p, const char* name) {
     return TP_OK;
 }
 
+// A buffer that may have no elements, and then no address.
+int elems_ptr(const void* p, bool none, const char* name) { return none ? opt_ptr(p, name) : need_ptr(p, name); }
+
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 int check_device(const tp_plan_s* p) {
@@ -1538,7 +1541,9 @@ int check_cache(const tp_plan_s* plan, const tp_kv_cache* c, bool needs_rows) {
         return fail(TP_ERR_INVALID_ARG, "max_pages %d x page_size %d is not in [1, 2^30] positions", c->max_pages,
                     c->page_size);
     if (c->max_new < 0) return fail(TP_ERR_INVALID_ARG, "max_new must be >= 0 (got %d)", c->max_new);
-    if ((rc = need_ptr(c->page_table, "page_table")) || (rc = need_ptr(c->kv_len, "kv_len")) ||
+    // Arrays without elements have no address.
+    const bool none = c->n_seqs == 0;
+    if ((rc = elems_ptr(c->page_table, none, "page_table")) || (rc = elems_ptr(c->kv_len, none, "kv_len")) ||
         (needs_rows && (rc = need_ptr(c->q_start, "q_start"))))
         return rc;
     return TP_OK;
@@ -1606,11 +1611,11 @@ extern "C" int tp_kv_cache_read(tp_plan_t plan, const tp_kv_cache* cache, int64_
                                 tp_bf16* V_out, void* stream) {
     tpi::PagedArgs a;
     int rc;
-    if ((rc = paged_args(plan, cache, false, &a)) || (rc = need_ptr(K_out, "K_out")) ||
-        (rc = need_ptr(V_out, "V_out")))
-        return rc;
+    if ((rc = paged_args(plan, cache, false, &a))) return rc;
     if (max_len < 0 || max_len > (int64_t)1 << 30)
         return fail(TP_ERR_INVALID_ARG, "max_len %lld is not in [0, 2^30]", (long long)max_len);
+    const bool none = cache->n_seqs == 0 || max_len == 0;
+    if ((rc = elems_ptr(K_out, none, "K_out")) || (rc = elems_ptr(V_out, none, "V_out"))) return rc;
     std::string err;
     return run(tpi::kv_read_launch(a, max_len, K_out, V_out, as_stream(stream), &err), err);
 }

@@ -350,6 +350,32 @@ def test_offsets_past_32_bits(kv):
     assert same(got, [K, V] if kv == "bf16" else [K, V, ks, vs])
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_batch_of_no_sequences(kv):
+    # Nothing is written or read; the block still computes the rows that no sequence owns.
+    x = Paged(8, 2, 64, 2, 16, [(2, 20)], kv, seed=28)
+    plan, full = x.upload()
+    scales = dict(zip(("k_scale", "v_scale"), full.tensors[2:4])) if kv == "e4m3" else {}
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    cache = tp.make_kv_cache(full.tensors[0], full.tensors[1], i32(0, 4), i32(1), i32(0), **scales)
+    before = stored(full)
+    tp.tp_kv_cache_write(plan, cache, dev(x.QKV))
+    out = torch.zeros(0, 5, x.k, x.d, dtype=torch.bfloat16, device="cuda")
+    tp.tp_kv_cache_read(plan, cache, 5, out, out)
+    tp.tp_kv_cache_read(plan, full, 0, out, out)
+    plan, O = attend(x, plan_cache=(plan, cache))
+    assert (O == 7).all() and same(stored(full), before)
+    h = 64
+    W = [dev(synth.normal_bf16(s, 0.1, 80 + i)) for i, s in enumerate([(x.a * x.d, h), (x.k * x.d, h), (x.k * x.d, h), (h, x.a * x.d)])]
+    n = tp.tp_plan_workspace_bytes(plan, tp.TP_OP_ATTN_CACHED)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    X, y = dev(synth.normal_bf16((x.rows, h), 1.0, 90)), torch.empty(x.rows, h, dtype=torch.bfloat16, device="cuda")
+    tp.tp_attn_cached_forward(plan, cache, X, *W, X, None, y, ws, n)
+    sync_ok(plan)
+    assert torch.equal(y, X)            # the residual, and o_proj of zeros
+    assert same(stored(full), before)
+
+
 def test_refusals():
     x = Paged(8, 2, 64, 2, 16, [(1, 20)], seed=18)
     plan, cache = x.upload()

@@ -63,6 +63,20 @@ def test_cache_check(cfg, kw, want):
     assert tp.tp_kv_cache_check(config(**cfg), cache(**kw)) == want, tp.tp_last_error()
 
 
+def test_a_batch_of_no_sequences_is_a_batch():
+    # Tensors without elements have no address.
+    K, i = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16), lambda *s: torch.zeros(*s, dtype=torch.int32)
+    c = tp.make_kv_cache(K, K.clone(), i(0, 4), i(1), i(0))
+    assert c.page_table is None and c.kv_len is None
+    c.q_start = 1 << 20                 # (alignment of host tensors aside)
+    c.K, c.V = 1 << 21, 1 << 22
+    for rows in (True, False):
+        assert tp.tp_kv_cache_check(config(), c, rows) == tp.TP_OK, tp.tp_last_error()
+    c.n_seqs = 1
+    assert tp.tp_kv_cache_check(config(), c) == tp.TP_ERR_INVALID_ARG
+    assert tp.tp_kv_cache_check(config(), cache(n_seqs=0, kv_len=4)) == tp.TP_ERR_INVALID_ARG  # misaligned
+
+
 def test_cache_check_without_rows():
     assert tp.tp_kv_cache_check(config(), cache(q_start=None), needs_rows=False) == tp.TP_OK
 
