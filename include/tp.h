@@ -655,7 +655,8 @@ TP_API int tp_attn_cached_forward(tp_plan_t plan, const tp_kv_cache* cache, cons
  * no sequence owns are left as they are.  A row without any probability (all
  * logits -inf) draws -1.  A device-side wait that gives up (2 s) settles
  * nothing: accepted[s] is -1 then, and so are the tokens of all rows of that
- * sequence.  (v / t) % 8 == 0. */
+ * sequence.  n_seqs and M may be 0, and arrays without elements NULL then.
+ * (v / t) % 8 == 0. */
 TP_API int tp_vocab_verify_drafts(const tp_bf16* logits, const tp_bf16* draft_logits, int64_t M, int64_t v,
                                   int32_t t, const int32_t* ids, const int32_t* q_start, int32_t n_seqs,
                                   const float* temperature, const float* u, const float* noise,

@@ -1666,10 +1666,11 @@ int verify_drafts(const tp_bf16* logits, const tp_bf16* draft_logits, int64_t M,
                   const int32_t* q_start, int32_t n_seqs, const float* temperature, const float* u, const float* noise,
                   int32_t* accepted, int32_t* tokens, int give_up, void* stream) {
     int rc;
-    if ((rc = need_ptr(logits, "logits")) || (rc = opt_ptr(draft_logits, "draft_logits")) ||
-        (rc = need_ptr(ids, "ids")) || (rc = need_ptr(q_start, "q_start")) ||
-        (rc = opt_ptr(temperature, "temperature")) || (rc = need_ptr(u, "u")) || (rc = opt_ptr(noise, "noise")) ||
-        (rc = need_ptr(accepted, "accepted")) || (rc = need_ptr(tokens, "tokens")))
+    const bool rows = M != 0;  // arrays without elements have no address
+    if ((rc = elems_ptr(logits, !rows, "logits")) || (rc = opt_ptr(draft_logits, "draft_logits")) ||
+        (rc = elems_ptr(ids, !rows, "ids")) || (rc = need_ptr(q_start, "q_start")) ||
+        (rc = opt_ptr(temperature, "temperature")) || (rc = elems_ptr(u, !rows, "u")) || (rc = opt_ptr(noise, "noise")) ||
+        (rc = elems_ptr(accepted, n_seqs == 0, "accepted")) || (rc = elems_ptr(tokens, !rows, "tokens")))
         return rc;
     if ((rc = check_vocab(M, v, t, 8))) return rc;
     if (v >= (int64_t)1 << 31) return fail(TP_ERR_INVALID_ARG, "v out of range");

@@ -236,6 +236,22 @@ def test_a_wait_that_gives_up_settles_nothing(v, where):
     assert tok[0] == -7 and (tok[own.stop:] == -7).all()
 
 
+def test_sequences_without_rows_alone():
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    acc, none = i32(3) - 7, i32(0)
+    logits = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    tp.tp_vocab_verify_drafts(logits, logits, 0, 64, 2, none, i32(4), 3, None, none.float(),
+                              torch.ones(3, 64, device="cuda"), acc, none)
+    sync_ok()
+    assert acc.tolist() == [0, 0, 0]
+    tp.tp_vocab_verify_drafts(logits, None, 0, 64, 2, none, i32(1), 0, None, none.float(), None, none, none)
+    d = Drafts([2, 1], 64, seed=35)     # rows of nobody
+    tok = i32(3) - 2
+    tp.tp_vocab_verify_drafts(dev(d.logits), dev(d.draft), 3, 64, 1, dev(d.ids), i32(1), 0, None, dev(d.u), None, none, tok)
+    sync_ok()
+    assert tok.tolist() == [-2, -2, -2]
+
+
 def test_captured_and_replayed_with_new_numbers():
     d = Drafts([3, 2], 256, seed=13)
     n, M = 2, d.logits.shape[0]

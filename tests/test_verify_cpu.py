@@ -23,6 +23,20 @@ def test_the_cluster_has_started_before_a_store_into_another_block():
     assert "return" not in src[:barrier]
 
 
+def test_no_sequences_need_no_addresses():
+    # Nothing is launched for them, and empty tensors have no address.
+    L, p = tp.lib(), 1 << 20
+
+    def verify(M, n, x, accepted):
+        return L.tp_vocab_verify_drafts(x, None, M, 64, 4, x, p, n, None, x, None, accepted, x, None)
+
+    assert verify(0, 0, None, None) == tp.TP_OK, tp.tp_last_error()
+    assert verify(3, 0, p, None) == tp.TP_OK, tp.tp_last_error()
+    assert verify(3, 0, None, None) == tp.TP_ERR_INVALID_ARG
+    assert verify(0, 2, None, None) == tp.TP_ERR_INVALID_ARG
+    assert verify(0, 0, p + 4, None) == tp.TP_ERR_INVALID_ARG
+
+
 def test_the_self_test_refuses_places_that_are_not_there():
     p = 1 << 20
     for where in (-1, 0, 3):
