@@ -335,3 +335,95 @@ def test_decoding_with_drafts_is_decoding_without():
         assert len(got) == len(drafts) + 1
         text += got
     assert text == plain_text[:len(text)]
+
+
+def test_every_replay_is_compared():
+    d = Drafts([3, 1, 4, 2] * 10, 256, seed=36, greedy=5)
+    n, M = len(d.start) - 1, d.logits.shape[0]
+    x = [dev(t) for t in (d.logits, d.draft, d.ids, torch.as_tensor(d.start, dtype=torch.int32), d.temperature, d.u, d.noise)]
+    acc, tok = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(M, dtype=torch.int32, device="cuda")
+
+    def step():
+        tp.tp_vocab_verify_drafts(x[0], x[1], M, 256, 2, x[2], x[3], n, x[4], x[5], x[6], acc, tok)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    seen = []
+    for seed in (37, 38, 39):
+        g = torch.Generator().manual_seed(seed)
+        d.u, d.noise = torch.rand(M, generator=g), torch.empty(n, 256).exponential_(generator=g)
+        x[5].copy_(d.u)
+        x[6].copy_(d.noise)
+        graph.replay()
+        sync_ok()
+        a, k, margin = d.want()
+        clear = margin > MARGIN
+        assert clear.mean() > 0.8
+        assert np.array_equal(acc.cpu().numpy()[clear], a[clear])
+        rows = np.repeat(clear, np.diff(d.start))
+        assert np.array_equal(tok.cpu().numpy()[rows], k[rows])
+        seen.append(tuple(k.tolist()))
+    assert len(set(seen)) == 3              # each replay had answers of its own
+
+
+def test_drafts_settle_what_single_steps_settle():
+    """A toy language model (embedding, attention block over a cache, output layer) decodes 200 tokens greedily, one
+    a step; then again with those as drafts and a wrong one behind them, refused drafts dropped from the
+    cache.  Wherever the largest logit leads by more than roundings upstream move it, the drafted steps take the
+    right drafts, refuse the wrong one and draw the same token."""
+    import synth
+    a, k, d, t, h, v, page, total = 4, 2, 64, 2, 128, 512, 16, 200
+    E = dev(synth.integer_bf16((v, h), -2, 2, 60))
+    W = [dev(synth.normal_bf16(s, 0.1, 61 + i)) for i, s in enumerate([(a * d, h), (k * d, h), (k * d, h), (h, a * d)])]
+    U = dev(synth.normal_bf16((v, h), 0.3, 70))
+    pages = -(-total // page)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(71)).int().reshape(1, pages).cuda()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    empty = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+
+    class Model:
+        def __init__(self):
+            self.K, self.V = (torch.zeros(pages, k, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+        def step(self, ids, length):
+            """Settled tokens behind ids[0], which stands at position `length`, and the lead of the last one's logit."""
+            M = len(ids)
+            plan = tp.Plan(tp.make_config(tokens=M, hidden=h, n_heads=a, n_kv_heads=k, head_dim=d, tp_degree=t))
+            n = tp.tp_plan_workspace_bytes(plan, tp.TP_OP_ATTN_CACHED)
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+            x, y, logits = empty(M, h), empty(M, h), empty(M, v)
+            cache = tp.make_kv_cache(self.K, self.V, table, i32(0, M), i32(length + M), max_new=M)
+            tp.tp_vocab_embedding_forward(i32(*ids), M, E, v, h, t, x)
+            tp.tp_attn_cached_forward(plan, cache, x, *W, x, None, y, ws, n)
+            tp.tp_vocab_logits_forward(y, M, h, U, v, t, logits)
+            acc, tok = i32(0), torch.zeros(M, dtype=torch.int32, device="cuda")
+            tp.tp_vocab_verify_drafts(logits, None, M, v, t, i32(*ids), i32(0, M), 1, torch.zeros(1, device="cuda"),
+                                      torch.zeros(M, device="cuda"), None, acc, tok)
+            sync_ok(plan)
+            taken = int(acc)
+            top = logits[taken].float().topk(2).values
+            return tok.tolist()[:taken + 1], float(top[0] - top[1])
+
+    plain, text, sure = Model(), [17], [True]
+    while len(text) < total:
+        got, lead = plain.step(text[-1:], len(text) - 1)
+        text += got
+        sure.append(lead > 0.5)             # a bf16 step of a logit near 16 is 2^-3, and the hidden state's steps add about as much
+    fast, rng, at, steps, taken = Model(), np.random.default_rng(3), 1, 0, 0
+    while at + 5 < total:
+        right = int(rng.integers(0, 5))
+        drafts, wrong = text[at:at + right], (text[at + right] + 1) % v
+        got, _ = fast.step([text[at - 1]] + drafts + [wrong], at - 1)
+        same = 0
+        while same < len(got) and got[same] == text[at + same]:
+            same += 1
+        if same < len(got):
+            assert not sure[at + same]
+        if all(sure[at:at + right + 1]):
+            assert got == text[at:at + right + 1]
+            steps, taken = steps + 1, taken + right
+        at += max(min(same, right + 1), 1)
+    assert steps >= 5 and taken >= 5
