@@ -834,8 +834,15 @@ cudaError_t join(Kernel kernel, const tpi::PagedArgs& a, void* O, uint8_t* w, co
                            reinterpret_cast<const int4*>(w + s.desc), static_cast<__nv_bfloat16*>(O), zero_rest ? 1 : 0);
 }
 
+// Rows of a sequence and KV head that the kernel for few rows is built for.
+int few_rows(const tpi::PagedArgs& a) { return a.e4m3 || a.head_dim == 64 ? R : 8; }
+
 // Tiles of 8 rows, or of 16 (not for heads of 128 from bf16).
 int few(const tpi::PagedArgs& a, int64_t rows, void* O, void* scratch, bool zero_rest, cudaStream_t stream, std::string* err) {
+    if (rows > few_rows(a)) {
+        if (err) *err = "paged attention: no kernel for few rows takes " + std::to_string(rows) + " rows of this cache";
+        return TP_ERR_UNSUPPORTED;
+    }
     if (rows <= 8) {
         if (a.head_dim == 128)
             return a.e4m3 ? launch_few<Cfg<128, true, 1, 8, 4, 2, 4>>(a, O, scratch, zero_rest, stream, err)
@@ -882,8 +889,7 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
     //          128:    23.8 / 103        33.7 / 170        33.7 / 165        38.6 / 199
     const int group = a.heads / a.kv_heads;
     const int64_t most = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
-    const int64_t bound = a.e4m3 || a.head_dim == 64 ? R : 8;
-    if (most * group <= bound) return few(a, most * group, O, scratch, zero_rest, stream, err);
+    if (most * group <= few_rows(a)) return few(a, most * group, O, scratch, zero_rest, stream, err);
     // A mixture from an 8-bit cache: at most half of n_seqs x most tokens are there, so many sequences have few.
     // Those go to the few-row kernel, which reads codes at the memory's rate, where the 128-row tiles take 1.7 us a
     // block whatever their rows.  One chunk of 500 tokens and 23 single ones, one launch and two: over 8000 keys 240 and
