@@ -25,12 +25,16 @@
 // matters at mma.sync's 1000 multiply-adds a clock and SM.  P^T goes from S^T's
 // registers to the second product's operand by movmatrix.  mma.sync rather than
 // tcgen05, whose tile has 64 rows at least and whose P makes a round trip
-// through tensor memory.
+// through tensor memory.  P is rounded to V's type for that product, whose operands
+// have one type: to bf16, at most 2^-8 of each weight, at random (outputs off by
+// 0.0023 of their size where one rounding at the end gives 0.0017), or beside codes
+// to fp16, 2^-11 (0.0017).  Sums, maxima and O are fp32.
 //
 // Measured, 32 query heads on 8 KV heads of 128: 64 single tokens over 500 to
 // 16000 keys from bf16 (1.04 GB) 160 us, 6.5 TB/s or 0.96 of the copy rate; over
-// 1000 to 32000 keys from 8 bits (1.17 GB) 203 us, 5.7 TB/s or 0.85: the codes'
-// conversion to fp16 and twice the keys a byte keep the schedulers busy.  One token
+// 1000 to 32000 keys from 8 bits (1.17 GB) 203 us, 5.7 TB/s or 0.85: twice the keys a
+// byte and the codes' conversion to fp16 make a block's chain of dependent steps as
+// long as its loads (45% of the issue slots used, 15% of the matrix pipe).  One token
 // over 4096 keys 10.9 us: two launches, the look-up of the shares and one block a
 // CTA, each at its latency.
 #include <cuda.h>
@@ -890,11 +894,15 @@ int attn_paged_launch(const PagedArgs& a, void* O, void* scratch, bool zero_rest
     const int group = a.heads / a.kv_heads;
     const int64_t most = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
     if (most * group <= few_rows(a)) return few(a, most * group, O, scratch, zero_rest, stream, err);
-    // A mixture from an 8-bit cache: at most half of n_seqs x most tokens are there, so many sequences have few.
-    // Those go to the few-row kernel, which reads codes at the memory's rate, where the 128-row tiles take 1.7 us a
-    // block whatever their rows.  One chunk of 500 tokens and 23 single ones, one launch and two: over 8000 keys 240 and
-    // 183 us, over 2000 79 and 71, over 500 37 and 39 (a table of that size stays with one).  From bf16 one launch is
-    // faster: 149 and 184 us over 8000.
+    // An 8-bit call that may be a mixture, its mean of new tokens a sequence at most half of the bound on them: a launch
+    // of the few-row kernel, which reads codes at the memory's rate, for the sequences of few rows, and one of the
+    // 128-row tiles, which take 1.7 us a block whatever their rows, for the others.  One chunk of 500 tokens and 23
+    // single ones, one launch and two: over 8000 keys 244 and 186 us, over 2000 80 and 74, over 500 38 and 41 (a table
+    // below 1024 keys stays with one).  The host knows no more than that mean.  Where no sequence has few, the empty pair
+    // of launches costs 3 to 5 us: 100, 100, 100 and 900 tokens behind 500 keys 49 and 53, behind 8000 263 and 267.
+    // So it does where max_new is 0, and all of the call's tokens are the bound: 4 x 500 behind 500 62 and 67, behind
+    // 8000 399 and 402; single tokens pay for the empty pair of the 128-row tiles, 32 behind 2000 keys 35 and 40, behind
+    // 8000 93 and 99.  From bf16 one launch is faster: 149 and 184 us over 8000.
     if (a.e4m3 && group <= R && 2 * a.tokens <= a.n_seqs * most && static_cast<int64_t>(a.max_pages) * a.page_size >= 1024) {
         const int rows = group <= 8 ? 8 : R;
         PagedArgs part = a;

@@ -21,12 +21,18 @@
 // instructions a logit (unpacking, the maximum, a product, 2^x, a sum) come to
 // half of that time, so the sums are kept short: the four states stay in
 // registers and are joined across lanes once for both rows.  Measured: 64
-// sequences of 2 to 5 drafts over 128256 words 43.7 us where the rows that are
-// needed take 24 at the memory's rate (issue, and each batch's exchange); 2
+// sequences of 2 to 5 drafts over 128256 words 48 us with fresh logits, 44.6 with
+// the same ones again, where the rows that are needed take 24 at the memory's
+// rate.  Neither memory (3.0 TB/s) nor issue (49% of the slots) is at its limit: a
+// batch's decision waits for its last logits and an exchange of the cluster, and
+// the producer with it, so that the ring is empty when the next batch begins.  2
 // sequences of 3 drafts over 32768 words 11.3 us, all of it latency: a batch's
 // loads, sums and exchange take about 2.5 us, the race as much.  Four rows a batch
-// bring that to 10.3 but 64 sequences to 53 and a refused first draft from 4.4 to
-// 6.2; deeper rings and prefetches of later rows change nothing.
+// brought that to 10.3 but 64 sequences from 43.7 to 53 and a refused first draft
+// from 4.4 to 6.2; deeper rings and prefetches of later rows changed nothing.
+//
+// A wait that gives up (2 s) tells every CTA of the cluster with its statistics,
+// and the sequence's answer is -1 everywhere.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
