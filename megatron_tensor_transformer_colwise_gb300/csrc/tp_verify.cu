@@ -237,6 +237,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         fence_barrier_init();
     }
     // Every CTA of the cluster runs, and its barriers are there, before one stores into another's shared memory.
+    __syncwarp();
     cluster_arrive();
     pdl_trigger();
     pdl_wait();
@@ -489,6 +490,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
                 if (abort_word) b.v = NAN;
                 store_cluster(smem_u32(&raced[attempt][rank]), tid, __float_as_uint(b.v), static_cast<uint32_t>(b.i));
             }
+            __syncwarp();
             cluster_sync_all();
             Best b = raced[attempt][0];
             failed = isnan(b.v);

@@ -23,6 +23,14 @@ def test_the_cluster_has_started_before_a_store_into_another_block():
     assert "return" not in src[:barrier]
 
 
+def test_warps_meet_before_a_barrier_of_the_cluster():
+    # The barrier's instructions are for whole warps; behind code of some lanes alone the warp is brought together.
+    src = kernel_source()
+    for of_some in (src.index("if (tid == 0) {"), src.index("if (tid < CS) {")):
+        barrier = min(x for x in (src.find("cluster_arrive()", of_some), src.find("cluster_sync_all()", of_some)) if x > 0)
+        assert src.rindex("__sync", 0, barrier) > of_some
+
+
 def test_no_sequences_need_no_addresses():
     # Nothing is launched for them, and empty tensors have no address.
     L, p = tp.lib(), 1 << 20
