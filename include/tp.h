@@ -640,6 +640,8 @@ TP_API int tp_attn_cached_forward(tp_plan_t plan, const tp_kv_cache* cache, cons
  * distribution.  T <= 0 (or NaN) is greedy: a draft is taken if it is the
  * first of the row's largest logits, and that index is the token drawn.
  * An infinite T is uniform over the words whose logits are above -inf.
+ * Probabilities are fp32: those below 2^-126 count as 0; 1 / T is held to
+ * 6.9e29, and logits / T to fp32's finite numbers.
  * A sequence without drafts is ordinary sampling from one row.
  *
  * logits, draft_logits: device [M][v] bf16, vocabulary-sharded like

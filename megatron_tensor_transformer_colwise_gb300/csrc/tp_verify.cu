@@ -82,14 +82,19 @@ struct Stat {
     float m, s;
 };
 constexpr float NEAR = 268435456.0f;  // 2^28
+// 1 / T as logits are scaled by it, and the |m| below which they are scaled and subtracted in one step: none for an
+// infinite T, where that step would take -inf times 0.
+struct Scale {
+    float it, near;
+};
 // x it, held to the finite numbers: a logit at the type's ends stays one, only
 // -inf is no probability.
 __device__ __forceinline__ float scaled(float x, float it) {
     return x == -INFINITY ? x : fminf(fmaxf(x * it, -3.4028234663852886e38f), 3.4028234663852886e38f);
 }
-// 2^(x it - m).  The product is not rounded by itself below NEAR.
-__device__ __forceinline__ float weight(float x, float it, float m) {
-    return fabsf(m) < NEAR ? ex2f(fmaf(x, it, -m)) : ex2f(scaled(x, it) - m);
+// 2^(x it - m).  The product is not rounded by itself below `near`.
+__device__ __forceinline__ float weight(float x, Scale t, float m) {
+    return fabsf(m) < t.near ? ex2f(fmaf(x, t.it, -m)) : ex2f(scaled(x, t.it) - m);
 }
 
 // Largest value and its lowest index.
@@ -136,8 +141,8 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, int rank, uint32_t 
                  : "memory");
 }
 
-__device__ __forceinline__ float prob(float x, float it, Stat st) {
-    return st.s > 0.0f ? weight(x, it, st.m) / st.s : 0.0f;
+__device__ __forceinline__ float prob(float x, Scale t, Stat st) {
+    return st.s > 0.0f ? weight(x, t, st.m) / st.s : 0.0f;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -146,7 +151,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // What few calls need stays out of line, and a batch's rows share one loop's code: less to fetch in a call that
 // runs it once (97 -> 64 KB; 2 sequences of 3 drafts 11.7 -> 11.3 us, 64 sequences as before).
 
-// sum_pieces from NEAR on: low temperatures, logits at the type's ends.  m: the new maximum.
+// sum_pieces from `near` on: low temperatures, an infinite one, logits at the type's ends.  m: the new maximum.
 __device__ __noinline__ Stat sum_ends(Stat a, uint4 u1, uint4 u2, float it, float m) {
     const uint32_t w[8] = {u1.x, u1.y, u1.z, u1.w, u2.x, u2.y, u2.z, u2.w};
     float sum = 0.0f;
@@ -156,7 +161,8 @@ __device__ __noinline__ Stat sum_ends(Stat a, uint4 u1, uint4 u2, float it, floa
 }
 
 // Two pieces of logits into a running state (u2 only if both).
-__device__ __forceinline__ void sum_pieces(Stat& a, const uint4& u1, const uint4& u2, float it) {
+__device__ __forceinline__ void sum_pieces(Stat& a, const uint4& u1, const uint4& u2, Scale t) {
+    const float it = t.it;
     const uint32_t w[8] = {u1.x, u1.y, u1.z, u1.w, u2.x, u2.y, u2.z, u2.w};
     float v[16];
 #pragma unroll
@@ -168,7 +174,7 @@ __device__ __forceinline__ void sum_pieces(Stat& a, const uint4& u1, const uint4
 #pragma unroll
     for (int k = 0; k < 4; ++k) bm[k] = max3(fmaxf(v[k], v[k + 4]), v[k + 8], v[k + 12]);
     const float m = fmaxf(a.m, scaled(max3(fmaxf(bm[0], bm[1]), bm[2], bm[3]), it));
-    if (!(fabsf(m) < NEAR)) {  // nothing but -inf so far, or from NEAR on
+    if (!(fabsf(m) < t.near)) {  // nothing but -inf so far, or from `near` on
         if (m != -INFINITY) a = sum_ends(a, u1, u2, it, m);
         return;
     }
@@ -203,12 +209,12 @@ __device__ __forceinline__ uint64_t weight2(uint32_t w, uint64_t its, uint64_t m
     return f2_pack(ex2f(x0), ex2f(x1));
 }
 
-// The same two of p - r q from NEAR on.
-__device__ __noinline__ uint64_t weight2_ends(uint32_t z, uint32_t y, float it, float zm, float ym, float r) {
-    float a0 = weight(bf16_lo(z), it, zm), a1 = weight(bf16_hi(z), it, zm);
+// The same two of p - r q from `near` on.
+__device__ __noinline__ uint64_t weight2_ends(uint32_t z, uint32_t y, Scale t, float zm, float ym, float r) {
+    float a0 = weight(bf16_lo(z), t, zm), a1 = weight(bf16_hi(z), t, zm);
     if (r != 0.0f) {
-        a0 = fmaf(-r, weight(bf16_lo(y), it, ym), a0);
-        a1 = fmaf(-r, weight(bf16_hi(y), it, ym), a1);
+        a0 = fmaf(-r, weight(bf16_lo(y), t, ym), a0);
+        a1 = fmaf(-r, weight(bf16_hi(y), t, ym), a1);
     }
     return f2_pack(a0, a1);
 }
@@ -251,9 +257,8 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         return;
     }
     const bool greedy = !(T > 0.0f);
-    // Above zero also for an infinite T (the least number of fp32): a logit of -inf times it stays -inf, and every
-    // other one vanishes.
-    const float it = fminf(fmaxf(LOG2E / T, 1.4e-45f), 1e30f);
+    const float it = fminf(LOG2E / T, 1e30f);
+    const Scale scale = {it, it > 0.0f ? NEAR : 0.0f};
     const int pieces = static_cast<int>(p.v / 8), mine = (pieces + CS - 1) / CS;
     const int begin = min(rank * mine, pieces), end = min(begin + mine, pieces);
 
@@ -355,7 +360,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
                                 b = best_piece(b, u1, (at + e * VT + tid) * 8);
                                 b = best_piece(b, u2, (at + (e + 1) * VT + tid) * 8);
                             } else {
-                                sum_pieces(b, u1, u2, it);
+                                sum_pieces(b, u1, u2, scale);
                             }
                         }
                     }
@@ -396,7 +401,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         if (lane < rows) {
             const int at = (b0 + lane) % 64, x = xs[at];
             if (greedy) take = x >= 0 && tp_.m > -INFINITY && __float_as_int(tp_.s) == x;
-            else if (x >= 0) take = us[at] * prob(ys[at], it, tq) < prob(zs[at], it, tp_);
+            else if (x >= 0) take = us[at] * prob(ys[at], scale, tq) < prob(zs[at], scale, tp_);
         }
         const unsigned kept = __ballot_sync(0xffffffffu, lane < rows && !take);
         if (kept) {
@@ -418,7 +423,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
         const float4* noise = p.noise ? reinterpret_cast<const float4*>(p.noise + s * p.v) : nullptr;
         // p - q up to the factor 1 / p's sum.
         const float r = y ? sp.s / sq.s : 0.0f;
-        const bool plain = fabsf(sp.m) < NEAR && (!y || fabsf(sq.m) < NEAR);
+        const bool plain = fabsf(sp.m) < scale.near && (!y || fabsf(sq.m) < scale.near);
         for (int attempt = 0; attempt < 2; ++attempt) {
             if (warp == WARPS) {
                 if (lane == 0)
@@ -448,7 +453,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(VT + 32, 4) verify_
                             }
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) w[h][k] = weight2_ends(zw[k], yw[k], it, sp.m, sq.m, y ? r : 0.0f);
+                            for (int k = 0; k < 4; ++k) w[h][k] = weight2_ends(zw[k], yw[k], scale, sp.m, sq.m, y ? r : 0.0f);
                         }
                     }
                     release();

@@ -188,6 +188,22 @@ def test_infinite_temperature_is_uniform_over_what_is_left():
     assert 0 < a.sum() and (k >= 0).mean() > 0.3
 
 
+def test_infinite_temperature_counts_masks_of_the_lowest_value():
+    # 0 times any finite logit is 0: words masked with bf16's lowest value are as likely as the others, so that p
+    # and q are equal and every draft is taken.
+    d = Drafts([3, 1, 2, 4] * 20, 264, seed=40)
+    g = torch.Generator().manual_seed(41)
+    for x in (d.logits, d.draft):
+        x[torch.rand(x.shape, generator=g) < 0.4] = torch.finfo(torch.bfloat16).min
+    d.logits[::4, 3], d.draft[::3, 9] = 3e38, 1e38
+    d.u[::2] = 1 - 2.0 ** -22           # taken by a hair
+    d.temperature[:] = float("inf")
+    acc, tok = d.run()
+    assert np.array_equal(acc, np.diff(d.start) - 1)
+    want = torch.from_numpy(1 / d.noise.double().numpy()).argmax(1).numpy()
+    assert np.array_equal(tok[d.start[1:] - 1], want)
+
+
 @pytest.mark.parametrize("T", [1e-3, 1e-5, 1e-7, 1e-8, 3e-9, 1e-12, 1e-20, 1e-30, 1e-38])
 def test_low_temperatures(T):
     # x / T goes up to 10^39: all but the largest logits vanish.  bf16 logits tie, so that drafts and draws among
