@@ -607,6 +607,8 @@ TP_API int tp_kv_cache_read(tp_plan_t plan, const tp_kv_cache* cache, int64_t ma
  * A non-finite V of a new token may reach the outputs of earlier tokens of the
  * same sequence in this call (0 * inf), never another sequence's; what the
  * pages hold past a sequence's length has no influence.
+ * Values V above 2^88 in magnitude may overflow: the sums are fp32 and divided
+ * by the weights' sum at their end.
  * workspace >= tp_plan_workspace_bytes(TP_OP_ATTN_PAGED); its contents need no
  * preparation, and calls that overlap on the GPU need one each. */
 TP_API int tp_attn_paged_forward(tp_plan_t plan, const tp_kv_cache* cache, const tp_bf16* QKV, tp_bf16* O,
