@@ -32,7 +32,7 @@
 // 2^-109 at least as the cache writes them, so that such a weight is below 2^-17.
 //
 // Measured, 32 query heads on 8 KV heads of 128: 2048 tokens behind 8192 cached
-// ones 250 us with fresh inputs (0.66 of cuBLAS's rate for the keys that are seen),
+// ones 249 us with fresh inputs (0.67 of cuBLAS's rate for the keys that are seen),
 // 236 us, 1300 TFLOP/s and 0.70 with the same inputs again.  A block of
 // 128 keys then takes 1900 cycles where its products need 1024: the softmax bounds
 // it (eight warps: maximum, 2^x, rounding and the way through tensor memory).
