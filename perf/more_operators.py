@@ -250,6 +250,7 @@ def _buffers(st):
         st["loss"], st["dlogits"] = _f32(c["tokens"]), _bf16(c["tokens"], c["v"])
     elif op == "output":
         st["dH"], st["dW"] = _bf16(c["tokens"], c["h"]), _f32(c["v"], c["h"])
+        st["ws_bytes"] = tp.tp_vocab_logits_backward_workspace_bytes(c["tokens"], c["v"], c["h"])
     else:
         st["clipped"] = [torch.empty_like(x) for x in st["grads"]]
         st["list"], st["norm"] = tp.make_grad_list(st["grads"], st["clipped"]), _f32(1)
@@ -341,7 +342,7 @@ def _run_output(st):
     if own:
         import megatron_tensor_transformer_colwise_gb300 as tp
         tp.tp_vocab_logits_backward(st["H"], c["tokens"], c["h"], st["W"], c["v"], c["tp"], st["dlogits"], st["dH"], st["dW"],
-                                    False)
+                                    False, st["ws"], st["ws_bytes"])
         return [st["dH"], st["dW"]]
     d = st["dlogits"].float()
     return [(d @ st["W"].float()).to(torch.bfloat16), d.T @ st["H"].float()]
