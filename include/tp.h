@@ -215,6 +215,39 @@ TP_API int tp_reduce_partials(const void* partials, int partial_dtype, int32_t t
  * x, y: device [rows][h]; h % 8 == 0, h <= 8192. */
 TP_API int tp_rmsnorm(const tp_bf16* x, int64_t rows, int32_t h, float eps, tp_bf16* y, void* stream);
 
+/* ------------------------------------------------------------ layer norm */
+
+/* y = (x - mu) r gain + bias per row of h, with mu = mean_j x_j and
+ * r = 1 / sqrt(mean_j (x_j - mu)^2 + eps): the other replicated norm of
+ * [wiki] "통신 연산 f와 g" (GPT-style blocks).  bf16 in and out, fp32
+ * arithmetic, the variance from the differences to the mean.
+ * x, y: device [rows][h] (y may be x); gain, bias: device [h] bf16 or NULL
+ * (1 and 0).  stats: device [2][rows] fp32 or NULL, gets mu and then r of each
+ * row, for tp_layernorm_backward.  h % 8 == 0, h <= 16384, eps >= 0; rows may
+ * be 0.  Values above 2^56 in magnitude may overflow a row's variance. */
+TP_API int tp_layernorm_forward(const tp_bf16* x, int64_t rows, int32_t h, const tp_bf16* gain, const tp_bf16* bias,
+                                float eps, tp_bf16* y, float* stats, void* stream);
+
+/* Bytes of workspace of tp_layernorm_backward.  Host-only. */
+TP_API int tp_layernorm_backward_workspace_bytes(int64_t rows, int32_t h, size_t* bytes);
+
+/* Gradients of tp_layernorm_forward, with xh = (x - mu) r and g = dy gain:
+ *   dx = dres + r (g - mean_j g_j - xh mean_j (g_j xh_j))
+ *   dgain = sum over rows of dy xh,  dbias = sum over rows of dy
+ * stats: what the forward saved, or NULL to find it again from x and eps.
+ * dres: device [rows][h] bf16 or NULL, the gradient that passes the norm by (a
+ * residual connection's), added before the one rounding of dx.  dx may be dy or
+ * dres.  dgain, dbias: device [h] fp32, overwritten, or added to when
+ * accumulate != 0; either may be NULL.  Sums are fp32 in an order that depends
+ * on rows and h alone: repeated calls give the same bits on one GPU model.
+ * rows = 0 clears dgain and dbias (accumulate = 0).
+ * workspace >= tp_layernorm_backward_workspace_bytes (needed if dgain or dbias
+ * is), its contents need no preparation; calls that overlap on the GPU need one
+ * each. */
+TP_API int tp_layernorm_backward(const tp_bf16* x, int64_t rows, int32_t h, const tp_bf16* gain, float eps,
+                                 const float* stats, const tp_bf16* dy, const tp_bf16* dres, tp_bf16* dx, float* dgain,
+                                 float* dbias, int accumulate, void* workspace, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------ MLP */
 
 /* Colwise projection with the activation fused ([wiki] "MLP": the first
@@ -448,6 +481,31 @@ TP_API int tp_sp_reduce_scatter(const void* partials, int partial_dtype, int32_t
 TP_API int tp_vocab_embedding_forward(const int32_t* ids, int64_t M, const tp_bf16* E, int64_t v,
                                       int32_t h, int32_t t, tp_bf16* out, void* stream);
 
+/* tp_vocab_embedding_forward times a scale: out[m] = scale * E[ids[m]], one
+ * rounding (a scale of sqrt(h) is usual where the output projection shares E).
+ * Rows of ids outside [0, v) are zeros whatever the scale.  ids, E and out may
+ * be NULL where M = 0. */
+TP_API int tp_vocab_embedding_scaled_forward(const int32_t* ids, int64_t M, const tp_bf16* E, int64_t v, int32_t h,
+                                             int32_t t, float scale, tp_bf16* out, void* stream);
+
+/* Bytes of workspace of tp_vocab_embedding_backward.  Host-only. */
+TP_API int tp_vocab_embedding_backward_workspace_bytes(int64_t M, int64_t v, int32_t h, size_t* bytes);
+
+/* Gradient of the (scaled) embedding lookup:
+ *   dE[r] = scale * sum over the m with ids[m] = r of dOut[m],
+ * fp32 sums over the tokens sorted by word, in an order that depends on the
+ * arguments and ids alone, so repeated calls give the same bits.  Shard i's
+ * gradient is rows [i v/t, (i+1) v/t) of dE; tokens whose id no shard owns are
+ * left out.  ids: device [M] int32; dOut: device [M][h] bf16; dE: device [v][h]
+ * fp32.  accumulate = 0 writes every row (zeros for words without a token);
+ * accumulate != 0 adds, and touches no other row.  h % 8 == 0, M and v below
+ * 2^31; M may be 0 (ids and dOut may be NULL then).  workspace >=
+ * tp_vocab_embedding_backward_workspace_bytes, its contents need no
+ * preparation; calls that overlap on the GPU need one each. */
+TP_API int tp_vocab_embedding_backward(const int32_t* ids, int64_t M, int64_t v, int32_t h, int32_t t, float scale,
+                                       const tp_bf16* dOut, float* dE, int accumulate, void* workspace, size_t ws_bytes,
+                                       void* stream);
+
 /* Vocab-parallel output projection: logits[M][v] = H W^T with W [v][h]
  * split by rows (colwise over the vocabulary), all shards in one launch;
  * shard i's logits are columns [i v/t, (i+1) v/t).  bf16 in and out, fp32
@@ -468,6 +526,40 @@ TP_API int tp_vocab_logits_forward(const tp_bf16* H, int64_t M, int32_t h, const
 TP_API int tp_vocab_parallel_cross_entropy(const tp_bf16* logits, int64_t M, int64_t v, int32_t t,
                                            const int32_t* labels, float* stats, float* loss,
                                            void* stream);
+
+/* tp_vocab_parallel_cross_entropy with the gradient of its logits in the same
+ * pass, for a training step, where the loss's own gradient is known (a mean's is
+ * 1 / count):
+ *   loss[m] = log(sum_j exp z_j) - z_y,   y = labels[m]
+ *   dlogits[m][j] = dloss[m] * (exp(z_j) / sum_k exp(z_k) - [j = y]).
+ * A label of -100 gives a loss and a gradient of 0 whatever dloss and the
+ * logits are; any other label outside [0, v) gives NaN in both.  Logits of -inf
+ * (masked words) have probability 0; a row of nothing else, or one with NaN or
+ * +inf, gives NaN.  The label's gradient and small losses come from the sum over
+ * the other words, not from a difference.
+ * logits, dlogits: device [M][v] bf16, vocabulary-sharded like
+ * tp_vocab_logits_forward's; dlogits may be logits.  dloss: device [M] fp32,
+ * NULL = 1.  loss: device [M] fp32.  (v / t) % 8 == 0, M and v below 2^31; M may
+ * be 0, and arrays without elements NULL then. */
+TP_API int tp_vocab_parallel_cross_entropy_train(const tp_bf16* logits, int64_t M, int64_t v, int32_t t,
+                                                 const int32_t* labels, const float* dloss, float* loss,
+                                                 tp_bf16* dlogits, void* stream);
+
+/* Bytes of workspace of tp_vocab_logits_backward.  Host-only. */
+TP_API int tp_vocab_logits_backward_workspace_bytes(int64_t M, int64_t v, int32_t h, size_t* bytes);
+
+/* Gradients of tp_vocab_logits_forward:
+ *   dH = sum_i dlogits_i W_i   (f's all-reduce: the sum over shards runs inside
+ *        one accumulator),     dW_i = dlogits_i^T H  (rows of shard i).
+ * H: device [M][h], W: [v][h], dlogits: [M][v], dH: [M][h], all bf16; dW: device
+ * [v][h] fp32, overwritten, or added to when accumulate != 0 (a weight that the
+ * embedding shares gets both gradients that way).  Either of dH and dW may be
+ * NULL.  M may be 0 (dW is cleared then unless accumulate).  h % 8 == 0,
+ * (v / t) % 8 == 0, M and v below 2^31.  workspace >=
+ * tp_vocab_logits_backward_workspace_bytes (NULL where that is 0). */
+TP_API int tp_vocab_logits_backward(const tp_bf16* H, int64_t M, int32_t h, const tp_bf16* W, int64_t v, int32_t t,
+                                    const tp_bf16* dlogits, tp_bf16* dH, float* dW, int accumulate, void* workspace,
+                                    size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------ attention */
 
@@ -523,6 +615,39 @@ TP_API int tp_layer_forward(tp_plan_t plan, const tp_bf16* X, const tp_layer_wei
 TP_API int tp_layer_forward_traced(tp_plan_t plan, const tp_bf16* X, const tp_layer_weights* w,
                                    tp_bf16* Y, void* workspace, size_t ws_bytes, void* stream,
                                    void* const* events, int n_events);
+
+/* ------------------------------------------------------------ gradient clipping */
+
+/* One gradient tensor: n elements of TP_F32 or TP_BF16 at src, its clipped form
+ * (same type) at dst.  dst may be src (clipping in place) or NULL (the tensor
+ * counts in the norm and is not written).  With n = 0 both may be NULL. */
+typedef struct {
+    const void* src;
+    void* dst;
+    int64_t n;
+    int32_t dtype; /* TP_F32 or TP_BF16 */
+} tp_grad_tensor;
+
+/* Bytes of workspace of tp_grad_clip for `count` tensors.  Host-only. */
+TP_API int tp_grad_clip_workspace_bytes(int32_t count, size_t* bytes);
+
+/* Clipping of all gradients by their norm together, between the backward passes
+ * and an optimizer's step:
+ *   N = sqrt(sum over all tensors and elements of g^2),
+ *   dst = g * min(1, max_norm / N).
+ * Weights are whole here, so a replicated parameter counts once.  Squares are
+ * summed in fp32, a few dozen at a time, and the sums in fp64 in a fixed order:
+ * repeated calls give the same bits, and no finite gradients over- or underflow.
+ * With an infinity or NaN among the gradients norm says so (inf or NaN) and dst
+ * = g.  Tensors whose factor is 1 and whose dst is src are not written.
+ * grads: host array [count], read during the call; its device pointers must be
+ * 16-byte aligned, and what one tensor writes may not overlap what another one
+ * reads or writes.  count >= 0, at most 65536.  max_norm >= 0, inf = no
+ * clipping.  norm: device [1] fp32 (inf if N is above fp32's range).
+ * workspace >= tp_grad_clip_workspace_bytes, its contents need no preparation;
+ * calls that overlap on the GPU need one each. */
+TP_API int tp_grad_clip(const tp_grad_tensor* grads, int32_t count, float max_norm, float* norm, void* workspace,
+                        size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------ paged key/value cache */
 

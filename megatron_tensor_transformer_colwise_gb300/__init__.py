@@ -37,6 +37,10 @@ __all__ = [
     "tp_attn_forward_train", "tp_attn_backward", "tp_layer_backward", "TPKVCache", "make_kv_cache",
     "TP_KV_BF16", "TP_KV_E4M3", "TP_OP_ATTN_PAGED", "TP_OP_ATTN_CACHED", "tp_kv_cache_check", "tp_kv_cache_write",
     "tp_kv_cache_read", "tp_attn_paged_forward", "tp_attn_cached_forward", "tp_vocab_verify_drafts",
+    "tp_vocab_embedding_scaled_forward", "tp_vocab_embedding_backward_workspace_bytes", "tp_vocab_embedding_backward",
+    "tp_vocab_parallel_cross_entropy_train", "tp_vocab_logits_backward_workspace_bytes", "tp_vocab_logits_backward",
+    "tp_layernorm_forward", "tp_layernorm_backward_workspace_bytes", "tp_layernorm_backward",
+    "tp_grad_clip_workspace_bytes", "tp_grad_clip", "TPGradTensor", "make_grad_list",
     "EXPORTED",
 ]
 
@@ -102,6 +106,12 @@ class TPKVCache(C.Structure):
     ]
 
 
+class TPGradTensor(C.Structure):
+    """tp_grad_tensor of the header; make_grad_list fills an array of them from tensors."""
+
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32)]
+
+
 _VP = C.c_void_p
 _SIGS = {
     "tp_plan_create": [C.POINTER(TPConfig), C.POINTER(C.c_void_p)],
@@ -147,6 +157,19 @@ _SIGS = {
     "tp_attn_paged_forward": [_VP, C.POINTER(TPKVCache), _VP, _VP, _VP, C.c_size_t, _VP],
     "tp_attn_cached_forward": [_VP, C.POINTER(TPKVCache)] + [_VP] * 9 + [C.c_size_t, _VP],
     "tp_vocab_verify_drafts": [_VP, _VP, C.c_int64, C.c_int64, C.c_int32, _VP, _VP, C.c_int32] + [_VP] * 6,
+    "tp_vocab_embedding_scaled_forward": [_VP, C.c_int64, _VP, C.c_int64, C.c_int32, C.c_int32, C.c_float, _VP, _VP],
+    "tp_vocab_embedding_backward_workspace_bytes": [C.c_int64, C.c_int64, C.c_int32, C.POINTER(C.c_size_t)],
+    "tp_vocab_embedding_backward": [_VP, C.c_int64, C.c_int64, C.c_int32, C.c_int32, C.c_float, _VP, _VP, C.c_int, _VP,
+                                    C.c_size_t, _VP],
+    "tp_vocab_parallel_cross_entropy_train": [_VP, C.c_int64, C.c_int64, C.c_int32, _VP, _VP, _VP, _VP, _VP],
+    "tp_vocab_logits_backward_workspace_bytes": [C.c_int64, C.c_int64, C.c_int32, C.POINTER(C.c_size_t)],
+    "tp_vocab_logits_backward": [_VP, C.c_int64, C.c_int32, _VP, C.c_int64, C.c_int32, _VP, _VP, _VP, C.c_int, _VP,
+                                 C.c_size_t, _VP],
+    "tp_layernorm_forward": [_VP, C.c_int64, C.c_int32, _VP, _VP, C.c_float, _VP, _VP, _VP],
+    "tp_layernorm_backward_workspace_bytes": [C.c_int64, C.c_int32, C.POINTER(C.c_size_t)],
+    "tp_layernorm_backward": [_VP, C.c_int64, C.c_int32, _VP, C.c_float] + [_VP] * 6 + [C.c_int, _VP, C.c_size_t, _VP],
+    "tp_grad_clip_workspace_bytes": [C.c_int32, C.POINTER(C.c_size_t)],
+    "tp_grad_clip": [C.POINTER(TPGradTensor), C.c_int32, C.c_float, _VP, _VP, C.c_size_t, _VP],
     "tp_selftest_verify_timeout": [_VP, C.c_int64, C.c_int64, _VP, _VP, C.c_int32, _VP, _VP, _VP, C.c_int, _VP],
 }
 EXPORTED = tuple(sorted(list(_SIGS) + ["tp_last_error"]))
@@ -534,3 +557,88 @@ def tp_vocab_verify_drafts(logits, draft_logits, M: int, v: int, t: int, ids, q_
     """Take or refuse drafted tokens against the target's probabilities and draw the next one."""
     _call("tp_vocab_verify_drafts", _p(logits), _p(draft_logits), M, v, t, _p(ids), _p(q_start), n_seqs,
           _p(temperature), _p(u), _p(noise), _p(accepted), _p(tokens), _s(stream))
+
+
+def _bytes(name: str, *args) -> int:
+    n = C.c_size_t(0)
+    _call(name, *args, C.byref(n))
+    return n.value
+
+
+def tp_vocab_embedding_scaled_forward(ids, M: int, E, v: int, h: int, t: int, scale: float, out, stream=None) -> None:
+    """Embedding rows times a scale, rounded once."""
+    _call("tp_vocab_embedding_scaled_forward", _p(ids), M, _p(E), v, h, t, scale, _p(out), _s(stream))
+
+
+def tp_vocab_embedding_backward_workspace_bytes(M: int, v: int, h: int) -> int:
+    return _bytes("tp_vocab_embedding_backward_workspace_bytes", M, v, h)
+
+
+def tp_vocab_embedding_backward(ids, M: int, v: int, h: int, t: int, scale: float, dOut, dE, accumulate: bool, workspace,
+                                ws_bytes: int, stream=None) -> None:
+    """dE (+)= scale * the sum of each word's rows of dOut."""
+    _call("tp_vocab_embedding_backward", _p(ids), M, v, h, t, scale, _p(dOut), _p(dE), 1 if accumulate else 0,
+          _p(workspace), ws_bytes, _s(stream))
+
+
+def tp_vocab_parallel_cross_entropy_train(logits, M: int, v: int, t: int, labels, dloss, loss, dlogits,
+                                          stream=None) -> None:
+    """The loss of each token and the gradient of its logits (dlogits may be logits; dloss None: 1)."""
+    _call("tp_vocab_parallel_cross_entropy_train", _p(logits), M, v, t, _p(labels), _p(dloss), _p(loss), _p(dlogits),
+          _s(stream))
+
+
+def tp_vocab_logits_backward_workspace_bytes(M: int, v: int, h: int) -> int:
+    return _bytes("tp_vocab_logits_backward_workspace_bytes", M, v, h)
+
+
+def tp_vocab_logits_backward(H, M: int, h: int, W, v: int, t: int, dlogits, dH, dW, accumulate: bool, workspace,
+                             ws_bytes: int, stream=None) -> None:
+    """Gradients of the output projection: dH = dlogits W, dW (+)= dlogits^T H (either None: not wanted)."""
+    _call("tp_vocab_logits_backward", _p(H), M, h, _p(W), v, t, _p(dlogits), _p(dH), _p(dW), 1 if accumulate else 0,
+          _p(workspace), ws_bytes, _s(stream))
+
+
+def tp_layernorm_forward(x, rows: int, h: int, gain, bias, eps: float, y, stats=None, stream=None) -> None:
+    """Layer norm of each row; stats [2][rows] gets its mean and 1 / sqrt(variance + eps)."""
+    _call("tp_layernorm_forward", _p(x), rows, h, _p(gain), _p(bias), eps, _p(y), _p(stats), _s(stream))
+
+
+def tp_layernorm_backward_workspace_bytes(rows: int, h: int) -> int:
+    return _bytes("tp_layernorm_backward_workspace_bytes", rows, h)
+
+
+def tp_layernorm_backward(x, rows: int, h: int, gain, eps: float, stats, dy, dres, dx, dgain, dbias, accumulate: bool,
+                          workspace, ws_bytes: int, stream=None) -> None:
+    """Gradients of tp_layernorm_forward (stats None: found again; dres None: no residual's gradient)."""
+    _call("tp_layernorm_backward", _p(x), rows, h, _p(gain), eps, _p(stats), _p(dy), _p(dres), _p(dx), _p(dgain),
+          _p(dbias), 1 if accumulate else 0, _p(workspace), ws_bytes, _s(stream))
+
+
+def make_grad_list(grads, out=None):
+    """The tensors of a tp_grad_clip call: contiguous float32 or bfloat16 gradients, and where each one's clipped form
+    goes (out None: in place; an entry None: nowhere).  The object keeps the tensors alive."""
+    import torch
+    code = {torch.float32: TP_F32, torch.bfloat16: TP_BF16}
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError(f"{len(grads)} gradients and {len(out)} outputs")
+    for g, o in zip(grads, out):
+        if g.dtype not in code or (o is not None and (o.dtype != g.dtype or o.numel() != g.numel())):
+            raise ValueError("gradients must be float32 or bfloat16, and outputs like them")
+        if not g.is_contiguous() or (o is not None and not o.is_contiguous()):
+            raise ValueError("gradients and outputs must be contiguous")
+    array = (TPGradTensor * len(grads))(*[TPGradTensor(_p(g), _p(o), g.numel(), code[g.dtype])
+                                          for g, o in zip(grads, out)])
+    array.tensors = [grads, out]
+    return array
+
+
+def tp_grad_clip_workspace_bytes(count: int) -> int:
+    return _bytes("tp_grad_clip_workspace_bytes", count)
+
+
+def tp_grad_clip(grads, max_norm: float, norm, workspace, ws_bytes: int, stream=None) -> None:
+    """Clip the tensors of make_grad_list by their norm together, which goes to norm [1]."""
+    _call("tp_grad_clip", grads, len(grads), max_norm, _p(norm), _p(workspace), ws_bytes, _s(stream))

@@ -1513,6 +1513,243 @@ extern "C" int tp_vocab_parallel_cross_entropy(const tp_bf16* logits, int64_t M,
 }
 
 // ---------------------------------------------------------------------------
+// A training step around the blocks: the vocabulary's gradients, layer norm,
+// gradient clipping.
+namespace {
+
+int check_train_vocab(int64_t M, int64_t v, int32_t t, int64_t align) {
+    const int rc = check_vocab(M, v, t, align);
+    if (rc) return rc;
+    if (M >= (int64_t)1 << 31) return fail(TP_ERR_INVALID_ARG, "M out of range");
+    if (v >= (int64_t)1 << 31) return fail(TP_ERR_INVALID_ARG, "v out of range");
+    return TP_OK;
+}
+
+int check_width(int32_t h, int32_t most) {
+    if (h < 8 || h % 8) return fail(TP_ERR_INVALID_ARG, "h must be a positive multiple of 8");
+    if (most && h > most) return fail(TP_ERR_INVALID_ARG, "h must be at most %d", most);
+    return TP_OK;
+}
+
+int check_scratch(const void* ws, size_t bytes, size_t need) {
+    if (need == 0) return TP_OK;
+    if (!ws) return fail(TP_ERR_WORKSPACE, "workspace is NULL but %zu bytes are needed", need);
+    if (!aligned16(ws)) return fail(TP_ERR_WORKSPACE, "workspace is not 16-byte aligned");
+    if (bytes < need) return fail(TP_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", bytes, need);
+    return TP_OK;
+}
+
+constexpr int64_t kMaxNormRows = (int64_t)1 << 30;
+constexpr int32_t kMaxNormWidth = 16384;
+constexpr int32_t kMaxGradTensors = 65536;
+
+int check_norm(int64_t rows, int32_t h, float eps) {
+    if (rows < 0 || rows > kMaxNormRows) return fail(TP_ERR_INVALID_ARG, "rows out of range");
+    if (!(eps >= 0.0f)) return fail(TP_ERR_INVALID_ARG, "eps must be >= 0");
+    return check_width(h, kMaxNormWidth);
+}
+
+// Bytes that a gradient tensor's elements take, from where.
+struct Span {
+    uintptr_t from, to;
+    bool written;
+};
+
+int check_grads(const tp_grad_tensor* g, int32_t count) {
+    if (count < 0 || count > kMaxGradTensors)
+        return fail(TP_ERR_INVALID_ARG, "count %d is not in [0, %d]", count, kMaxGradTensors);
+    if (count && !g) return fail(TP_ERR_INVALID_ARG, "grads is NULL");
+    int spans = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (g[i].n < 0 || g[i].n > (int64_t)1 << 40)
+            return fail(TP_ERR_INVALID_ARG, "tensor %d: n = %lld is not in [0, 2^40]", i, (long long)g[i].n);
+        if (g[i].dtype != TP_F32 && g[i].dtype != TP_BF16)
+            return fail(TP_ERR_INVALID_ARG, "tensor %d: dtype %d is not TP_F32(0) or TP_BF16(1)", i, g[i].dtype);
+        if (g[i].n && !g[i].src) return fail(TP_ERR_INVALID_ARG, "tensor %d: src is NULL", i);
+        if (!aligned16(g[i].src) || !aligned16(g[i].dst))
+            return fail(TP_ERR_INVALID_ARG, "tensor %d is not 16-byte aligned", i);
+        spans += g[i].dst && g[i].dst != g[i].src ? 2 : 1;
+    }
+    // What is written may overlap nothing else: one sorted sweep.
+    Span* s = new (std::nothrow) Span[spans + 1];
+    if (!s) return fail(TP_ERR_CUDA, "out of host memory");
+    int n = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (!g[i].n) continue;
+        const uintptr_t bytes = static_cast<uintptr_t>(g[i].n) * (g[i].dtype == TP_F32 ? 4 : 2);
+        const uintptr_t src = reinterpret_cast<uintptr_t>(g[i].src), dst = reinterpret_cast<uintptr_t>(g[i].dst);
+        s[n++] = {src, src + bytes, dst == src};
+        if (dst && dst != src) s[n++] = {dst, dst + bytes, true};
+    }
+    std::sort(s, s + n, [](const Span& a, const Span& b) { return a.from < b.from; });
+    uintptr_t read = 0, written = 0;  // ends of what lies before
+    bool clash = false;
+    for (int i = 0; i < n && !clash; ++i) {
+        clash = s[i].from < written || (s[i].written && s[i].from < read);
+        uintptr_t& end = s[i].written ? written : read;
+        end = std::max(end, s[i].to);
+    }
+    delete[] s;
+    if (clash) return fail(TP_ERR_INVALID_ARG, "a tensor that is written overlaps another one");
+    return TP_OK;
+}
+
+}  // namespace
+
+extern "C" int tp_vocab_embedding_scaled_forward(const int32_t* ids, int64_t M, const tp_bf16* E, int64_t v, int32_t h,
+                                                 int32_t t, float scale, tp_bf16* out, void* stream) {
+    int rc;
+    if ((rc = elems_ptr(ids, M == 0, "ids")) || (rc = elems_ptr(E, M == 0, "E")) || (rc = elems_ptr(out, M == 0, "out")) ||
+        (rc = check_train_vocab(M, v, t, 1)) || (rc = check_width(h, 0)))
+        return rc;
+    std::string err;
+    return run(tpi::vocab_embedding_scaled_launch(ids, M, E, v, h, scale, out, as_stream(stream), &err), err);
+}
+
+extern "C" int tp_vocab_embedding_backward_workspace_bytes(int64_t M, int64_t v, int32_t h, size_t* bytes) {
+    int rc;
+    if (!bytes) return fail(TP_ERR_INVALID_ARG, "bytes is NULL");
+    if ((rc = check_train_vocab(M, v, 1, 1)) || (rc = check_width(h, 0))) return rc;
+    *bytes = tpi::vocab_embedding_bwd_scratch_bytes(M, v, h);
+    return TP_OK;
+}
+
+extern "C" int tp_vocab_embedding_backward(const int32_t* ids, int64_t M, int64_t v, int32_t h, int32_t t, float scale,
+                                           const tp_bf16* dOut, float* dE, int accumulate, void* workspace,
+                                           size_t ws_bytes, void* stream) {
+    int rc;
+    if ((rc = elems_ptr(ids, M == 0, "ids")) || (rc = elems_ptr(dOut, M == 0, "dOut")) || (rc = need_ptr(dE, "dE")) ||
+        (rc = check_train_vocab(M, v, t, 1)) || (rc = check_width(h, 0)) ||
+        (rc = check_scratch(workspace, ws_bytes, tpi::vocab_embedding_bwd_scratch_bytes(M, v, h))))
+        return rc;
+    std::string err;
+    return run(tpi::vocab_embedding_bwd_launch(ids, M, v, h, scale, dOut, dE, accumulate ? 1 : 0, workspace,
+                                               as_stream(stream), &err),
+               err);
+}
+
+extern "C" int tp_vocab_parallel_cross_entropy_train(const tp_bf16* logits, int64_t M, int64_t v, int32_t t,
+                                                     const int32_t* labels, const float* dloss, float* loss,
+                                                     tp_bf16* dlogits, void* stream) {
+    int rc;
+    const bool none = M == 0;
+    if ((rc = elems_ptr(logits, none, "logits")) || (rc = elems_ptr(labels, none, "labels")) ||
+        (rc = opt_ptr(dloss, "dloss")) || (rc = elems_ptr(loss, none, "loss")) ||
+        (rc = elems_ptr(dlogits, none, "dlogits")) || (rc = check_train_vocab(M, v, t, 8)))
+        return rc;
+    std::string err;
+    return run(tpi::vocab_loss_launch(logits, M, v, labels, dloss, loss, dlogits, as_stream(stream), &err), err);
+}
+
+extern "C" int tp_vocab_logits_backward_workspace_bytes(int64_t M, int64_t v, int32_t h, size_t* bytes) {
+    int rc;
+    if (!bytes) return fail(TP_ERR_INVALID_ARG, "bytes is NULL");
+    if ((rc = check_train_vocab(M, v, 1, 8)) || (rc = check_width(h, 0))) return rc;
+    *bytes = 0;
+    return TP_OK;
+}
+
+extern "C" int tp_vocab_logits_backward(const tp_bf16* H, int64_t M, int32_t h, const tp_bf16* W, int64_t v, int32_t t,
+                                        const tp_bf16* dlogits, tp_bf16* dH, float* dW, int accumulate, void* workspace,
+                                        size_t ws_bytes, void* stream) {
+    int rc;
+    const bool none = M == 0;
+    if ((rc = elems_ptr(H, none || !dW, "H")) || (rc = elems_ptr(W, none || !dH, "W")) ||
+        (rc = elems_ptr(dlogits, none, "dlogits")) || (rc = opt_ptr(dH, "dH")) || (rc = opt_ptr(dW, "dW")) ||
+        (rc = check_train_vocab(M, v, t, 8)) || (rc = check_width(h, 0)))
+        return rc;
+    (void)workspace;
+    (void)ws_bytes;
+    cudaStream_t s = as_stream(stream);
+    std::string err;
+    if (none) {
+        if (!dW || accumulate) return TP_OK;
+        const cudaError_t e = cudaMemsetAsync(dW, 0, static_cast<size_t>(v) * h * sizeof(float), s);
+        return e == cudaSuccess ? TP_OK : fail(TP_ERR_CUDA, "clearing dW: %s", cudaGetErrorString(e));
+    }
+    if (dH) {  // dH = dlogits W: the K loop runs over all shards' words
+        tpi::GemmArgs g;
+        g.mode = tpi::GEMM_NN;
+        g.M = M;
+        g.N = h;
+        g.K = v;
+        g.A = dlogits;
+        g.B0 = W;
+        g.out = dH;
+        g.ldo = h;
+        if ((rc = run(tpi::gemm_launch(g, s, &err), err))) return rc;
+    }
+    if (dW) {  // dW = dlogits^T H (shard i: rows i v/t ..)
+        tpi::GemmArgs g;
+        g.mode = tpi::GEMM_TN;
+        g.M = v;
+        g.N = h;
+        g.K = M;
+        g.A = dlogits;
+        g.lda = v;
+        g.B0 = H;
+        g.out = dW;
+        g.ldo = h;
+        g.accumulate = accumulate ? 1 : 0;
+        return run(tpi::gemm_launch(g, s, &err), err);
+    }
+    return TP_OK;
+}
+
+extern "C" int tp_layernorm_forward(const tp_bf16* x, int64_t rows, int32_t h, const tp_bf16* gain, const tp_bf16* bias,
+                                    float eps, tp_bf16* y, float* stats, void* stream) {
+    int rc;
+    if ((rc = elems_ptr(x, rows == 0, "x")) || (rc = opt_ptr(gain, "gain")) || (rc = opt_ptr(bias, "bias")) ||
+        (rc = elems_ptr(y, rows == 0, "y")) || (rc = opt_ptr(stats, "stats")) || (rc = check_norm(rows, h, eps)))
+        return rc;
+    std::string err;
+    return run(tpi::layernorm_launch(x, rows, h, gain, bias, eps, y, stats, as_stream(stream), &err), err);
+}
+
+extern "C" int tp_layernorm_backward_workspace_bytes(int64_t rows, int32_t h, size_t* bytes) {
+    int rc;
+    if (!bytes) return fail(TP_ERR_INVALID_ARG, "bytes is NULL");
+    if ((rc = check_norm(rows, h, 0.0f))) return rc;
+    *bytes = tpi::layernorm_bwd_scratch_bytes(rows, h);
+    return TP_OK;
+}
+
+extern "C" int tp_layernorm_backward(const tp_bf16* x, int64_t rows, int32_t h, const tp_bf16* gain, float eps,
+                                     const float* stats, const tp_bf16* dy, const tp_bf16* dres, tp_bf16* dx,
+                                     float* dgain, float* dbias, int accumulate, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+    int rc;
+    const bool none = rows == 0;
+    if ((rc = elems_ptr(x, none, "x")) || (rc = opt_ptr(gain, "gain")) || (rc = opt_ptr(stats, "stats")) ||
+        (rc = elems_ptr(dy, none, "dy")) || (rc = opt_ptr(dres, "dres")) || (rc = elems_ptr(dx, none, "dx")) ||
+        (rc = opt_ptr(dgain, "dgain")) || (rc = opt_ptr(dbias, "dbias")) || (rc = check_norm(rows, h, eps)))
+        return rc;
+    if ((dgain || dbias) && (rc = check_scratch(workspace, ws_bytes, tpi::layernorm_bwd_scratch_bytes(rows, h)))) return rc;
+    std::string err;
+    return run(tpi::layernorm_bwd_launch(x, rows, h, gain, eps, stats, dy, dres, dx, dgain, dbias, accumulate ? 1 : 0,
+                                         workspace, as_stream(stream), &err),
+               err);
+}
+
+extern "C" int tp_grad_clip_workspace_bytes(int32_t count, size_t* bytes) {
+    if (!bytes) return fail(TP_ERR_INVALID_ARG, "bytes is NULL");
+    if (count < 0 || count > kMaxGradTensors)
+        return fail(TP_ERR_INVALID_ARG, "count %d is not in [0, %d]", count, kMaxGradTensors);
+    *bytes = tpi::grad_clip_scratch_bytes(count);
+    return TP_OK;
+}
+
+extern "C" int tp_grad_clip(const tp_grad_tensor* grads, int32_t count, float max_norm, float* norm, void* workspace,
+                            size_t ws_bytes, void* stream) {
+    int rc;
+    if ((rc = check_grads(grads, count)) || (rc = need_ptr(norm, "norm"))) return rc;
+    if (!(max_norm >= 0.0f)) return fail(TP_ERR_INVALID_ARG, "max_norm must be >= 0");
+    if ((rc = check_scratch(workspace, ws_bytes, tpi::grad_clip_scratch_bytes(count)))) return rc;
+    std::string err;
+    return run(tpi::grad_clip_launch(grads, count, max_norm, norm, workspace, as_stream(stream), &err), err);
+}
+
+// ---------------------------------------------------------------------------
 // Paged key/value cache: append, read back, attention over it.
 namespace {
 

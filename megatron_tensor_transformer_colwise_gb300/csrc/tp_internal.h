@@ -8,6 +8,8 @@
 
 #include <string>
 
+#include "tp.h"
+
 namespace tpi {
 
 // Launch with programmatic stream serialization: the kernel may start while
@@ -207,6 +209,29 @@ int vocab_embedding_launch(const int32_t* ids, int64_t M, const void* E, int64_t
                            cudaStream_t stream, std::string* err);
 int vocab_ce_launch(const void* logits, int64_t M, int64_t v, int t, const int32_t* labels,
                     float* stats, float* loss, cudaStream_t stream, std::string* err);
+
+// Scaled embedding lookup, the embedding's gradient, and the loss with the
+// gradient of its logits (tp_vocab_grad.cu).
+int vocab_embedding_scaled_launch(const int32_t* ids, int64_t M, const void* E, int64_t v, int h, float scale, void* out,
+                                  cudaStream_t stream, std::string* err);
+size_t vocab_embedding_bwd_scratch_bytes(int64_t M, int64_t v, int h);
+int vocab_embedding_bwd_launch(const int32_t* ids, int64_t M, int64_t v, int h, float scale, const void* dOut, float* dE,
+                               int accumulate, void* scratch, cudaStream_t stream, std::string* err);
+int vocab_loss_launch(const void* logits, int64_t M, int64_t v, const int32_t* labels, const float* dloss, float* loss,
+                      void* dlogits, cudaStream_t stream, std::string* err);
+
+// Layer norm and its gradients (tp_layernorm.cu).
+int layernorm_launch(const void* x, int64_t rows, int h, const void* gain, const void* bias, float eps, void* y,
+                     float* stats, cudaStream_t stream, std::string* err);
+size_t layernorm_bwd_scratch_bytes(int64_t rows, int h);
+int layernorm_bwd_launch(const void* x, int64_t rows, int h, const void* gain, float eps, const float* stats,
+                         const void* dy, const void* dres, void* dx, float* dgain, float* dbias, int accumulate,
+                         void* scratch, cudaStream_t stream, std::string* err);
+
+// Global gradient norm and clipping (tp_clip.cu).
+size_t grad_clip_scratch_bytes(int count);
+int grad_clip_launch(const tp_grad_tensor* grads, int count, float max_norm, float* norm, void* scratch,
+                     cudaStream_t stream, std::string* err);
 
 // A paged key/value cache and one call's new tokens (tp_kv_cache with its
 // plan's geometry).
