@@ -21,7 +21,7 @@ namespace {
 
 using namespace tpk;
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 256, CTAS = 4;  // CTAs an SM
 constexpr int CHUNK = 8192;       // elements that a CTA takes at a time
 constexpr int MAX_GRID = 2048;    // CTAs of a launch, and the sums kept for it
 constexpr int FEW = 32, MANY = 512;  // tensors of a launch
@@ -50,12 +50,94 @@ __device__ __forceinline__ const Tensor& tensor_of(const Tensors<CAP>& p, long l
     return p.t[lo];
 }
 
-__device__ __forceinline__ float value_at(const Tensor& t, long long i) {
-    return t.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.src)[i]) : static_cast<const float*>(t.src)[i];
+// A chunk is PIECES 16-byte pieces a thread of fp32, half as many of bf16, all
+// read before the first is used: 32 KB in flight a CTA.
+constexpr int PIECES = CHUNK / 4 / THREADS;
+
+template <bool BF16>
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[BF16 ? 8 : 4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF16) {
+            const float2 p = unpack_bf16x2(w[i]);
+            f[(2 * i) % (BF16 ? 8 : 4)] = p.x;
+            f[(2 * i + 1) % (BF16 ? 8 : 4)] = p.y;
+        } else {
+            f[i] = __uint_as_float(w[i]);
+        }
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float value_at(const void* src, long long i) {
+    return BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(src)[i]) : static_cast<const float*>(src)[i];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_at(void* dst, long long i, float g) {
+    if (BF16) static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(g);
+    else static_cast<float*>(dst)[i] = g;
+}
+
+// Calls one(i) for this thread's elements [from, to) of a tensor that are not
+// in a whole 16-byte piece: the last chunk's last few.
+template <int N, typename F>
+__device__ __forceinline__ void for_rest(long long from, long long to, F&& one) {
+    const long long i = from + (to - from) / N * N + threadIdx.x;
+    if (threadIdx.x < N && i < to) one(i);
+}
+
+// This thread's part of a chunk's sum of squares.
+template <bool BF16>
+__device__ __forceinline__ double chunk_sum(const void* src, long long from, long long to) {
+    constexpr int N = BF16 ? 8 : 4, P = BF16 ? PIECES / 2 : PIECES;
+    const uint4* at = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + from * (16 / N));
+    const int pieces = static_cast<int>((to - from) / N);
+    uint4 u[P];
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        const int v = threadIdx.x + k * THREADS;
+        u[k] = v < pieces ? at[v] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        float f[N];
+        unpack<BF16>(u[k], f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e & 3] = fmaf(f[e], f[e], s[e & 3]);
+        any |= u[k].x | u[k].y | u[k].z | u[k].w;
+    }
+    float t = (s[0] + s[1]) + (s[2] + s[3]);
+    for_rest<N>(from, to, [&](long long i) {
+        const float g = value_at<BF16>(src, i);
+        t = fmaf(g, g, t);
+        any |= __float_as_uint(g);
+    });
+    // Squares that leave fp32's range (a sum below 2^-90 may have lost some,
+    // one above the largest number has) are summed again in 64 bits.
+    if (t >= 0x1p-90f && t <= FLT_MAX) return t;
+    if (!(any & (BF16 ? 0x7fff7fffu : 0x7fffffffu))) return 0.0;  // zeros of either sign
+    double d = 0.0;
+#pragma unroll 1
+    for (int v = threadIdx.x; v < pieces; v += THREADS) {
+        float f[N];
+        unpack<BF16>(at[v], f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) d = fma(static_cast<double>(f[e]), static_cast<double>(f[e]), d);
+    }
+    for_rest<N>(from, to, [&](long long i) {
+        const double g = value_at<BF16>(src, i);
+        d = fma(g, g, d);
+    });
+    return d;
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(THREADS) grad_sum_kernel(const __grid_constant__ Tensors<CAP> p, double* __restrict__ sums) {
+__global__ void __launch_bounds__(THREADS, CTAS) grad_sum_kernel(const __grid_constant__ Tensors<CAP> p,
+                                                                 double* __restrict__ sums) {
     __shared__ double red[THREADS / 32];
     pdl_trigger();
     pdl_wait();
@@ -63,25 +145,7 @@ __global__ void __launch_bounds__(THREADS) grad_sum_kernel(const __grid_constant
     for (long long chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
         const Tensor& t = tensor_of(p, chunk);
         const long long from = (chunk - t.first) * CHUNK, to = min(from + CHUNK, t.n);
-        float s = 0.0f;
-        unsigned any = 0;
-        for (long long i = from + threadIdx.x; i < to; i += THREADS) {
-            const float g = value_at(t, i);
-            s = fmaf(g, g, s);
-            any |= __float_as_uint(g) << 1;
-        }
-        // Squares that leave fp32's range (a sum below 2^-90 may have lost
-        // some, one above the largest number has) are summed again in 64 bits.
-        if (any && !(s >= 0x1p-90f && s <= FLT_MAX)) {
-            double d = 0.0;
-            for (long long i = from + threadIdx.x; i < to; i += THREADS) {
-                const double g = value_at(t, i);
-                d = fma(g, g, d);
-            }
-            total += d;
-        } else {
-            total += s;
-        }
+        total += t.bf16 ? chunk_sum<true>(t.src, from, to) : chunk_sum<false>(t.src, from, to);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -94,11 +158,58 @@ __global__ void __launch_bounds__(THREADS) grad_sum_kernel(const __grid_constant
     }
 }
 
-// n_sums: CTAs of all launches of grad_sum_kernel together.
+// This thread's part of a chunk: dst = src times the factor.  Both sides are
+// used once here, so neither stays in L2 ahead of what is still to be read.
+template <bool BF16>
+__device__ __forceinline__ void chunk_scale(const void* src, void* dst, long long from, long long to, double by) {
+    constexpr int N = BF16 ? 8 : 4, P = BF16 ? PIECES / 2 : PIECES;
+    const float factor = static_cast<float>(by);
+    const uint4* at = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + from * (16 / N));
+    uint4* out = reinterpret_cast<uint4*>(static_cast<char*>(dst) + from * (16 / N));
+    const int pieces = static_cast<int>((to - from) / N);
+    uint4 u[P];
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        const int v = threadIdx.x + k * THREADS;
+        if (v < pieces) u[k] = __ldcs(at + v);
+    }
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        const int v = threadIdx.x + k * THREADS;
+        if (v >= pieces) continue;
+        float f[N];
+        unpack<BF16>(u[k], f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[e] *= factor;
+        uint4 o;
+        if (BF16)
+            o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4 % N], f[5 % N]),
+                           pack_bf16x2(f[6 % N], f[7 % N]));
+        else
+            o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        __stcs(out + v, o);
+    }
+    for_rest<N>(from, to, [&](long long i) {
+        store_at<BF16>(dst, i, value_at<BF16>(src, i) * factor);
+    });
+}
+
+// The same where fp32 does not hold the factor in full (gradients near its
+// largest number): in 64 bits, in code of its own.  With the choice made for
+// each element, both products were computed: 1100 us for 218 million gradients.
+template <bool BF16>
+__device__ __noinline__ void chunk_scale_far(const void* src, void* dst, long long from, long long to, double by) {
+#pragma unroll 1
+    for (long long i = from + threadIdx.x; i < to; i += THREADS)
+        store_at<BF16>(dst, i, static_cast<float>(value_at<BF16>(src, i) * by));
+}
+
+// n_sums: CTAs of all launches of grad_sum_kernel together.  The chunks run
+// from the last to the first: the last ones that the sums read are in L2.
 template <int CAP>
-__global__ void __launch_bounds__(THREADS) grad_scale_kernel(const __grid_constant__ Tensors<CAP> p,
-                                                             const double* __restrict__ sums, int n_sums, float max_norm,
-                                                             float* norm) {
+__global__ void __launch_bounds__(THREADS, CTAS) grad_scale_kernel(const __grid_constant__ Tensors<CAP> p,
+                                                                   const double* __restrict__ sums, int n_sums,
+                                                                   float max_norm, float* norm) {
     __shared__ double red[THREADS / 32];
     pdl_trigger();
     pdl_wait();
@@ -116,18 +227,16 @@ __global__ void __launch_bounds__(THREADS) grad_scale_kernel(const __grid_consta
     // scales nothing; the caller sees it and skips the step.
     double by = 1.0;
     if (length > max_norm && length <= DBL_MAX) by = max_norm / length;
-    // A factor that fp32 does not hold in full (gradients near its largest
-    // number) multiplies in 64 bits.
-    const bool tiny = by < 0x1p-120;
-    const float factor = static_cast<float>(by);
-    for (long long chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
+    for (long long chunk = p.chunks - 1 - blockIdx.x; chunk >= 0; chunk -= gridDim.x) {
         const Tensor& t = tensor_of(p, chunk);
         if (!t.dst || (by == 1.0 && t.dst == t.src)) continue;
         const long long from = (chunk - t.first) * CHUNK, to = min(from + CHUNK, t.n);
-        for (long long i = from + threadIdx.x; i < to; i += THREADS) {
-            const float v = value_at(t, i), g = tiny ? static_cast<float>(v * by) : v * factor;
-            if (t.bf16) static_cast<__nv_bfloat16*>(t.dst)[i] = __float2bfloat16_rn(g);
-            else static_cast<float*>(t.dst)[i] = g;
+        if (by < 0x1p-120) {
+            if (t.bf16) chunk_scale_far<true>(t.src, t.dst, from, to, by);
+            else chunk_scale_far<false>(t.src, t.dst, from, to, by);
+        } else {
+            if (t.bf16) chunk_scale<true>(t.src, t.dst, from, to, by);
+            else chunk_scale<false>(t.src, t.dst, from, to, by);
         }
     }
 }
@@ -150,7 +259,7 @@ int fill(Tensors<CAP>& p, const tp_grad_tensor* g, int count) {
         at += (g[i].n + CHUNK - 1) / CHUNK;
     }
     p.chunks = at;
-    return static_cast<int>(std::max(1LL, std::min<long long>({at, tpi::device_sm_count() * 8LL, MAX_GRID})));
+    return static_cast<int>(std::max(1LL, std::min<long long>({at, tpi::device_sm_count() * static_cast<long long>(CTAS), MAX_GRID})));
 }
 
 template <int CAP>
