@@ -23,6 +23,7 @@
 
 #include "tp_device.cuh"
 #include "tp_internal.h"
+#include "tp_packed.cuh"
 
 namespace {
 
@@ -31,226 +32,307 @@ using namespace tpk;
 constexpr int THREADS = 512;
 constexpr int MAX_PARTS = 512;  // most CTAs of the gradients' kernel
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 p = unpack_bf16x2(w[e]);
-        f[2 * e] = p.x;
-        f[2 * e + 1] = p.y;
-    }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
-
 __device__ __forceinline__ uint4 zeros8() { return make_uint4(0u, 0u, 0u, 0u); }
 __device__ __forceinline__ uint4 ones8() { return make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u); }
 
-// Sums of N values over the W warps of a row.  `red` holds two slots of W
-// values for each of N, used in turn, so that one barrier a sum is enough.
-template <int W, int N>
-struct RowSum {
-    float* red;
-    int turn = 0;
-    __device__ __forceinline__ explicit RowSum(float* r) : red(r) {}
-    __device__ __forceinline__ void operator()(float (&v)[N]) {
+// Eight bf16 values as four pairs of fp32, and back.
+__device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&p)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_bf16x2(w[i]);
+        p[i] = f2_pack(f.x, f.y);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const uint64_t (&p)[4]) {
+    uint32_t w[4];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        }
-        if (W == 1) return;
-        const int group = threadIdx.x / (32 * W), w = threadIdx.x / 32 % W;
-        float* at = red + (group * 2 + turn) * N * W;
-        if ((threadIdx.x & 31) == 0) {
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_unpack(p[i], lo, hi);
+        w[i] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint64_t both(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ float sum2(uint64_t p) {
+    float lo, hi;
+    f2_unpack(p, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) at[i * W + w] = v[i];
-        }
-        named_bar_sync(1 + group, 32 * W);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A row's pieces: W warps, VPT a thread, nv in all; this thread's are first,
+// first + 32 W, ...  count(w): the values that warp w holds.
+template <int W, int VPT>
+struct Pieces {
+    int first, nv;
+    __device__ __forceinline__ explicit Pieces(int h) : first(threadIdx.x % (32 * W)), nv(h >> 3) {}
+    __device__ __forceinline__ bool has(int i) const { return first + i * 32 * W < nv; }
+    __device__ __forceinline__ int at(int i) const { return first + i * 32 * W; }
+    __device__ __forceinline__ float count(int w) const {
+        int n = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v[i] = 0.0f;
+        for (int i = 0; i < VPT; ++i) n += min(max(nv - (i * W + w) * 32, 0), 32);
+        return static_cast<float>(n * 8);
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16* row, uint4 (&u)[VPT]) const {
 #pragma unroll
-            for (int k = 0; k < W; ++k) v[i] += at[i * W + k];
-        }
-        turn ^= 1;
+        for (int i = 0; i < VPT; ++i) u[i] = has(i) ? reinterpret_cast<const uint4*>(row)[at(i)] : zeros8();
     }
 };
 
-// Mean and 1 / sqrt(variance + eps) of a row in registers: the mean first, so
-// that a row whose mean is far from zero keeps its variance.
+// N values of each of a row's W warps, brought together in shared memory: two
+// slots in turn, so that one barrier a row is enough.
+template <int W, int N>
+struct Exchange {
+    float* at;
+    int turn = 0;
+    __device__ __forceinline__ explicit Exchange(float* shared) : at(shared + threadIdx.x / (32 * W) * 2 * W * N) {}
+    // Every warp's v[] -> the row of the warps' values, [W][N].
+    __device__ __forceinline__ const float* operator()(const float (&v)[N]) {
+        float* slot = at + turn * W * N;
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) slot[threadIdx.x / 32 % W * N + i] = v[i];
+        }
+        if (W == 1) __syncwarp();
+        else named_bar_sync(1 + threadIdx.x / (32 * W), 32 * W);
+        turn ^= 1;
+        return slot;
+    }
+};
+
+// The mean of a warp's values and the sum of their squared distances from it:
+// no difference of large sums, so a row whose mean is far from zero keeps its
+// variance.
 template <int W, int VPT>
-__device__ __forceinline__ float2 row_stats(const float (&f)[VPT][8], int first, int nv, float inv_h, float eps,
-                                            RowSum<W, 1>& sum) {
-    float s[1] = {0.0f};
+__device__ __forceinline__ float2 warp_moments(const Pieces<W, VPT>& p, const uint4 (&u)[VPT], float count) {
+    uint64_t s = both(0.0f), x[4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += f[i][e];  // pieces past the row hold zeros
+        unpack8(u[i], x);  // pieces past the row hold zeros
+        s = f2_add(s, f2_add(f2_add(x[0], x[1]), f2_add(x[2], x[3])));
     }
-    sum(s);
-    const float mean = s[0] * inv_h;
-    s[0] = 0.0f;
+    const float mean = warp_sum(sum2(s)) / fmaxf(count, 1.0f);
+    uint64_t a = both(0.0f), b = both(0.0f);
+    const uint64_t off = both(-mean);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        if (first + i * 32 * W >= nv) continue;
+        if (!p.has(i)) continue;
+        unpack8(u[i], x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] = fmaf(f[i][e] - mean, f[i][e] - mean, s[0]);
+        for (int e = 0; e < 4; ++e) {
+            x[e] = f2_add(x[e], off);
+            if (e & 1) a = f2_fma(x[e], x[e], a);
+            else b = f2_fma(x[e], x[e], b);
+        }
     }
-    sum(s);
-    return make_float2(mean, rsqrtf(s[0] * inv_h + eps));
+    return make_float2(mean, warp_sum(sum2(a) + sum2(b)));
+}
+
+// A row's mean and 1 / sqrt(variance + eps) from its warps' moments, which are
+// the first two of N values each.
+template <int W, int VPT, int N>
+__device__ __forceinline__ float2 row_stats(const Pieces<W, VPT>& p, const float* all, float inv_h, float eps) {
+    float mean = 0.0f, m2 = 0.0f;
+    if (W == 1) {
+        mean = all[0];
+        m2 = all[1];
+    } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k) mean = fmaf(p.count(k) * inv_h, all[k * N], mean);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float d = all[k * N] - mean;
+            m2 += fmaf(p.count(k) * d, d, all[k * N + 1]);
+        }
+    }
+    return make_float2(mean, rsqrtf(m2 * inv_h + eps));
 }
 
 template <int W, int VPT>
-__global__ void __launch_bounds__(THREADS) layernorm_kernel(const __nv_bfloat16* x, long long rows, int h,
-                                                            const __nv_bfloat16* __restrict__ gain,
-                                                            const __nv_bfloat16* __restrict__ bias, float eps,
-                                                            __nv_bfloat16* y, float* __restrict__ stats) {
+__global__ void __launch_bounds__(THREADS, VPT > 2 ? 1 : 2) layernorm_kernel(const __nv_bfloat16* x, long long rows, int h,
+                                                                             const __nv_bfloat16* __restrict__ gain,
+                                                                             const __nv_bfloat16* __restrict__ bias, float eps,
+                                                                             __nv_bfloat16* y, float* __restrict__ stats) {
     constexpr int GROUPS = THREADS / (32 * W);
-    __shared__ float red[GROUPS * 2 * W];
+    __shared__ float shared[GROUPS * 2 * W * 2];
     pdl_trigger();
     pdl_wait();
-    RowSum<W, 1> sum(red);
-    const int first = threadIdx.x % (32 * W), nv = h >> 3;
-    const float inv_h = 1.0f / static_cast<float>(h);
-    uint4 gv[VPT], bv[VPT];
+    const Pieces<W, VPT> p(h);
+    Exchange<W, 2> exchange(shared);
+    const float inv_h = 1.0f / static_cast<float>(h), count = p.count(threadIdx.x / 32 % W);
+    const long long step = static_cast<long long>(gridDim.x) * GROUPS;
+    long long row = static_cast<long long>(blockIdx.x) * GROUPS + threadIdx.x / (32 * W);
+    uint4 next[VPT];
+    if (row < rows) p.load(x + row * h, next);
+    for (; row < rows; row += step) {
+        uint4 u[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = first + i * 32 * W;
-        gv[i] = gain && v < nv ? reinterpret_cast<const uint4*>(gain)[v] : ones8();
-        bv[i] = bias && v < nv ? reinterpret_cast<const uint4*>(bias)[v] : zeros8();
-    }
-    for (long long row = static_cast<long long>(blockIdx.x) * GROUPS + threadIdx.x / (32 * W); row < rows;
-         row += static_cast<long long>(gridDim.x) * GROUPS) {
-        float f[VPT][8];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = first + i * 32 * W;
-            unpack8(v < nv ? reinterpret_cast<const uint4*>(x + row * h)[v] : zeros8(), f[i]);
-        }
-        const float2 st = row_stats<W, VPT>(f, first, nv, inv_h, eps, sum);
-        if (stats && first == 0) {
+        for (int i = 0; i < VPT; ++i) u[i] = next[i];
+        if (row + step < rows) p.load(x + (row + step) * h, next);
+        const float2 m = warp_moments<W, VPT>(p, u, count);
+        const float v[2] = {m.x, m.y};
+        const float2 st = row_stats<W, VPT, 2>(p, exchange(v), inv_h, eps);
+        if (stats && p.first == 0) {
             stats[row] = st.x;
             stats[rows + row] = st.y;
         }
+        const uint64_t off = both(-st.x), r = both(st.y);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = first + i * 32 * W;
-            if (v >= nv) continue;
-            float g[8], b[8];
-            unpack8(gv[i], g);
-            unpack8(bv[i], b);
+            if (!p.has(i)) continue;
+            uint64_t f[4], g[4], b[4];
+            unpack8(u[i], f);
+            unpack8(gain ? reinterpret_cast<const uint4*>(gain)[p.at(i)] : ones8(), g);
+            unpack8(bias ? reinterpret_cast<const uint4*>(bias)[p.at(i)] : zeros8(), b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[i][e] = fmaf((f[i][e] - st.x) * st.y, g[e], b[e]);
-            reinterpret_cast<uint4*>(y + row * h)[v] = pack8(f[i]);
+            for (int e = 0; e < 4; ++e) f[e] = f2_fma(f2_mul(f2_add(f[e], off), r), g[e], b[e]);
+            reinterpret_cast<uint4*>(y + row * h)[p.at(i)] = pack8(f);
         }
     }
 }
 
 // dx of every row, and the CTA's sums for dgain and dbias in parts
 // [CTAs][2][h].  dx may be dy or dres: a row's inputs are in registers before
-// its outputs are stored, and no other row's are touched.
+// its outputs are stored, and no other row's are touched.  The sums over a row
+// are taken about the warps' own means, so that they need one exchange with
+// those that give the statistics:
+//   sum g xh = r sum_w (sum g (x - mean_w) + (mean_w - mu) sum g).
 template <int W, int VPT>
-__global__ void __launch_bounds__(THREADS) layernorm_bwd_kernel(const __nv_bfloat16* __restrict__ x, long long rows, int h,
-                                                                const __nv_bfloat16* __restrict__ gain, float eps,
-                                                                const float* __restrict__ stats, const __nv_bfloat16* dy,
-                                                                const __nv_bfloat16* dres, __nv_bfloat16* dx,
-                                                                float* __restrict__ parts) {
+__global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bfloat16* __restrict__ x, long long rows, int h,
+                                                                   const __nv_bfloat16* __restrict__ gain, float eps,
+                                                                   const float* __restrict__ stats, const __nv_bfloat16* dy,
+                                                                   const __nv_bfloat16* dres, __nv_bfloat16* dx,
+                                                                   float* __restrict__ parts) {
     constexpr int GROUPS = THREADS / (32 * W);
-    __shared__ float red[GROUPS * 2 * W * 3];
+    __shared__ float shared[GROUPS * 2 * W * 4];
     pdl_trigger();
     pdl_wait();
-    RowSum<W, 1> sum(red);
-    RowSum<W, 2> sums(red + GROUPS * 2 * W);
-    const int first = threadIdx.x % (32 * W), nv = h >> 3, group = threadIdx.x / (32 * W);
-    const float inv_h = 1.0f / static_cast<float>(h);
-    uint4 gv[VPT];
-    float dg[VPT][8], db[VPT][8];
+    const Pieces<W, VPT> p(h);
+    Exchange<W, 4> exchange(shared);
+    const int group = threadIdx.x / (32 * W);
+    const float inv_h = 1.0f / static_cast<float>(h), count = p.count(threadIdx.x / 32 % W);
+    const long long step = static_cast<long long>(gridDim.x) * GROUPS;
+    long long row = static_cast<long long>(blockIdx.x) * GROUPS + group;
+    uint64_t dg[VPT][4], db[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = first + i * 32 * W;
-        gv[i] = gain && v < nv ? reinterpret_cast<const uint4*>(gain)[v] : ones8();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) dg[i][e] = db[i][e] = both(0.0f);
     }
-    for (long long row = static_cast<long long>(blockIdx.x) * GROUPS + group; row < rows;
-         row += static_cast<long long>(gridDim.x) * GROUPS) {
-        float f[VPT][8];
-        uint4 dv[VPT];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = first + i * 32 * W;
-            unpack8(v < nv ? reinterpret_cast<const uint4*>(x + row * h)[v] : zeros8(), f[i]);
-            dv[i] = v < nv ? reinterpret_cast<const uint4*>(dy + row * h)[v] : zeros8();
+    constexpr bool AHEAD = VPT <= 2;  // the next row's inputs on their way: as many registers as there are
+    uint4 xnext[VPT], dnext[VPT];
+    if (AHEAD && row < rows) {
+        p.load(x + row * h, xnext);
+        p.load(dy + row * h, dnext);
+    }
+    for (; row < rows; row += step) {
+        uint4 xv[VPT], dv[VPT], res[VPT];
+        if (!AHEAD) {
+            p.load(x + row * h, xnext);
+            p.load(dy + row * h, dnext);
         }
-        const float2 st = stats ? make_float2(stats[row], stats[rows + row])
-                                : row_stats<W, VPT>(f, first, nv, inv_h, eps, sum);
-        float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            float g[8], d[8];
-            unpack8(gv[i], g);
-            unpack8(dv[i], d);
+            xv[i] = xnext[i];
+            dv[i] = dnext[i];
+            res[i] = zeros8();
+        }
+        if (dres && AHEAD) p.load(dres + row * h, res);
+        if (AHEAD && row + step < rows) {
+            p.load(x + (row + step) * h, xnext);
+            p.load(dy + (row + step) * h, dnext);
+        }
+        const float2 m = stats ? make_float2(stats[row], 0.0f) : warp_moments<W, VPT>(p, xv, count);
+        uint64_t sg = both(0.0f), sgx = both(0.0f);
+        uint64_t off = both(-m.x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[i][e] = (f[i][e] - st.x) * st.y;
-                dg[i][e] = fmaf(d[e], f[i][e], dg[i][e]);
-                db[i][e] += d[e];
-                s[0] = fmaf(d[e], g[e], s[0]);
-                s[1] = fmaf(d[e] * g[e], f[i][e], s[1]);
+        for (int i = 0; i < VPT; ++i) {
+            if (!p.has(i)) continue;
+            uint64_t f[4], g[4], d[4];
+            unpack8(xv[i], f);
+            unpack8(dv[i], d);
+            unpack8(gain ? reinterpret_cast<const uint4*>(gain)[p.at(i)] : ones8(), g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g[e] = f2_mul(g[e], d[e]);
+                sg = f2_add(sg, g[e]);
+                sgx = f2_fma(g[e], f2_add(f[e], off), sgx);
             }
         }
-        sums(s);
-        const float c1 = s[0] * inv_h, c2 = s[1] * inv_h;
+        const float v[4] = {m.x, m.y, warp_sum(sum2(sg)), warp_sum(sum2(sgx))};
+        const float* all = exchange(v);
+        const float2 st = stats ? make_float2(m.x, stats[rows + row]) : row_stats<W, VPT, 4>(p, all, inv_h, eps);
+        float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            c1 += all[k * 4 + 2];
+            c2 += fmaf(all[k * 4] - st.x, all[k * 4 + 2], all[k * 4 + 3]);
+        }
+        c1 *= inv_h;
+        c2 *= inv_h * st.y;
+        if (dres && !AHEAD) p.load(dres + row * h, res);
+        const uint64_t r = both(st.y), n1 = both(-c1), n2 = both(-c2);
+        off = both(-st.x);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = first + i * 32 * W;
-            if (v >= nv) continue;
-            float g[8], d[8], a[8];
-            unpack8(gv[i], g);
+            if (!p.has(i)) continue;
+            uint64_t f[4], g[4], d[4], a[4];
+            unpack8(xv[i], f);
             unpack8(dv[i], d);
-            unpack8(dres ? reinterpret_cast<const uint4*>(dres + row * h)[v] : zeros8(), a);
+            unpack8(gain ? reinterpret_cast<const uint4*>(gain)[p.at(i)] : ones8(), g);
+            unpack8(res[i], a);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) a[e] = fmaf(st.y, fmaf(-f[i][e], c2, fmaf(d[e], g[e], -c1)), a[e]);
-            reinterpret_cast<uint4*>(dx + row * h)[v] = pack8(a);
+            for (int e = 0; e < 4; ++e) {
+                f[e] = f2_mul(f2_add(f[e], off), r);
+                dg[i][e] = f2_fma(d[e], f[e], dg[i][e]);
+                db[i][e] = f2_add(db[i][e], d[e]);
+                a[e] = f2_fma(r, f2_fma(f[e], n2, f2_fma(d[e], g[e], n1)), a[e]);
+            }
+            reinterpret_cast<uint4*>(dx + row * h)[p.at(i)] = pack8(a);
         }
     }
     if (!parts) return;
-    // The CTA's rows at a time are added in shared memory, group by group.
-    extern __shared__ float cols[];  // [2][h] where GROUPS > 1
-    float* out = parts + static_cast<long long>(blockIdx.x) * 2 * h;
-    for (int k = 0; k < GROUPS; ++k) {
-        if (k == group) {
+    // The rows that the CTA holds at a time are added in shared memory.
+    extern __shared__ float2 cols[];  // [GROUPS][h / 2] pairs of columns
+    float2* out = reinterpret_cast<float2*>(parts + static_cast<long long>(blockIdx.x) * 2 * h);
+    const int half = h >> 1;
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int v = first + i * 32 * W;
-                if (v >= nv) continue;
+    for (int k = 0; k < 2; ++k) {  // dgain, dbias
+        float2* mine = GROUPS > 1 ? cols + group * half : out + k * half;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int c = v * 8 + e;
-                    if (k) {
-                        dg[i][e] += cols[c];
-                        db[i][e] += cols[h + c];
-                    }
-                    if (k + 1 < GROUPS) {
-                        cols[c] = dg[i][e];
-                        cols[h + c] = db[i][e];
-                    } else {
-                        out[c] = dg[i][e];
-                        out[h + c] = db[i][e];
-                    }
-                }
+        for (int i = 0; i < VPT; ++i) {
+            if (!p.has(i)) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float2 s;
+                f2_unpack(k ? db[i][e] : dg[i][e], s.x, s.y);
+                mine[p.at(i) * 4 + e] = s;
             }
         }
-        if (GROUPS > 1) __syncthreads();
+        if (GROUPS == 1) continue;
+        __syncthreads();
+        for (int c = threadIdx.x; c < half; c += THREADS) {
+            float2 s = cols[c];
+            for (int g = 1; g < GROUPS; ++g) {
+                s.x += cols[g * half + c].x;
+                s.y += cols[g * half + c].y;
+            }
+            out[k * half + c] = s;
+        }
+        __syncthreads();
     }
 }
 
-// dgain (+)= and dbias (+)= the CTAs' sums, in order: 32 columns a CTA, eight
-// warps that take every eighth part, joined in order.
-constexpr int JOIN_WARPS = 8;
+// dgain (+)= and dbias (+)= the CTAs' sums in a fixed order: 32 columns a CTA,
+// warps that take every JOIN_WARPS-th part, joined in order.
+constexpr int JOIN_WARPS = 16;
 
 __global__ void __launch_bounds__(JOIN_WARPS * 32) layernorm_join_kernel(const float* __restrict__ parts, int n, int h,
                                                                         float* dgain, float* dbias, int accumulate) {
@@ -262,6 +344,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) layernorm_join_kernel(const f
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < h) {
+#pragma unroll 8
         for (int k = w; k < n; k += JOIN_WARPS) s += parts[(static_cast<long long>(k) * 2 + blockIdx.y) * h + c];
     }
     sum[w][lane] = s;
@@ -308,7 +391,7 @@ int layernorm_launch(const void* x, int64_t rows, int h, const void* gain, const
     if (rows == 0) return TP_OK;
     return for_width(h, [&](auto W, auto VPT) {
         constexpr int GROUPS = THREADS / (32 * decltype(W)::value);
-        const int64_t grid = std::min<int64_t>((rows + GROUPS - 1) / GROUPS, device_sm_count() * 4);
+        const int64_t grid = std::min<int64_t>((rows + GROUPS - 1) / GROUPS, device_sm_count() * 2);
         launch_pdl(layernorm_kernel<decltype(W)::value, decltype(VPT)::value>, dim3((unsigned)grid), dim3(THREADS), 0,
                    stream, static_cast<const __nv_bfloat16*>(x), static_cast<long long>(rows), h,
                    static_cast<const __nv_bfloat16*>(gain), static_cast<const __nv_bfloat16*>(bias), eps,
@@ -331,7 +414,9 @@ int layernorm_bwd_launch(const void* x, int64_t rows, int h, const void* gain, f
             constexpr int GROUPS = THREADS / (32 * decltype(W)::value);
             auto kern = layernorm_bwd_kernel<decltype(W)::value, decltype(VPT)::value>;
             grid = std::min<int64_t>({(rows + GROUPS - 1) / GROUPS, device_sm_count(), MAX_PARTS});
-            const size_t smem = GROUPS > 1 && weights ? static_cast<size_t>(h) * 2 * sizeof(float) : 0;
+            const size_t smem = GROUPS > 1 && weights ? static_cast<size_t>(GROUPS) * h * sizeof(float) : 0;
+            static_assert(GROUPS == 1 || GROUPS * 256 * decltype(W)::value * decltype(VPT)::value * sizeof(float) <= 32768,
+                          "fits without a larger limit on shared memory");
             launch_pdl(kern, dim3((unsigned)grid), dim3(THREADS), smem, stream, static_cast<const __nv_bfloat16*>(x),
                        static_cast<long long>(rows), h, static_cast<const __nv_bfloat16*>(gain), eps, stats,
                        static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(dres),
