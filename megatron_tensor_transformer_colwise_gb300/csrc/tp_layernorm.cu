@@ -87,44 +87,50 @@ struct Pieces {
 };
 
 // N values of each of a row's W warps, brought together in shared memory: two
-// slots in turn, so that one barrier a row is enough.
+// slots in turn, so that one barrier a row is enough.  Lane k gets those of warp
+// k % W; all(x) adds x over the warps.
 template <int W, int N>
 struct Exchange {
     float* at;
     int turn = 0;
     __device__ __forceinline__ explicit Exchange(float* shared) : at(shared + threadIdx.x / (32 * W) * 2 * W * N) {}
-    // Every warp's v[] -> the row of the warps' values, [W][N].
-    __device__ __forceinline__ const float* operator()(const float (&v)[N]) {
+    __device__ __forceinline__ void operator()(float (&v)[N]) {
+        if (W == 1) return;
         float* slot = at + turn * W * N;
         if ((threadIdx.x & 31) == 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i) slot[threadIdx.x / 32 % W * N + i] = v[i];
         }
-        if (W == 1) __syncwarp();
-        else named_bar_sync(1 + threadIdx.x / (32 * W), 32 * W);
+        named_bar_sync(1 + threadIdx.x / (32 * W), 32 * W);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = slot[threadIdx.x % W * N + i];
         turn ^= 1;
-        return slot;
+    }
+    static __device__ __forceinline__ float all(float x) {
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
     }
 };
 
 // The mean of a warp's values and the sum of their squared distances from it:
 // no difference of large sums, so a row whose mean is far from zero keeps its
 // variance.
-template <int W, int VPT>
-__device__ __forceinline__ float2 warp_moments(const Pieces<W, VPT>& p, const uint4 (&u)[VPT], float count) {
+template <int W, int VPT, typename F>
+__device__ __forceinline__ float2 warp_moments(const Pieces<W, VPT>& p, float inv_count, F&& piece) {
     uint64_t s = both(0.0f), x[4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        unpack8(u[i], x);  // pieces past the row hold zeros
+        piece(i, x);  // pieces past the row hold zeros
         s = f2_add(s, f2_add(f2_add(x[0], x[1]), f2_add(x[2], x[3])));
     }
-    const float mean = warp_sum(sum2(s)) / fmaxf(count, 1.0f);
+    const float mean = warp_sum(sum2(s)) * inv_count;
     uint64_t a = both(0.0f), b = both(0.0f);
     const uint64_t off = both(-mean);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         if (!p.has(i)) continue;
-        unpack8(u[i], x);
+        piece(i, x);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             x[e] = f2_add(x[e], off);
@@ -135,24 +141,13 @@ __device__ __forceinline__ float2 warp_moments(const Pieces<W, VPT>& p, const ui
     return make_float2(mean, warp_sum(sum2(a) + sum2(b)));
 }
 
-// A row's mean and 1 / sqrt(variance + eps) from its warps' moments, which are
-// the first two of N values each.
-template <int W, int VPT, int N>
-__device__ __forceinline__ float2 row_stats(const Pieces<W, VPT>& p, const float* all, float inv_h, float eps) {
-    float mean = 0.0f, m2 = 0.0f;
-    if (W == 1) {
-        mean = all[0];
-        m2 = all[1];
-    } else {
-#pragma unroll
-        for (int k = 0; k < W; ++k) mean = fmaf(p.count(k) * inv_h, all[k * N], mean);
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-            const float d = all[k * N] - mean;
-            m2 += fmaf(p.count(k) * d, d, all[k * N + 1]);
-        }
-    }
-    return make_float2(mean, rsqrtf(m2 * inv_h + eps));
+// A row's mean and 1 / sqrt(variance + eps) from its warps' moments (lane k has
+// those of warp k % W, and that warp's share of the row).
+template <int W, int N>
+__device__ __forceinline__ float2 row_stats(float warp_mean, float m2, float share, float inv_h, float eps) {
+    using X = Exchange<W, N>;
+    const float mean = W == 1 ? warp_mean : X::all(share * warp_mean), d = warp_mean - mean;
+    return make_float2(mean, rsqrtf(X::all(fmaf(share * d, d, m2 * inv_h)) + eps));
 }
 
 template <int W, int VPT>
@@ -166,19 +161,24 @@ __global__ void __launch_bounds__(THREADS, VPT > 2 ? 1 : 2) layernorm_kernel(con
     pdl_wait();
     const Pieces<W, VPT> p(h);
     Exchange<W, 2> exchange(shared);
-    const float inv_h = 1.0f / static_cast<float>(h), count = p.count(threadIdx.x / 32 % W);
+    const float inv_h = 1.0f / static_cast<float>(h), share = p.count(threadIdx.x % W) * inv_h;
+    const float inv_count = 1.0f / fmaxf(p.count(threadIdx.x / 32 % W), 1.0f);
     const long long step = static_cast<long long>(gridDim.x) * GROUPS;
     long long row = static_cast<long long>(blockIdx.x) * GROUPS + threadIdx.x / (32 * W);
     uint4 next[VPT];
     if (row < rows) p.load(x + row * h, next);
     for (; row < rows; row += step) {
-        uint4 u[VPT];
+        uint64_t f[VPT][4];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) u[i] = next[i];
+        for (int i = 0; i < VPT; ++i) unpack8(next[i], f[i]);
         if (row + step < rows) p.load(x + (row + step) * h, next);
-        const float2 m = warp_moments<W, VPT>(p, u, count);
-        const float v[2] = {m.x, m.y};
-        const float2 st = row_stats<W, VPT, 2>(p, exchange(v), inv_h, eps);
+        const float2 m = warp_moments<W, VPT>(p, inv_count, [&](int i, uint64_t(&out)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[e] = f[i][e];
+        });
+        float v[2] = {m.x, m.y};
+        exchange(v);
+        const float2 st = row_stats<W, 2>(v[0], v[1], share, inv_h, eps);
         if (stats && p.first == 0) {
             stats[row] = st.x;
             stats[rows + row] = st.y;
@@ -187,13 +187,12 @@ __global__ void __launch_bounds__(THREADS, VPT > 2 ? 1 : 2) layernorm_kernel(con
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (!p.has(i)) continue;
-            uint64_t f[4], g[4], b[4];
-            unpack8(u[i], f);
+            uint64_t g[4], b[4];
             unpack8(gain ? reinterpret_cast<const uint4*>(gain)[p.at(i)] : ones8(), g);
             unpack8(bias ? reinterpret_cast<const uint4*>(bias)[p.at(i)] : zeros8(), b);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = f2_fma(f2_mul(f2_add(f[e], off), r), g[e], b[e]);
-            reinterpret_cast<uint4*>(y + row * h)[p.at(i)] = pack8(f);
+            for (int e = 0; e < 4; ++e) f[i][e] = f2_fma(f2_mul(f2_add(f[i][e], off), r), g[e], b[e]);
+            reinterpret_cast<uint4*>(y + row * h)[p.at(i)] = pack8(f[i]);
         }
     }
 }
@@ -217,7 +216,8 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
     const Pieces<W, VPT> p(h);
     Exchange<W, 4> exchange(shared);
     const int group = threadIdx.x / (32 * W);
-    const float inv_h = 1.0f / static_cast<float>(h), count = p.count(threadIdx.x / 32 % W);
+    const float inv_h = 1.0f / static_cast<float>(h), share = p.count(threadIdx.x % W) * inv_h;
+    const float inv_count = 1.0f / fmaxf(p.count(threadIdx.x / 32 % W), 1.0f);
     const long long step = static_cast<long long>(gridDim.x) * GROUPS;
     long long row = static_cast<long long>(blockIdx.x) * GROUPS + group;
     uint64_t dg[VPT][4], db[VPT][4];
@@ -228,11 +228,15 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
     }
     constexpr bool AHEAD = VPT <= 2;  // the next row's inputs on their way: as many registers as there are
     uint4 xnext[VPT], dnext[VPT];
+    float2 snext = make_float2(0.0f, 0.0f);
     if (AHEAD && row < rows) {
         p.load(x + row * h, xnext);
         p.load(dy + row * h, dnext);
     }
+    if (stats && row < rows) snext = make_float2(stats[row], stats[rows + row]);
     for (; row < rows; row += step) {
+        const float2 saved = snext;
+        if (stats && row + step < rows) snext = make_float2(stats[row + step], stats[rows + row + step]);
         uint4 xv[VPT], dv[VPT], res[VPT];
         if (!AHEAD) {
             p.load(x + row * h, xnext);
@@ -249,7 +253,8 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
             p.load(x + (row + step) * h, xnext);
             p.load(dy + (row + step) * h, dnext);
         }
-        const float2 m = stats ? make_float2(stats[row], 0.0f) : warp_moments<W, VPT>(p, xv, count);
+        const float2 m = stats ? make_float2(saved.x, 0.0f)
+                               : warp_moments<W, VPT>(p, inv_count, [&](int i, uint64_t(&out)[4]) { unpack8(xv[i], out); });
         uint64_t sg = both(0.0f), sgx = both(0.0f);
         uint64_t off = both(-m.x);
 #pragma unroll
@@ -266,17 +271,11 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
                 sgx = f2_fma(g[e], f2_add(f[e], off), sgx);
             }
         }
-        const float v[4] = {m.x, m.y, warp_sum(sum2(sg)), warp_sum(sum2(sgx))};
-        const float* all = exchange(v);
-        const float2 st = stats ? make_float2(m.x, stats[rows + row]) : row_stats<W, VPT, 4>(p, all, inv_h, eps);
-        float c1 = 0.0f, c2 = 0.0f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-            c1 += all[k * 4 + 2];
-            c2 += fmaf(all[k * 4] - st.x, all[k * 4 + 2], all[k * 4 + 3]);
-        }
-        c1 *= inv_h;
-        c2 *= inv_h * st.y;
+        float v[4] = {m.x, m.y, warp_sum(sum2(sg)), warp_sum(sum2(sgx))};
+        exchange(v);
+        using X = Exchange<W, 4>;
+        const float2 st = stats ? saved : row_stats<W, 4>(v[0], v[1], share, inv_h, eps);
+        const float c1 = X::all(v[2]) * inv_h, c2 = X::all(fmaf(v[0] - st.x, v[2], v[3])) * (inv_h * st.y);
         if (dres && !AHEAD) p.load(dres + row * h, res);
         const uint64_t r = both(st.y), n1 = both(-c1), n2 = both(-c2);
         off = both(-st.x);
