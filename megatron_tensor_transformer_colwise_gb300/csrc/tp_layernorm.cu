@@ -33,7 +33,6 @@ constexpr int THREADS = 512;
 constexpr int MAX_PARTS = 512;  // most CTAs of the gradients' kernel
 
 __device__ __forceinline__ uint4 zeros8() { return make_uint4(0u, 0u, 0u, 0u); }
-__device__ __forceinline__ uint4 ones8() { return make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u); }
 
 // Eight bf16 values as four pairs of fp32, and back.
 __device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&p)[4]) {
@@ -64,6 +63,30 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// The gain (or the bias) as fp32 in shared memory, so that a row costs neither
+// its conversion nor the choice of a default: the first four values of piece v at
+// [v], the other four at [nv + v], free of bank conflicts.
+__device__ __forceinline__ void stage_weights(const __nv_bfloat16* from, float value, int nv, float4* to) {
+    for (int v = threadIdx.x; v < nv; v += THREADS) {
+        float4 a = make_float4(value, value, value, value), b = a;
+        if (from) {
+            const uint4 u = reinterpret_cast<const uint4*>(from)[v];
+            const float2 f0 = unpack_bf16x2(u.x), f1 = unpack_bf16x2(u.y), f2 = unpack_bf16x2(u.z), f3 = unpack_bf16x2(u.w);
+            a = make_float4(f0.x, f0.y, f1.x, f1.y);
+            b = make_float4(f2.x, f2.y, f3.x, f3.y);
+        }
+        to[v] = a;
+        to[nv + v] = b;
+    }
+}
+__device__ __forceinline__ void weights8(const float4* from, int nv, int v, uint64_t (&p)[4]) {
+    const float4 a = from[v], b = from[nv + v];
+    p[0] = f2_pack(a.x, a.y);
+    p[1] = f2_pack(a.z, a.w);
+    p[2] = f2_pack(b.x, b.y);
+    p[3] = f2_pack(b.z, b.w);
 }
 
 // A row's pieces: W warps, VPT a thread, nv in all; this thread's are first,
@@ -167,6 +190,10 @@ __global__ void __launch_bounds__(THREADS, VPT > 2 ? 1 : 2) layernorm_kernel(con
     long long row = static_cast<long long>(blockIdx.x) * GROUPS + threadIdx.x / (32 * W);
     uint4 next[VPT];
     if (row < rows) p.load(x + row * h, next);
+    extern __shared__ float4 weights[];  // gain, bias
+    stage_weights(gain, 1.0f, p.nv, weights);
+    stage_weights(bias, 0.0f, p.nv, weights + 2 * p.nv);
+    __syncthreads();
     for (; row < rows; row += step) {
         uint64_t f[VPT][4];
 #pragma unroll
@@ -188,8 +215,8 @@ __global__ void __launch_bounds__(THREADS, VPT > 2 ? 1 : 2) layernorm_kernel(con
         for (int i = 0; i < VPT; ++i) {
             if (!p.has(i)) continue;
             uint64_t g[4], b[4];
-            unpack8(gain ? reinterpret_cast<const uint4*>(gain)[p.at(i)] : ones8(), g);
-            unpack8(bias ? reinterpret_cast<const uint4*>(bias)[p.at(i)] : zeros8(), b);
+            weights8(weights, p.nv, p.at(i), g);
+            weights8(weights + 2 * p.nv, p.nv, p.at(i), b);
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[i][e] = f2_fma(f2_mul(f2_add(f[i][e], off), r), g[e], b[e]);
             reinterpret_cast<uint4*>(y + row * h)[p.at(i)] = pack8(f[i]);
@@ -234,6 +261,9 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
         p.load(dy + row * h, dnext);
     }
     if (stats && row < rows) snext = make_float2(stats[row], stats[rows + row]);
+    extern __shared__ float4 weights[];  // gain, and after the rows the sums of columns
+    stage_weights(gain, 1.0f, p.nv, weights);
+    __syncthreads();
     for (; row < rows; row += step) {
         const float2 saved = snext;
         if (stats && row + step < rows) snext = make_float2(stats[row + step], stats[rows + row + step]);
@@ -263,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
             uint64_t f[4], g[4], d[4];
             unpack8(xv[i], f);
             unpack8(dv[i], d);
-            unpack8(gain ? reinterpret_cast<const uint4*>(gain)[p.at(i)] : ones8(), g);
+            weights8(weights, p.nv, p.at(i), g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 g[e] = f2_mul(g[e], d[e]);
@@ -285,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
             uint64_t f[4], g[4], d[4], a[4];
             unpack8(xv[i], f);
             unpack8(dv[i], d);
-            unpack8(gain ? reinterpret_cast<const uint4*>(gain)[p.at(i)] : ones8(), g);
+            weights8(weights, p.nv, p.at(i), g);
             unpack8(res[i], a);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -299,7 +329,8 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
     }
     if (!parts) return;
     // The rows that the CTA holds at a time are added in shared memory.
-    extern __shared__ float2 cols[];  // [GROUPS][h / 2] pairs of columns
+    float2* cols = reinterpret_cast<float2*>(weights);  // [GROUPS][h / 2] pairs of columns
+    if (GROUPS > 1) __syncthreads();
     float2* out = reinterpret_cast<float2*>(parts + static_cast<long long>(blockIdx.x) * 2 * h);
     const int half = h >> 1;
 #pragma unroll
@@ -364,6 +395,20 @@ int check(const char* what, std::string* err) {
     return TP_OK;
 }
 
+// Raises a kernel's limit on dynamic shared memory to BYTES (0: as it is), once
+// a device.
+template <auto KERNEL, int BYTES>
+int allow_shared(std::string* err) {
+    if (BYTES == 0) return TP_OK;
+    static bool done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && done[dev]) return TP_OK;
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES) != cudaSuccess)
+        return check("layer norm's shared memory", err);
+    if (dev >= 0 && dev < 64) done[dev] = true;
+    return TP_OK;
+}
+
 template <int N>
 using Int = std::integral_constant<int, N>;
 
@@ -389,10 +434,13 @@ int layernorm_launch(const void* x, int64_t rows, int h, const void* gain, const
                      float* stats, cudaStream_t stream, std::string* err) {
     if (rows == 0) return TP_OK;
     return for_width(h, [&](auto W, auto VPT) {
-        constexpr int GROUPS = THREADS / (32 * decltype(W)::value);
+        constexpr int GROUPS = THREADS / (32 * decltype(W)::value), MOST = GROUPS == 1 ? 2 * 16384 * 4 : 0;
+        constexpr auto kern = layernorm_kernel<decltype(W)::value, decltype(VPT)::value>;
+        const int rc = allow_shared<kern, MOST>(err);
+        if (rc) return rc;
         const int64_t grid = std::min<int64_t>((rows + GROUPS - 1) / GROUPS, device_sm_count() * 2);
-        launch_pdl(layernorm_kernel<decltype(W)::value, decltype(VPT)::value>, dim3((unsigned)grid), dim3(THREADS), 0,
-                   stream, static_cast<const __nv_bfloat16*>(x), static_cast<long long>(rows), h,
+        launch_pdl(kern, dim3((unsigned)grid), dim3(THREADS), static_cast<size_t>(h) * 2 * sizeof(float), stream,
+                   static_cast<const __nv_bfloat16*>(x), static_cast<long long>(rows), h,
                    static_cast<const __nv_bfloat16*>(gain), static_cast<const __nv_bfloat16*>(bias), eps,
                    static_cast<__nv_bfloat16*>(y), stats);
         return check("layer norm kernel", err);
@@ -411,9 +459,12 @@ int layernorm_bwd_launch(const void* x, int64_t rows, int h, const void* gain, f
     if (rows > 0) {
         const int rc = for_width(h, [&](auto W, auto VPT) {
             constexpr int GROUPS = THREADS / (32 * decltype(W)::value);
-            auto kern = layernorm_bwd_kernel<decltype(W)::value, decltype(VPT)::value>;
+            constexpr auto kern = layernorm_bwd_kernel<decltype(W)::value, decltype(VPT)::value>;
             grid = std::min<int64_t>({(rows + GROUPS - 1) / GROUPS, device_sm_count(), MAX_PARTS});
-            const size_t smem = GROUPS > 1 && weights ? static_cast<size_t>(GROUPS) * h * sizeof(float) : 0;
+            constexpr int MOST = GROUPS == 1 ? 16384 * 4 : 0;
+            const int rc = allow_shared<kern, MOST>(err);
+            if (rc) return rc;
+            const size_t smem = static_cast<size_t>(GROUPS) * h * sizeof(float);
             static_assert(GROUPS == 1 || GROUPS * 256 * decltype(W)::value * decltype(VPT)::value * sizeof(float) <= 32768,
                           "fits without a larger limit on shared memory");
             launch_pdl(kern, dim3((unsigned)grid), dim3(THREADS), smem, stream, static_cast<const __nv_bfloat16*>(x),

@@ -379,12 +379,21 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_long_kernel(const __nv_bflo
 }
 
 // Rows that a cluster of CTAs holds in its registers: LOSS_VPT 16-byte pieces a
-// thread, the next row's on their way meanwhile.  Each warp's maximum and sum go
-// to every CTA of the cluster (two slots in turn: one barrier a row), so each
-// logit is read once and each gradient written once.  Eight pieces a thread on
-// 256 threads rather than four on 512: what a warp does once a row (addresses,
-// the exchange) is half of it at four.
-constexpr int LOSS_VPT = 8, LOSS_ROW_THREADS = 256, LOSS_PIECES = LOSS_VPT * LOSS_ROW_THREADS, LOSS_RANKS = 16;
+// thread, those of the next two rows on their way to shared memory meanwhile
+// (a thread copies and reads its own pieces, so no barrier guards them).  Each
+// warp's maximum and sum go to every CTA of the cluster (two slots in turn: one
+// barrier a row), so each logit is read once and each gradient written once.
+constexpr int LOSS_VPT = 8, LOSS_ROW_THREADS = 256, LOSS_CTAS = 3, LOSS_STAGES = 2;
+constexpr int LOSS_PIECES = LOSS_VPT * LOSS_ROW_THREADS, LOSS_RANKS = 16;
+
+__device__ __forceinline__ void copy_piece(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all groups of this thread but the last N
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -407,7 +416,7 @@ struct LossRow {
     float up, y;  // the loss's gradient, the label's logit
 };
 
-__global__ void __launch_bounds__(LOSS_ROW_THREADS, 2) loss_kernel(const __nv_bfloat16* logits, long long M, int v, int per,
+__global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const __nv_bfloat16* logits, long long M, int v, int per,
                                                                    int ranks, const int32_t* __restrict__ labels,
                                                                    const float* __restrict__ dloss, float* __restrict__ loss,
                                                                    __nv_bfloat16* dlogits) {
@@ -421,57 +430,60 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, 2) loss_kernel(const __nv_bf
     if (ranks > 1) cluster_sync_all();  // the others run, before anything is stored there
     pdl_wait();
     const uint64_t log2e = f2_pack(LOG2E, LOG2E);
-    LossRow ahead = {-100, 0.0f, 0.0f};
-    uint4 next[LOSS_VPT];
+    extern __shared__ uint4 ring[];  // [LOSS_STAGES][LOSS_VPT][threads]
+    const int stage_pieces = LOSS_VPT * blockDim.x;
+    for (int i = threadIdx.x; i < LOSS_STAGES * stage_pieces; i += blockDim.x)
+        ring[i] = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);  // -inf behind the row's end
+    // A row's copies and scalars; its label has been read a row before, so that
+    // nothing here waits for memory.
+    auto load = [&](long long m, int label, int stage) {
+        LossRow row = {label, 0.0f, 0.0f};
+        if (label >= 0 && label < v) {
+            row.up = dloss ? dloss[m] : 1.0f;
+            row.y = __bfloat162float(logits[m * v + label]);
+            const uint4* z = reinterpret_cast<const uint4*>(logits + m * v) + lo + lane;
+            const uint32_t to = smem_u32(ring + stage * stage_pieces + threadIdx.x);
 #pragma unroll
-    for (int i = 0; i < LOSS_VPT; ++i) next[i] = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);  // -inf
-    auto load = [&](long long m) {
-        ahead.label = labels[m];
-        if (ahead.label < 0 || ahead.label >= v) return;
-        ahead.up = dloss ? dloss[m] : 1.0f;
-        ahead.y = __bfloat162float(logits[m * v + ahead.label]);
-        const uint4* z = reinterpret_cast<const uint4*>(logits + m * v) + lo + lane;
-#pragma unroll
-        for (int i = 0; i < LOSS_VPT; ++i)
-            if (32 * i + lane < pieces) next[i] = z[32 * i];
+            for (int i = 0; i < LOSS_VPT; ++i)
+                if (32 * i + lane < pieces) copy_piece(to + i * blockDim.x * 16, z + 32 * i);
+        }
+        copies_commit();
+        return row;
     };
-    int turn = 0;
+    auto label_at = [&](long long m) { return m < M ? labels[m] : -100; };
+    int turn = 0, slot_turn = 0;  // the stage of the ring, the slots of the exchange
     long long m = blockIdx.x / ranks;
-    if (m < M) load(m);
-    for (; m < M; m += step) {
-        const LossRow row = ahead;
-        uint4 u[LOSS_VPT];
-#pragma unroll
-        for (int i = 0; i < LOSS_VPT; ++i) u[i] = next[i];
-        if (m + step < M) load(m + step);
+    LossRow next = load(m, label_at(m), 0), after = load(m + step, label_at(m + step), 1);
+    int label = label_at(m + 2 * step);
+    for (; m < M; m += step, turn ^= 1) {
+        const LossRow row = next;
+        next = after;
+        const int label2 = label;
+        label = label_at(m + 3 * step);
         uint4* d = reinterpret_cast<uint4*>(dlogits + m * v) + lo + lane;
+        copies_wait<1>();
         if (row.label < 0 || row.label >= v) {
             const uint32_t fill = fill_of(row.label);
 #pragma unroll
             for (int i = 0; i < LOSS_VPT; ++i)
                 if (32 * i + lane < pieces) d[32 * i] = make_uint4(fill, fill, fill, fill);
             if (rank == 0 && threadIdx.x == 0) loss[m] = __uint_as_float(fill & 0xffff0000u);
+            after = load(m + 2 * step, label2, turn);
             continue;
         }
         // The label's logit leaves the sum: -inf in its place.
         const int own = (row.label >> 3) - lo;
         const bool mine = own >= 0 && own < min(pieces, 32 * LOSS_VPT) && (own & 31) == lane;
-        if (mine) {
-            const uint32_t half = row.label & 1 ? 0xffff0000u : 0x0000ffffu, masked = 0xff80ff80u & half;
-            const int word = row.label >> 1 & 3;
+        uint4* here = ring + turn * stage_pieces + threadIdx.x;
+        if (mine) reinterpret_cast<uint16_t*>(here + (own >> 5) * blockDim.x)[row.label & 7] = 0xff80u;
+        uint4 u[LOSS_VPT];
 #pragma unroll
-            for (int i = 0; i < LOSS_VPT; ++i) {
-                if (i != own >> 5) continue;
-                if (word == 0) u[i].x = (u[i].x & ~half) | masked;
-                if (word == 1) u[i].y = (u[i].y & ~half) | masked;
-                if (word == 2) u[i].z = (u[i].z & ~half) | masked;
-                if (word == 3) u[i].w = (u[i].w & ~half) | masked;
-            }
-        }
+        for (int i = 0; i < LOSS_VPT; ++i) u[i] = here[i * blockDim.x];
         uint32_t top = 0xff80ff80u;
 #pragma unroll
         for (int i = 0; i < LOSS_VPT; ++i)
             top = max_bf16x2(top, max_bf16x2(max_bf16x2(u[i].x, u[i].y), max_bf16x2(u[i].z, u[i].w)));
+        after = load(m + 2 * step, label2, turn);  // the maximum has used all that was read from there
         const float2 tops = unpack_bf16x2(top);
         const float most = warp_max(fmaxf(tops.x, tops.y)), near = finite_max(most);
         uint64_t s0 = f2_pack(0.0f, 0.0f), s1 = s0;
@@ -492,7 +504,8 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, 2) loss_kernel(const __nv_bf
         float a, b;
         f2_unpack(f2_add(s0, s1), a, b);
         const float sum = warp_sum(a + b);
-        MS* slot = slots[turn];
+        MS* slot = slots[slot_turn];
+        slot_turn ^= 1;
         if (ranks > 1) {
             if (lane < ranks) {
                 const uint32_t to = mapa_shared(smem_u32(slot + rank * warps + w), lane);
@@ -503,7 +516,6 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, 2) loss_kernel(const __nv_bf
             if (lane == 0) slot[w] = {most, sum};
             __syncthreads();
         }
-        turn ^= 1;
         MS all[LOSS_RANKS * LOSS_ROW_THREADS / 32 / 32];
         float highest = -INFINITY;
 #pragma unroll
@@ -535,8 +547,10 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, 2) loss_kernel(const __nv_bf
     }
 }
 
-// Clusters of `ranks` CTAs of loss_kernel that the current device holds at once
-// (LOSS_ROW_THREADS threads a CTA); 0 when they do not fit at all.
+size_t loss_ring_bytes(int threads) { return static_cast<size_t>(LOSS_STAGES) * LOSS_VPT * threads * sizeof(uint4); }
+
+// Clusters of `ranks` full CTAs of loss_kernel that the current device holds at
+// once; 0 when they do not fit at all.
 int loss_clusters(int ranks) {
     static int counts[64][5] = {};
     int dev = 0, log = 0;
@@ -549,6 +563,7 @@ int loss_clusters(int ranks) {
         memset(&cfg, 0, sizeof(cfg));
         cfg.gridDim = dim3(ranks * 64);
         cfg.blockDim = dim3(LOSS_ROW_THREADS);
+        cfg.dynamicSmemBytes = loss_ring_bytes(LOSS_ROW_THREADS);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = ranks;
@@ -556,6 +571,8 @@ int loss_clusters(int ranks) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         if (cudaFuncSetAttribute(loss_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaFuncSetAttribute(loss_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(cfg.dynamicSmemBytes)) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, loss_kernel, &cfg) != cudaSuccess)
             n = 0;
         cudaGetLastError();
@@ -633,7 +650,7 @@ int vocab_loss_launch(const void* logits, int64_t M, int64_t v, const int32_t* l
     while (ranks < LOSS_RANKS && nv > static_cast<int64_t>(ranks) * LOSS_PIECES) ranks *= 2;
     const int64_t per = (nv + ranks - 1) / ranks;
     const int threads = static_cast<int>(std::min<int64_t>((per + 32 * LOSS_VPT - 1) / (32 * LOSS_VPT) * 32, LOSS_ROW_THREADS));
-    const int64_t clusters = per > LOSS_PIECES ? 0 : ranks == 1 ? device_sm_count() * 2LL * (LOSS_ROW_THREADS / threads) : loss_clusters(ranks);
+    const int64_t clusters = per > LOSS_PIECES ? 0 : loss_clusters(ranks) * static_cast<int64_t>(ranks == 1 ? LOSS_ROW_THREADS / threads : 1);
     if (clusters < 1) {
         launch_pdl(loss_long_kernel, dim3((unsigned)M), dim3(LOSS_THREADS), 0, stream, z, static_cast<int>(v), labels, dloss,
                    loss, d);
@@ -643,6 +660,7 @@ int vocab_loss_launch(const void* logits, int64_t M, int64_t v, const int32_t* l
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3((unsigned)(std::min<int64_t>(M, clusters) * ranks));
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = loss_ring_bytes(threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     pdl_attribute(attr[0]);
