@@ -29,7 +29,6 @@ namespace {
 
 using namespace tpk;
 
-constexpr int THREADS = 512;
 constexpr int MAX_PARTS = 512;  // most CTAs of the gradients' kernel
 
 __device__ __forceinline__ uint4 zeros8() { return make_uint4(0u, 0u, 0u, 0u); }
@@ -69,7 +68,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // its conversion nor the choice of a default: the first four values of piece v at
 // [v], the other four at [nv + v], free of bank conflicts.
 __device__ __forceinline__ void stage_weights(const __nv_bfloat16* from, float value, int nv, float4* to) {
-    for (int v = threadIdx.x; v < nv; v += THREADS) {
+    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
         float4 a = make_float4(value, value, value, value), b = a;
         if (from) {
             const uint4 u = reinterpret_cast<const uint4*>(from)[v];
@@ -90,22 +89,50 @@ __device__ __forceinline__ void weights8(const float4* from, int nv, int v, uint
 }
 
 // A row's pieces: W warps, VPT a thread, nv in all; this thread's are first,
-// first + 32 W, ...  count(w): the values that warp w holds.
-template <int W, int VPT>
+// first + 32 W, ...  count(w): the values that warp w holds.  FULL: rows of just
+// as many pieces as there are places.
+template <int W, int VPT, bool FULL>
 struct Pieces {
     int first, nv;
     __device__ __forceinline__ explicit Pieces(int h) : first(threadIdx.x % (32 * W)), nv(h >> 3) {}
-    __device__ __forceinline__ bool has(int i) const { return first + i * 32 * W < nv; }
+    __device__ __forceinline__ bool has(int i) const { return FULL || first + i * 32 * W < nv; }
     __device__ __forceinline__ int at(int i) const { return first + i * 32 * W; }
     __device__ __forceinline__ float count(int w) const {
+        if (FULL) return 256.0f * VPT;
         int n = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) n += min(max(nv - (i * W + w) * 32, 0), 32);
         return static_cast<float>(n * 8);
     }
-    __device__ __forceinline__ void load(const __nv_bfloat16* row, uint4 (&u)[VPT]) const {
+};
+
+// Rows on their way to shared memory: ARRAYS of them at a time, STAGES deep.  A
+// thread copies and reads its own pieces, so no barrier guards them; what lies
+// past a row's end stays zero.  A stage is filled again after what was read from
+// it has been used.
+template <int VPT, int ARRAYS, int STAGES, int THREADS>
+struct Ring {
+    static constexpr int PIECES = STAGES * ARRAYS * VPT * THREADS;
+    uint4* mine;
+    __device__ __forceinline__ explicit Ring(uint4* shared) : mine(shared + threadIdx.x) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) u[i] = has(i) ? reinterpret_cast<const uint4*>(row)[at(i)] : zeros8();
+        for (int i = 0; i < PIECES / THREADS; ++i) mine[i * THREADS] = zeros8();
+    }
+    __device__ __forceinline__ uint4& at(int stage, int array, int i) const {
+        return mine[((stage * ARRAYS + array) * VPT + i) * THREADS];
+    }
+    template <typename P>
+    __device__ __forceinline__ void copy(const P& p, int stage, int array, const __nv_bfloat16* row) const {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (p.has(i))
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&at(stage, array, i))),
+                             "l"(reinterpret_cast<const uint4*>(row) + p.at(i))
+                             : "memory");
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait() {  // all of this thread's copies but those of the last STAGES - 1 commits
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
     }
 };
 
@@ -139,8 +166,8 @@ struct Exchange {
 // The mean of a warp's values and the sum of their squared distances from it:
 // no difference of large sums, so a row whose mean is far from zero keeps its
 // variance.
-template <int W, int VPT, typename F>
-__device__ __forceinline__ float2 warp_moments(const Pieces<W, VPT>& p, float inv_count, F&& piece) {
+template <int VPT, typename P, typename F>
+__device__ __forceinline__ float2 warp_moments(const P& p, float inv_count, F&& piece) {
     uint64_t s = both(0.0f), x[4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -174,35 +201,49 @@ __device__ __forceinline__ float2 row_stats(float warp_mean, float m2, float sha
 }
 
 template <int W, int VPT>
-__global__ void __launch_bounds__(THREADS, VPT > 2 ? 1 : 2) layernorm_kernel(const __nv_bfloat16* x, long long rows, int h,
-                                                                             const __nv_bfloat16* __restrict__ gain,
-                                                                             const __nv_bfloat16* __restrict__ bias, float eps,
-                                                                             __nv_bfloat16* y, float* __restrict__ stats) {
-    constexpr int GROUPS = THREADS / (32 * W);
-    __shared__ float shared[GROUPS * 2 * W * 2];
+struct Forward {
+    static constexpr int THREADS = 256, CTAS = VPT > 4 ? 1 : W > 4 ? 2 : 3, STAGES = 2;  // CTAs an SM
+    static constexpr int GROUPS = THREADS / (32 * W);                                    // rows of a CTA at a time
+    using Rows = Ring<VPT, 1, STAGES, THREADS>;
+    static size_t shared_bytes(int h) { return (Rows::PIECES + h / 2) * sizeof(uint4); }
+};
+
+template <int W, int VPT, bool FULL>
+__global__ void __launch_bounds__(Forward<W, VPT>::THREADS, Forward<W, VPT>::CTAS)
+    layernorm_kernel(const __nv_bfloat16* x, long long rows, int h, const __nv_bfloat16* __restrict__ gain,
+                     const __nv_bfloat16* __restrict__ bias, float eps, __nv_bfloat16* y, float* __restrict__ stats) {
+    using C = Forward<W, VPT>;
+    __shared__ float shared[C::GROUPS * 2 * W * 2];
+    extern __shared__ uint4 dynamic[];
     pdl_trigger();
     pdl_wait();
-    const Pieces<W, VPT> p(h);
+    const Pieces<W, VPT, FULL> p(h);
+    const typename C::Rows ring(dynamic);
     Exchange<W, 2> exchange(shared);
     const float inv_h = 1.0f / static_cast<float>(h), share = p.count(threadIdx.x % W) * inv_h;
     const float inv_count = 1.0f / fmaxf(p.count(threadIdx.x / 32 % W), 1.0f);
-    const long long step = static_cast<long long>(gridDim.x) * GROUPS;
-    long long row = static_cast<long long>(blockIdx.x) * GROUPS + threadIdx.x / (32 * W);
-    uint4 next[VPT];
-    if (row < rows) p.load(x + row * h, next);
-    extern __shared__ float4 weights[];  // gain, bias
+    const long long step = static_cast<long long>(gridDim.x) * C::GROUPS;
+    long long row = static_cast<long long>(blockIdx.x) * C::GROUPS + threadIdx.x / (32 * W);
+    auto load = [&](long long r, int stage) {
+        if (r < rows) ring.copy(p, stage, 0, x + r * h);
+        ring.commit();
+    };
+#pragma unroll
+    for (int k = 0; k < C::STAGES; ++k) load(row + k * step, k);
+    float4* weights = reinterpret_cast<float4*>(dynamic + C::Rows::PIECES);  // gain, bias
     stage_weights(gain, 1.0f, p.nv, weights);
     stage_weights(bias, 0.0f, p.nv, weights + 2 * p.nv);
     __syncthreads();
-    for (; row < rows; row += step) {
+    for (int stage = 0; row < rows; row += step, stage ^= 1) {
+        ring.wait();
         uint64_t f[VPT][4];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) unpack8(next[i], f[i]);
-        if (row + step < rows) p.load(x + (row + step) * h, next);
-        const float2 m = warp_moments<W, VPT>(p, inv_count, [&](int i, uint64_t(&out)[4]) {
+        for (int i = 0; i < VPT; ++i) unpack8(ring.at(stage, 0, i), f[i]);
+        const float2 m = warp_moments<VPT>(p, inv_count, [&](int i, uint64_t(&out)[4]) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) out[e] = f[i][e];
         });
+        load(row + C::STAGES * step, stage);
         float v[2] = {m.x, m.y};
         exchange(v);
         const float2 st = row_stats<W, 2>(v[0], v[1], share, inv_h, eps);
@@ -211,6 +252,7 @@ __global__ void __launch_bounds__(THREADS, VPT > 2 ? 1 : 2) layernorm_kernel(con
             stats[rows + row] = st.y;
         }
         const uint64_t off = both(-st.x), r = both(st.y);
+        uint4* out = reinterpret_cast<uint4*>(y + row * h);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (!p.has(i)) continue;
@@ -219,80 +261,84 @@ __global__ void __launch_bounds__(THREADS, VPT > 2 ? 1 : 2) layernorm_kernel(con
             weights8(weights + 2 * p.nv, p.nv, p.at(i), b);
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[i][e] = f2_fma(f2_mul(f2_add(f[i][e], off), r), g[e], b[e]);
-            reinterpret_cast<uint4*>(y + row * h)[p.at(i)] = pack8(f[i]);
+            out[p.at(i)] = pack8(f[i]);
         }
     }
 }
 
+template <int W, int VPT>
+struct Backward {
+    // One CTA an SM: its rows' sums leave as one part.  Rows above 8192 leave room
+    // for one stage alone.
+    static constexpr int THREADS = 512, STAGES = W > 8 ? 1 : 2;
+    static constexpr int GROUPS = THREADS / (32 * W);
+    using Rows = Ring<VPT, 3, STAGES, THREADS>;  // x, dy, dres
+    static size_t shared_bytes(int h) { return (Rows::PIECES + h / 4) * sizeof(uint4); }
+    // The sums of columns at the end take the ring's place.
+    static_assert(Rows::PIECES * 16 >= GROUPS * 32 * W * VPT * 8 * 4, "");
+};
+
 // dx of every row, and the CTA's sums for dgain and dbias in parts
-// [CTAs][2][h].  dx may be dy or dres: a row's inputs are in registers before
-// its outputs are stored, and no other row's are touched.  The sums over a row
-// are taken about the warps' own means, so that they need one exchange with
+// [CTAs][2][h].  dx may be dy or dres: no row's inputs are read after its outputs
+// are stored, and no two threads read or store the same piece.  The sums over a
+// row are taken about the warps' own means, so that they need one exchange with
 // those that give the statistics:
 //   sum g xh = r sum_w (sum g (x - mean_w) + (mean_w - mu) sum g).
-template <int W, int VPT>
-__global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bfloat16* __restrict__ x, long long rows, int h,
-                                                                   const __nv_bfloat16* __restrict__ gain, float eps,
-                                                                   const float* __restrict__ stats, const __nv_bfloat16* dy,
-                                                                   const __nv_bfloat16* dres, __nv_bfloat16* dx,
-                                                                   float* __restrict__ parts) {
-    constexpr int GROUPS = THREADS / (32 * W);
-    __shared__ float shared[GROUPS * 2 * W * 4];
+template <int W, int VPT, bool FULL>
+__global__ void __launch_bounds__(Backward<W, VPT>::THREADS, 1)
+    layernorm_bwd_kernel(const __nv_bfloat16* x, long long rows, int h, const __nv_bfloat16* __restrict__ gain, float eps,
+                         const float* __restrict__ stats, const __nv_bfloat16* dy, const __nv_bfloat16* dres,
+                         __nv_bfloat16* dx, float* __restrict__ parts) {
+    using C = Backward<W, VPT>;
+    __shared__ float shared[C::GROUPS * 2 * W * 4];
+    extern __shared__ uint4 dynamic[];
     pdl_trigger();
     pdl_wait();
-    const Pieces<W, VPT> p(h);
+    const Pieces<W, VPT, FULL> p(h);
+    const typename C::Rows ring(dynamic);
     Exchange<W, 4> exchange(shared);
     const int group = threadIdx.x / (32 * W);
     const float inv_h = 1.0f / static_cast<float>(h), share = p.count(threadIdx.x % W) * inv_h;
     const float inv_count = 1.0f / fmaxf(p.count(threadIdx.x / 32 % W), 1.0f);
-    const long long step = static_cast<long long>(gridDim.x) * GROUPS;
-    long long row = static_cast<long long>(blockIdx.x) * GROUPS + group;
+    const long long step = static_cast<long long>(gridDim.x) * C::GROUPS;
+    long long row = static_cast<long long>(blockIdx.x) * C::GROUPS + group;
+    auto load = [&](long long r, int stage) {
+        if (r < rows) {
+            ring.copy(p, stage, 0, x + r * h);
+            ring.copy(p, stage, 1, dy + r * h);
+            if (dres) ring.copy(p, stage, 2, dres + r * h);
+        }
+        ring.commit();
+    };
+    auto saved_at = [&](long long r) {
+        return stats && r < rows ? make_float2(stats[r], stats[rows + r]) : make_float2(0.0f, 0.0f);
+    };
+#pragma unroll
+    for (int k = 0; k < C::STAGES; ++k) load(row + k * step, k);
+    float2 snext = saved_at(row);
+    float4* weights = reinterpret_cast<float4*>(dynamic + C::Rows::PIECES);  // gain
+    stage_weights(gain, 1.0f, p.nv, weights);
     uint64_t dg[VPT][4], db[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) dg[i][e] = db[i][e] = both(0.0f);
     }
-    constexpr bool AHEAD = VPT <= 2;  // the next row's inputs on their way: as many registers as there are
-    uint4 xnext[VPT], dnext[VPT];
-    float2 snext = make_float2(0.0f, 0.0f);
-    if (AHEAD && row < rows) {
-        p.load(x + row * h, xnext);
-        p.load(dy + row * h, dnext);
-    }
-    if (stats && row < rows) snext = make_float2(stats[row], stats[rows + row]);
-    extern __shared__ float4 weights[];  // gain, and after the rows the sums of columns
-    stage_weights(gain, 1.0f, p.nv, weights);
     __syncthreads();
-    for (; row < rows; row += step) {
+    for (int stage = 0; row < rows; row += step, stage = (stage + 1) % C::STAGES) {
         const float2 saved = snext;
-        if (stats && row + step < rows) snext = make_float2(stats[row + step], stats[rows + row + step]);
-        uint4 xv[VPT], dv[VPT], res[VPT];
-        if (!AHEAD) {
-            p.load(x + row * h, xnext);
-            p.load(dy + row * h, dnext);
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            xv[i] = xnext[i];
-            dv[i] = dnext[i];
-            res[i] = zeros8();
-        }
-        if (dres && AHEAD) p.load(dres + row * h, res);
-        if (AHEAD && row + step < rows) {
-            p.load(x + (row + step) * h, xnext);
-            p.load(dy + (row + step) * h, dnext);
-        }
+        snext = saved_at(row + step);
+        ring.wait();
         const float2 m = stats ? make_float2(saved.x, 0.0f)
-                               : warp_moments<W, VPT>(p, inv_count, [&](int i, uint64_t(&out)[4]) { unpack8(xv[i], out); });
+                               : warp_moments<VPT>(p, inv_count, [&](int i, uint64_t(&out)[4]) { unpack8(ring.at(stage, 0, i), out); });
         uint64_t sg = both(0.0f), sgx = both(0.0f);
         uint64_t off = both(-m.x);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (!p.has(i)) continue;
             uint64_t f[4], g[4], d[4];
-            unpack8(xv[i], f);
-            unpack8(dv[i], d);
+            unpack8(ring.at(stage, 0, i), f);
+            unpack8(ring.at(stage, 1, i), d);
             weights8(weights, p.nv, p.at(i), g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -306,17 +352,17 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
         using X = Exchange<W, 4>;
         const float2 st = stats ? saved : row_stats<W, 4>(v[0], v[1], share, inv_h, eps);
         const float c1 = X::all(v[2]) * inv_h, c2 = X::all(fmaf(v[0] - st.x, v[2], v[3])) * (inv_h * st.y);
-        if (dres && !AHEAD) p.load(dres + row * h, res);
         const uint64_t r = both(st.y), n1 = both(-c1), n2 = both(-c2);
         off = both(-st.x);
+        uint4* out = reinterpret_cast<uint4*>(dx + row * h);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (!p.has(i)) continue;
             uint64_t f[4], g[4], d[4], a[4];
-            unpack8(xv[i], f);
-            unpack8(dv[i], d);
+            unpack8(ring.at(stage, 0, i), f);
+            unpack8(ring.at(stage, 1, i), d);
             weights8(weights, p.nv, p.at(i), g);
-            unpack8(res[i], a);
+            unpack8(ring.at(stage, 2, i), a);  // zeros without dres
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 f[e] = f2_mul(f2_add(f[e], off), r);
@@ -324,18 +370,19 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
                 db[i][e] = f2_add(db[i][e], d[e]);
                 a[e] = f2_fma(r, f2_fma(f[e], n2, f2_fma(d[e], g[e], n1)), a[e]);
             }
-            reinterpret_cast<uint4*>(dx + row * h)[p.at(i)] = pack8(a);
+            out[p.at(i)] = pack8(a);
         }
+        load(row + C::STAGES * step, stage);
     }
     if (!parts) return;
     // The rows that the CTA holds at a time are added in shared memory.
-    float2* cols = reinterpret_cast<float2*>(weights);  // [GROUPS][h / 2] pairs of columns
-    if (GROUPS > 1) __syncthreads();
+    __syncthreads();
+    float2* cols = reinterpret_cast<float2*>(dynamic);  // [GROUPS][h / 2] pairs of columns
     float2* out = reinterpret_cast<float2*>(parts + static_cast<long long>(blockIdx.x) * 2 * h);
     const int half = h >> 1;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {  // dgain, dbias
-        float2* mine = GROUPS > 1 ? cols + group * half : out + k * half;
+        float2* mine = C::GROUPS > 1 ? cols + group * half : out + k * half;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (!p.has(i)) continue;
@@ -346,11 +393,12 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_bwd_kernel(const __nv_bf
                 mine[p.at(i) * 4 + e] = s;
             }
         }
-        if (GROUPS == 1) continue;
+        if (C::GROUPS == 1) continue;
         __syncthreads();
-        for (int c = threadIdx.x; c < half; c += THREADS) {
+        for (int c = threadIdx.x; c < half; c += C::THREADS) {
             float2 s = cols[c];
-            for (int g = 1; g < GROUPS; ++g) {
+#pragma unroll
+            for (int g = 1; g < C::GROUPS; ++g) {
                 s.x += cols[g * half + c].x;
                 s.y += cols[g * half + c].y;
             }
@@ -395,15 +443,15 @@ int check(const char* what, std::string* err) {
     return TP_OK;
 }
 
-// Raises a kernel's limit on dynamic shared memory to BYTES (0: as it is), once
-// a device.
-template <auto KERNEL, int BYTES>
+// Raises a kernel's limit on dynamic shared memory to what any row takes, once a
+// device.
+constexpr int MOST_SHARED = 227 * 1024 - 2048;
+template <auto KERNEL>
 int allow_shared(std::string* err) {
-    if (BYTES == 0) return TP_OK;
     static bool done[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && done[dev]) return TP_OK;
-    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES) != cudaSuccess)
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SHARED) != cudaSuccess)
         return check("layer norm's shared memory", err);
     if (dev >= 0 && dev < 64) done[dev] = true;
     return TP_OK;
@@ -411,19 +459,34 @@ int allow_shared(std::string* err) {
 
 template <int N>
 using Int = std::integral_constant<int, N>;
+template <int W, int VPT, int NV, typename F>
+int for_fill(int nv, F&& f) {
+    static_assert(NV == 32 * W * VPT, "");
+    return nv == NV ? f(Int<W>(), Int<VPT>(), std::true_type()) : f(Int<W>(), Int<VPT>(), std::false_type());
+}
 
-// Warps of a row and 16-byte pieces a thread for rows of h: one warp up to
-// 512 columns (no barrier), two pieces a thread up to 8192, then four.
+// Warps of a row and 16-byte pieces a thread for rows of h.
 template <typename F>
-int for_width(int h, F&& f) {
+int for_forward(int h, F&& f) {
     const int nv = h / 8;
-    if (nv <= 32) return f(Int<1>(), Int<1>());
-    if (nv <= 64) return f(Int<1>(), Int<2>());
-    if (nv <= 128) return f(Int<2>(), Int<2>());
-    if (nv <= 256) return f(Int<4>(), Int<2>());
-    if (nv <= 512) return f(Int<8>(), Int<2>());
-    if (nv <= 1024) return f(Int<16>(), Int<2>());
-    return f(Int<16>(), Int<4>());
+    if (nv <= 32) return for_fill<1, 1, 32>(nv, f);
+    if (nv <= 64) return for_fill<1, 2, 64>(nv, f);
+    if (nv <= 128) return for_fill<1, 4, 128>(nv, f);
+    if (nv <= 256) return for_fill<2, 4, 256>(nv, f);
+    if (nv <= 512) return for_fill<4, 4, 512>(nv, f);
+    if (nv <= 1024) return for_fill<8, 4, 1024>(nv, f);
+    return for_fill<8, 8, 2048>(nv, f);
+}
+template <typename F>
+int for_backward(int h, F&& f) {
+    const int nv = h / 8;
+    if (nv <= 32) return for_fill<1, 1, 32>(nv, f);
+    if (nv <= 64) return for_fill<1, 2, 64>(nv, f);
+    if (nv <= 128) return for_fill<1, 4, 128>(nv, f);
+    if (nv <= 256) return for_fill<2, 4, 256>(nv, f);
+    if (nv <= 512) return for_fill<4, 4, 512>(nv, f);
+    if (nv <= 1024) return for_fill<8, 4, 1024>(nv, f);
+    return for_fill<16, 4, 2048>(nv, f);
 }
 
 }  // namespace
@@ -433,13 +496,13 @@ namespace tpi {
 int layernorm_launch(const void* x, int64_t rows, int h, const void* gain, const void* bias, float eps, void* y,
                      float* stats, cudaStream_t stream, std::string* err) {
     if (rows == 0) return TP_OK;
-    return for_width(h, [&](auto W, auto VPT) {
-        constexpr int GROUPS = THREADS / (32 * decltype(W)::value), MOST = GROUPS == 1 ? 2 * 16384 * 4 : 0;
-        constexpr auto kern = layernorm_kernel<decltype(W)::value, decltype(VPT)::value>;
-        const int rc = allow_shared<kern, MOST>(err);
+    return for_forward(h, [&](auto W, auto VPT, auto FULL) {
+        using C = Forward<decltype(W)::value, decltype(VPT)::value>;
+        constexpr auto kern = layernorm_kernel<decltype(W)::value, decltype(VPT)::value, decltype(FULL)::value>;
+        const int rc = allow_shared<kern>(err);
         if (rc) return rc;
-        const int64_t grid = std::min<int64_t>((rows + GROUPS - 1) / GROUPS, device_sm_count() * 2);
-        launch_pdl(kern, dim3((unsigned)grid), dim3(THREADS), static_cast<size_t>(h) * 2 * sizeof(float), stream,
+        const int64_t grid = std::min<int64_t>((rows + C::GROUPS - 1) / C::GROUPS, device_sm_count() * C::CTAS);
+        launch_pdl(kern, dim3((unsigned)grid), dim3(C::THREADS), C::shared_bytes(h), stream,
                    static_cast<const __nv_bfloat16*>(x), static_cast<long long>(rows), h,
                    static_cast<const __nv_bfloat16*>(gain), static_cast<const __nv_bfloat16*>(bias), eps,
                    static_cast<__nv_bfloat16*>(y), stats);
@@ -457,20 +520,17 @@ int layernorm_bwd_launch(const void* x, int64_t rows, int h, const void* gain, f
     int64_t grid = 0;
     const bool weights = dgain || dbias;
     if (rows > 0) {
-        const int rc = for_width(h, [&](auto W, auto VPT) {
-            constexpr int GROUPS = THREADS / (32 * decltype(W)::value);
-            constexpr auto kern = layernorm_bwd_kernel<decltype(W)::value, decltype(VPT)::value>;
-            grid = std::min<int64_t>({(rows + GROUPS - 1) / GROUPS, device_sm_count(), MAX_PARTS});
-            constexpr int MOST = GROUPS == 1 ? 16384 * 4 : 0;
-            const int rc = allow_shared<kern, MOST>(err);
+        const int rc = for_backward(h, [&](auto W, auto VPT, auto FULL) {
+            using C = Backward<decltype(W)::value, decltype(VPT)::value>;
+            constexpr auto kern = layernorm_bwd_kernel<decltype(W)::value, decltype(VPT)::value, decltype(FULL)::value>;
+            const int rc = allow_shared<kern>(err);
             if (rc) return rc;
-            const size_t smem = static_cast<size_t>(GROUPS) * h * sizeof(float);
-            static_assert(GROUPS == 1 || GROUPS * 256 * decltype(W)::value * decltype(VPT)::value * sizeof(float) <= 32768,
-                          "fits without a larger limit on shared memory");
-            launch_pdl(kern, dim3((unsigned)grid), dim3(THREADS), smem, stream, static_cast<const __nv_bfloat16*>(x),
-                       static_cast<long long>(rows), h, static_cast<const __nv_bfloat16*>(gain), eps, stats,
-                       static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(dres),
-                       static_cast<__nv_bfloat16*>(dx), weights ? static_cast<float*>(scratch) : nullptr);
+            grid = std::min<int64_t>({(rows + C::GROUPS - 1) / C::GROUPS, device_sm_count(), MAX_PARTS});
+            launch_pdl(kern, dim3((unsigned)grid), dim3(C::THREADS), C::shared_bytes(h), stream,
+                       static_cast<const __nv_bfloat16*>(x), static_cast<long long>(rows), h,
+                       static_cast<const __nv_bfloat16*>(gain), eps, stats, static_cast<const __nv_bfloat16*>(dy),
+                       static_cast<const __nv_bfloat16*>(dres), static_cast<__nv_bfloat16*>(dx),
+                       weights ? static_cast<float*>(scratch) : nullptr);
             return check("layer norm gradient kernel", err);
         });
         if (rc) return rc;

@@ -70,8 +70,9 @@ __global__ void __launch_bounds__(EMB_WARPS * 32) embedding_scaled_kernel(const 
 // ------------------------------------------------------------ embedding gradient
 
 // Two launches, the same bits every time:
-//  1. tokens sorted by word, and zeros for words without a token;
-//  2. the sorted tokens in parts of equal length, summed by word.  A word that
+//  1. tokens sorted by word;
+//  2. the sorted tokens in parts of equal length, summed by word, and behind
+//     these CTAs others that write the zeros of words without a token.  A word that
 //     a part's border cuts leaves partial sums, and the last of its parts to
 //     arrive (a counter that the first launch cleared) adds them in order.
 // Parts of equal length keep a frequent word (in text, one token in ten is the
@@ -110,10 +111,9 @@ __device__ __forceinline__ void for_ids(const int32_t* __restrict__ ids, long lo
 
 __global__ void __launch_bounds__(SORT_WARPS * 32) sort_tokens_kernel(const int32_t* __restrict__ ids, long long M, int v,
                                                                      Entry* __restrict__ sorted, int32_t* __restrict__ start,
-                                                                     int32_t* __restrict__ counters, long long n_counters, int h,
-                                                                     float* __restrict__ clear) {
+                                                                     int32_t* __restrict__ counters, long long n_counters) {
     __shared__ int32_t count[SORT_WARPS][BINS];
-    __shared__ int32_t below[SORT_WARPS], sums[BINS / 32], tokens[BINS];
+    __shared__ int32_t below[SORT_WARPS], sums[BINS / 32];
     pdl_trigger();
     pdl_wait();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(SORT_WARPS * 32) sort_tokens_kernel(const int3
             total += n;
             base += below[k];
         }
-        tokens[threadIdx.x] = total;
         int upto = total;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -173,12 +172,6 @@ __global__ void __launch_bounds__(SORT_WARPS * 32) sort_tokens_kernel(const int3
         }
         __syncwarp();
     });
-    if (!clear) return;
-    for (int b = w; b < bins; b += SORT_WARPS) {
-        if (tokens[b]) continue;
-        float4* row = reinterpret_cast<float4*>(clear + (static_cast<long long>(lo) + b) * h);
-        for (int c = lane; c < h >> 2; c += 32) row[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
 }
 
 // Columns (in eights) and sorted tokens of a CTA.
@@ -195,19 +188,46 @@ __device__ __forceinline__ void store_sum(float* row, int c, const float (&s)[8]
     out[1] = make_float4(fmaf(scale, s[4], b.x), fmaf(scale, s[5], b.y), fmaf(scale, s[6], b.z), fmaf(scale, s[7], b.w));
 }
 
-// Sorted tokens [a part, (a + 1) part) for one slice of columns.  A word that
+// Zeros for the words without a token among `words` from `first` on, which are
+// few enough for `from` to hold where their tokens start.
+constexpr int CLEAR_BYTES = 65536, MAX_CLEAR = MAX_PART;  // of a CTA: bytes about, words at most
+
+__device__ __forceinline__ void clear_words(const int32_t* __restrict__ start, long long first, int words, int h,
+                                            float* __restrict__ dE, int32_t* from) {
+    for (int k = threadIdx.x; k <= words; k += blockDim.x) from[k] = start[first + k];
+    __syncthreads();
+    // Short rows side by side, long ones by all threads.
+    const int pieces = h >> 2, rows = max(1, static_cast<int>(blockDim.x) / pieces), mine = threadIdx.x / pieces;
+    for (int r = rows > 1 ? mine : 0; mine < rows && r < words; r += rows) {
+        if (from[r] != from[r + 1]) continue;
+        float4* row = reinterpret_cast<float4*>(dE + (first + r) * h);
+        for (int c = threadIdx.x - (rows > 1 ? mine * pieces : 0); c < pieces; c += blockDim.x)
+            row[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+}
+
+// CTAs [0, n_parts slices): sorted tokens [a part, (a + 1) part) for one slice of
+// columns each; those behind them: zeros for clear_rows words.  A word that
 // began before the part leaves its sum in parts[a][0], one that began here and
 // goes on behind the part in parts[a][1], all others are done.
 __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const Entry* __restrict__ sorted,
-                                                                   const int32_t* __restrict__ start, int v, int part, int h,
+                                                                   const int32_t* __restrict__ start, int v, int part,
+                                                                   long long n_parts, int slices, int clear_rows, int h,
                                                                    float scale, const __nv_bfloat16* __restrict__ dOut,
                                                                    float* dE, int accumulate, float* parts,
                                                                    int32_t* counters) {
     __shared__ Entry mine[MAX_PART + 2];  // with the neighbours of both ends
     __shared__ int last;
+    static_assert(sizeof(mine) >= (MAX_CLEAR + 1) * sizeof(int32_t), "");
     pdl_trigger();
     pdl_wait();
-    const long long a = blockIdx.x, n = start[v], from = a * part;
+    const long long a = blockIdx.x / slices, n = start[v], from = a * part;
+    const int slice = blockIdx.x % slices;
+    if (a >= n_parts) {
+        const long long first = (blockIdx.x - n_parts * slices) * clear_rows;
+        clear_words(start, first, static_cast<int>(min(static_cast<long long>(clear_rows), v - first)), h, dE, &mine[0].word);
+        return;
+    }
     const int tokens = static_cast<int>(min(static_cast<long long>(part), n - from));
     if (tokens <= 0) return;
     for (int k = threadIdx.x; k < tokens + 2; k += blockDim.x) {
@@ -215,8 +235,17 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const Entry*
         mine[k] = i >= 0 && i < n ? sorted[i] : Entry{-1, 0};
     }
     __syncthreads();
-    const int c = blockIdx.y * blockDim.x + threadIdx.x;
+    const int c = slice * blockDim.x + threadIdx.x;
     const bool in = c < h >> 3;
+    // The words that this part's borders cut, and the parts that they span: the
+    // first one's sum is part of a word that came, the last one's of a word that
+    // goes on (one word, one sum).
+    bool ends[2] = {mine[0].word == mine[1].word, mine[tokens].word == mine[tokens + 1].word};
+    if (ends[0] && mine[1].word == mine[tokens].word) ends[1] = false;
+    int2 span[2] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (ends[k]) span[k] = make_int2(start[mine[k ? tokens : 1].word], start[mine[k ? tokens : 1].word + 1]);
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     bool came = mine[0].word == mine[1].word;
     for (int at = 0; in && at < tokens; at += SUM_LOADS) {
@@ -244,17 +273,14 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const Entry*
             for (int e = 0; e < 8; ++e) s[e] = 0.0f;
         }
     }
-    // The words that this part's borders cut: the first one's sum is part of a
-    // word that came, the last one's of a word that goes on.
-    const bool ends[2] = {mine[0].word == mine[1].word, mine[tokens].word == mine[tokens + 1].word};
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
-        if (!ends[k] || (k == 1 && ends[0] && mine[1].word == mine[tokens].word)) continue;  // one word, one sum
+        if (!ends[k]) continue;
         const int word = mine[k ? tokens : 1].word;
-        const long long first = start[word] / part, past = (start[word + 1] - 1) / part;
+        const long long first = span[k].x / part, past = (span[k].y - 1) / part;
         __threadfence();  // this thread's sums, before the count that announces them
         __syncthreads();
-        if (threadIdx.x == 0) last = atomicAdd(counters + first * gridDim.y + blockIdx.y, 1) == past - first;
+        if (threadIdx.x == 0) last = atomicAdd(counters + first * slices + slice, 1) == past - first;
         __syncthreads();
         if (!last || !in) continue;
         __threadfence();
@@ -381,8 +407,12 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_long_kernel(const __nv_bflo
 // Rows that a cluster of CTAs holds in its registers: LOSS_VPT 16-byte pieces a
 // thread, those of the next two rows on their way to shared memory meanwhile
 // (a thread copies and reads its own pieces, so no barrier guards them).  Each
-// warp's maximum and sum go to every CTA of the cluster (two slots in turn: one
-// barrier a row), so each logit is read once and each gradient written once.
+// warp's maximum and sum go to every CTA of the cluster, so each logit is read
+// once and each gradient written once.  They go by st.async, counted on the
+// receiver's mbarrier, in two slots in turn: a warp's values for row r tell that it
+// has read those of row r - 1, so a slot is free when it is written again.  With
+// a cluster barrier a row, its release waited for the last row's stores to global
+// memory (8192 x 128256: 800 to 850 us).
 constexpr int LOSS_VPT = 8, LOSS_ROW_THREADS = 256, LOSS_CTAS = 3, LOSS_STAGES = 2;
 constexpr int LOSS_PIECES = LOSS_VPT * LOSS_ROW_THREADS, LOSS_RANKS = 16;
 
@@ -411,6 +441,35 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
+// mbar_wait for what other CTAs of the cluster stored.
+constexpr uint64_t LOSS_TIMEOUT_NS = 2000000000ull;
+
+__device__ __forceinline__ bool cluster_try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0u;
+}
+__device__ __forceinline__ bool cluster_wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (cluster_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (cluster_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > LOSS_TIMEOUT_NS) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
 struct LossRow {
     int label;
     float up, y;  // the loss's gradient, the label's logit
@@ -427,8 +486,19 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
     // This warp's pieces of a row: lo + lane, lo + 32 + lane, ... up to `pieces` (none where <= 0).
     const int lo = rank * per + w * 32 * LOSS_VPT, pieces = min(rank * per + per, v >> 3) - lo;
     const long long step = gridDim.x / ranks;
+    __shared__ __align__(8) uint64_t arrived[2];
+    __shared__ int abort_flag, no_abort;
+    if (threadIdx.x == 0) {
+        no_abort = 0;
+        mbar_init(smem_u32(&arrived[0]), 1);
+        mbar_init(smem_u32(&arrived[1]), 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
     if (ranks > 1) cluster_sync_all();  // the others run, before anything is stored there
+    else __syncthreads();
     pdl_wait();
+    bool ok = true;
     const uint64_t log2e = f2_pack(LOG2E, LOG2E);
     extern __shared__ uint4 ring[];  // [LOSS_STAGES][LOSS_VPT][threads]
     const int stage_pieces = LOSS_VPT * blockDim.x;
@@ -451,7 +521,8 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
         return row;
     };
     auto label_at = [&](long long m) { return m < M ? labels[m] : -100; };
-    int turn = 0, slot_turn = 0;  // the stage of the ring, the slots of the exchange
+    int turn = 0;            // the stage of the ring
+    unsigned exchanges = 0;  // rows whose sums went round
     long long m = blockIdx.x / ranks;
     LossRow next = load(m, label_at(m), 0), after = load(m + step, label_at(m + step), 1);
     int label = label_at(m + 2 * step);
@@ -483,9 +554,9 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
 #pragma unroll
         for (int i = 0; i < LOSS_VPT; ++i)
             top = max_bf16x2(top, max_bf16x2(max_bf16x2(u[i].x, u[i].y), max_bf16x2(u[i].z, u[i].w)));
-        after = load(m + 2 * step, label2, turn);  // the maximum has used all that was read from there
         const float2 tops = unpack_bf16x2(top);
         const float most = warp_max(fmaxf(tops.x, tops.y)), near = finite_max(most);
+        after = load(m + 2 * step, label2, turn);  // the lanes' maximum has used all that was read from there
         uint64_t s0 = f2_pack(0.0f, 0.0f), s1 = s0;
         uint64_t off = f2_pack(-near, -near);
         auto power = [&](uint32_t word) {  // e^{z - n} of two logits
@@ -504,18 +575,23 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
         float a, b;
         f2_unpack(f2_add(s0, s1), a, b);
         const float sum = warp_sum(a + b);
-        MS* slot = slots[slot_turn];
-        slot_turn ^= 1;
+        MS* slot = slots[exchanges & 1];
         if (ranks > 1) {
-            if (lane < ranks) {
-                const uint32_t to = mapa_shared(smem_u32(slot + rank * warps + w), lane);
-                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(most), "f"(sum) : "memory");
-            }
-            cluster_sync_all();
+            const uint32_t bar = smem_u32(&arrived[exchanges & 1]);
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, entries * sizeof(MS));
+            if (lane < ranks)
+                asm volatile(
+                    "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                        mapa_shared(smem_u32(slot + rank * warps + w), lane)),
+                    "f"(most), "f"(sum), "r"(mapa_shared(bar, lane))
+                    : "memory");
+            ok = __all_sync(0xffffffffu, cluster_wait_bar(bar, exchanges >> 1 & 1, &abort_flag));
+            if (!ok) break;
         } else {
             if (lane == 0) slot[w] = {most, sum};
             __syncthreads();
         }
+        ++exchanges;
         MS all[LOSS_RANKS * LOSS_ROW_THREADS / 32 / 32];
         float highest = -INFINITY;
 #pragma unroll
@@ -544,6 +620,18 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
             if (32 * i + lane < pieces) d[32 * i] = make_uint4(grad(u[i].x), grad(u[i].y), grad(u[i].z), grad(u[i].w));
         // The label's gradient over what its piece's store left in its place.
         if (mine) reinterpret_cast<__nv_bfloat16*>(d + (own & ~31))[row.label & 7] = __float2bfloat16_rn(-r.others * scale);
+    }
+    if (!ok) {  // a wait gave up: the losses of the rows left say so
+        copies_wait<0>();
+        for (; rank == 0 && threadIdx.x == 0 && m < M; m += step) loss[m] = __int_as_float(0x7fc00000);
+    }
+    if (ranks > 1) {
+        __syncwarp();
+        cluster_sync_all();  // nothing more is stored in another CTA's shared memory
+        if (!ok) {         // what was on its way here has arrived, as far as it comes
+            cluster_wait_bar(smem_u32(&arrived[exchanges & 1]), exchanges >> 1 & 1, &no_abort);
+            cluster_wait_bar(smem_u32(&arrived[exchanges + 1 & 1]), exchanges + 1 >> 1 & 1, &no_abort);
+        }
     }
 }
 
@@ -631,11 +719,14 @@ int vocab_embedding_bwd_launch(const int32_t* ids, int64_t M, int64_t v, int h, 
     Entry* sorted = reinterpret_cast<Entry*>(base + at.sorted);
     launch_pdl(sort_tokens_kernel, dim3((unsigned)((v + BINS - 1) / BINS)), dim3(SORT_WARPS * 32), 0, stream, ids,
                static_cast<long long>(M), static_cast<int>(v), sorted, start, counters,
-               static_cast<long long>(at.parts * at.slices), h, accumulate ? nullptr : dE);
+               static_cast<long long>(at.parts * at.slices));
     const int rc = check("token sort kernel", err);
-    if (rc || M == 0) return rc;
-    launch_pdl(embedding_sum_kernel, dim3((unsigned)at.parts, (unsigned)at.slices), dim3(at.threads), 0, stream,
-               static_cast<const Entry*>(sorted), static_cast<const int32_t*>(start), static_cast<int>(v), at.part, h, scale,
+    const int64_t clear_rows = std::min<int64_t>(std::max<int64_t>(1, CLEAR_BYTES / 4 / h), MAX_CLEAR);
+    const int64_t grid = at.parts * at.slices + (accumulate ? 0 : (v + clear_rows - 1) / clear_rows);
+    if (rc || grid == 0) return rc;
+    launch_pdl(embedding_sum_kernel, dim3((unsigned)grid), dim3(at.threads), 0, stream, static_cast<const Entry*>(sorted),
+               static_cast<const int32_t*>(start), static_cast<int>(v), at.part, static_cast<long long>(at.parts),
+               static_cast<int>(at.slices), static_cast<int>(clear_rows), h, scale,
                static_cast<const __nv_bfloat16*>(dOut), dE, accumulate, reinterpret_cast<float*>(base + at.sums), counters);
     return check("embedding gradient kernel", err);
 }
