@@ -270,7 +270,8 @@ template <int W, int VPT>
 struct Backward {
     // One CTA an SM: its rows' sums leave as one part.  Rows above 8192 leave room
     // for one stage alone.
-    static constexpr int THREADS = 512, STAGES = W > 8 ? 1 : 2;
+    static constexpr int THREADS = 512, STAGES = W > 8 && VPT > 2 ? 1 : 2;
+    static constexpr bool HOLD = VPT <= 2;
     static constexpr int GROUPS = THREADS / (32 * W);
     using Rows = Ring<VPT, 3, STAGES, THREADS>;  // x, dy, dres
     static size_t shared_bytes(int h) { return (Rows::PIECES + h / 4) * sizeof(uint4); }
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(Backward<W, VPT>::THREADS, 1)
                          const float* __restrict__ stats, const __nv_bfloat16* dy, const __nv_bfloat16* dres,
                          __nv_bfloat16* dx, float* __restrict__ parts) {
     using C = Backward<W, VPT>;
+    constexpr bool HOLD = C::HOLD;
     __shared__ float shared[C::GROUPS * 2 * W * 4];
     extern __shared__ uint4 dynamic[];
     pdl_trigger();
@@ -329,16 +331,34 @@ __global__ void __launch_bounds__(Backward<W, VPT>::THREADS, 1)
         const float2 saved = snext;
         snext = saved_at(row + step);
         ring.wait();
+        // Up to two pieces a thread stay unpacked in registers; more are read and
+        // unpacked again (twelve values each of x, dy and the two sums would spill).
+        uint64_t xk[HOLD ? VPT : 1][4], dk[HOLD ? VPT : 1][4];
+        if (HOLD) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                unpack8(ring.at(stage, 0, i), xk[HOLD ? i : 0]);
+                unpack8(ring.at(stage, 1, i), dk[HOLD ? i : 0]);
+            }
+        }
+        auto piece = [&](int i, int array, uint64_t(&out)[4]) {
+            if (HOLD) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[e] = array ? dk[HOLD ? i : 0][e] : xk[HOLD ? i : 0][e];
+            } else {
+                unpack8(ring.at(stage, array, i), out);
+            }
+        };
         const float2 m = stats ? make_float2(saved.x, 0.0f)
-                               : warp_moments<VPT>(p, inv_count, [&](int i, uint64_t(&out)[4]) { unpack8(ring.at(stage, 0, i), out); });
+                               : warp_moments<VPT>(p, inv_count, [&](int i, uint64_t(&out)[4]) { piece(i, 0, out); });
         uint64_t sg = both(0.0f), sgx = both(0.0f);
         uint64_t off = both(-m.x);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (!p.has(i)) continue;
             uint64_t f[4], g[4], d[4];
-            unpack8(ring.at(stage, 0, i), f);
-            unpack8(ring.at(stage, 1, i), d);
+            piece(i, 0, f);
+            piece(i, 1, d);
             weights8(weights, p.nv, p.at(i), g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -359,8 +379,8 @@ __global__ void __launch_bounds__(Backward<W, VPT>::THREADS, 1)
         for (int i = 0; i < VPT; ++i) {
             if (!p.has(i)) continue;
             uint64_t f[4], g[4], d[4], a[4];
-            unpack8(ring.at(stage, 0, i), f);
-            unpack8(ring.at(stage, 1, i), d);
+            piece(i, 0, f);
+            piece(i, 1, d);
             weights8(weights, p.nv, p.at(i), g);
             unpack8(ring.at(stage, 2, i), a);  // zeros without dres
 #pragma unroll
@@ -465,27 +485,41 @@ int for_fill(int nv, F&& f) {
     return nv == NV ? f(Int<W>(), Int<VPT>(), std::true_type()) : f(Int<W>(), Int<VPT>(), std::false_type());
 }
 
-// Warps of a row and 16-byte pieces a thread for rows of h.
+// Warps of a row and 16-byte pieces a thread for rows of h.  Forward: as many
+// pieces a thread as keep three CTAs on an SM, since what a warp does once a row
+// costs as much as 20 values (16384 x 768: 10.3 us with three pieces, 11.2 with four
+// places).
 template <typename F>
 int for_forward(int h, F&& f) {
     const int nv = h / 8;
     if (nv <= 32) return for_fill<1, 1, 32>(nv, f);
     if (nv <= 64) return for_fill<1, 2, 64>(nv, f);
+    if (nv <= 96) return for_fill<1, 3, 96>(nv, f);
     if (nv <= 128) return for_fill<1, 4, 128>(nv, f);
+    if (nv <= 192) return for_fill<2, 3, 192>(nv, f);
     if (nv <= 256) return for_fill<2, 4, 256>(nv, f);
+    if (nv <= 384) return for_fill<4, 3, 384>(nv, f);
     if (nv <= 512) return for_fill<4, 4, 512>(nv, f);
+    if (nv <= 768) return for_fill<8, 3, 768>(nv, f);
     if (nv <= 1024) return for_fill<8, 4, 1024>(nv, f);
+    if (nv <= 1536) return for_fill<8, 6, 1536>(nv, f);
     return for_fill<8, 8, 2048>(nv, f);
 }
+// Backward: two pieces a thread, three where they fill the places better (3001 x
+// 2568: 23.0 us on four warps of three pieces, 24.2 on eight of two; 4096 x 5000:
+// 34 and 39 us; but 8192 x 768: 22 us on one warp, 17 on two).
 template <typename F>
 int for_backward(int h, F&& f) {
     const int nv = h / 8;
     if (nv <= 32) return for_fill<1, 1, 32>(nv, f);
     if (nv <= 64) return for_fill<1, 2, 64>(nv, f);
-    if (nv <= 128) return for_fill<1, 4, 128>(nv, f);
-    if (nv <= 256) return for_fill<2, 4, 256>(nv, f);
-    if (nv <= 512) return for_fill<4, 4, 512>(nv, f);
-    if (nv <= 1024) return for_fill<8, 4, 1024>(nv, f);
+    if (nv <= 128) return for_fill<2, 2, 128>(nv, f);
+    if (nv <= 256) return for_fill<4, 2, 256>(nv, f);
+    if (nv <= 384) return for_fill<4, 3, 384>(nv, f);
+    if (nv <= 512) return for_fill<8, 2, 512>(nv, f);
+    if (nv <= 768) return for_fill<8, 3, 768>(nv, f);
+    if (nv <= 1024) return for_fill<16, 2, 1024>(nv, f);
+    if (nv <= 1536) return for_fill<16, 3, 1536>(nv, f);
     return for_fill<16, 4, 2048>(nv, f);
 }
 
