@@ -404,16 +404,17 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_long_kernel(const __nv_bflo
     }
 }
 
-// Rows that a cluster of CTAs holds in its registers: LOSS_VPT 16-byte pieces a
-// thread, those of the next two rows on their way to shared memory meanwhile
-// (a thread copies and reads its own pieces, so no barrier guards them).  Each
-// warp's maximum and sum go to every CTA of the cluster, so each logit is read
-// once and each gradient written once.  They go by st.async, counted on the
-// receiver's mbarrier, in two slots in turn: a warp's values for row r tell that it
-// has read those of row r - 1, so a slot is free when it is written again.  With
-// a cluster barrier a row, its release waited for the last row's stores to global
-// memory (8192 x 128256: 800 to 850 us).
-constexpr int LOSS_VPT = 8, LOSS_ROW_THREADS = 256, LOSS_CTAS = 3, LOSS_STAGES = 2;
+// Rows that a cluster of CTAs holds in shared memory: LOSS_VPT 16-byte pieces a
+// thread and row, which that thread alone copies and reads, so that no barrier
+// guards them; each logit is read once and each gradient written once.  Each
+// warp's maximum and sum, and the label's logit, go to every CTA of the cluster by
+// st.async, counted on the receiver's mbarrier.  A row's gradients are computed after the next row's sums,
+// so nothing waits for the exchange: with a wait between a row's two passes 8192 x
+// 128256 took 843 us, with a cluster barrier there (whose release waits for the
+// last row's stores) about as much.
+// Four slots in turn: a CTA that sends row r's sums has all sums of row r - 2, whose
+// senders had finished with row r - 4, so its slot is free everywhere.
+constexpr int LOSS_VPT = 8, LOSS_ROW_THREADS = 256, LOSS_CTAS = 2, LOSS_STAGES = 3, LOSS_SLOTS = 4;
 constexpr int LOSS_PIECES = LOSS_VPT * LOSS_ROW_THREADS, LOSS_RANKS = 16;
 
 __device__ __forceinline__ void copy_piece(uint32_t to, const void* from) {
@@ -472,45 +473,64 @@ __device__ __forceinline__ bool cluster_wait_bar(uint32_t bar, uint32_t parity, 
 
 struct LossRow {
     int label;
-    float up, y;  // the loss's gradient, the label's logit
+    float up;  // the loss's gradient
 };
 
-__global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const __nv_bfloat16* logits, long long M, int v, int per,
-                                                                   int ranks, const int32_t* __restrict__ labels,
-                                                                   const float* __restrict__ dloss, float* __restrict__ loss,
-                                                                   __nv_bfloat16* dlogits) {
-    __shared__ MS slots[2][LOSS_RANKS * LOSS_ROW_THREADS / 32];
+// 2^(z scale - shift), two logits at a time, for e^(z - n) = 2^((z - n) log2 e):
+// shift is n scale rounded, and what it lacks goes into the sums as `rest`, exactly.
+// Above 2^23 logits that differ are 2^15 apart: any scale serves there, and 1 does
+// without rounding.
+struct Power {
+    uint64_t scale, shift;
+    float rest;
+    __device__ __forceinline__ explicit Power(float n) {
+        const float c = fabsf(n) < 0x1p23f ? LOG2E : 1.0f, s = n * c;
+        scale = f2_pack(c, c);
+        shift = f2_pack(-s, -s);
+        rest = c == 1.0f ? 1.0f : ex2f(-fmaf(n, c, -s));
+    }
+    __device__ __forceinline__ uint64_t operator()(uint32_t word) const {
+        float a, b;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(word << 16), __uint_as_float(word & 0xffff0000u)), scale, shift), a, b);
+        return f2_pack(ex2f(a), ex2f(b));
+    }
+};
+
+__global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const __nv_bfloat16* logits, long long M, int v,
+                                                                           int per, int ranks,
+                                                                           const int32_t* __restrict__ labels,
+                                                                           const float* __restrict__ dloss,
+                                                                           float* __restrict__ loss, __nv_bfloat16* dlogits) {
+    __shared__ MS slots[LOSS_SLOTS][LOSS_RANKS * LOSS_ROW_THREADS / 32 + 1];  // the warps', the label's
+    __shared__ __align__(8) uint64_t arrived[LOSS_SLOTS];
+    __shared__ int abort_flag, no_abort;
+    extern __shared__ uint4 ring[];  // [LOSS_STAGES][LOSS_VPT][threads]
     pdl_trigger();
     const int rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5, entries = ranks * warps;
     // This warp's pieces of a row: lo + lane, lo + 32 + lane, ... up to `pieces` (none where <= 0).
     const int lo = rank * per + w * 32 * LOSS_VPT, pieces = min(rank * per + per, v >> 3) - lo;
     const long long step = gridDim.x / ranks;
-    __shared__ __align__(8) uint64_t arrived[2];
-    __shared__ int abort_flag, no_abort;
     if (threadIdx.x == 0) {
-        no_abort = 0;
-        mbar_init(smem_u32(&arrived[0]), 1);
-        mbar_init(smem_u32(&arrived[1]), 1);
-        abort_flag = 0;
+        for (int k = 0; k < LOSS_SLOTS; ++k) mbar_init(smem_u32(&arrived[k]), 1);
+        abort_flag = no_abort = 0;
         fence_barrier_init();
     }
-    if (ranks > 1) cluster_sync_all();  // the others run, before anything is stored there
-    else __syncthreads();
-    pdl_wait();
-    bool ok = true;
-    const uint64_t log2e = f2_pack(LOG2E, LOG2E);
-    extern __shared__ uint4 ring[];  // [LOSS_STAGES][LOSS_VPT][threads]
     const int stage_pieces = LOSS_VPT * blockDim.x;
     for (int i = threadIdx.x; i < LOSS_STAGES * stage_pieces; i += blockDim.x)
         ring[i] = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);  // -inf behind the row's end
+    if (ranks > 1) cluster_sync_all();  // the others run, before anything is stored there
+    else __syncthreads();
+    pdl_wait();
+
+    auto label_at = [&](long long m) { return m < M ? labels[m] : -100; };
+    auto exists = [&](int label) { return label >= 0 && label < v; };
     // A row's copies and scalars; its label has been read a row before, so that
     // nothing here waits for memory.
     auto load = [&](long long m, int label, int stage) {
-        LossRow row = {label, 0.0f, 0.0f};
-        if (label >= 0 && label < v) {
+        LossRow row = {label, 0.0f};
+        if (exists(label)) {
             row.up = dloss ? dloss[m] : 1.0f;
-            row.y = __bfloat162float(logits[m * v + label]);
             const uint4* z = reinterpret_cast<const uint4*>(logits + m * v) + lo + lane;
             const uint32_t to = smem_u32(ring + stage * stage_pieces + threadIdx.x);
 #pragma unroll
@@ -520,51 +540,51 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
         copies_commit();
         return row;
     };
-    auto label_at = [&](long long m) { return m < M ? labels[m] : -100; };
-    int turn = 0;            // the stage of the ring
-    unsigned exchanges = 0;  // rows whose sums went round
-    long long m = blockIdx.x / ranks;
-    LossRow next = load(m, label_at(m), 0), after = load(m + step, label_at(m + step), 1);
-    int label = label_at(m + 2 * step);
-    for (; m < M; m += step, turn ^= 1) {
-        const LossRow row = next;
-        next = after;
-        const int label2 = label;
-        label = label_at(m + 3 * step);
-        uint4* d = reinterpret_cast<uint4*>(dlogits + m * v) + lo + lane;
-        copies_wait<1>();
-        if (row.label < 0 || row.label >= v) {
-            const uint32_t fill = fill_of(row.label);
-#pragma unroll
-            for (int i = 0; i < LOSS_VPT; ++i)
-                if (32 * i + lane < pieces) d[32 * i] = make_uint4(fill, fill, fill, fill);
-            if (rank == 0 && threadIdx.x == 0) loss[m] = __uint_as_float(fill & 0xffff0000u);
-            after = load(m + 2 * step, label2, turn);
-            continue;
+    // Where the label's logit lies, if it is this thread's; else -1.
+    auto own_piece = [&](int label) {
+        const int own = (label >> 3) - lo;
+        return own >= 0 && own < min(pieces, 32 * LOSS_VPT) && (own & 31) == lane ? own : -1;
+    };
+    // First pass: the sums of the other words' powers, on their way to every CTA.
+    auto send = [&](const LossRow& row, int stage, unsigned number) {
+        uint4* here = ring + stage * stage_pieces + threadIdx.x;
+        const int own = own_piece(row.label);
+        MS* slot = slots[number % LOSS_SLOTS];
+        const uint32_t bar = smem_u32(&arrived[number % LOSS_SLOTS]);
+        if (ranks > 1 && threadIdx.x == 0) mbar_arrive_expect_tx(bar, (entries + 1) * sizeof(MS));
+        auto put = [&](int at, float a, float b) {
+            if (ranks == 1) {
+                if (lane == 0) slot[at] = {a, b};
+            } else if (lane < ranks) {
+                asm volatile(
+                    "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                        mapa_shared(smem_u32(slot + at), lane)),
+                    "f"(a), "f"(b), "r"(mapa_shared(bar, lane))
+                    : "memory");
+            }
+        };
+        // The label's logit goes round by itself and leaves the sum: -inf in its place.
+        const unsigned owner = __ballot_sync(0xffffffffu, own >= 0);
+        if (owner) {
+            float y = 0.0f;
+            if (own >= 0) {
+                uint16_t* at = reinterpret_cast<uint16_t*>(here + (own >> 5) * blockDim.x) + (row.label & 7);
+                y = __uint_as_float(static_cast<uint32_t>(*at) << 16);
+                *at = 0xff80u;
+            }
+            put(entries, __shfl_sync(0xffffffffu, y, __ffs(owner) - 1), 0.0f);
         }
-        // The label's logit leaves the sum: -inf in its place.
-        const int own = (row.label >> 3) - lo;
-        const bool mine = own >= 0 && own < min(pieces, 32 * LOSS_VPT) && (own & 31) == lane;
-        uint4* here = ring + turn * stage_pieces + threadIdx.x;
-        if (mine) reinterpret_cast<uint16_t*>(here + (own >> 5) * blockDim.x)[row.label & 7] = 0xff80u;
         uint4 u[LOSS_VPT];
-#pragma unroll
-        for (int i = 0; i < LOSS_VPT; ++i) u[i] = here[i * blockDim.x];
         uint32_t top = 0xff80ff80u;
 #pragma unroll
-        for (int i = 0; i < LOSS_VPT; ++i)
+        for (int i = 0; i < LOSS_VPT; ++i) {
+            u[i] = here[i * blockDim.x];
             top = max_bf16x2(top, max_bf16x2(max_bf16x2(u[i].x, u[i].y), max_bf16x2(u[i].z, u[i].w)));
+        }
         const float2 tops = unpack_bf16x2(top);
-        const float most = warp_max(fmaxf(tops.x, tops.y)), near = finite_max(most);
-        after = load(m + 2 * step, label2, turn);  // the lanes' maximum has used all that was read from there
+        const float most = warp_max(fmaxf(tops.x, tops.y));
+        const Power power(finite_max(most));
         uint64_t s0 = f2_pack(0.0f, 0.0f), s1 = s0;
-        uint64_t off = f2_pack(-near, -near);
-        auto power = [&](uint32_t word) {  // e^{z - n} of two logits
-            float a, b;
-            f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(word << 16), __uint_as_float(word & 0xffff0000u)), off), log2e),
-                      a, b);
-            return f2_pack(ex2f(a), ex2f(b));
-        };
 #pragma unroll
         for (int i = 0; i < LOSS_VPT; ++i) {
             s0 = f2_add(s0, power(u[i].x));
@@ -574,24 +594,25 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
         }
         float a, b;
         f2_unpack(f2_add(s0, s1), a, b);
-        const float sum = warp_sum(a + b);
-        MS* slot = slots[exchanges & 1];
-        if (ranks > 1) {
-            const uint32_t bar = smem_u32(&arrived[exchanges & 1]);
-            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, entries * sizeof(MS));
-            if (lane < ranks)
-                asm volatile(
-                    "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
-                        mapa_shared(smem_u32(slot + rank * warps + w), lane)),
-                    "f"(most), "f"(sum), "r"(mapa_shared(bar, lane))
-                    : "memory");
-            ok = __all_sync(0xffffffffu, cluster_wait_bar(bar, exchanges >> 1 & 1, &abort_flag));
-            if (!ok) break;
-        } else {
-            if (lane == 0) slot[w] = {most, sum};
-            __syncthreads();
+        const float sum = warp_sum(a + b) * power.rest;
+        put(rank * warps + w, most, sum);
+        if (ranks == 1) __syncthreads();
+    };
+    // Second pass: the row's loss and gradients.  False where a wait gave up.
+    auto finish = [&](const LossRow& row, long long m, int stage, unsigned number) {
+        uint4* d = reinterpret_cast<uint4*>(dlogits + m * v) + lo + lane;
+        if (!exists(row.label)) {
+            const uint32_t fill = fill_of(row.label);
+#pragma unroll
+            for (int i = 0; i < LOSS_VPT; ++i)
+                if (32 * i + lane < pieces) d[32 * i] = make_uint4(fill, fill, fill, fill);
+            if (rank == 0 && threadIdx.x == 0) loss[m] = __uint_as_float(fill & 0xffff0000u);
+            return true;
         }
-        ++exchanges;
+        if (ranks > 1 && !__all_sync(0xffffffffu, cluster_wait_bar(smem_u32(&arrived[number % LOSS_SLOTS]),
+                                                                   number / LOSS_SLOTS & 1, &abort_flag)))
+            return false;
+        const MS* slot = slots[number % LOSS_SLOTS];
         MS all[LOSS_RANKS * LOSS_ROW_THREADS / 32 / 32];
         float highest = -INFINITY;
 #pragma unroll
@@ -599,7 +620,8 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
             all[k] = 32 * k + lane < entries ? slot[32 * k + lane] : MS{-INFINITY, 0.0f};
             highest = fmaxf(highest, all[k].m);
         }
-        const RowEnd r = row_end(row.y, warp_max(highest), [&](float n) {
+        const float y = slot[entries].m;
+        const RowEnd r = row_end(y, warp_max(highest), [&](float n) {
             float s = 0.0f;
 #pragma unroll
             for (int k = 0; k < LOSS_RANKS * LOSS_ROW_THREADS / 32 / 32; ++k)
@@ -607,31 +629,61 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
             return warp_sum(s);
         });
         const float scale = __fdividef(row.up, r.sum);
-        if (rank == 0 && threadIdx.x == 0) loss[m] = loss_of(r, row.y);
-        off = f2_pack(-r.n, -r.n);
-        const uint64_t by = f2_pack(scale, scale);
+        if (rank == 0 && threadIdx.x == 0) loss[m] = loss_of(r, y);
+        const Power power(r.n);
+        const uint64_t by = f2_pack(scale * power.rest, scale * power.rest);
         auto grad = [&](uint32_t word) {
             float lo_z, hi_z;
             f2_unpack(f2_mul(power(word), by), lo_z, hi_z);
             return pack_bf16x2(lo_z, hi_z);
         };
+        const uint4* here = ring + stage * stage_pieces + threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < LOSS_VPT; ++i)
-            if (32 * i + lane < pieces) d[32 * i] = make_uint4(grad(u[i].x), grad(u[i].y), grad(u[i].z), grad(u[i].w));
+        for (int i = 0; i < LOSS_VPT; ++i) {
+            const uint4 u = here[i * blockDim.x];
+            if (32 * i + lane < pieces) d[32 * i] = make_uint4(grad(u.x), grad(u.y), grad(u.z), grad(u.w));
+        }
         // The label's gradient over what its piece's store left in its place.
-        if (mine) reinterpret_cast<__nv_bfloat16*>(d + (own & ~31))[row.label & 7] = __float2bfloat16_rn(-r.others * scale);
+        const int own = own_piece(row.label);
+        if (own >= 0) reinterpret_cast<__nv_bfloat16*>(d + (own & ~31))[row.label & 7] = __float2bfloat16_rn(-r.others * scale);
+        return true;
+    };
+
+    long long m = blockIdx.x / ranks;
+    LossRow last = {-100, 0.0f}, row = load(m, label_at(m), 0), next = load(m + step, label_at(m + step), 1);
+    int label = label_at(m + 2 * step), stage = 0;
+    unsigned sent = 0;  // rows whose sums went round
+    bool ok = true;
+    // Row m's sums, then the gradients of the row before it.
+    for (; m < M + step; m += step) {
+        const bool here = m < M && exists(row.label);
+        copies_wait<1>();
+        const int before = stage == 0 ? LOSS_STAGES - 1 : stage - 1;
+        if (here) send(row, stage, sent);
+        if (m >= step) {  // (no row before the first one)
+            ok = finish(last, m - step, before, sent - 1);
+            if (!ok) break;
+        }
+        if (here) ++sent;
+        const int now = label;
+        label = label_at(m + 3 * step);
+        last = row;
+        row = next;
+        next = load(m + 2 * step, now, before);
+        stage = stage == LOSS_STAGES - 1 ? 0 : stage + 1;
     }
-    if (!ok) {  // a wait gave up: the losses of the rows left say so
+    if (!ok) {  // the losses of the rows left say so
         copies_wait<0>();
-        for (; rank == 0 && threadIdx.x == 0 && m < M; m += step) loss[m] = __int_as_float(0x7fc00000);
+        for (long long r = m - step; rank == 0 && threadIdx.x == 0 && r < M; r += step) loss[r] = __int_as_float(0x7fc00000);
     }
     if (ranks > 1) {
         __syncwarp();
         cluster_sync_all();  // nothing more is stored in another CTA's shared memory
-        if (!ok) {         // what was on its way here has arrived, as far as it comes
-            cluster_wait_bar(smem_u32(&arrived[exchanges & 1]), exchanges >> 1 & 1, &no_abort);
-            cluster_wait_bar(smem_u32(&arrived[exchanges + 1 & 1]), exchanges + 1 >> 1 & 1, &no_abort);
-        }
+        if (!ok)             // what was on its way here has arrived, as far as it comes
+            for (unsigned k = 0; k < LOSS_SLOTS; ++k) {
+                const unsigned number = sent + k >= 1 ? sent + k - 1 : 0;
+                cluster_wait_bar(smem_u32(&arrived[number % LOSS_SLOTS]), number / LOSS_SLOTS & 1, &no_abort);
+            }
     }
 }
 
