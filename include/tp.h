@@ -556,7 +556,7 @@ TP_API int tp_vocab_logits_backward_workspace_bytes(int64_t M, int64_t v, int32_
  * embedding shares gets both gradients that way).  Either of dH and dW may be
  * NULL.  M may be 0 (dW is cleared then unless accumulate).  h % 8 == 0,
  * (v / t) % 8 == 0, M and v below 2^31.  workspace >=
- * tp_vocab_logits_backward_workspace_bytes (NULL where that is 0). */
+ * tp_vocab_logits_backward_workspace_bytes (needed if dH is; NULL where that is 0). */
 TP_API int tp_vocab_logits_backward(const tp_bf16* H, int64_t M, int32_t h, const tp_bf16* W, int64_t v, int32_t t,
                                     const tp_bf16* dlogits, tp_bf16* dH, float* dW, int accumulate, void* workspace,
                                     size_t ws_bytes, void* stream);

@@ -1641,11 +1641,19 @@ extern "C" int tp_vocab_parallel_cross_entropy_train(const tp_bf16* logits, int6
     return run(tpi::vocab_loss_launch(logits, M, v, labels, dloss, loss, dlogits, as_stream(stream), &err), err);
 }
 
+// Where dH has few output tiles for its long sum over the vocabulary, parts of
+// that sum go to fp32 partials and are added: fewer than half of the SMs would have
+// a tile otherwise.
+static size_t logits_bwd_bytes(int64_t M, int64_t v, int32_t h) {
+    const int pieces = M ? tpi::nn_pieces(M, h, v) : 1;
+    return pieces > 1 ? static_cast<size_t>(pieces) * M * h * sizeof(float) : 0;
+}
+
 extern "C" int tp_vocab_logits_backward_workspace_bytes(int64_t M, int64_t v, int32_t h, size_t* bytes) {
     int rc;
     if (!bytes) return fail(TP_ERR_INVALID_ARG, "bytes is NULL");
     if ((rc = check_train_vocab(M, v, 1, 8)) || (rc = check_width(h, 0))) return rc;
-    *bytes = 0;
+    *bytes = logits_bwd_bytes(M, v, h);
     return TP_OK;
 }
 
@@ -1658,8 +1666,7 @@ extern "C" int tp_vocab_logits_backward(const tp_bf16* H, int64_t M, int32_t h, 
         (rc = elems_ptr(dlogits, none, "dlogits")) || (rc = opt_ptr(dH, "dH")) || (rc = opt_ptr(dW, "dW")) ||
         (rc = check_train_vocab(M, v, t, 8)) || (rc = check_width(h, 0)))
         return rc;
-    (void)workspace;
-    (void)ws_bytes;
+    if (dH && (rc = check_scratch(workspace, ws_bytes, logits_bwd_bytes(M, v, h)))) return rc;
     cudaStream_t s = as_stream(stream);
     std::string err;
     if (none) {
@@ -1669,29 +1676,39 @@ extern "C" int tp_vocab_logits_backward(const tp_bf16* H, int64_t M, int32_t h, 
     }
     if (dH) {  // dH = dlogits W: the K loop runs over all shards' words
         tpi::GemmArgs g;
-        g.mode = tpi::GEMM_NN;
+        g.k_pieces = tpi::nn_pieces(M, h, v);
+        const bool parts = g.k_pieces > 1;
+        g.mode = parts ? tpi::GEMM_NN_PARTIAL : tpi::GEMM_NN;
         g.M = M;
         g.N = h;
         g.K = v;
         g.A = dlogits;
         g.B0 = W;
-        g.out = dH;
+        g.out = parts ? workspace : dH;
         g.ldo = h;
         if ((rc = run(tpi::gemm_launch(g, s, &err), err))) return rc;
+        if (parts &&
+            (rc = run(tpi::reduce_launch(workspace, 1, g.k_pieces, M * h, h, nullptr, nullptr, dH, s, &err), err)))
+            return rc;
     }
-    if (dW) {  // dW = dlogits^T H (shard i: rows i v/t ..)
+    // dW = dlogits^T H (shard i: rows i v/t ..).  The tensor cores' fp32 sums round
+    // towards zero at each step, an error that grows with their length (2.1e-6 of the
+    // norm over 2048 tokens, 9.1e-6 over 8192), so longer batches are added kTokens at
+    // a time, each sum rounded to nearest.
+    constexpr int64_t kTokens = 4096;
+    for (int64_t m = 0; dW && m < M; m += kTokens) {
         tpi::GemmArgs g;
         g.mode = tpi::GEMM_TN;
         g.M = v;
         g.N = h;
-        g.K = M;
-        g.A = dlogits;
+        g.K = std::min(kTokens, M - m);
+        g.A = dlogits + m * v;
         g.lda = v;
-        g.B0 = H;
+        g.B0 = H + m * h;
         g.out = dW;
         g.ldo = h;
-        g.accumulate = accumulate ? 1 : 0;
-        return run(tpi::gemm_launch(g, s, &err), err);
+        g.accumulate = accumulate || m ? 1 : 0;
+        if ((rc = run(tpi::gemm_launch(g, s, &err), err))) return rc;
     }
     return TP_OK;
 }

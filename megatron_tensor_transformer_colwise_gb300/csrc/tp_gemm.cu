@@ -210,7 +210,7 @@ template <int MODE>
 struct Major {
     static constexpr bool A_MN = MODE == tpi::GEMM_TN;
     static constexpr bool B_MN =
-        MODE == tpi::GEMM_BWD_ACT || MODE == tpi::GEMM_NN || MODE == tpi::GEMM_TN;
+        MODE == tpi::GEMM_BWD_ACT || MODE == tpi::GEMM_NN || MODE == tpi::GEMM_NN_PARTIAL || MODE == tpi::GEMM_TN;
 };
 // An MN-major operand tile is stored as 64-element (128-byte) MN blocks of
 // BK = 64 swizzled K rows each, MN_BLOCK_BYTES apart.
@@ -523,7 +523,8 @@ __device__ __forceinline__ void producer_loop(const GemmParams& p, uint32_t base
                 const uint32_t full_l = (CG == 2) ? mapa_shared(full, rank & ~1u) : full;
                 const uint32_t a_dst = base + stage * C::STAGE_BYTES;
                 const uint32_t b_dst = a_dst + A_BYTES;
-                const int kc = kb * BK;
+                // (K past its end reads zeros: the last of several parts may be shorter.)
+                const int kc = (MODE == tpi::GEMM_NN_PARTIAL ? s_grid * p.kb_per_shard + kb : kb) * BK;
 #pragma unroll
                 for (int c = -1; c < C::CHUNKS; ++c) {
                     const int cc = static_cast<int>(prank) * C::CHUNKS + c;  // B box of the tile
@@ -893,7 +894,7 @@ __device__ __forceinline__ void std_tile(const GemmParams& p, uint32_t t0, int c
         tmem_ld32(t0 + c * 32, r);
         tmem_ld_wait();
         if (!row_ok) {
-        } else if (MODE == tpi::GEMM_ROW_PARTIAL && p.out_f32) {
+        } else if (MODE == tpi::GEMM_NN_PARTIAL || (MODE == tpi::GEMM_ROW_PARTIAL && p.out_f32)) {
             float* out = reinterpret_cast<float*>(p.out) + s_grid * p.shard_stride +
                          static_cast<long long>(row) * p.ldo;
 #pragma unroll
@@ -1669,6 +1670,28 @@ constexpr int kPairTiles = TP_GEMM_CTA_PAIR;
 // Output columns of the narrow rowwise tile (UMMA N = 128).
 constexpr int kNarrowBN = 128;
 
+// A wave of pair tiles takes as long as one tile; the partials are written and
+// read once (an fp32 word each way at about 5 bytes a nanosecond and thousand pair
+// clocks: the cost of 3 k-blocks a part and 76 tiles), and the second launch is
+// worth eight k-blocks.
+int nn_pieces(int64_t M, int64_t N, int64_t K) {
+    constexpr int TILE_M = BM * kPairTiles;
+    const int64_t tiles = ((M + TILE_M - 1) / TILE_M) * ((N + BN - 1) / BN), kb = (K + BK - 1) / BK;
+    const int64_t pairs = std::max(1, device_sm_count() / kPairTiles);
+    int best = 1;
+    int64_t least = (tiles + pairs - 1) / pairs * kb * 9 / 10;  // a tenth less, or the scratch is not worth it
+    for (int s = 2; s <= 8; ++s) {
+        const int64_t each = (kb + s - 1) / s;
+        if ((s - 1) * each >= kb) continue;  // a part without any K
+        const int64_t cost = (tiles * s + pairs - 1) / pairs * each + 8 + 3 * s * tiles / pairs;
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
 int gemm_launch(const GemmArgs& a, cudaStream_t stream, std::string* err) {
     GemmParams p;
     memset(&p, 0, sizeof(p));
@@ -1706,7 +1729,7 @@ int gemm_launch(const GemmArgs& a, cudaStream_t stream, std::string* err) {
     p.m_tiles = static_cast<int>((a.M + TILE_M - 1) / TILE_M);
     const int bn_out = (a.mode == GEMM_COL_SWIGLU) ? BN / 2 : BN;
     p.n_tiles = static_cast<int>((a.N + bn_out - 1) / bn_out);
-    p.grid_shards = (a.mode == GEMM_ROW_PARTIAL) ? a.t : 1;
+    p.grid_shards = a.mode == GEMM_ROW_PARTIAL ? a.t : a.mode == GEMM_NN_PARTIAL ? a.k_pieces : 1;
     // Rowwise GEMMs of small problems (few output tiles, long K) take
     // 128-column tiles when those still fit in one wave: twice the CTAs
     // busy, each tile half as long.
@@ -1733,8 +1756,9 @@ int gemm_launch(const GemmArgs& a, cudaStream_t stream, std::string* err) {
         const uint64_t dB[3] = {(uint64_t)a.Ks, (uint64_t)a.t, (uint64_t)a.N};
         const uint32_t bB[3] = {BK, 1, B_CHUNK_ROWS};
         if (!make_map(&p.mapB[0], a.B0, 3, dB, sA, bB, err)) return TP_ERR_CUDA;
-    } else if (a.mode == GEMM_BWD_ACT || a.mode == GEMM_NN || a.mode == GEMM_TN) {
+    } else if (a.mode == GEMM_BWD_ACT || a.mode == GEMM_NN || a.mode == GEMM_NN_PARTIAL || a.mode == GEMM_TN) {
         p.kb_per_shard = static_cast<int>((a.K + BK - 1) / BK);
+        if (a.mode == GEMM_NN_PARTIAL) p.kb_per_shard = (p.kb_per_shard + a.k_pieces - 1) / a.k_pieces;
         p.k_shards = 1;
         const uint32_t box_mn[2] = {64, BK};  // 64 MN elements x 64 K rows
         if (a.mode == GEMM_TN) {
@@ -1900,6 +1924,7 @@ int gemm_launch(const GemmArgs& a, cudaStream_t stream, std::string* err) {
         case GEMM_COL_PACKED: return launch_mode<GEMM_COL_PACKED, CG>(p, grid, stream, err);
         case GEMM_BWD_ACT: return launch_mode<GEMM_BWD_ACT, CG>(p, grid, stream, err);
         case GEMM_NN: return launch_mode<GEMM_NN, CG>(p, grid, stream, err);
+        case GEMM_NN_PARTIAL: return launch_mode<GEMM_NN_PARTIAL, CG>(p, grid, stream, err);
         case GEMM_TN: return launch_mode<GEMM_TN, CG>(p, grid, stream, err);
         default:
             if (err) *err = "unknown GEMM mode";

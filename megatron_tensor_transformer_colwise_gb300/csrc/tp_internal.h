@@ -49,6 +49,7 @@ enum GemmMode {
     GEMM_BWD_ACT = 6,     // dH = dZ W2 (B MN-major), epilogue: dU, dG, H from saved U, G
     GEMM_NN = 7,          // A K-major, B MN-major [K][N] (K rows split over B0 / B1)
     GEMM_TN = 8,          // A and B MN-major ([K][M], [K][N]), fp32 out split by rows
+    GEMM_NN_PARTIAL = 10, // GEMM_NN in k_pieces parts of K, one fp32 [M][N] partial each
     GEMM_MLP = 9          // the whole sharded MLP in one persistent launch (see MlpArgs)
 };
 
@@ -124,6 +125,7 @@ struct GemmArgs {
     void* out2 = nullptr;
     int64_t ldo2 = 0;
     int64_t k_split = 0, k_split2 = 0;
+    int k_pieces = 1;  // GEMM_NN_PARTIAL (B0 alone)
     void* out3 = nullptr;
     int64_t ldo3 = 0;
     int64_t row_split = 0, row_split2 = 0;
@@ -135,6 +137,10 @@ struct GemmArgs {
 // Encodes the tensor maps and launches the persistent tcgen05 GEMM on
 // `stream`.  Returns 0 or a TP_ERR_* code with a message in *err.
 int gemm_launch(const GemmArgs& a, cudaStream_t stream, std::string* err);
+
+// Parts of K that a GEMM_NN with few output tiles is worth on the current device
+// (1: none), for GEMM_NN_PARTIAL and a reduction of its partials.
+int nn_pieces(int64_t M, int64_t N, int64_t K);
 
 // Number of kernel launches gemm_launch issues (always 1).
 constexpr int kGemmLaunches = 1;
