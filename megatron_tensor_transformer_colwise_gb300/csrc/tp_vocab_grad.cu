@@ -44,8 +44,10 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 // ------------------------------------------------------------ scaled lookup
 
-// One warp per token: out = scale * E[id] (rounded once), or zeros.
-constexpr int EMB_WARPS = 8;
+// One warp per token: out = scale * E[id] (rounded once), or zeros.  Eight
+// 16-byte pieces a lane are read before the first is used: with one at a time the
+// lanes waited for memory (8192 x 4096: 19.7 us).
+constexpr int EMB_WARPS = 4, EMB_LOADS = 8;
 
 __global__ void __launch_bounds__(EMB_WARPS * 32) embedding_scaled_kernel(const int32_t* __restrict__ ids, long long M,
                                                                          const __nv_bfloat16* __restrict__ E, long long v,
@@ -58,12 +60,19 @@ __global__ void __launch_bounds__(EMB_WARPS * 32) embedding_scaled_kernel(const 
     const bool owned = id >= 0 && id < v;
     const uint4* src = reinterpret_cast<const uint4*>(E + (owned ? id : 0) * h);
     uint4* dst = reinterpret_cast<uint4*>(out + m * h);
-    for (int c = threadIdx.x & 31; c < (h >> 3); c += 32) {
-        float f[8];
-        unpack8(owned ? src[c] : make_uint4(0, 0, 0, 0), f);
+    const int nv = owned ? h >> 3 : 0;
+    for (int c = threadIdx.x & 31; c < (h >> 3); c += 32 * EMB_LOADS) {
+        uint4 u[EMB_LOADS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = owned ? f[e] * scale : 0.0f;
-        dst[c] = pack8(f);
+        for (int k = 0; k < EMB_LOADS; ++k) u[k] = c + 32 * k < nv ? src[c + 32 * k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < EMB_LOADS; ++k) {
+            float f[8];
+            unpack8(u[k], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = owned ? f[e] * scale : 0.0f;
+            if (c + 32 * k < (h >> 3)) dst[c + 32 * k] = pack8(f);
+        }
     }
 }
 
