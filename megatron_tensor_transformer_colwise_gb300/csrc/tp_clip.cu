@@ -88,9 +88,23 @@ __device__ __forceinline__ void for_rest(long long from, long long to, F&& one) 
     if (threadIdx.x < N && i < to) one(i);
 }
 
-// This thread's part of a chunk's sum of squares.
+// A sum as a number and what its roundings left (two-sum: exact but for the
+// roundings of lo), since 64-bit arithmetic is 64 times slower here: with doubles
+// in every thread the two launches spent 15 of 25 us on a GeLU MLP's gradients in
+// them.
+struct Sum {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float t) {
+        const float s = hi + t, b = s - hi;
+        lo += (hi - (s - b)) + (t - b);
+        hi = s;
+    }
+};
+
+// Adds this thread's part of a chunk's sum of squares to sum, or, where it is out
+// of sum's range, to far.
 template <bool BF16>
-__device__ __forceinline__ double chunk_sum(const void* src, long long from, long long to) {
+__device__ __forceinline__ void chunk_sum(const void* src, long long from, long long to, Sum& sum, double& far) {
     constexpr int N = BF16 ? 8 : 4, P = BF16 ? PIECES / 2 : PIECES;
     const uint4* at = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + from * (16 / N));
     const int pieces = static_cast<int>((to - from) / N);
@@ -116,10 +130,14 @@ __device__ __forceinline__ double chunk_sum(const void* src, long long from, lon
         t = fmaf(g, g, t);
         any |= __float_as_uint(g);
     });
-    // Squares that leave fp32's range (a sum below 2^-90 may have lost some,
-    // one above the largest number has) are summed again in 64 bits.
-    if (t >= 0x1p-90f && t <= FLT_MAX) return t;
-    if (!(any & (BF16 ? 0x7fff7fffu : 0x7fffffffu))) return 0.0;  // zeros of either sign
+    // Squares near the ends of fp32's range are summed again in 64 bits: a sum
+    // below 2^-90 may have lost some, and 2^18 chunks of 32 lanes stay finite below
+    // 2^100.
+    if (t >= 0x1p-90f && t <= 0x1p100f) {
+        sum.add(t);
+        return;
+    }
+    if (!(any & (BF16 ? 0x7fff7fffu : 0x7fffffffu))) return;  // zeros of either sign
     double d = 0.0;
 #pragma unroll 1
     for (int v = threadIdx.x; v < pieces; v += THREADS) {
@@ -132,30 +150,41 @@ __device__ __forceinline__ double chunk_sum(const void* src, long long from, lon
         const double g = value_at<BF16>(src, i);
         d = fma(g, g, d);
     });
-    return d;
+    far += d;
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(THREADS, CTAS) grad_sum_kernel(const __grid_constant__ Tensors<CAP> p,
                                                                  double* __restrict__ sums) {
-    __shared__ double red[THREADS / 32];
+    constexpr int WARPS = THREADS / 32;
+    __shared__ Sum red[WARPS];
+    __shared__ double all[THREADS];
     pdl_trigger();
     pdl_wait();
-    double total = 0.0;
+    Sum sum;
+    double far = 0.0;
     for (long long chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
         const Tensor& t = tensor_of(p, chunk);
         const long long from = (chunk - t.first) * CHUNK, to = min(from + CHUNK, t.n);
-        total += t.bf16 ? chunk_sum<true>(t.src, from, to) : chunk_sum<false>(t.src, from, to);
+        if (t.bf16) chunk_sum<true>(t.src, from, to, sum, far);
+        else chunk_sum<false>(t.src, from, to, sum, far);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = total;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        total = 0.0;
-        for (int w = 0; w < THREADS / 32; ++w) total += red[w];
-        sums[blockIdx.x] = total;
+    for (int o = 16; o > 0; o >>= 1) {
+        const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, o), lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
+        sum.add(hi);
+        sum.lo += lo;
     }
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    all[threadIdx.x] = far;
+    const bool any_far = __syncthreads_or(far != 0.0);  // (true for NaN)
+    if (threadIdx.x >= 32) return;
+    double total = 0.0;
+    if (threadIdx.x < WARPS) total = static_cast<double>(red[threadIdx.x].hi) + static_cast<double>(red[threadIdx.x].lo);
+    for (int i = threadIdx.x; any_far && i < THREADS; i += 32) total += all[i];
+#pragma unroll
+    for (int o = any_far ? 16 : WARPS / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (threadIdx.x == 0) sums[blockIdx.x] = total;
 }
 
 // This thread's part of a chunk: dst = src times the factor.  Both sides are
@@ -204,29 +233,46 @@ __device__ __noinline__ void chunk_scale_far(const void* src, void* dst, long lo
         store_at<BF16>(dst, i, static_cast<float>(value_at<BF16>(src, i) * by));
 }
 
+// 1 / sqrt(s) of a finite s > 0, by fp32's and one step of Newton's method (an
+// error of 2^-22 becomes one of 2^-43); s is brought between 1 and 4 first, where
+// fp32 holds it.
+__device__ __forceinline__ double inverse_root(double s) {
+    const int half = ((__double2hiint(s) >> 20) - 1023) >> 1;  // s is between 4^half and 4^(half + 1)
+    const double m = __hiloint2double(__double2hiint(s) - half * (1 << 21), __double2loint(s));
+    const double y = rsqrtf(static_cast<float>(m)), z = y * (1.5 - 0.5 * m * y * y);
+    return z * __hiloint2double((1023 - half) << 20, 0);
+}
+
 // n_sums: CTAs of all launches of grad_sum_kernel together.  The chunks run
 // from the last to the first: the last ones that the sums read are in L2.
 template <int CAP>
 __global__ void __launch_bounds__(THREADS, CTAS) grad_scale_kernel(const __grid_constant__ Tensors<CAP> p,
                                                                    const double* __restrict__ sums, int n_sums,
                                                                    float max_norm, float* norm) {
-    __shared__ double red[THREADS / 32];
+    __shared__ double factor;
     pdl_trigger();
     pdl_wait();
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n_sums; i += THREADS) s += sums[i];
+    if (threadIdx.x < 32) {
+        double s = 0.0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n_sums; i += 32) s += sums[i];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) {
+            // A norm that is not finite (an infinity or NaN among the gradients)
+            // scales nothing; the caller sees it and skips the step.
+            double length = s, by = 1.0;
+            if (s > 0.0 && s <= DBL_MAX) {
+                const double inverse = inverse_root(s);
+                length = s * inverse;
+                if (length > max_norm) by = fmin(1.0, max_norm * inverse);
+            }
+            if (norm && blockIdx.x == 0) *norm = static_cast<float>(length);
+            factor = by;
+        }
+    }
     __syncthreads();
-    s = 0.0;
-    for (int w = 0; w < THREADS / 32; ++w) s += red[w];
-    const double length = sqrt(s);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(length);
-    // A norm that is not finite (an infinity or NaN among the gradients)
-    // scales nothing; the caller sees it and skips the step.
-    double by = 1.0;
-    if (length > max_norm && length <= DBL_MAX) by = max_norm / length;
+    const double by = factor;
     for (long long chunk = p.chunks - 1 - blockIdx.x; chunk >= 0; chunk -= gridDim.x) {
         const Tensor& t = tensor_of(p, chunk);
         if (!t.dst || (by == 1.0 && t.dst == t.src)) continue;
