@@ -698,21 +698,21 @@ __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const
 
 size_t loss_ring_bytes(int threads) { return static_cast<size_t>(LOSS_STAGES) * LOSS_VPT * threads * sizeof(uint4); }
 
-// Clusters of `ranks` full CTAs of loss_kernel that the current device holds at
-// once; 0 when they do not fit at all.
-int loss_clusters(int ranks) {
-    static int counts[64][5] = {};
+// Clusters of `ranks` CTAs of loss_kernel that the current device holds at once; 0
+// when they do not fit at all.
+int loss_clusters(int ranks, int threads) {
+    static int counts[64][5][LOSS_ROW_THREADS / 32] = {};
     int dev = 0, log = 0;
     while (1 << log < ranks) ++log;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int& count = counts[dev][log];
+    int& count = counts[dev][log][threads / 32 - 1];
     if (!count) {
         int n = 0;
         cudaLaunchConfig_t cfg;
         memset(&cfg, 0, sizeof(cfg));
         cfg.gridDim = dim3(ranks * 64);
-        cfg.blockDim = dim3(LOSS_ROW_THREADS);
-        cfg.dynamicSmemBytes = loss_ring_bytes(LOSS_ROW_THREADS);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = loss_ring_bytes(threads);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = ranks;
@@ -721,7 +721,7 @@ int loss_clusters(int ranks) {
         cfg.numAttrs = 1;
         if (cudaFuncSetAttribute(loss_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
             cudaFuncSetAttribute(loss_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(cfg.dynamicSmemBytes)) != cudaSuccess ||
+                                 static_cast<int>(loss_ring_bytes(LOSS_ROW_THREADS))) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, loss_kernel, &cfg) != cudaSuccess)
             n = 0;
         cudaGetLastError();
@@ -802,7 +802,7 @@ int vocab_loss_launch(const void* logits, int64_t M, int64_t v, const int32_t* l
     while (ranks < LOSS_RANKS && nv > static_cast<int64_t>(ranks) * LOSS_PIECES) ranks *= 2;
     const int64_t per = (nv + ranks - 1) / ranks;
     const int threads = static_cast<int>(std::min<int64_t>((per + 32 * LOSS_VPT - 1) / (32 * LOSS_VPT) * 32, LOSS_ROW_THREADS));
-    const int64_t clusters = per > LOSS_PIECES ? 0 : loss_clusters(ranks) * static_cast<int64_t>(ranks == 1 ? LOSS_ROW_THREADS / threads : 1);
+    const int64_t clusters = per > LOSS_PIECES ? 0 : loss_clusters(ranks, threads);
     if (clusters < 1) {
         launch_pdl(loss_long_kernel, dim3((unsigned)M), dim3(LOSS_THREADS), 0, stream, z, static_cast<int>(v), labels, dloss,
                    loss, d);
