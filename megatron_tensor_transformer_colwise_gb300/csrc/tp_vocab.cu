@@ -73,7 +73,7 @@ struct MS {
 
 __device__ __forceinline__ MS ms_merge(MS a, MS b) {
     const float m = fmaxf(a.m, b.m);
-    if (m == -INFINITY) return {m, 0.0f};
+    if (m == -INFINITY) return {m, a.s + b.s};  // nothing yet, masked words (-inf) alone, or NaN
     return {m, a.s * ex2f(a.m - m) + b.s * ex2f(b.m - m)};
 }
 
@@ -103,9 +103,10 @@ __global__ void __launch_bounds__(CE_THREADS) ce_shard_stats_kernel(
 #pragma unroll
         for (int e = 1; e < 8; ++e) bm = fmaxf(bm, x[e]);
         const float nm = fmaxf(acc.m, bm);
-        float s = (acc.m == -INFINITY) ? 0.0f : acc.s * ex2f(acc.m - nm);
+        const float off = nm == -INFINITY ? 0.0f : nm;  // masked words (-inf) alone: powers of 0
+        float s = (acc.m == -INFINITY) ? acc.s : acc.s * ex2f(acc.m - nm);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += ex2f(x[e] - nm);
+        for (int e = 0; e < 8; ++e) s += ex2f(x[e] - off);
         acc = {nm, s};
     }
 #pragma unroll

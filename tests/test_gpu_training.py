@@ -384,6 +384,29 @@ def test_loss_of_masked_logits():
     assert float(loss[2]) == np.inf and d[3].isnan().all() and d[4].isnan().all() and d[5].isnan().all()
 
 
+@pytest.mark.parametrize("t", [1, 3])
+def test_plain_loss_of_masked_words(t):
+    # tp_vocab_parallel_cross_entropy: words that a thread or a shard sees alone may all be masked.
+    M, v = 6, 4104
+    z = normal((M, v), 8, 2.0)
+    z[0, 1368:] = -np.inf
+    z[1, :2736] = -np.inf
+    z[2, :] = -np.inf
+    z[2, 17] = 1.5
+    z[3, 8:] = -np.inf
+    z[4, :] = -np.inf
+    z[5, :] = -np.inf
+    z[5, 2000] = np.nan
+    labels = torch.tensor([17, 4000, 17, 3, 17, 17], dtype=torch.int32)
+    loss, stats = empty(M), empty(3 * t * M)
+    tp.tp_vocab_parallel_cross_entropy(dev(z), M, v, t, dev(labels), stats, loss)
+    ref = refs.loss(host64(z), labels.numpy(), np.ones(M))[0]
+    got = host64(loss)
+    assert np.isnan(got[4:]).all()
+    # exponents off by 2^-24 of up to 16, a logarithm and a difference of numbers up to 16.
+    within(got[:4], ref[:4], 2.0 ** -18 * (1 + np.abs(ref[:4])), "loss")
+
+
 def test_loss_small_ones_and_far_logits():
     # The label far ahead of all others: 1 - p would vanish in fp32.
     v = 1000
