@@ -1670,10 +1670,11 @@ constexpr int kPairTiles = TP_GEMM_CTA_PAIR;
 // Output columns of the narrow rowwise tile (UMMA N = 128).
 constexpr int kNarrowBN = 128;
 
-// A wave of pair tiles takes as long as one tile; the partials are written and
-// read once (an fp32 word each way at about 5 bytes a nanosecond and thousand pair
-// clocks: the cost of 3 k-blocks a part and 76 tiles), and the second launch is
-// worth eight k-blocks.
+// A wave of pair tiles takes as long as one tile.  In k-blocks of a pair (0.28 us),
+// the second launch costs 18 and a tile's partial, written and read, 2/5.  Measured
+// for dH, us: 2048 x 1024 over K = 32768 without parts 146, in two 85, four 92, seven
+// 95; 512 x 1024 145, four 46, eight 35; 64 x 4096 over 128256 546, four 165, five
+// 254; 2048 x 4096 over 128256 1171, four 1133.
 int nn_pieces(int64_t M, int64_t N, int64_t K) {
     constexpr int TILE_M = BM * kPairTiles;
     const int64_t tiles = ((M + TILE_M - 1) / TILE_M) * ((N + BN - 1) / BN), kb = (K + BK - 1) / BK;
@@ -1683,7 +1684,7 @@ int nn_pieces(int64_t M, int64_t N, int64_t K) {
     for (int s = 2; s <= 8; ++s) {
         const int64_t each = (kb + s - 1) / s;
         if ((s - 1) * each >= kb) continue;  // a part without any K
-        const int64_t cost = (tiles * s + pairs - 1) / pairs * each + 8 + 3 * s * tiles / pairs;
+        const int64_t cost = (tiles * s + pairs - 1) / pairs * each + 18 + 2 * s * tiles / 5;
         if (cost < least) {
             least = cost;
             best = s;
