@@ -94,7 +94,9 @@ __global__ void __launch_bounds__(EMB_WARPS * 32) embedding_scaled_kernel(const 
 // contiguous part of the tokens and has counters of its own, so the positions
 // of a word come out ascending whatever the order of the work.
 //   sorted: tokens by word; start[r] .. start[r + 1]: those of word r.
-constexpr int BINS = 128, SORT_WARPS = 32, SORT_LOADS = 8;
+// As many warps (4 to 32) as have a batch of loads each: what a CTA does for its
+// counters grows with them (64 tokens over 128256 words: 14.9 us with 32).
+constexpr int BINS = 128, SORT_LOADS = 8, MAX_SORT_WARPS = 32;
 
 struct Entry {
     int32_t word, at;  // a token's word and its position
@@ -118,11 +120,13 @@ __device__ __forceinline__ void for_ids(const int32_t* __restrict__ ids, long lo
     }
 }
 
-__global__ void __launch_bounds__(SORT_WARPS * 32) sort_tokens_kernel(const int32_t* __restrict__ ids, long long M, int v,
+__global__ void __launch_bounds__(MAX_SORT_WARPS * 32) sort_tokens_kernel(const int32_t* __restrict__ ids, long long M, int v,
                                                                      Entry* __restrict__ sorted, int32_t* __restrict__ start,
                                                                      int32_t* __restrict__ counters, long long n_counters) {
-    __shared__ int32_t count[SORT_WARPS][BINS];
-    __shared__ int32_t below[SORT_WARPS], sums[BINS / 32];
+    extern __shared__ int32_t counts[];  // [warps][BINS]
+    int32_t(*count)[BINS] = reinterpret_cast<int32_t(*)[BINS]>(counts);
+    __shared__ int32_t below[MAX_SORT_WARPS], sums[BINS / 32];
+    const int warps = blockDim.x >> 5;
     pdl_trigger();
     pdl_wait();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(SORT_WARPS * 32) sort_tokens_kernel(const int3
         counters[i] = 0;
     for (int b = lane; b < BINS; b += 32) count[w][b] = 0;
     __syncwarp();
-    const long long part = ((M + SORT_WARPS - 1) / SORT_WARPS + 31) / 32 * 32;
+    const long long part = ((M + warps - 1) / warps + 31) / 32 * 32;
     const long long from = w * part, to = min(from + part, M);
     int under = 0;
     for_ids(ids, from, to, [&](int id, long long) {
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(SORT_WARPS * 32) sort_tokens_kernel(const int3
     // count[w][b] becomes the place of warp w's first token of word lo + b.
     int total = 0, base = 0;
     if (threadIdx.x < BINS) {
-        for (int k = 0; k < SORT_WARPS; ++k) {
+        for (int k = 0; k < warps; ++k) {
             const int n = count[k][threadIdx.x];
             count[k][threadIdx.x] = total;
             total += n;
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(SORT_WARPS * 32) sort_tokens_kernel(const int3
     __syncthreads();
     if (threadIdx.x < BINS) {
         for (int k = 0; k < w; ++k) base += sums[k];
-        for (int k = 0; k < SORT_WARPS; ++k) count[k][threadIdx.x] += base;
+        for (int k = 0; k < warps; ++k) count[k][threadIdx.x] += base;
         if (threadIdx.x < bins) start[lo + threadIdx.x] = base;
         if (lo + static_cast<int>(threadIdx.x) == v - 1) start[v] = base + total;
     }
@@ -304,12 +308,13 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const Entry*
     }
 }
 
-// Sorted tokens of a part: so many that about 2048 CTAs (parts times slices of
+constexpr int PART_CTAS = 1024;
+// Sorted tokens of a part: so many that about PART_CTAS CTAs (parts times slices of
 // columns) share the work, between 8 and MAX_PART.
 int part_tokens(int64_t M, int h) {
     const int64_t slices = (h / 8 + SUM_THREADS - 1) / SUM_THREADS;
     int64_t part = 8;
-    while (part < MAX_PART && part * 2048 < M * slices) part *= 2;
+    while (part < MAX_PART && part * PART_CTAS < M * slices) part *= 2;
     return static_cast<int>(part);
 }
 
@@ -778,7 +783,10 @@ int vocab_embedding_bwd_launch(const int32_t* ids, int64_t M, int64_t v, int h, 
     char* base = static_cast<char*>(scratch);
     int32_t *start = reinterpret_cast<int32_t*>(base), *counters = reinterpret_cast<int32_t*>(base + at.counters);
     Entry* sorted = reinterpret_cast<Entry*>(base + at.sorted);
-    launch_pdl(sort_tokens_kernel, dim3((unsigned)((v + BINS - 1) / BINS)), dim3(SORT_WARPS * 32), 0, stream, ids,
+    const int warps = static_cast<int>(std::min<int64_t>(std::max<int64_t>((M + 32 * SORT_LOADS - 1) / (32 * SORT_LOADS), BINS / 32),
+                                                         MAX_SORT_WARPS));
+    launch_pdl(sort_tokens_kernel, dim3((unsigned)((v + BINS - 1) / BINS)), dim3(warps * 32),
+               static_cast<size_t>(warps) * BINS * sizeof(int32_t), stream, ids,
                static_cast<long long>(M), static_cast<int>(v), sorted, start, counters,
                static_cast<long long>(at.parts * at.slices));
     const int rc = check("token sort kernel", err);
