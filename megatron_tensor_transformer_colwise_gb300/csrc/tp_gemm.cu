@@ -173,6 +173,7 @@ struct GemmParams {
     long long ldaux, n_half;
     void* out2;
     long long ldo2;
+    int seg_kb;                 // GEMM_TN: k-blocks that one accumulator sums
     int k_split, k_split2;      // GEMM_NN: first K rows read from mapB[1], mapB[2]
     int row_split, row_split2;  // GEMM_TN: first output rows written to out2, out3
     void* out3;
@@ -231,6 +232,18 @@ __device__ __forceinline__ void decode_tile(const GemmParams& p, int tile, int& 
     // Odd groups sweep the n-tiles backwards: a group starts on the weight
     // tiles the previous group ended on, which are still in L2.
     if (g & 1) nb = p.n_dec - 1 - nb;
+}
+
+// The next unit of work of a cluster: GEMM_TN takes a tile's K in segments of
+// seg_kb k-blocks, one after the other, everything else whole tiles.
+template <int MODE>
+__device__ __forceinline__ void next_unit(const GemmParams& p, int ncl, int& tile, int& seg) {
+    if (MODE == tpi::GEMM_TN && (seg + 1) * p.seg_kb < p.kb_per_shard) {
+        ++seg;
+    } else {
+        tile += ncl;
+        seg = 0;
+    }
 }
 
 // GEMM_MLP unit u of a cluster: colwise units first (all m-blocks of one
@@ -500,9 +513,11 @@ __device__ __forceinline__ void producer_loop(const GemmParams& p, uint32_t base
     uint32_t issued_mask = 0, last_parity = 0;
     bool ok = true;
     const int cid = blockIdx.x / CL, ncl = gridDim.x / CL;
-    for (int tile = cid; ok && tile < p.num_tiles; tile += ncl) {
+    for (int tile = cid, seg = 0; ok && tile < p.num_tiles; next_unit<MODE>(p, ncl, tile, seg)) {
         int s_grid, mb, nb;
         decode_tile(p, tile, s_grid, mb, nb);
+        const int kb0 = MODE == tpi::GEMM_TN ? seg * p.seg_kb : 0;
+        const int kb1 = MODE == tpi::GEMM_TN ? min(kb0 + p.seg_kb, p.kb_per_shard) : p.kb_per_shard;
         if (MC) nb = 2 * nb + pc;  // past the matrix when n_tiles is odd: B reads zeros
         const int arow = mb * C::TILE_M + static_cast<int>(prank) * BM + (MC ? pc * (BM / 2) : 0);
         const CUtensorMap* bmap[C::CHUNKS];
@@ -510,7 +525,7 @@ __device__ __forceinline__ void producer_loop(const GemmParams& p, uint32_t base
         if (!ROW) b_boxes<MODE, C::CHUNKS>(p, nb, static_cast<int>(prank) * C::CHUNKS, bmap, brow);
         for (int ks = 0; ok && ks < p.k_shards; ++ks) {
             const int shard = (MODE == tpi::GEMM_ROW_PARTIAL) ? s_grid : ks;
-            for (int kb = 0; kb < p.kb_per_shard; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 const uint32_t full = bar0 + 8 * stage, empty = bar0 + 8 * (C::STAGES + stage);
                 // MC: both pairs have consumed this stage (each pair's MMA
                 // commit arrives on every CTA's empty barrier).
@@ -696,7 +711,7 @@ __device__ __forceinline__ void mma_loop(const GemmParams& p, uint32_t base, uin
     bool ok = true;
     const int kblocks = p.k_shards * p.kb_per_shard;
     const int cid = blockIdx.x / CL, ncl = gridDim.x / CL;
-    for (int tile = cid; ok && tile < p.num_tiles; tile += ncl) {
+    for (int tile = cid, seg = 0; ok && tile < p.num_tiles; next_unit<MODE>(p, ncl, tile, seg)) {
         const uint32_t tfull = bar0 + 8 * (2 * C::STAGES + acc);
         const uint32_t tempty = bar0 + 8 * (2 * C::STAGES + 2 + acc);
         if (!mbar_wait(tempty, acc_phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
@@ -706,6 +721,7 @@ __device__ __forceinline__ void mma_loop(const GemmParams& p, uint32_t base, uin
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BNT;
         int nkb = kblocks;
+        if constexpr (MODE == tpi::GEMM_TN) nkb = min(p.seg_kb, kblocks - seg * p.seg_kb);
         if constexpr (MODE == tpi::GEMM_MLP)
             nkb = tile < p.mlp_col_units ? p.kb_per_shard : p.mlp_spp * p.mlp_kb_row;
         for (int kb = 0; kb < nkb; ++kb) {
@@ -1276,7 +1292,7 @@ __device__ __forceinline__ void epilogue_loop(const GemmParams& p, uint32_t bar0
     const int pc = MC ? static_cast<int>(rank >> 1) : 0;
     const uint32_t prank = MC ? (rank & 1u) : rank;
     const int cid = blockIdx.x / CL, ncl = gridDim.x / CL;
-    for (int tile = cid; tile < p.num_tiles; tile += ncl) {
+    for (int tile = cid, seg = 0; tile < p.num_tiles; next_unit<MODE>(p, ncl, tile, seg)) {
         int s_grid, mb, nb;
         decode_tile(p, tile, s_grid, mb, nb);
         if (MC) nb = 2 * nb + pc;  // past the matrix when n_tiles is odd: the column checks store nothing
@@ -1339,6 +1355,9 @@ __device__ __forceinline__ void epilogue_loop(const GemmParams& p, uint32_t bar0
             const int ybase = row0 - (which == 2 ? p.row_split2 : (which == 1 ? p.row_split : 0));
             const uint32_t sw_base = epi0 + static_cast<uint32_t>(warp - 2) * 4 * EPI_BOX_BYTES;
             const uint32_t srow = static_cast<uint32_t>(lane) * 128;
+            // A later segment is added to what the earlier ones left: in order,
+            // so that the roundings are the same every time.
+            if (seg && lane == 0) bulk_wait_group0();
 #pragma unroll 1
             for (int c = cb; c < cb + CPW; ++c) {
                 const int col0 = nb * BN + c * 32;
@@ -1356,7 +1375,7 @@ __device__ __forceinline__ void epilogue_loop(const GemmParams& p, uint32_t bar0
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && box_ok) {
-                    if (p.accumulate) tma_reduce_add_2d(&p.mapO[which], buf, col0, ybase);
+                    if (p.accumulate || seg) tma_reduce_add_2d(&p.mapO[which], buf, col0, ybase);
                     else tma_store_2d(&p.mapO[which], buf, col0, ybase);
                     bulk_commit_group();
                 }
@@ -1759,6 +1778,7 @@ int gemm_launch(const GemmArgs& a, cudaStream_t stream, std::string* err) {
         if (!make_map(&p.mapB[0], a.B0, 3, dB, sA, bB, err)) return TP_ERR_CUDA;
     } else if (a.mode == GEMM_BWD_ACT || a.mode == GEMM_NN || a.mode == GEMM_NN_PARTIAL || a.mode == GEMM_TN) {
         p.kb_per_shard = static_cast<int>((a.K + BK - 1) / BK);
+        p.seg_kb = a.k_seg > 0 ? static_cast<int>((a.k_seg + BK - 1) / BK) : std::max(p.kb_per_shard, 1);
         if (a.mode == GEMM_NN_PARTIAL) p.kb_per_shard = (p.kb_per_shard + a.k_pieces - 1) / a.k_pieces;
         p.k_shards = 1;
         const uint32_t box_mn[2] = {64, BK};  // 64 MN elements x 64 K rows

@@ -126,6 +126,10 @@ struct GemmArgs {
     int64_t ldo2 = 0;
     int64_t k_split = 0, k_split2 = 0;
     int k_pieces = 1;  // GEMM_NN_PARTIAL (B0 alone)
+    // GEMM_TN: rows of K that one tensor-core sum takes (0: all).  The sums of
+    // several are added in fp32, to nearest, where the tensor cores round towards
+    // zero at every step.
+    int64_t k_seg = 0;
     void* out3 = nullptr;
     int64_t ldo3 = 0;
     int64_t row_split = 0, row_split2 = 0;
