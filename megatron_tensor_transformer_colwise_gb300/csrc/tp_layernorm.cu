@@ -7,13 +7,22 @@
 //   dx     = dres + r (g - mean_j g_j - xh mean_j g_j xh_j),   g = dy gain
 //   dgain  = sum over rows of dy xh,   dbias = sum over rows of dy
 //
-// Both directions are bound by memory.  A row stays in the registers of W
-// warps (VPT 16-byte pieces a thread), so each input is read once and each
-// output written once; a CTA of THREADS holds THREADS / (32 W) rows at a time
-// and strides over the rows, with the gain and the bias kept in registers.
-// The weights' gradients are summed in registers over a CTA's rows, and a
-// second kernel adds the CTAs' sums in a fixed order: no atomics, so repeated
-// calls give the same bits.
+// Both directions have to move their rows once.  A CTA strides over the rows,
+// GROUPS of them at a time, each on W warps with VPT 16-byte pieces a thread; the
+// next rows are on their way to shared memory meanwhile (Ring), and the gain and
+// the bias lie there as fp32.  A row's statistics take one exchange between its
+// warps.  The weights' gradients are summed in registers over a CTA's rows, and a
+// second kernel adds the CTAs' sums in a fixed order: no atomics, so repeated calls
+// give the same bits.
+//
+// Measured (the bytes' time at the copy rate in brackets): forward 8192 x 4096
+// 23.8 us (19.8), 16384 x 768 10.3 (7.4), 2000 x 12288 23.5 (14.5); gradients 8192 x
+// 4096 43.8 (29.7), 2048 x 1024 9 to 11 (1.9), 3001 x 2568 with a residual 23.0 (9.1).
+// The forward kernel is at the memory's rate once it runs (16384 x 4096: 6.4 TB/s of
+// 268 MB), what is above that is the launch and the first rows.  The gradients' kernel
+// issues in half of all cycles with 16 warps on an SM (two sums of a column for every
+// value held leave no registers for more), and its weights' part costs 5 us: the
+// CTA's sums to memory, a launch, and the sum over 152 CTAs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -85,8 +85,13 @@ __global__ void __launch_bounds__(EMB_WARPS * 32) embedding_scaled_kernel(const 
 //     a part's border cuts leaves partial sums, and the last of its parts to
 //     arrive (a counter that the first launch cleared) adds them in order.
 // Parts of equal length keep a frequent word (in text, one token in ten is the
-// same one) from being one CTA's work.  With the partial sums added by a third
-// launch, 2048 tokens of 1024 over 32768 words took 42 us.
+// same one) from being one CTA's work.
+// Bound by the zeros' way to memory: 8192 tokens of 4096 over 128256 words 308 us
+// (2.1 GB of dE; 320 us at the rate of a copy), 2048 of 1024 over 32768 32 us (20.4),
+// of which the sorting launch is about 5 and a frequent word's last parts the end.
+// Added to dE instead: 60 us (28) and 15.  With one CTA a word the first took 1100
+// us, with the partial sums added by a third launch the second 42, with the zeros
+// written by the sorting kernel 40.
 
 // Sorting: a CTA owns BINS words and looks through all ids: it counts the
 // tokens of words below its own (its place in the order) and of each of its
