@@ -536,7 +536,8 @@ TP_API int tp_vocab_parallel_cross_entropy(const tp_bf16* logits, int64_t M, int
  * logits are; any other label outside [0, v) gives NaN in both.  Logits of -inf
  * (masked words) have probability 0; a row of nothing else, or one with NaN or
  * +inf, gives NaN.  The label's gradient and small losses come from the sum over
- * the other words, not from a difference.
+ * the other words, not from a difference.  A device-side wait that gives up (2 s)
+ * leaves NaN in the losses of the rows that it kept from being computed.
  * logits, dlogits: device [M][v] bf16, vocabulary-sharded like
  * tp_vocab_logits_forward's; dlogits may be logits.  dloss: device [M] fp32,
  * NULL = 1.  loss: device [M] fp32.  (v / t) % 8 == 0, M and v below 2^31; M may
@@ -545,7 +546,7 @@ TP_API int tp_vocab_parallel_cross_entropy_train(const tp_bf16* logits, int64_t 
                                                  const int32_t* labels, const float* dloss, float* loss,
                                                  tp_bf16* dlogits, void* stream);
 
-/* Bytes of workspace of tp_vocab_logits_backward.  Host-only. */
+/* Bytes of workspace of tp_vocab_logits_backward on the current device.  Host-only. */
 TP_API int tp_vocab_logits_backward_workspace_bytes(int64_t M, int64_t v, int32_t h, size_t* bytes);
 
 /* Gradients of tp_vocab_logits_forward:

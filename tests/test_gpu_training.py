@@ -142,6 +142,42 @@ def test_layernorm_backward(rows, h, kind):
     assert torch.equal(again[0], dx)
 
 
+# Every shape of a row's warps, rows that fill it and rows that do not, more rows than the CTAs hold at a time.
+@pytest.mark.parametrize("rows,h", [(3, 1536), (2, 1400), (2, 6144), (3, 6000), (2, 12288), (3, 10248), (5000, 520), (3100, 1032), (2500, 1536),
+                                    (2100, 2568), (1500, 4096), (1300, 5000), (1000, 8192), (400, 12288)])
+def test_layernorm_of_many_rows(rows, h):
+    x, gain, bias, dy, dres = (dev(a) for a in norm_inputs(rows, h, rows + 3 * h))
+    y, stats = empty(rows, h, dtype=torch.bfloat16), empty(2, rows)
+    tp.tp_layernorm_forward(x, rows, h, gain, bias, EPS, y, stats)
+    # The formulas in 64 bits on the GPU, tolerances as above.
+    X, G, B, D, R = (a.double() for a in (x, gain, bias, dy, dres))
+    mean = X.mean(1, keepdim=True)
+    rstd = 1 / ((X - mean).square().mean(1, keepdim=True) + EPS).sqrt()
+    xh = (X - mean) * rstd
+    ref = xh * G + B
+    dmean = 64 * U * X.abs().mean(1, keepdim=True)
+    drstd = 64 * U + 0.5 * (dmean * rstd) ** 2 + mean.abs() * 2 * U * rstd
+    inner = (xh * G).abs() * (drstd + 4 * U) + dmean * rstd * G.abs() + 2 * U * ref.abs()
+    assert ((y.double() - ref).abs() <= BF16 * ref.abs() + (1 + BF16) * inner).all()
+    assert ((stats[0].double() - mean[:, 0]).abs() <= dmean[:, 0]).all() and ((stats[1].double() / rstd[:, 0] - 1).abs() <= drstd[:, 0]).all()
+    g = D * G
+    gx = (g * xh).mean(1, keepdim=True)
+    rx = R + rstd * (g - g.mean(1, keepdim=True) - xh * gx)
+    terms = R.abs() + rstd * (g.abs() + g.abs().mean(1, keepdim=True) + xh.abs() * (g * xh).abs().mean(1, keepdim=True))
+    off = dmean * rstd + 2 * drstd + 64 * U
+    spread = rstd * dmean * rstd * (gx.abs() + g.abs().mean(1, keepdim=True) * xh.abs())
+    for st in (None, stats):
+        dx, dgain, dbias = run_norm_backward(x, gain, dy, dres, st, rows, h)
+        assert ((dx.double() - rx).abs() <= BF16 * rx.abs() + (1 + BF16) * (4 * off * terms + 4 * spread)).all()
+        assert ((dgain.double() - (D * xh).sum(0)).abs() <= 128 * U * (D * xh).abs().sum(0) + (off * D.abs() * (1 + xh.abs())).sum(0)).all()
+        assert ((dbias.double() - D.sum(0)).abs() <= 128 * U * D.abs().sum(0)).all()
+        same = run_norm_backward(x, gain, dy, dres, st, rows, h)
+        assert all(torch.equal(a, b) for a, b in zip(same, (dx, dgain, dbias)))
+    inplace = x.clone()
+    tp.tp_layernorm_forward(inplace, rows, h, gain, bias, EPS, inplace)
+    assert torch.equal(inplace, y)
+
+
 def test_layernorm_without_rows():
     g, b = dev(torch.ones(64)), dev(torch.ones(64))
     n = tp.tp_layernorm_backward_workspace_bytes(0, 64)
@@ -291,11 +327,11 @@ def test_embedding_beyond_32_bit_offsets():
     assert torch.equal(out, 2 * E[ids.long()])
 
 
-def test_embedding_backward_of_many_tokens():
+@pytest.mark.parametrize("M,v,h", [(70001, 3000, 64), (700001, 40, 8), (9000, 70000, 1032)])
+def test_embedding_backward_of_many_tokens(M, v, h):
     # More tokens than a word's part holds, half of them one word: against torch's sums in 64 bits.
-    M, v, h = 70001, 3000, 64
     ids, dOut = words(M, v, "text", 9), normal((M, h), 10)
-    ids[::2] = 1717
+    ids[::2] = 1717 % v
     dE = run_embedding_backward(dev(ids), v, dev(dOut), 1.0)
     at = dev(ids).long()
     ref = torch.zeros(v, h, dtype=torch.float64, device="cuda").index_add_(0, at, dev(dOut).double())
@@ -382,6 +418,37 @@ def test_loss_of_masked_logits():
     loss_close(z, labels, w.double().numpy(), loss, d)
     assert float(loss[1]) == 0 and not d[1].any() and float(loss[8]) == 0 and not d[8].any()
     assert float(loss[2]) == np.inf and d[3].isnan().all() and d[4].isnan().all() and d[5].isnan().all()
+
+
+@pytest.mark.parametrize("M,v", [(6000, 520), (1500, 16384), (700, 20000), (400, 50264), (160, 128256), (80, 200000)])
+def test_loss_of_many_rows(M, v):
+    # More rows than the clusters hold at a time, ignored and wrong labels among them, in runs and alone.
+    z = normal((M, v), M, 3.0)
+    g = torch.Generator().manual_seed(v)
+    labels = torch.randint(0, v, (M,), generator=g, dtype=torch.int32)
+    labels[torch.rand(M, generator=g) < 0.3] = -100
+    labels[M // 3 : M // 3 + M // 5] = -100
+    labels[torch.rand(M, generator=g) < 0.02] = v
+    labels[-1] = -100
+    w = torch.rand(M, generator=g)
+    loss, d = run_loss(dev(z), dev(labels), dev(w))
+    loss_close(z, labels, w.double().numpy(), loss, d)
+    # The same bits in place, captured and replayed, and beside another call on another stream.
+    own, other = dev(z).clone(), dev(z).clone()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    lab, up = dev(labels), dev(w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run_loss(own, lab, up, out=own)[0]
+    assert torch.equal(own, dev(z))
+    torch.cuda.synchronize()
+    for stream, call in ((a, graph.replay), (b, lambda: run_loss(other, lab, up, out=other))):
+        with torch.cuda.stream(stream):
+            call()
+    torch.cuda.synchronize()
+    for x in (own, other):
+        assert torch.equal(x.view(torch.int16), d.view(torch.int16))
+    assert torch.equal(held.view(torch.int32), loss.view(torch.int32))
 
 
 @pytest.mark.parametrize("t", [1, 3])
@@ -484,6 +551,25 @@ def test_output_gradients(M, v, h, t):
     old = normal((v, h), 4, 1.0, torch.float32)
     more = run_output(dev(H), dev(W), dev(d), dW=dev(old).clone(), accumulate=True, t=t)[1]
     within(host64(more), host64(old) + host64(dW), U * np.abs(host64(old) + host64(dW)), "dW added")
+
+
+@pytest.mark.parametrize("M,v,h", [(2500, 520, 264), (4100, 1032, 128), (1025, 264, 520)])
+def test_output_gradients_of_many_tokens(M, v, h):
+    # Several sums of 1024 tokens each, added to what is there, the same bits every time.
+    H, W, d, old = normal((M, h), 1), normal((v, h), 2), normal((M, v), 3), normal((v, h), 4, 30.0, torch.float32)
+    x = [dev(a) for a in (H, W, d)]
+    dW = run_output(*x)[1]
+    D, Hd = x[2].double(), x[0].double()
+    ref, size = D.T @ Hd, D.abs().T @ Hd.abs()
+    bound = (1024 / 16 + 16) * 2.0 ** -22 * size + (M / 1024 + 1) * U * (size + dev(old).double().abs())
+    assert ((dW.double() - ref).abs() <= bound).all()
+    more = run_output(*x, dW=dev(old).clone(), accumulate=True)[1]
+    assert ((more.double() - ref - dev(old).double()).abs() <= bound).all()
+    for _ in range(5):
+        assert torch.equal(run_output(*x)[1], dW) and torch.equal(run_output(*x, dW=dev(old).clone(), accumulate=True)[1], more)
+    # Whole numbers: exact, whatever the segments.
+    Hi, di = ((torch.randint(-3, 4, a.shape, generator=torch.Generator().manual_seed(5))).bfloat16() for a in (H, d))
+    assert torch.equal(run_output(dev(Hi), x[1], dev(di))[1].double(), dev(di).double().T @ dev(Hi).double())
 
 
 def test_output_gradients_integers_bit_exact():
