@@ -160,7 +160,7 @@ __device__ __forceinline__ void chunk_sum(const void* src, long long from, long 
 
 template <int CAP>
 __global__ void __launch_bounds__(THREADS, CTAS) grad_sum_kernel(const __grid_constant__ Tensors<CAP> p,
-                                                                 double* __restrict__ sums) {
+                                                                 double* sums) {
     constexpr int WARPS = THREADS / 32;
     __shared__ Sum red[WARPS];
     __shared__ double all[THREADS];
@@ -252,15 +252,21 @@ __device__ __forceinline__ double inverse_root(double s) {
 // from the last to the first: the last ones that the sums read are in L2.
 template <int CAP>
 __global__ void __launch_bounds__(THREADS, CTAS) grad_scale_kernel(const __grid_constant__ Tensors<CAP> p,
-                                                                   const double* __restrict__ sums, int n_sums,
+                                                                   const double* sums, int n_sums,
                                                                    float max_norm, float* norm) {
     __shared__ double factor;
     pdl_trigger();
     pdl_wait();
     if (threadIdx.x < 32) {
         double s = 0.0;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < n_sums; i += 32) s += sums[i];
+        constexpr int LOADS = 20;  // a launch's sums at once, or nearly
+        for (int i0 = threadIdx.x; i0 < n_sums; i0 += 32 * LOADS) {
+            double v[LOADS];
+#pragma unroll
+            for (int k = 0; k < LOADS; ++k) v[k] = i0 + 32 * k < n_sums ? sums[i0 + 32 * k] : 0.0;
+#pragma unroll
+            for (int k = 0; k < LOADS; ++k) s += v[k];
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (threadIdx.x == 0) {

@@ -99,12 +99,13 @@ __device__ __forceinline__ void weights8(const float4* from, int nv, int v, uint
 
 // A row's pieces: W warps, VPT a thread, nv in all; this thread's are first,
 // first + 32 W, ...  count(w): the values that warp w holds.  FULL: rows of just
-// as many pieces as there are places.
+// as many pieces as there are places; with up to four a thread, all but the last
+// are there in any case (for_fill sees to it).
 template <int W, int VPT, bool FULL>
 struct Pieces {
     int first, nv;
     __device__ __forceinline__ explicit Pieces(int h) : first(threadIdx.x % (32 * W)), nv(h >> 3) {}
-    __device__ __forceinline__ bool has(int i) const { return FULL || first + i * 32 * W < nv; }
+    __device__ __forceinline__ bool has(int i) const { return FULL || (VPT <= 4 && i + 1 < VPT) || first + i * 32 * W < nv; }
     __device__ __forceinline__ int at(int i) const { return first + i * 32 * W; }
     __device__ __forceinline__ float count(int w) const {
         if (FULL) return 256.0f * VPT;
@@ -219,8 +220,8 @@ struct Forward {
 
 template <int W, int VPT, bool FULL>
 __global__ void __launch_bounds__(Forward<W, VPT>::THREADS, Forward<W, VPT>::CTAS)
-    layernorm_kernel(const __nv_bfloat16* x, long long rows, int h, const __nv_bfloat16* __restrict__ gain,
-                     const __nv_bfloat16* __restrict__ bias, float eps, __nv_bfloat16* y, float* __restrict__ stats) {
+    layernorm_kernel(const __nv_bfloat16* x, long long rows, int h, const __nv_bfloat16* gain,
+                     const __nv_bfloat16* bias, float eps, __nv_bfloat16* y, float* stats) {
     using C = Forward<W, VPT>;
     __shared__ float shared[C::GROUPS * 2 * W * 2];
     extern __shared__ uint4 dynamic[];
@@ -296,9 +297,9 @@ struct Backward {
 //   sum g xh = r sum_w (sum g (x - mean_w) + (mean_w - mu) sum g).
 template <int W, int VPT, bool FULL>
 __global__ void __launch_bounds__(Backward<W, VPT>::THREADS, 1)
-    layernorm_bwd_kernel(const __nv_bfloat16* x, long long rows, int h, const __nv_bfloat16* __restrict__ gain, float eps,
-                         const float* __restrict__ stats, const __nv_bfloat16* dy, const __nv_bfloat16* dres,
-                         __nv_bfloat16* dx, float* __restrict__ parts) {
+    layernorm_bwd_kernel(const __nv_bfloat16* x, long long rows, int h, const __nv_bfloat16* gain, float eps,
+                         const float* stats, const __nv_bfloat16* dy, const __nv_bfloat16* dres,
+                         __nv_bfloat16* dx, float* parts) {
     using C = Backward<W, VPT>;
     constexpr bool HOLD = C::HOLD;
     __shared__ float shared[C::GROUPS * 2 * W * 4];
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(Backward<W, VPT>::THREADS, 1)
 // warps that take every JOIN_WARPS-th part, joined in order.
 constexpr int JOIN_WARPS = 16;
 
-__global__ void __launch_bounds__(JOIN_WARPS * 32) layernorm_join_kernel(const float* __restrict__ parts, int n, int h,
+__global__ void __launch_bounds__(JOIN_WARPS * 32) layernorm_join_kernel(const float* parts, int n, int h,
                                                                         float* dgain, float* dbias, int accumulate) {
     pdl_trigger();
     pdl_wait();
@@ -450,9 +451,18 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) layernorm_join_kernel(const f
     if (!out) return;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    if (c < h) {
-#pragma unroll 8
-        for (int k = w; k < n; k += JOIN_WARPS) s += parts[(static_cast<long long>(k) * 2 + blockIdx.y) * h + c];
+    // All of a warp's loads at once: with eight and the rest one by one the rest
+    // waited for memory as long as the eight, each.
+    constexpr int LOADS = 10;
+    for (int k0 = w; c < h && k0 < n; k0 += JOIN_WARPS * LOADS) {
+        float v[LOADS];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int k = k0 + i * JOIN_WARPS;
+            v[i] = k < n ? parts[(static_cast<long long>(k) * 2 + blockIdx.y) * h + c] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) s += v[i];
     }
     sum[w][lane] = s;
     __syncthreads();
@@ -488,9 +498,10 @@ int allow_shared(std::string* err) {
 
 template <int N>
 using Int = std::integral_constant<int, N>;
-template <int W, int VPT, int NV, typename F>
+// Rows of LEAST to NV pieces.
+template <int W, int VPT, int LEAST, int NV, typename F>
 int for_fill(int nv, F&& f) {
-    static_assert(NV == 32 * W * VPT, "");
+    static_assert(NV == 32 * W * VPT && (VPT > 4 || LEAST >= 32 * W * (VPT - 1)), "");
     return nv == NV ? f(Int<W>(), Int<VPT>(), std::true_type()) : f(Int<W>(), Int<VPT>(), std::false_type());
 }
 
@@ -501,18 +512,18 @@ int for_fill(int nv, F&& f) {
 template <typename F>
 int for_forward(int h, F&& f) {
     const int nv = h / 8;
-    if (nv <= 32) return for_fill<1, 1, 32>(nv, f);
-    if (nv <= 64) return for_fill<1, 2, 64>(nv, f);
-    if (nv <= 96) return for_fill<1, 3, 96>(nv, f);
-    if (nv <= 128) return for_fill<1, 4, 128>(nv, f);
-    if (nv <= 192) return for_fill<2, 3, 192>(nv, f);
-    if (nv <= 256) return for_fill<2, 4, 256>(nv, f);
-    if (nv <= 384) return for_fill<4, 3, 384>(nv, f);
-    if (nv <= 512) return for_fill<4, 4, 512>(nv, f);
-    if (nv <= 768) return for_fill<8, 3, 768>(nv, f);
-    if (nv <= 1024) return for_fill<8, 4, 1024>(nv, f);
-    if (nv <= 1536) return for_fill<8, 6, 1536>(nv, f);
-    return for_fill<8, 8, 2048>(nv, f);
+    if (nv <= 32) return for_fill<1, 1, 0, 32>(nv, f);
+    if (nv <= 64) return for_fill<1, 2, 33, 64>(nv, f);
+    if (nv <= 96) return for_fill<1, 3, 65, 96>(nv, f);
+    if (nv <= 128) return for_fill<1, 4, 97, 128>(nv, f);
+    if (nv <= 192) return for_fill<2, 3, 129, 192>(nv, f);
+    if (nv <= 256) return for_fill<2, 4, 193, 256>(nv, f);
+    if (nv <= 384) return for_fill<4, 3, 257, 384>(nv, f);
+    if (nv <= 512) return for_fill<4, 4, 385, 512>(nv, f);
+    if (nv <= 768) return for_fill<8, 3, 513, 768>(nv, f);
+    if (nv <= 1024) return for_fill<8, 4, 769, 1024>(nv, f);
+    if (nv <= 1536) return for_fill<8, 6, 1025, 1536>(nv, f);
+    return for_fill<8, 8, 1537, 2048>(nv, f);
 }
 // Backward: two pieces a thread, three where they fill the places better (3001 x
 // 2568: 23.0 us on four warps of three pieces, 24.2 on eight of two; 4096 x 5000:
@@ -520,16 +531,16 @@ int for_forward(int h, F&& f) {
 template <typename F>
 int for_backward(int h, F&& f) {
     const int nv = h / 8;
-    if (nv <= 32) return for_fill<1, 1, 32>(nv, f);
-    if (nv <= 64) return for_fill<1, 2, 64>(nv, f);
-    if (nv <= 128) return for_fill<2, 2, 128>(nv, f);
-    if (nv <= 256) return for_fill<4, 2, 256>(nv, f);
-    if (nv <= 384) return for_fill<4, 3, 384>(nv, f);
-    if (nv <= 512) return for_fill<8, 2, 512>(nv, f);
-    if (nv <= 768) return for_fill<8, 3, 768>(nv, f);
-    if (nv <= 1024) return for_fill<16, 2, 1024>(nv, f);
-    if (nv <= 1536) return for_fill<16, 3, 1536>(nv, f);
-    return for_fill<16, 4, 2048>(nv, f);
+    if (nv <= 32) return for_fill<1, 1, 0, 32>(nv, f);
+    if (nv <= 64) return for_fill<1, 2, 33, 64>(nv, f);
+    if (nv <= 128) return for_fill<2, 2, 65, 128>(nv, f);
+    if (nv <= 256) return for_fill<4, 2, 129, 256>(nv, f);
+    if (nv <= 384) return for_fill<4, 3, 257, 384>(nv, f);
+    if (nv <= 512) return for_fill<8, 2, 385, 512>(nv, f);
+    if (nv <= 768) return for_fill<8, 3, 513, 768>(nv, f);
+    if (nv <= 1024) return for_fill<16, 2, 769, 1024>(nv, f);
+    if (nv <= 1536) return for_fill<16, 3, 1025, 1536>(nv, f);
+    return for_fill<16, 4, 1537, 2048>(nv, f);
 }
 
 }  // namespace

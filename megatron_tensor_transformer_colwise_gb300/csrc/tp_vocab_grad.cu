@@ -49,9 +49,9 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // lanes waited for memory (8192 x 4096: 19.7 us).
 constexpr int EMB_WARPS = 4, EMB_LOADS = 8;
 
-__global__ void __launch_bounds__(EMB_WARPS * 32) embedding_scaled_kernel(const int32_t* __restrict__ ids, long long M,
-                                                                         const __nv_bfloat16* __restrict__ E, long long v,
-                                                                         int h, float scale, __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(EMB_WARPS * 32) embedding_scaled_kernel(const int32_t* ids, long long M,
+                                                                         const __nv_bfloat16* E, long long v,
+                                                                         int h, float scale, __nv_bfloat16* out) {
     pdl_trigger();
     pdl_wait();
     const long long m = static_cast<long long>(blockIdx.x) * EMB_WARPS + (threadIdx.x >> 5);
@@ -110,7 +110,7 @@ struct Entry {
 // Calls f(id, position) for this lane's tokens of [from, to), 32 consecutive
 // ones a warp and call; -1 past the end.
 template <typename F>
-__device__ __forceinline__ void for_ids(const int32_t* __restrict__ ids, long long from, long long to, F&& f) {
+__device__ __forceinline__ void for_ids(const int32_t* ids, long long from, long long to, F&& f) {
     const int lane = threadIdx.x & 31;
     for (long long at = from; at < to; at += 32 * SORT_LOADS) {
         int32_t id[SORT_LOADS];
@@ -125,9 +125,9 @@ __device__ __forceinline__ void for_ids(const int32_t* __restrict__ ids, long lo
     }
 }
 
-__global__ void __launch_bounds__(MAX_SORT_WARPS * 32) sort_tokens_kernel(const int32_t* __restrict__ ids, long long M, int v,
-                                                                     Entry* __restrict__ sorted, int32_t* __restrict__ start,
-                                                                     int32_t* __restrict__ counters, long long n_counters) {
+__global__ void __launch_bounds__(MAX_SORT_WARPS * 32) sort_tokens_kernel(const int32_t* ids, long long M, int v,
+                                                                     Entry* sorted, int32_t* start,
+                                                                     int32_t* counters, long long n_counters) {
     extern __shared__ int32_t counts[];  // [warps][BINS]
     int32_t(*count)[BINS] = reinterpret_cast<int32_t(*)[BINS]>(counts);
     __shared__ int32_t below[MAX_SORT_WARPS], sums[BINS / 32];
@@ -210,8 +210,8 @@ __device__ __forceinline__ void store_sum(float* row, int c, const float (&s)[8]
 // few enough for `from` to hold where their tokens start.
 constexpr int CLEAR_BYTES = 65536, MAX_CLEAR = MAX_PART;  // of a CTA: bytes about, words at most
 
-__device__ __forceinline__ void clear_words(const int32_t* __restrict__ start, long long first, int words, int h,
-                                            float* __restrict__ dE, int32_t* from) {
+__device__ __forceinline__ void clear_words(const int32_t* start, long long first, int words, int h,
+                                            float* dE, int32_t* from) {
     for (int k = threadIdx.x; k <= words; k += blockDim.x) from[k] = start[first + k];
     __syncthreads();
     // Short rows side by side, long ones by all threads.
@@ -228,10 +228,10 @@ __device__ __forceinline__ void clear_words(const int32_t* __restrict__ start, l
 // columns each; those behind them: zeros for clear_rows words.  A word that
 // began before the part leaves its sum in parts[a][0], one that began here and
 // goes on behind the part in parts[a][1], all others are done.
-__global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const Entry* __restrict__ sorted,
-                                                                   const int32_t* __restrict__ start, int v, int part,
+__global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const Entry* sorted,
+                                                                   const int32_t* start, int v, int part,
                                                                    long long n_parts, int slices, int clear_rows, int h,
-                                                                   float scale, const __nv_bfloat16* __restrict__ dOut,
+                                                                   float scale, const __nv_bfloat16* dOut,
                                                                    float* dE, int accumulate, float* parts,
                                                                    int32_t* counters) {
     __shared__ Entry mine[MAX_PART + 2];  // with the neighbours of both ends
@@ -303,11 +303,20 @@ __global__ void __launch_bounds__(SUM_THREADS) embedding_sum_kernel(const Entry*
         if (!last || !in) continue;
         __threadfence();
         float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (long long b = first; b <= past; ++b) {
-            const float4* p = reinterpret_cast<const float4*>(parts + (2 * b + (b == first)) * h) + 2 * c;
-            const float4 x = __ldcg(p), y = __ldcg(p + 1);
-            t[0] += x.x, t[1] += x.y, t[2] += x.z, t[3] += x.w, t[4] += y.x, t[5] += y.y, t[6] += y.z, t[7] += y.w;
+        for (long long b0 = first; b0 <= past; b0 += SUM_LOADS) {
+            float4 x[SUM_LOADS], y[SUM_LOADS];
+#pragma unroll
+            for (int k = 0; k < SUM_LOADS; ++k) {
+                const long long b = b0 + k;
+                const float4* p = reinterpret_cast<const float4*>(parts + (2 * b + (b == first)) * h) + 2 * c;
+                x[k] = b <= past ? __ldcg(p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                y[k] = b <= past ? __ldcg(p + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < SUM_LOADS; ++k) {
+                t[0] += x[k].x, t[1] += x[k].y, t[2] += x[k].z, t[3] += x[k].w;
+                t[4] += y[k].x, t[5] += y[k].y, t[6] += y[k].z, t[7] += y[k].w;
+            }
         }
         store_sum(dE + static_cast<long long>(word) * h, c, t, scale, accumulate);
     }
@@ -362,8 +371,8 @@ __device__ __forceinline__ uint32_t fill_of(int label) { return label == -100 ? 
 constexpr int LOSS_THREADS = 512;
 
 __global__ void __launch_bounds__(LOSS_THREADS) loss_long_kernel(const __nv_bfloat16* logits, int v,
-                                                                 const int32_t* __restrict__ labels,
-                                                                 const float* __restrict__ dloss, float* __restrict__ loss,
+                                                                 const int32_t* labels,
+                                                                 const float* dloss, float* loss,
                                                                  __nv_bfloat16* dlogits) {
     __shared__ MS red[LOSS_THREADS / 32];
     __shared__ float label_z;
@@ -517,9 +526,9 @@ struct Power {
 
 __global__ void __launch_bounds__(LOSS_ROW_THREADS, LOSS_CTAS) loss_kernel(const __nv_bfloat16* logits, long long M, int v,
                                                                            int per, int ranks,
-                                                                           const int32_t* __restrict__ labels,
-                                                                           const float* __restrict__ dloss,
-                                                                           float* __restrict__ loss, __nv_bfloat16* dlogits) {
+                                                                           const int32_t* labels,
+                                                                           const float* dloss,
+                                                                           float* loss, __nv_bfloat16* dlogits) {
     __shared__ MS slots[LOSS_SLOTS][LOSS_RANKS * LOSS_ROW_THREADS / 32 + 1];  // the warps', the label's
     __shared__ __align__(8) uint64_t arrived[LOSS_SLOTS];
     __shared__ int abort_flag, no_abort;
