@@ -51,10 +51,10 @@ __device__ __forceinline__ void add_bf16x8(float (&acc)[8], const uint4& v) {
 // out[e] = sum_i P[i][e] (+ bias[e % h]) (+ residual[e]); T known at compile
 // time (0 = runtime t).
 template <int T, bool F32>
-__global__ void __launch_bounds__(RED_THREADS) reduce_kernel(const void* __restrict__ partials, int t,
+__global__ void __launch_bounds__(RED_THREADS) reduce_kernel(const void* partials, int t,
                                                              long long n, int h,
-                                                             const __nv_bfloat16* __restrict__ bias,
-                                                             const __nv_bfloat16* __restrict__ residual,
+                                                             const __nv_bfloat16* bias,
+                                                             const __nv_bfloat16* residual,
                                                              __nv_bfloat16* out) {
     pdl_trigger();
     pdl_wait();
@@ -137,9 +137,9 @@ __device__ __forceinline__ long long sp_out_row(long long row, long long sp_batc
 }
 
 template <bool HAS_P, bool F32>
-__global__ void __launch_bounds__(ROW_THREADS) row_kernel(const void* __restrict__ partials, int t,
+__global__ void __launch_bounds__(ROW_THREADS) row_kernel(const void* partials, int t,
                                                           long long n, int h,
-                                                          const __nv_bfloat16* __restrict__ src,
+                                                          const __nv_bfloat16* src,
                                                           __nv_bfloat16* h1_out,
                                                           __nv_bfloat16* xn_out, float eps,
                                                           long long sp_batch, long long sp_seq,
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(ROW_THREADS) row_kernel(const void* __restrict
 // loads; also clears the next norm's accumulator row.
 constexpr int SS_WARPS = 8;
 
-__global__ void __launch_bounds__(SS_WARPS * 32) row_sumsq_kernel(const __nv_bfloat16* __restrict__ x,
+__global__ void __launch_bounds__(SS_WARPS * 32) row_sumsq_kernel(const __nv_bfloat16* x,
                                                                   long long rows, int h, float* ss,
                                                                   float* zero) {
     pdl_trigger();
@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(SS_WARPS * 32) row_sumsq_kernel(const __nv_bfl
 constexpr int AG_WARPS = 8;
 
 __global__ void __launch_bounds__(AG_WARPS * 32) sp_all_gather_kernel(
-    const __nv_bfloat16* __restrict__ sp, long long rows, int h, long long batch, long long seq,
-    int t, __nv_bfloat16* __restrict__ full) {
+    const __nv_bfloat16* sp, long long rows, int h, long long batch, long long seq,
+    int t, __nv_bfloat16* full) {
     pdl_trigger();
     pdl_wait();
     const long long row = static_cast<long long>(blockIdx.x) * AG_WARPS + (threadIdx.x >> 5);
@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(AG_WARPS * 32) sp_all_gather_kernel(
 // backward uses it as the reduce-scatter of dX, whose sum over the shards the
 // fused backward GEMMs already hold ("텐서 병렬화", "시퀀스 병렬화").
 __global__ void __launch_bounds__(AG_WARPS * 32) sp_split_kernel(
-    const __nv_bfloat16* __restrict__ full, long long rows, int h, long long batch, long long seq,
-    int t, __nv_bfloat16* __restrict__ sp) {
+    const __nv_bfloat16* full, long long rows, int h, long long batch, long long seq,
+    int t, __nv_bfloat16* sp) {
     pdl_trigger();
     pdl_wait();
     const long long row = static_cast<long long>(blockIdx.x) * AG_WARPS + (threadIdx.x >> 5);
@@ -345,11 +345,11 @@ int check_launch(const char* what, std::string* err) {
 constexpr int RB_THREADS = 128;
 
 template <int VPT>
-__global__ void __launch_bounds__(RB_THREADS) rmsnorm_bwd_kernel(const __nv_bfloat16* __restrict__ x,
-                                                                const __nv_bfloat16* __restrict__ g,
-                                                                const __nv_bfloat16* __restrict__ res,
+__global__ void __launch_bounds__(RB_THREADS) rmsnorm_bwd_kernel(const __nv_bfloat16* x,
+                                                                const __nv_bfloat16* g,
+                                                                const __nv_bfloat16* res,
                                                                 int h, float eps,
-                                                                __nv_bfloat16* __restrict__ out) {
+                                                                __nv_bfloat16* out) {
     pdl_trigger();
     pdl_wait();
     __shared__ float red[2][RB_THREADS / 32];
@@ -425,9 +425,9 @@ __global__ void __launch_bounds__(RB_THREADS) rmsnorm_bwd_kernel(const __nv_bflo
 // so repeated calls give identical bits.
 constexpr int CS_X = 4, CS_Y = 128;
 
-__global__ void __launch_bounds__(CS_X * CS_Y) colsum_kernel(const __nv_bfloat16* __restrict__ x,
+__global__ void __launch_bounds__(CS_X * CS_Y) colsum_kernel(const __nv_bfloat16* x,
                                                             long long rows, int h,
-                                                            float* __restrict__ out, int accumulate) {
+                                                            float* out, int accumulate) {
     pdl_trigger();
     pdl_wait();
     __shared__ float part[CS_Y][CS_X * 8 + 1];

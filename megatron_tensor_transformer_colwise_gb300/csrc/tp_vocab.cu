@@ -31,7 +31,7 @@ namespace {
 
 using namespace tpk;
 
-constexpr int EMB_WARPS = 8;
+constexpr int EMB_WARPS = 4, EMB_LOADS = 8;
 constexpr int CE_THREADS = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -50,10 +50,11 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
     return v;
 }
 
-// One warp per token: copy row E[id] (16-byte vectors), or zeros.
+// One warp per token: copy row E[id] (16-byte vectors), or zeros; EMB_LOADS
+// vectors a lane are read before the first is stored.
 __global__ void __launch_bounds__(EMB_WARPS * 32) vocab_embedding_kernel(
-    const int32_t* __restrict__ ids, long long M, const __nv_bfloat16* __restrict__ E, long long v,
-    int h, __nv_bfloat16* __restrict__ out) {
+    const int32_t* ids, long long M, const __nv_bfloat16* E, long long v,
+    int h, __nv_bfloat16* out) {
     pdl_trigger();
     pdl_wait();
     const long long m = static_cast<long long>(blockIdx.x) * EMB_WARPS + (threadIdx.x >> 5);
@@ -63,7 +64,15 @@ __global__ void __launch_bounds__(EMB_WARPS * 32) vocab_embedding_kernel(
     const bool owned = id >= 0 && id < v;  // some shard owns it
     const uint4* src = reinterpret_cast<const uint4*>(E + (owned ? id : 0) * h);
     uint4* dst = reinterpret_cast<uint4*>(out + m * h);
-    for (int c = lane; c < (h >> 3); c += 32) dst[c] = owned ? src[c] : make_uint4(0, 0, 0, 0);
+    const int nv = owned ? h >> 3 : 0;
+    for (int c = lane; c < (h >> 3); c += 32 * EMB_LOADS) {
+        uint4 u[EMB_LOADS];
+#pragma unroll
+        for (int k = 0; k < EMB_LOADS; ++k) u[k] = c + 32 * k < nv ? src[c + 32 * k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < EMB_LOADS; ++k)
+            if (c + 32 * k < (h >> 3)) dst[c + 32 * k] = u[k];
+    }
 }
 
 // Online (max, sum of 2^(x - max)) pair in the log2 domain.
@@ -79,8 +88,8 @@ __device__ __forceinline__ MS ms_merge(MS a, MS b) {
 
 // One CTA per (token, shard): the shard's statistics of its logits slice.
 __global__ void __launch_bounds__(CE_THREADS) ce_shard_stats_kernel(
-    const __nv_bfloat16* __restrict__ logits, long long M, long long v, int t,
-    const int32_t* __restrict__ labels, float* __restrict__ stats) {
+    const __nv_bfloat16* logits, long long M, long long v, int t,
+    const int32_t* labels, float* stats) {
     pdl_trigger();
     pdl_wait();
     __shared__ MS red[CE_THREADS / 32];
@@ -128,8 +137,8 @@ __global__ void __launch_bounds__(CE_THREADS) ce_shard_stats_kernel(
 }
 
 // One thread per token: combine the t shards' (max, sum, target).
-__global__ void ce_combine_kernel(const float* __restrict__ stats, long long M, long long v, int t,
-                                  const int32_t* __restrict__ labels, float* __restrict__ loss) {
+__global__ void ce_combine_kernel(const float* stats, long long M, long long v, int t,
+                                  const int32_t* labels, float* loss) {
     pdl_trigger();
     pdl_wait();
     const long long m = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
