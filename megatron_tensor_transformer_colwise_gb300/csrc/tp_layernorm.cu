@@ -17,7 +17,7 @@
 //
 // Measured (the bytes' time at the copy rate in brackets): forward 8192 x 4096
 // 23.8 us (19.8), 16384 x 768 10.3 (7.4), 2000 x 12288 23.5 (14.5); gradients 8192 x
-// 4096 43.8 (29.7), 2048 x 1024 9 to 11 (1.9), 3001 x 2568 with a residual 23.0 (9.1).
+// 4096 43.8 (29.7), 2048 x 1024 9 to 11 (1.9), 3001 x 2568 with a residual 22.2 (9.1).
 // The forward kernel is at the memory's rate once it runs (16384 x 4096: 6.4 TB/s of
 // 268 MB), what is above that is the launch and the first rows.  The gradients' kernel
 // issues in half of all cycles with 16 warps on an SM (two sums of a column for every

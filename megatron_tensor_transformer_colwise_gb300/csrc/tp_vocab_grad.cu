@@ -87,9 +87,9 @@ __global__ void __launch_bounds__(EMB_WARPS * 32) embedding_scaled_kernel(const 
 // Parts of equal length keep a frequent word (in text, one token in ten is the
 // same one) from being one CTA's work.
 // Bound by the zeros' way to memory: 8192 tokens of 4096 over 128256 words 308 us
-// (2.1 GB of dE; 320 us at the rate of a copy), 2048 of 1024 over 32768 32 us (20.4),
+// (2.1 GB of dE; 320 us at the rate of a copy), 2048 of 1024 over 32768 29 us (20.4),
 // of which the sorting launch is about 5 and a frequent word's last parts the end.
-// Added to dE instead: 60 us (28) and 15.  With one CTA a word the first took 1100
+// Added to dE instead: 65 us (28) and 15.  With one CTA a word the first took 1100
 // us, with the partial sums added by a third launch the second 42, with the zeros
 // written by the sorting kernel 40.
 
