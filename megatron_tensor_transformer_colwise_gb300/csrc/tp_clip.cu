@@ -8,7 +8,7 @@
 // sizes travel in the kernels' parameters, so nothing is copied to the device
 // before a call and a captured call is complete by itself.
 //
-// Both passes are bound by memory: 218 million fp32 gradients 404 us, where reading
+// Both passes are bound by memory: 218 million fp32 gradients 395 us, where reading
 // them twice and writing them once takes 386 at the copy rate (the sum alone 6.1
 // TB/s, the second pass 6.6); 8.4 million 18.4 us, where the second pass reads from
 // L2, of which two launches and the sums' way from one to the other are about 8.
@@ -28,6 +28,10 @@ using namespace tpk;
 
 constexpr int THREADS = 256, CTAS = 4;  // CTAs an SM
 constexpr int CHUNK = 8192;       // elements that a CTA takes at a time
+// Chunks at the end (half of L2) that the sums leave there for the second pass, all
+// others giving way first: 218 million gradients 395 us, 400 without, 398 with half
+// as many.
+constexpr int KEEP = 2000;
 constexpr int MAX_GRID = 2048;    // CTAs of a launch, and the sums kept for it
 constexpr int FEW = 32, MANY = 512;  // tensors of a launch
 
@@ -109,7 +113,7 @@ struct Sum {
 // Adds this thread's part of a chunk's sum of squares to sum, or, where it is out
 // of sum's range, to far.
 template <bool BF16>
-__device__ __forceinline__ void chunk_sum(const void* src, long long from, long long to, Sum& sum, double& far) {
+__device__ __forceinline__ void chunk_sum(const void* src, long long from, long long to, bool keep, Sum& sum, double& far) {
     constexpr int N = BF16 ? 8 : 4, P = BF16 ? PIECES / 2 : PIECES;
     const uint4* at = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + from * (16 / N));
     const int pieces = static_cast<int>((to - from) / N);
@@ -117,7 +121,7 @@ __device__ __forceinline__ void chunk_sum(const void* src, long long from, long 
 #pragma unroll
     for (int k = 0; k < P; ++k) {
         const int v = threadIdx.x + k * THREADS;
-        u[k] = v < pieces ? at[v] : make_uint4(0u, 0u, 0u, 0u);
+        u[k] = v < pieces ? (keep ? at[v] : __ldcs(at + v)) : make_uint4(0u, 0u, 0u, 0u);
     }
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t any = 0;
@@ -171,8 +175,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) grad_sum_kernel(const __grid_co
     for (long long chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
         const Tensor& t = tensor_of(p, chunk);
         const long long from = (chunk - t.first) * CHUNK, to = min(from + CHUNK, t.n);
-        if (t.bf16) chunk_sum<true>(t.src, from, to, sum, far);
-        else chunk_sum<false>(t.src, from, to, sum, far);
+        const bool keep = chunk >= p.chunks - KEEP;
+        if (t.bf16) chunk_sum<true>(t.src, from, to, keep, sum, far);
+        else chunk_sum<false>(t.src, from, to, keep, sum, far);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
