@@ -551,13 +551,15 @@ TP_API int tp_vocab_logits_backward_workspace_bytes(int64_t M, int64_t v, int32_
 
 /* Gradients of tp_vocab_logits_forward:
  *   dH = sum_i dlogits_i W_i   (f's all-reduce: the sum over shards runs inside
- *        one accumulator),     dW_i = dlogits_i^T H  (rows of shard i).
+ *        one accumulator, or in parts of the vocabulary that are added in order
+ *        where dH is small),   dW_i = dlogits_i^T H  (rows of shard i).
  * H: device [M][h], W: [v][h], dlogits: [M][v], dH: [M][h], all bf16; dW: device
  * [v][h] fp32, overwritten, or added to when accumulate != 0 (a weight that the
  * embedding shares gets both gradients that way).  Either of dH and dW may be
  * NULL.  M may be 0 (dW is cleared then unless accumulate).  h % 8 == 0,
  * (v / t) % 8 == 0, M and v below 2^31.  workspace >=
- * tp_vocab_logits_backward_workspace_bytes (needed if dH is; NULL where that is 0). */
+ * tp_vocab_logits_backward_workspace_bytes (needed if dH is; NULL where that is 0),
+ * its contents need no preparation; calls that overlap on the GPU need one each. */
 TP_API int tp_vocab_logits_backward(const tp_bf16* H, int64_t M, int32_t h, const tp_bf16* W, int64_t v, int32_t t,
                                     const tp_bf16* dlogits, tp_bf16* dH, float* dW, int accumulate, void* workspace,
                                     size_t ws_bytes, void* stream);
@@ -637,8 +639,8 @@ TP_API int tp_grad_clip_workspace_bytes(int32_t count, size_t* bytes);
  *   N = sqrt(sum over all tensors and elements of g^2),
  *   dst = g * min(1, max_norm / N).
  * Weights are whole here, so a replicated parameter counts once.  Squares are
- * summed in fp32, a few dozen at a time, and the sums in fp64 in a fixed order:
- * repeated calls give the same bits, and no finite gradients over- or underflow.
+ * summed in fp32, a few dozen at a time, their sums as pairs of fp32 and then in
+ * fp64, in a fixed order: repeated calls give the same bits, and no finite gradients over- or underflow.
  * With an infinity or NaN among the gradients norm says so (inf or NaN) and dst
  * = g.  Tensors whose factor is 1 and whose dst is src are not written.
  * grads: host array [count], read during the call; its device pointers must be
