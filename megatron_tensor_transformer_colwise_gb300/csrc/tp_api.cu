@@ -1698,10 +1698,13 @@ extern "C" int tp_vocab_logits_backward(const tp_bf16* H, int64_t M, int32_t h, 
         g.N = h;
         g.K = M;
         // The tensor cores' fp32 sums round towards zero at each step, an error that
-        // grows with their length (2.1e-6 of the norm over 2048 tokens, 9.1e-6 over
-        // 8192): the sums of 1024 tokens each are added to nearest (1.0e-6 at any
-        // length; both gradients of 2048 x 1024 x 32768 take 185 us instead of 171).
-        g.k_seg = 1024;
+        // grows with their length (2.5e-6 of the norm over 2048 tokens, 9.1e-6 over
+        // 8192): the sums of 768 tokens each are added to nearest (9.0e-7).  2048 x
+        // 32768 x 1024, dW alone / its error: whole 87 us / 2.5e-6, by 1024 100 /
+        // 1.27e-6, by 768 116 / 9.0e-7, by 640 140 / 7.9e-7, by 512 135 / 6.6e-7 (an
+        // fp32 product in a library's order: 8.1e-7); each sum beyond the first adds
+        // 128 MB of dW in L2.
+        g.k_seg = 768;
         g.A = dlogits;
         g.lda = v;
         g.B0 = H;

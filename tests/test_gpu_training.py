@@ -534,6 +534,9 @@ def run_output(H, W, d, dH=None, dW=None, accumulate=False, t=1, want=(True, Tru
     return dH, dW
 
 
+SEG = 768  # tokens of dW that one tensor-core sum takes
+
+
 @pytest.mark.parametrize("M,v,h,t", [(1, 8, 8, 1), (5, 64, 16, 8), (130, 2048, 64, 2), (300, 4608, 128, 8), (257, 1032, 264, 1), (64, 32768, 256, 4),
                                      (700, 8200, 520, 1), (1024, 50264, 72, 1)])
 def test_output_gradients(M, v, h, t):
@@ -550,18 +553,30 @@ def test_output_gradients(M, v, h, t):
     assert torch.equal(one, dH) and torch.equal(two, dW)
     old = normal((v, h), 4, 1.0, torch.float32)
     more = run_output(dev(H), dev(W), dev(d), dW=dev(old).clone(), accumulate=True, t=t)[1]
-    within(host64(more), host64(old) + host64(dW), U * np.abs(host64(old) + host64(dW)), "dW added")
+    # Sums s1, s2, .. of SEG tokens each, the same bits in both calls, are added in order:
+    # each partial sum old + s1 + .. + sj is rounded once, and without old each but s1 itself,
+    # so that the two differ by at most U (sum over j of |old + s1 + .. + sj| + sum over j > 1
+    # of |s1 + .. + sj|).  The partial sums are taken from 64 bits; what the tensor cores'
+    # fall short of those, below 2^-20 of the sum of magnitudes here, counts beside them.
+    old64, bound = host64(old), U * np.abs(host64(old) + host64(dW))
+    for at in range(SEG, M, SEG):
+        s = (D[:at].T @ Hd[:at]).cpu().numpy()
+        bound = bound + U * (1 + 2.0 ** -10) * np.abs(old64 + s) + U * 2.0 ** -20 * (np.abs(old64) + sw.cpu().numpy())
+    if M > SEG:
+        parts = [np.abs((D[:at].T @ Hd[:at]).cpu().numpy()) for at in range(2 * SEG, M, SEG)] + [np.abs(host64(dW))]
+        bound = bound + U * (1 + 2.0 ** -10) * sum(parts)
+    within(host64(more), old64 + host64(dW), bound, "dW added")
 
 
 @pytest.mark.parametrize("M,v,h", [(2500, 520, 264), (4100, 1032, 128), (1025, 264, 520)])
 def test_output_gradients_of_many_tokens(M, v, h):
-    # Several sums of 1024 tokens each, added to what is there, the same bits every time.
+    # Several sums of SEG tokens each, added to what is there, the same bits every time.
     H, W, d, old = normal((M, h), 1), normal((v, h), 2), normal((M, v), 3), normal((v, h), 4, 30.0, torch.float32)
     x = [dev(a) for a in (H, W, d)]
     dW = run_output(*x)[1]
     D, Hd = x[2].double(), x[0].double()
     ref, size = D.T @ Hd, D.abs().T @ Hd.abs()
-    bound = (1024 / 16 + 16) * 2.0 ** -22 * size + (M / 1024 + 1) * U * (size + dev(old).double().abs())
+    bound = (SEG / 16 + 16) * 2.0 ** -22 * size + (M / SEG + 1) * U * (size + dev(old).double().abs())
     assert ((dW.double() - ref).abs() <= bound).all()
     more = run_output(*x, dW=dev(old).clone(), accumulate=True)[1]
     assert ((more.double() - ref - dev(old).double()).abs() <= bound).all()
